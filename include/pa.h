@@ -479,6 +479,177 @@ pa_status pa_copy_blocks(void* k_cache, void* v_cache, const int32_t* block_pair
                          int num_blocks, int elem_bytes, pa_stream_t stream);
 
 /*
+ * pa_tree -- attention of trees of drafted tokens over the paged cache.
+ *
+ * Source: "PagedAttention in mistral.rs" (speculative decoding in the feature
+ * list: a draft's tokens are verified against the paged cache at once). Where
+ * a draft branches, a node must not see its siblings, so causal prefill does
+ * not serve it. Sequence s owns query tokens (nodes) [cu_q[s], cu_q[s+1])
+ * (q_len_s of them, q_len_s <= max_q_len); node i's K and V are cached at
+ * position n_s - q_len_s + i of its n_s = context_lens[s] tokens (written by
+ * pa_reshape_and_cache in any order of the tree). Node i sees every context
+ * token j < n_s - q_len_s and the nodes k whose bit is set in its mask:
+ *   bit (k % 64) of tree_mask[cu_q[s] + i][k / 64]
+ * (k = i must be set for a node to see itself; any set of bits is allowed, and
+ * bits of k >= q_len_s are ignored).
+ *   out[cu_q[s] + i][h][:] = sum_j softmax_j seen(scale * q . K_j) V_j,
+ * kv head h / G; a zero row where nothing is seen. fp32 accumulation; the
+ * weights are rounded to the input type before P.V (tensor cores), the running
+ * sum takes them unrounded; output rounded to q_dtype. No window. The cached
+ * rows of a sequence's n_s tokens must be finite for every node to be
+ * (an unseen token's weight is zero, and zero times infinity is NaN); rows past n_s may
+ * hold anything.
+ *
+ * out, query   : [T][Hq][D] of q_dtype (BF16 or F16, else PA_ERR_DTYPE).
+ * k_cache,
+ * v_cache      : [NB][Hkv][bs][D] of q_dtype.
+ * block_tables : int32 [S][MB].  cu_q : int32 [S + 1].  context_lens :
+ *                int32 [S].  tree_mask : 64-bit words [T][mask_words].
+ * workspace    : at least pa_tree_workspace_size() bytes (PA_ERR_NULL /
+ *                PA_ERR_WORKSPACE), 16-byte aligned; contents on entry do not
+ *                matter. Calls that may overlap on the GPU need one each.
+ * Supported: D in {64, 128} (PA_ERR_HEAD_DIM); bs in {16, 32, 64}
+ * (PA_ERR_BLOCK_SIZE); G in 1..8; 1 <= max_q_len <= T, 64 * mask_words >=
+ * max_q_len, Hkv * ceil(max_q_len * G / 128) <= 65535 and NB * Hkv * bs <=
+ * 2^31 - 1 cache rows (PA_ERR_SHAPE). Pointers 16-byte aligned (tree_mask: 8).
+ * Device-side checks: offsets that do not fit [0, T] or a q_len above
+ * max_q_len set PA_DEVERR_SEQ and that sequence is not written; n_s < q_len_s
+ * or n_s > MB * bs sets PA_DEVERR_CONTEXT_LEN and its rows are zero; a block
+ * id outside [0, NB) sets PA_DEVERR_BLOCK_ID and reads as zeros. T == 0 or
+ * S == 0 is a no-op. Two launches: the attention on equal shares of the work,
+ * then the join of the rows that the shares cut, in a fixed order (the same
+ * inputs give the same bits on the same device).
+ */
+size_t pa_tree_workspace_size(int num_heads, int num_kv_heads, int head_dim);
+pa_status pa_tree(void* out, const void* query, const void* k_cache, const void* v_cache,
+                  const int32_t* block_tables, const int32_t* cu_q,
+                  const int32_t* context_lens, const uint64_t* tree_mask, int num_tokens,
+                  int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                  int num_blocks, int max_blocks_per_seq, int max_q_len, int mask_words,
+                  float scale, pa_dtype q_dtype, void* workspace, size_t workspace_bytes,
+                  pa_stream_t stream);
+
+/*
+ * pa_tree_int8 / pa_tree_fp8 -- pa_tree over an INT8 cache with per-row
+ * scales or an FP8 E4M3 cache with per-tensor scales. Same computation,
+ * arguments and errors, with the dequantisation, the f16 operands and the
+ * additional errors of pa_prefill_int8 / pa_prefill_fp8; pages are moved by
+ * 1-D bulk copies (no limit on the cache's rows).
+ */
+pa_status pa_tree_int8(void* out, const void* query, const int8_t* k_cache,
+                       const int8_t* v_cache, const float* k_scales, const float* v_scales,
+                       const int32_t* block_tables, const int32_t* cu_q,
+                       const int32_t* context_lens, const uint64_t* tree_mask, int num_tokens,
+                       int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                       int block_size, int num_blocks, int max_blocks_per_seq, int max_q_len,
+                       int mask_words, float scale, pa_dtype q_dtype, void* workspace,
+                       size_t workspace_bytes, pa_stream_t stream);
+pa_status pa_tree_fp8(void* out, const void* query, const uint8_t* k_cache,
+                      const uint8_t* v_cache, const int32_t* block_tables, const int32_t* cu_q,
+                      const int32_t* context_lens, const uint64_t* tree_mask, int num_tokens,
+                      int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                      int block_size, int num_blocks, int max_blocks_per_seq, int max_q_len,
+                      int mask_words, float scale, float k_scale, float v_scale,
+                      pa_dtype q_dtype, void* workspace, size_t workspace_bytes,
+                      pa_stream_t stream);
+
+/*
+ * pa_decode_scored / pa_decode_scored_int8 -- pa_decode (window 0) that also
+ * accumulates every cached token's attention weight.
+ *
+ * Sources: the decode of "PagedAttention in mistral.rs", whose cache is a pool
+ * of fixed size; "Rolling buffer cache" bounds a cache by age, these calls with
+ * pa_evict_select and pa_compact bound it by use.
+ *   out            as pa_decode / pa_decode_int8,
+ *   scores[s][g][j] += sum over the G heads h of kv head g of softmax(logit_h)_j
+ * for j in [0, n_s); other entries are left as they are. scores: in/out, fp32
+ * [S][Hkv][MB * bs], in the sequence's own token order (not by block, so
+ * sequences that share blocks do not add to the same word), 16-byte aligned.
+ * The weights are those of the fp32 softmax (the running sum takes them
+ * before any rounding for the tensor cores). A bad block id's tokens add
+ * nothing. workspace: at least pa_decode_scored_workspace_size() bytes
+ * (PA_ERR_NULL / PA_ERR_WORKSPACE), 16-byte aligned, contents on entry do not
+ * matter; its size grows with S * Hq * MB * bs (the logits wait in it for
+ * their row's sum). Other arguments and errors as pa_decode / pa_decode_int8.
+ * Same inputs give the same bits on the same device. S == 0 is a no-op.
+ */
+size_t pa_decode_scored_workspace_size(int num_seqs, int num_heads, int num_kv_heads,
+                                       int head_dim, int block_size, int max_blocks_per_seq);
+pa_status pa_decode_scored(void* out, float* scores, const void* query, const void* k_cache,
+                           const void* v_cache, const int32_t* block_tables,
+                           const int32_t* context_lens, int num_seqs, int num_heads,
+                           int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                           int max_blocks_per_seq, float scale, pa_dtype q_dtype,
+                           pa_kv_dtype kv_dtype, float k_scale, float v_scale, void* workspace,
+                           size_t workspace_bytes, pa_stream_t stream);
+pa_status pa_decode_scored_int8(void* out, float* scores, const void* query,
+                                const int8_t* k_cache, const int8_t* v_cache,
+                                const float* k_scales, const float* v_scales,
+                                const int32_t* block_tables, const int32_t* context_lens,
+                                int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                int block_size, int num_blocks, int max_blocks_per_seq,
+                                float scale, pa_dtype q_dtype, void* workspace,
+                                size_t workspace_bytes, pa_stream_t stream);
+
+/*
+ * pa_evict_select -- the tokens that an eviction to `budget` keeps, per
+ * sequence and kv head.
+ *
+ * Source: "Rolling buffer cache" (a cache of fixed size that forgets), by
+ * accumulated attention weight instead of by age. With n_s = context_lens[s]:
+ *   n_s <= budget: every token.
+ *   else: the first num_sink, the last num_recent, and of the others the
+ *   budget - num_sink - num_recent best scored (equal scores: the earlier
+ *   token; a NaN ranks below every number, -0 equals +0).
+ * keep      : out, int32 [S][Hkv][budget], ascending token positions; -1 past
+ *             new_lens[s].
+ * new_lens  : out, int32 [S] = min(n_s, budget).
+ * scores    : in, fp32 [S][Hkv][score_len].  context_lens : int32 [S].
+ * 1 <= budget, 0 <= num_sink, 0 <= num_recent, num_sink + num_recent <= budget,
+ * 1 <= score_len, S and Hkv <= 65535 (else PA_ERR_SHAPE). n_s outside [0, score_len] sets
+ * PA_DEVERR_CONTEXT_LEN and is clamped. S == 0 is a no-op.
+ */
+pa_status pa_evict_select(int32_t* keep, int32_t* new_lens, const float* scores,
+                          const int32_t* context_lens, int num_seqs, int num_kv_heads,
+                          int score_len, int budget, int num_sink, int num_recent,
+                          pa_stream_t stream);
+
+/*
+ * pa_compact -- move the kept rows of every sequence together, in place.
+ *
+ * Sources: as pa_evict_select, after an eviction; "PagedAttention in
+ * mistral.rs" (speculative decoding), after a verification: the accepted path
+ * of a tree becomes the sequence's next tokens. For every sequence s, kv head g and j <
+ * keep_lens[s], with a = starts ? starts[s] : 0 and n_s = context_lens[s]:
+ *   row a + j of (s, g)  <-  row keep[s][keep_heads == 1 ? 0 : g][j]
+ * for K, V, the row scales (k_scales, v_scales: both or neither) and the
+ * scores (may be NULL), whose entries [a + keep_lens[s], n_s) become zero. The
+ * result is as if every row were read before any is written. The sequence's
+ * new length is a + keep_lens[s]; the caller passes it on from there. Rows
+ * at or past the new length keep what they held.
+ * k_cache, v_cache : [NB][Hkv][bs][D] of elem_bytes (1, 2 or 4) an element;
+ *                D * elem_bytes a multiple of 16, at most 1024 (else
+ *                PA_ERR_HEAD_DIM). k_scales, v_scales: fp32 [NB][Hkv][bs].
+ *                scores: fp32 [S][Hkv][MB * bs].
+ * keep         : int32 [S][keep_heads][budget], keep_heads 1 or Hkv.
+ * keep_lens, starts, context_lens : int32 [S].  block_tables : int32 [S][MB].
+ * Precondition: the blocks written (those of positions [a, a + keep_lens[s]))
+ * belong to one sequence only (pa_copy_blocks first where they are shared).
+ * Device-side checks: a, keep_lens[s] or n_s that do not fit (0 <= a,
+ * 0 <= keep_lens[s] <= budget, a + keep_lens[s] <= n_s <= MB * bs) set
+ * PA_DEVERR_CONTEXT_LEN and the sequence is left as it is; an entry keep[j]
+ * outside [a + j, n_s) sets PA_DEVERR_SLOT, a block id outside [0, NB)
+ * PA_DEVERR_BLOCK_ID, and that row is not moved. block_size >= 1, S and Hkv
+ * <= 65535. Pointers 16-byte aligned. S == 0 is a no-op.
+ */
+pa_status pa_compact(void* k_cache, void* v_cache, float* k_scales, float* v_scales,
+                     float* scores, const int32_t* block_tables, const int32_t* context_lens,
+                     const int32_t* keep, const int32_t* keep_lens, const int32_t* starts,
+                     int num_seqs, int num_kv_heads, int keep_heads, int budget, int head_dim,
+                     int block_size, int num_blocks, int max_blocks_per_seq, int elem_bytes,
+                     pa_stream_t stream);
+
+/*
  * pa_decode_partials -- the split phase of pa_decode with an explicit plan.
  *
  * For split i of (s, h) (slots [i*P*bs, (i+1)*P*bs) intersected with

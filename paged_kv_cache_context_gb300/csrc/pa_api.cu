@@ -14,6 +14,8 @@
 #include "pa_cascade.cuh"
 #include "pa_decode.cuh"
 #include "pa_device.cuh"
+#include "pa_evict.cuh"
+#include "pa_tree.cuh"
 
 #define PA_API extern "C" __attribute__((visibility("default")))
 
@@ -1078,6 +1080,310 @@ PA_API pa_status pa_prefill_fp8(void* out, const void* query, const uint8_t* k_c
                       block_tables, cu_q, context_lens, num_tokens, num_seqs, num_heads,
                       num_kv_heads, head_dim, block_size, num_blocks, max_blocks_per_seq,
                       max_q_len, scale, q_dtype, stream);
+}
+
+// ================================================================ trees of drafted tokens
+PA_API size_t pa_tree_workspace_size(int num_heads, int num_kv_heads, int head_dim) {
+  if (num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads != 0 ||
+      (head_dim != 64 && head_dim != 128))
+    return 0;
+  return tree_workspace_bytes(head_dim);
+}
+
+// kind: the cache's, 0 = q_dtype, 1 = INT8 with row scales, 2 = FP8 E4M3.
+static pa_status tree_impl(int kind, void* out, const void* query, const void* k_cache,
+                           const void* v_cache, const float* k_scales, const float* v_scales,
+                           float k_scale, float v_scale, const int32_t* block_tables,
+                           const int32_t* cu_q, const int32_t* context_lens,
+                           const uint64_t* tree_mask, int num_tokens, int num_seqs, int num_heads,
+                           int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                           int max_blocks_per_seq, int max_q_len, int mask_words, float scale,
+                           pa_dtype q_dtype, void* workspace, size_t workspace_bytes,
+                           pa_stream_t stream) {
+  if (num_tokens < 0 || num_seqs < 0 || num_seqs > 65535) return PA_ERR_SHAPE;
+  if (num_tokens == 0 || num_seqs == 0) return PA_OK;
+  if (!out || !query || !k_cache || !v_cache || !block_tables || !cu_q || !context_lens ||
+      !tree_mask || !workspace || (kind == 1 && (!k_scales || !v_scales)))
+    return PA_ERR_NULL;
+  if (q_dtype != PA_BF16 && q_dtype != PA_F16) return PA_ERR_DTYPE;
+  if (num_heads <= 0 || num_kv_heads <= 0 || num_kv_heads > 65535 ||
+      num_heads % num_kv_heads != 0 || num_heads / num_kv_heads > 8)
+    return PA_ERR_SHAPE;
+  if (head_dim != 64 && head_dim != 128) return PA_ERR_HEAD_DIM;
+  if (block_size != 16 && block_size != 32 && block_size != 64) return PA_ERR_BLOCK_SIZE;
+  if (num_blocks <= 0 || max_blocks_per_seq <= 0 || max_q_len < 1 || max_q_len > num_tokens ||
+      mask_words < 1 || (int64_t)mask_words * 64 < max_q_len)
+    return PA_ERR_SHAPE;
+  if ((int64_t)max_blocks_per_seq * block_size > INT32_MAX - kTreeTile) return PA_ERR_SHAPE;
+  const int64_t G = num_heads / num_kv_heads;
+  if ((max_q_len * G + kTreeRows - 1) / kTreeRows * num_kv_heads > 65535) return PA_ERR_SHAPE;
+  const long long cache_rows = (long long)num_blocks * num_kv_heads * block_size;
+  if (kind == 0 && cache_rows > kMaxTcRows) return PA_ERR_SHAPE;
+  if (kind == 2 && !(isfinite(k_scale) && k_scale > 0.f && isfinite(v_scale) && v_scale > 0.f))
+    return PA_ERR_SCALE;
+  if (workspace_bytes < tree_workspace_bytes(head_dim)) return PA_ERR_WORKSPACE;
+  if (!aligned16(out) || !aligned16(query) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      !aligned16(workspace) || (reinterpret_cast<uintptr_t>(tree_mask) & 7u) ||
+      (kind == 1 && (!aligned16(k_scales) || !aligned16(v_scales))))
+    return PA_ERR_ALIGN;
+  constexpr float kLog2e = 1.4426950408889634f;
+  TreeParams p{};
+  if (kind == 0 &&
+      (!page_tensor_map(&p.tm_k, k_cache, q_dtype, head_dim, cache_rows, block_size) ||
+       !page_tensor_map(&p.tm_v, v_cache, q_dtype, head_dim, cache_rows, block_size)))
+    return PA_ERR_CUDA;
+  p.out = out;
+  p.query = query;
+  p.k_cache = static_cast<const uint8_t*>(k_cache);
+  p.v_cache = static_cast<const uint8_t*>(v_cache);
+  p.k_scales = k_scales;
+  p.v_scales = v_scales;
+  p.block_tables = block_tables;
+  p.cu_q = cu_q;
+  p.context_lens = context_lens;
+  p.mask = reinterpret_cast<const unsigned long long*>(tree_mask);
+  p.part_o = static_cast<float4*>(workspace);
+  p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) +
+                                        (size_t)kTreeMaxCtas * 2 * kTreeRows * head_dim * 4);
+  p.err = error_word();
+  p.num_seqs = num_seqs;
+  p.num_heads = num_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.group = static_cast<int>(G);
+  p.block_size = block_size;
+  p.num_blocks = num_blocks;
+  p.num_tokens = num_tokens;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.max_q_len = max_q_len;
+  p.mask_words = mask_words;
+  p.scale_log2 = scale * kLog2e * (kind == 2 ? k_scale : 1.f);
+  p.v_scale = kind == 2 ? v_scale : 1.f;
+  return launch_tree_attention(p, head_dim, q_dtype, kind,
+                               reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+PA_API pa_status pa_tree(void* out, const void* query, const void* k_cache, const void* v_cache,
+                         const int32_t* block_tables, const int32_t* cu_q,
+                         const int32_t* context_lens, const uint64_t* tree_mask, int num_tokens,
+                         int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                         int block_size, int num_blocks, int max_blocks_per_seq, int max_q_len,
+                         int mask_words, float scale, pa_dtype q_dtype, void* workspace,
+                         size_t workspace_bytes, pa_stream_t stream) {
+  return tree_impl(0, out, query, k_cache, v_cache, nullptr, nullptr, 1.f, 1.f, block_tables, cu_q,
+                   context_lens, tree_mask, num_tokens, num_seqs, num_heads, num_kv_heads, head_dim,
+                   block_size, num_blocks, max_blocks_per_seq, max_q_len, mask_words, scale, q_dtype,
+                   workspace, workspace_bytes, stream);
+}
+
+PA_API pa_status pa_tree_int8(void* out, const void* query, const int8_t* k_cache,
+                              const int8_t* v_cache, const float* k_scales, const float* v_scales,
+                              const int32_t* block_tables, const int32_t* cu_q,
+                              const int32_t* context_lens, const uint64_t* tree_mask,
+                              int num_tokens, int num_seqs, int num_heads, int num_kv_heads,
+                              int head_dim, int block_size, int num_blocks, int max_blocks_per_seq,
+                              int max_q_len, int mask_words, float scale, pa_dtype q_dtype,
+                              void* workspace, size_t workspace_bytes, pa_stream_t stream) {
+  return tree_impl(1, out, query, k_cache, v_cache, k_scales, v_scales, 1.f, 1.f, block_tables,
+                   cu_q, context_lens, tree_mask, num_tokens, num_seqs, num_heads, num_kv_heads,
+                   head_dim, block_size, num_blocks, max_blocks_per_seq, max_q_len, mask_words,
+                   scale, q_dtype, workspace, workspace_bytes, stream);
+}
+
+PA_API pa_status pa_tree_fp8(void* out, const void* query, const uint8_t* k_cache,
+                             const uint8_t* v_cache, const int32_t* block_tables,
+                             const int32_t* cu_q, const int32_t* context_lens,
+                             const uint64_t* tree_mask, int num_tokens, int num_seqs,
+                             int num_heads, int num_kv_heads, int head_dim, int block_size,
+                             int num_blocks, int max_blocks_per_seq, int max_q_len, int mask_words,
+                             float scale, float k_scale, float v_scale, pa_dtype q_dtype,
+                             void* workspace, size_t workspace_bytes, pa_stream_t stream) {
+  return tree_impl(2, out, query, k_cache, v_cache, nullptr, nullptr, k_scale, v_scale,
+                   block_tables, cu_q, context_lens, tree_mask, num_tokens, num_seqs, num_heads,
+                   num_kv_heads, head_dim, block_size, num_blocks, max_blocks_per_seq, max_q_len,
+                   mask_words, scale, q_dtype, workspace, workspace_bytes, stream);
+}
+
+// ================================================================ eviction by attention weight
+// Workspace of a scored decode: the balanced mode's, every row's statistics,
+// then the logits.
+static size_t scored_stats_offset(int GT, int D) { return align256(balanced_bytes(GT, D)); }
+static size_t scored_logits_offset(int GT, int D, int S, int Hq) {
+  return scored_stats_offset(GT, D) + align256((size_t)S * Hq * sizeof(float2));
+}
+
+PA_API size_t pa_decode_scored_workspace_size(int num_seqs, int num_heads, int num_kv_heads,
+                                              int head_dim, int block_size,
+                                              int max_blocks_per_seq) {
+  if (num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads != 0 ||
+      num_heads / num_kv_heads > 8 || head_dim <= 0 || block_size <= 0 || max_blocks_per_seq <= 0)
+    return 0;
+  const int GT = group_bucket(num_heads / num_kv_heads);
+  return scored_logits_offset(GT, head_dim, num_seqs, num_heads) +
+         (size_t)num_seqs * num_heads * max_blocks_per_seq * block_size * sizeof(float);
+}
+
+static cudaError_t run_scored(const DecodeParams& prm_in, const DecodeShape& a, cudaStream_t st) {
+  const int GT = group_bucket(a.Hq / a.Hkv);
+  const dim3 grid(0, 1, 1);
+  DecodeParams prm = prm_in;
+  if (decode_is_tma_staged(a)) {
+    const long long rows = (long long)a.NB * a.Hkv * a.bs;
+    const int mt = a.kv_dtype == PA_KV_AUTO ? a.q_dtype : -1;
+    if (rows > kMaxTcRows || !page_tensor_map(&prm.tm_k, prm.k_cache, mt, a.D, rows, a.bs) ||
+        !page_tensor_map(&prm.tm_v, prm.v_cache, mt, a.D, rows, a.bs))
+      return cudaErrorInvalidValue;
+  }
+  if (a.kv_dtype == PA_KV_AUTO) {
+    switch (a.q_dtype) {
+      case PA_F32: return pa_dispatch_scored_f32_f32(prm, grid, a.D, GT, a.bs, st);
+      case PA_BF16: return pa_dispatch_scored_bf16_bf16(prm, grid, a.D, GT, a.bs, st);
+      default: return pa_dispatch_scored_f16_f16(prm, grid, a.D, GT, a.bs, st);
+    }
+  }
+  if (a.kv_dtype == PA_KV_INT8)
+    return a.q_dtype == PA_BF16 ? pa_dispatch_scored_bf16_i8(prm, grid, a.D, GT, a.bs, st)
+                                : pa_dispatch_scored_f16_i8(prm, grid, a.D, GT, a.bs, st);
+  switch (a.q_dtype) {
+    case PA_F32: return pa_dispatch_scored_f32_e4m3(prm, grid, a.D, GT, a.bs, st);
+    case PA_BF16: return pa_dispatch_scored_bf16_e4m3(prm, grid, a.D, GT, a.bs, st);
+    default: return pa_dispatch_scored_f16_e4m3(prm, grid, a.D, GT, a.bs, st);
+  }
+}
+
+static pa_status scored_impl(const DecodeShape& a, void* out, float* scores, const void* query,
+                             const void* k_cache, const void* v_cache, const float* k_scales,
+                             const float* v_scales, const int32_t* block_tables,
+                             const int32_t* context_lens, float scale, void* workspace,
+                             size_t workspace_bytes, pa_stream_t stream) {
+  if (!scores || !workspace) return PA_ERR_NULL;
+  if ((int64_t)a.MB * a.bs > INT32_MAX - 4 * 256) return PA_ERR_SHAPE;
+  if (workspace_bytes <
+      pa_decode_scored_workspace_size(a.S, a.Hq, a.Hkv, a.D, a.bs, a.MB))
+    return PA_ERR_WORKSPACE;
+  if (!aligned16(scores) || !aligned16(workspace)) return PA_ERR_ALIGN;
+  const int GT = group_bucket(a.Hq / a.Hkv);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  DecodeParams p =
+      make_params(a, query, k_cache, v_cache, block_tables, context_lens, scale, error_word());
+  const BalancedWs w = balanced_carve(workspace, GT, a.D);
+  p.out = out;
+  p.k_scales = k_scales;
+  p.v_scales = v_scales;
+  p.piece_o = w.piece_o;
+  p.piece_ml = w.piece_ml;
+  p.arrived = w.arrived;
+  p.num_splits = 1;
+  p.pages_per_split = 1;
+  p.row_stats = reinterpret_cast<float2*>(ws + scored_stats_offset(GT, a.D));
+  p.logits = reinterpret_cast<float*>(ws + scored_logits_offset(GT, a.D, a.S, a.Hq));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const pa_status rc = pa_decode_workspace_clear(workspace, workspace_bytes, stream);
+  if (rc != PA_OK) return rc;
+  if (run_scored(p, a, st) != cudaSuccess) return PA_ERR_CUDA;
+  ScoresParams sp{scores, p.logits, p.row_stats, block_tables, context_lens, a.S,
+                  a.Hq,   a.Hkv,    a.Hq / a.Hkv, a.bs,        a.NB,         a.MB};
+  return launch_scores(sp, st) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+PA_API pa_status pa_decode_scored(void* out, float* scores, const void* query, const void* k_cache,
+                                  const void* v_cache, const int32_t* block_tables,
+                                  const int32_t* context_lens, int num_seqs, int num_heads,
+                                  int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                                  int max_blocks_per_seq, float scale, pa_dtype q_dtype,
+                                  pa_kv_dtype kv_dtype, float k_scale, float v_scale,
+                                  void* workspace, size_t workspace_bytes, pa_stream_t stream) {
+  const DecodeShape a{num_seqs, num_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                      max_blocks_per_seq, 0, q_dtype, kv_dtype, k_scale, v_scale};
+  const pa_status rc = check_decode(a, out, query, k_cache, v_cache, block_tables, context_lens);
+  if (rc != PA_OK || num_seqs == 0) return rc;
+  return scored_impl(a, out, scores, query, k_cache, v_cache, nullptr, nullptr, block_tables,
+                     context_lens, scale, workspace, workspace_bytes, stream);
+}
+
+PA_API pa_status pa_decode_scored_int8(void* out, float* scores, const void* query,
+                                       const int8_t* k_cache, const int8_t* v_cache,
+                                       const float* k_scales, const float* v_scales,
+                                       const int32_t* block_tables, const int32_t* context_lens,
+                                       int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                       int block_size, int num_blocks, int max_blocks_per_seq,
+                                       float scale, pa_dtype q_dtype, void* workspace,
+                                       size_t workspace_bytes, pa_stream_t stream) {
+  // the shared checks, on the shape with a native cache
+  DecodeShape a{num_seqs, num_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                max_blocks_per_seq, 0, q_dtype, PA_KV_AUTO, 1.f, 1.f};
+  const pa_status rc = check_decode(a, out, query, k_cache, v_cache, block_tables, context_lens);
+  if (rc != PA_OK || num_seqs == 0) return rc;
+  if (q_dtype != PA_BF16 && q_dtype != PA_F16) return PA_ERR_DTYPE;
+  if (!k_scales || !v_scales) return PA_ERR_NULL;
+  if (!aligned16(k_scales) || !aligned16(v_scales)) return PA_ERR_ALIGN;
+  a.kv_dtype = PA_KV_INT8;
+  return scored_impl(a, out, scores, query, k_cache, v_cache, k_scales, v_scales, block_tables,
+                     context_lens, scale, workspace, workspace_bytes, stream);
+}
+
+PA_API pa_status pa_evict_select(int32_t* keep, int32_t* new_lens, const float* scores,
+                                 const int32_t* context_lens, int num_seqs, int num_kv_heads,
+                                 int score_len, int budget, int num_sink, int num_recent,
+                                 pa_stream_t stream) {
+  if (num_seqs < 0 || num_seqs > 65535) return PA_ERR_SHAPE;
+  if (num_seqs == 0) return PA_OK;
+  if (!keep || !new_lens || !scores || !context_lens) return PA_ERR_NULL;
+  if (num_kv_heads <= 0 || num_kv_heads > 65535 || score_len < 1 || budget < 1 || num_sink < 0 ||
+      num_recent < 0 || (int64_t)num_sink + num_recent > budget)
+    return PA_ERR_SHAPE;
+  SelectParams p{keep,     new_lens,     scores,    context_lens, error_word(),
+                 num_seqs, num_kv_heads, score_len, budget,       num_sink,     num_recent};
+  return launch_select(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
+                                                                                 : PA_ERR_CUDA;
+}
+
+PA_API pa_status pa_compact(void* k_cache, void* v_cache, float* k_scales, float* v_scales,
+                            float* scores, const int32_t* block_tables,
+                            const int32_t* context_lens, const int32_t* keep,
+                            const int32_t* keep_lens, const int32_t* starts, int num_seqs,
+                            int num_kv_heads, int keep_heads, int budget, int head_dim,
+                            int block_size, int num_blocks, int max_blocks_per_seq, int elem_bytes,
+                            pa_stream_t stream) {
+  if (num_seqs < 0 || num_seqs > 65535) return PA_ERR_SHAPE;
+  if (num_seqs == 0) return PA_OK;
+  if (!k_cache || !v_cache || !block_tables || !context_lens || !keep || !keep_lens ||
+      (k_scales == nullptr) != (v_scales == nullptr))
+    return PA_ERR_NULL;
+  if (elem_bytes != 1 && elem_bytes != 2 && elem_bytes != 4) return PA_ERR_DTYPE;
+  if (num_kv_heads <= 0 || num_kv_heads > 65535 || (keep_heads != 1 && keep_heads != num_kv_heads) ||
+      budget < 1 || num_blocks <= 0 || max_blocks_per_seq <= 0)
+    return PA_ERR_SHAPE;
+  if (head_dim <= 0 || (int64_t)head_dim * elem_bytes % 16 != 0 ||
+      (int64_t)head_dim * elem_bytes > 1024)
+    return PA_ERR_HEAD_DIM;
+  if (block_size < 1) return PA_ERR_BLOCK_SIZE;
+  if ((int64_t)max_blocks_per_seq * block_size > INT32_MAX / 2) return PA_ERR_SHAPE;
+  if (!aligned16(k_cache) || !aligned16(v_cache) || (k_scales && !aligned16(k_scales)) ||
+      (v_scales && !aligned16(v_scales)) || (scores && !aligned16(scores)))
+    return PA_ERR_ALIGN;
+  CompactParams p{static_cast<uint8_t*>(k_cache),
+                  static_cast<uint8_t*>(v_cache),
+                  k_scales,
+                  v_scales,
+                  scores,
+                  block_tables,
+                  context_lens,
+                  keep,
+                  keep_lens,
+                  starts,
+                  error_word(),
+                  num_seqs,
+                  num_kv_heads,
+                  keep_heads,
+                  budget,
+                  head_dim * elem_bytes,
+                  block_size,
+                  num_blocks,
+                  max_blocks_per_seq};
+  return launch_compact(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
+                                                                                  : PA_ERR_CUDA;
 }
 
 // ================================================================ cascade

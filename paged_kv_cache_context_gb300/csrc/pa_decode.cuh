@@ -129,7 +129,12 @@ namespace pa {
 #define PA_TC8_MAX_STAGES 16
 #endif
 
-enum : int { kModeSplit = 0, kModeBalanced = 1 };
+// Scored mode is the balanced mode that also leaves every attended slot's
+// logit and every row's largest logit and sum, from which a second launch
+// adds the softmax weights to running scores. Its running sums take the
+// weights before they are rounded for the MMAs (the scores are held in 32
+// bits and want the exact normaliser).
+enum : int { kModeSplit = 0, kModeBalanced = 1, kModeScored = 2 };
 
 // Which consumers a (query type, cache type, head_dim, group bucket, block
 // size) instantiation runs, asked with the C ABI's type codes so that the
@@ -221,6 +226,8 @@ struct DecodeParams {
   float* piece_ml;      // [C][2][GT][2]: max logit (natural log), sum relative to it
   int* arrived;         // [C]: pages of a cut segment whose pieces are published,
                         // at the CTA holding the segment's last page (zero at launch)
+  float* logits;        // scored mode: [S][Hq][MB * bs], log2 units
+  float2* row_stats;    // scored mode: [S][Hq]: largest logit (log2 units), sum relative to it
   // inputs
   const void* query;    // [S][Hq][D] of QT
   const uint8_t* k_cache;
@@ -269,9 +276,12 @@ constexpr int choose_pb(int bytes) {
 
 template <typename QT, typename CT, int D, int GT, int BS, int MODE = kModeBalanced>
 struct Layout {
+  static constexpr bool BAL = MODE != kModeSplit;      // persistent CTAs, equal shares
+  static constexpr bool SCORED = MODE == kModeScored;
   static constexpr int EB = Elem<CT>::bytes;
   static constexpr int QB = Elem<QT>::bytes;
   static constexpr int ROWB = D * EB;      // bytes of one cached row
+  static constexpr int BSZ = BS;           // rows of a page
   static constexpr int PAGE = BS * ROWB;   // bytes of one (block, kv head) page
   static constexpr bool TC = uses_tc<QT, CT, D, GT, BS>();    // 16-bit cache on MMAs
   static constexpr bool TC8 = uses_tc8<QT, CT, D, GT, BS>();  // 8-bit cache on MMAs
@@ -483,7 +493,8 @@ __device__ __forceinline__ void process_pages(PieceState<Ly, GT>& st,
                                               const float* const (&Ks)[Ly::R],
                                               const float* const (&Vs)[Ly::R],
                                               const int (&lim)[Ly::R], float* wscr, int warp,
-                                              int lane, int c, int rg) {
+                                              int lane, int c, int rg, float* lg, size_t lcap,
+                                              int G) {
   constexpr int R = Ly::R, TPW = Ly::TPW, RPW = Ly::RPW, LPR = Ly::LPR, NV = Ly::NV;
   constexpr int NG = Ly::NG, NFIN = Ly::NFIN, RED = Ly::RED, EP2 = Ly::EP2, EL2 = Ly::EL2;
   constexpr float kLazy = 8.f;  // weights stay <= 2^kLazy
@@ -532,6 +543,11 @@ __device__ __forceinline__ void process_pages(PieceState<Ly, GT>& st,
         logit *= ks[warp * TPW + t % TPW];
       }
       sl[sg][kk] = (writer && (t % TPW) < lim_t) ? logit : -INFINITY;
+      if constexpr (Ly::SCORED) {
+        const int h = ((c * NV) / LPR + kk) % GT;
+        if (writer && h < G && (t % TPW) < lim_t)
+          lg[h * lcap + (t / TPW) * Ly::BSZ + warp * TPW + t % TPW] = logit;
+      }
     }
   }
 
@@ -662,7 +678,7 @@ template <typename QT, typename Ly, int D>
 __device__ __forceinline__ void process_tc(TcState<D>& st, const uint8_t* const (&Kp)[Ly::R],
                                            const uint8_t* const (&Vp)[Ly::R],
                                            const int (&rows)[Ly::R], int warp, int lane,
-                                           float q_scale, int G) {
+                                           float q_scale, int G, float* lg, size_t lcap) {
   constexpr int R = Ly::R, SPP = Ly::SPP;
   constexpr float kLazy = 8.f;  // weights stay <= 2^kLazy
   using M = Mma<QT>;
@@ -708,6 +724,14 @@ __device__ __forceinline__ void process_tc(TcState<D>& st, const uint8_t* const 
   const int tok[4] = {2 * t, 2 * t + 1, 8 + 2 * t, 9 + 2 * t};
 #pragma unroll
   for (int j = 0; j < 4; ++j) x[j] = (real && tok[j] < lim) ? x[j] : -INFINITY;
+  if constexpr (Ly::SCORED) {
+    // whole pairs: a page's 16-row slices lie inside the sequence's row of logits
+    if (real) {
+      float* dst = lg + g * lcap + pr * Ly::BSZ + r0 + 2 * t;
+      *reinterpret_cast<float2*>(dst) = make_float2(x[0], x[1]);
+      *reinterpret_cast<float2*>(dst + 8) = make_float2(x[2], x[3]);
+    }
+  }
   float tm = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
   tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 1));
   tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 2));
@@ -725,10 +749,15 @@ __device__ __forceinline__ void process_tc(TcState<D>& st, const uint8_t* const 
   }
 
   // ---- weights 2^(s - m), rounded to the cache type as the MMA takes them
-  uint32_t pa0 = M::pack(exp2f(x[0] - st.m_run), exp2f(x[1] - st.m_run));
-  uint32_t pa2 = M::pack(exp2f(x[2] - st.m_run), exp2f(x[3] - st.m_run));
+  const float w0 = exp2f(x[0] - st.m_run), w1 = exp2f(x[1] - st.m_run);
+  const float w2 = exp2f(x[2] - st.m_run), w3 = exp2f(x[3] - st.m_run);
+  uint32_t pa0 = M::pack(w0, w1);
+  uint32_t pa2 = M::pack(w2, w3);
   if (!real) pa0 = pa2 = 0u;  // padding rows: m_run stays -inf, weights would be NaN
-  st.l_run += M::sum2(pa0) + M::sum2(pa2);
+  if constexpr (Ly::SCORED)
+    st.l_run += real ? (w0 + w1) + (w2 + w3) : 0.f;
+  else
+    st.l_run += M::sum2(pa0) + M::sum2(pa2);
   const uint32_t a[4] = {pa0, 0u, pa2, 0u};
 
   // ---- O += P V (16 n8 tiles of head_dim for D 128); rows past the
@@ -934,7 +963,7 @@ __device__ __forceinline__ void process_tc8(Tc8State<D>& st, const uint8_t* cons
                                             const float* const (&Ks)[Ly::R],
                                             const float* const (&Vs)[Ly::R],
                                             const int (&rows)[Ly::R], int warp, int lane,
-                                            float q_scale) {
+                                            float q_scale, int G, float* lg, size_t lcap) {
   constexpr int R = Ly::R, SPP = Ly::SPP, SW = Ly::SW;
   constexpr float kLazy = 8.f;
   const int g = lane >> 2, t = lane & 3;
@@ -973,6 +1002,12 @@ __device__ __forceinline__ void process_tc8(Tc8State<D>& st, const uint8_t* cons
   for (int j = 0; j < SW; ++j) {
     if (j == 0 || lim[j] > 0) {
       tc8_logits<Ly, CT, D>(st, kp[j], ksc[j], r0[j], kr, t, lim[j], q_scale, x[j]);
+      if constexpr (Ly::SCORED) {
+        float* dst = lg + ((warp * SW + j) / SPP) * Ly::BSZ + r0[j] + kr;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)  // head 2t + e % 2, row kr or 8 + kr
+          if (2 * t + (e & 1) < G) dst[(2 * t + (e & 1)) * lcap + (e >> 1) * 8] = x[j][e];
+      }
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[j][e] = -INFINITY;
@@ -1028,9 +1063,14 @@ __device__ __forceinline__ void process_tc8(Tc8State<D>& st, const uint8_t* cons
     } else {
       p01 = __floats2half2_rn(pw[0], pw[1]);
       p23 = __floats2half2_rn(pw[2], pw[3]);
-      const float2 f01 = __half22float2(p01), f23 = __half22float2(p23);
-      st.l_run[0] += f01.x + f23.x;
-      st.l_run[1] += f01.y + f23.y;
+      if constexpr (Ly::SCORED) {
+        st.l_run[0] += pw[0] + pw[2];
+        st.l_run[1] += pw[1] + pw[3];
+      } else {
+        const float2 f01 = __half22float2(p01), f23 = __half22float2(p23);
+        st.l_run[0] += f01.x + f23.x;
+        st.l_run[1] += f01.y + f23.y;
+      }
     }
     const uint32_t pb0 = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&p01));
     const uint32_t pb1 = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&p23));
@@ -1133,7 +1173,8 @@ __device__ __forceinline__ void merge_warps(const float* mstat, const float* mac
                                             uint32_t& cphase, int G, int warp, int lane,
                                             float v_scale, unsigned* err, Sink&& sink) {
   constexpr int NC = Ly::NC;
-  constexpr float kLn2 = 0.69314718055994530942f;
+  // the maximum in natural-log units; in scored mode it stays in log2 units
+  constexpr float kLn2 = Ly::SCORED ? 1.f : 0.69314718055994530942f;
   const float* mm = mstat;
   const float* ml = mstat + NC * GT;
   const float* mt = mstat + 2 * NC * GT;
@@ -1320,13 +1361,14 @@ __device__ __forceinline__ void combine_segment(const DecodeParams& p, QT* out, 
       for (int u = 0; u < U; ++u) {
         if (ml[u].y > 0.f) {
           if (ml[u].x > M) {
-            const float f = expf(M - ml[u].x);
+            const float f = Ly::SCORED ? exp2f(M - ml[u].x) : expf(M - ml[u].x);
             lsum *= f;
 #pragma unroll
             for (int t = 0; t < DPL; ++t) acc[t] *= f;
             M = ml[u].x;
           }
-          const float w = ml[u].y * expf(ml[u].x - M);
+          const float w =
+              ml[u].y * (Ly::SCORED ? exp2f(ml[u].x - M) : expf(ml[u].x - M));
           lsum += w;
 #pragma unroll
           for (int t = 0; t < DPL; ++t) acc[t] = fmaf(w, o[u][t], acc[t]);
@@ -1336,6 +1378,10 @@ __device__ __forceinline__ void combine_segment(const DecodeParams& p, QT* out, 
     const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
 #pragma unroll
     for (int t = 0; t < DPL; ++t) out[h * D + lane + 32 * t] = Elem<QT>::from_f32(acc[t] * inv);
+    if constexpr (Ly::SCORED) {
+      if (lane == 0)
+        p.row_stats[(out - static_cast<const QT*>(p.out)) / D + h] = make_float2(M, lsum);
+    }
   }
 }
 
@@ -1520,7 +1566,7 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p) {
     // it, and the tail piece (the range ends inside its segment), recorded
     // for the consumers, who count it themselves at the end
     long long lo = 0, P = 1;
-    if constexpr (MODE == kModeBalanced) {
+    if constexpr (MODE != kModeSplit) {
       lo = misc64[0];
       P = misc64[1];
     }
@@ -1540,7 +1586,7 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p) {
         piece_end = k + len - 1;
         piece_flags = (pg == 0 ? kSegFirst : 0) | (pg + len == pages ? kSegLast : 0) |
                       (k > 0 ? kSlot1 : 0);
-        if constexpr (MODE == kModeBalanced) {
+        if constexpr (MODE != kModeSplit) {
           if (pg != 0 || pg + len != pages) {  // cut
             const bool tail = k + len == npages;
             if (!tail) {
@@ -1567,7 +1613,7 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p) {
           const int rows = ok ? min(BS, L - pg * BS) : 0;
           const int flags = piece_flags | (piece_start ? kFirst : 0) | (k == piece_end ? kLast : 0) |
                             (k == npages - 1 ? kCtaLast : 0);
-          desc[slot] = make_int4(rows, s * Hkv + g, flags, 0);
+          desc[slot] = make_int4(rows, s * Hkv + g, flags, pg);
           uint8_t* stage = smem + slot * Ly::STAGE;
           const uint32_t bytes =
               (ok ? 2u * (Ly::PAGE + Ly::SCB) : 0u) + (piece_start ? qbytes : 0u);
@@ -1606,7 +1652,7 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p) {
         }
       }
       if (__shfl_sync(0xffffffffu, aborted ? 1 : 0, 0)) break;
-      if constexpr (MODE == kModeBalanced) {
+      if constexpr (MODE != kModeSplit) {
         // the wait above saw the head piece's last stage released: count it
         // now, with this iteration's copies already in flight
         if (h_on && k == h_k + STAGES) {
@@ -1619,7 +1665,7 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p) {
       ++pg;
       if (k == piece_end) {
         piece_start = true;
-        if constexpr (MODE == kModeBalanced) {
+        if constexpr (MODE != kModeSplit) {
           if (pg == pages && k + 1 < npages) {
             pg = 0;
             if (++g == Hkv) {
@@ -1641,7 +1687,7 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p) {
         if (!mbar_wait_bounded(&full[k % STAGES], (k / STAGES) & 1))
           raise_error(p.err, PA_DEVERR_TIMEOUT);
     }
-    if constexpr (MODE == kModeBalanced) {
+    if constexpr (MODE != kModeSplit) {
       // a head piece whose last stage was not reused: wait for the consumers
       // to release it, then count it (skipped after any timeout)
       if (h_on && __shfl_sync(0xffffffffu, aborted ? 0 : 1, 0)) {
@@ -1688,7 +1734,7 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p) {
     const float* Ks[R];
     const float* Vs[R];
     int lim[R], rows[R];
-    int n_here = 0, last_flags = 0, seg = 0, last_slot = 0;
+    int n_here = 0, last_flags = 0, seg = 0, last_slot = 0, first_page = 0;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       lim[r] = 0;
@@ -1708,6 +1754,7 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p) {
       uint8_t* stage = smem + slot * Ly::STAGE;
       if (r == 0) {
         seg = d.y;
+        first_page = d.w;
         if (d.z & kFirst) {
           if constexpr (Ly::TC)
             begin_piece_tc<QT, D>(st, stage + Ly::OFF_Q, G, lane);
@@ -1729,12 +1776,20 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p) {
     }
     if (__any_sync(0xffffffffu, aborted)) break;
 
+    // scored mode: where the logits of head 0 of the group, row 0 of the first page go
+    float* lg = nullptr;
+    size_t lcap = 0;
+    if constexpr (Ly::SCORED) {
+      lcap = (size_t)MB * BS;
+      lg = p.logits + ((size_t)(seg / Hkv) * Hq + (size_t)(seg % Hkv) * G) * lcap +
+           (size_t)first_page * BS;
+    }
     if constexpr (Ly::TC)
-      process_tc<QT, Ly, D>(st, Kp, Vp, rows, warp, lane, p.q_scale, G);
+      process_tc<QT, Ly, D>(st, Kp, Vp, rows, warp, lane, p.q_scale, G, lg, lcap);
     else if constexpr (Ly::TC8)
-      process_tc8<Ly, CT, D>(st, Kp, Vp, Ks, Vs, rows, warp, lane, p.q_scale);
+      process_tc8<Ly, CT, D>(st, Kp, Vp, Ks, Vs, rows, warp, lane, p.q_scale, G, lg, lcap);
     else
-      process_pages<CT, Ly, GT>(st, Kp, Vp, Ks, Vs, lim, wscr, warp, lane, c, rg);
+      process_pages<CT, Ly, GT>(st, Kp, Vp, Ks, Vs, lim, wscr, warp, lane, c, rg, lg, lcap, G);
 
     const bool ends_piece = (last_flags & kLast) != 0;
     if (lane == 0) {
@@ -1774,9 +1829,13 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p) {
         QT* out = reinterpret_cast<QT*>(p.out) + ((size_t)s * Hq + (size_t)g * G) * D;
         float* piece_o = p.piece_o + base * GT * D;
         float* piece_ml = p.piece_ml + base * GT * 2;
+        float2* stats = p.row_stats + (size_t)s * Hq + (size_t)g * G;
         finish(macc, [=](int h, int d, float o, float m_nat, float l) {
               if (whole) {
                 out[h * D + d] = Elem<QT>::from_f32(o);
+                if constexpr (Ly::SCORED) {
+                  if (d == 0) stats[h] = make_float2(m_nat, l);
+                }
               } else {
                 piece_o[h * D + d] = o;
                 if (d == 0) {
@@ -1794,7 +1853,7 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p) {
     k += n_here;
     if (last_flags & kCtaLast) break;
   }
-  if constexpr (MODE == kModeBalanced) {
+  if constexpr (MODE != kModeSplit) {
     if (tail_cut) {
       // The tail piece, counted here. If every other piece of its segment
       // has been counted already, it completes the segment and needs no
@@ -1867,13 +1926,14 @@ cudaError_t launch_decode(const DecodeParams& prm, dim3 grid, int* ctas, cudaStr
       __atomic_fetch_or(&configured_devices, 1 << dev, __ATOMIC_RELEASE);
     }
   }
-  if (MODE == kModeBalanced && grid.x == 0)
+  if (MODE != kModeSplit && grid.x == 0)
     grid.x = dev < 32 && capacity[dev] > 0 ? capacity[dev] : kMaxBalancedCtas;
   if (ctas) *ctas = static_cast<int>(grid.x);
   return launch_pdl(kern, grid, dim3(Ly::THREADS), Ly::SMEM, stream, prm);
 }
 
-// Dispatch over (head_dim, group bucket, block size) for one (QT, CT) pair.
+// Dispatch over (head_dim, group bucket, block size) for one (QT, CT) pair:
+// the split and balanced modes, and (in units of their own) the scored mode.
 template <typename QT, typename CT>
 cudaError_t dispatch_decode(const DecodeParams& prm, dim3 grid, int D, int GT, int BS, int mode,
                             int* ctas, cudaStream_t stream) {
@@ -1912,6 +1972,37 @@ cudaError_t dispatch_decode(const DecodeParams& prm, dim3 grid, int D, int GT, i
 #undef PA_CASE_BS
 }
 
+template <typename QT, typename CT, int D, int GT>
+cudaError_t dispatch_scored_bs(const DecodeParams& prm, dim3 grid, int BS, cudaStream_t stream) {
+  switch (BS) {
+    case 16: return launch_decode<QT, CT, D, GT, 16, kModeScored>(prm, grid, nullptr, stream);
+    case 32: return launch_decode<QT, CT, D, GT, 32, kModeScored>(prm, grid, nullptr, stream);
+    case 64: return launch_decode<QT, CT, D, GT, 64, kModeScored>(prm, grid, nullptr, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+template <typename QT, typename CT, int D>
+cudaError_t dispatch_scored_gt(const DecodeParams& prm, dim3 grid, int GT, int BS,
+                               cudaStream_t stream) {
+  switch (GT) {
+    case 1: return dispatch_scored_bs<QT, CT, D, 1>(prm, grid, BS, stream);
+    case 2: return dispatch_scored_bs<QT, CT, D, 2>(prm, grid, BS, stream);
+    case 4: return dispatch_scored_bs<QT, CT, D, 4>(prm, grid, BS, stream);
+    case 8: return dispatch_scored_bs<QT, CT, D, 8>(prm, grid, BS, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+template <typename QT, typename CT>
+cudaError_t dispatch_scored(const DecodeParams& prm, dim3 grid, int D, int GT, int BS,
+                            cudaStream_t stream) {
+  switch (D) {
+    case 64: return dispatch_scored_gt<QT, CT, 64>(prm, grid, GT, BS, stream);
+    case 96: return dispatch_scored_gt<QT, CT, 96>(prm, grid, GT, BS, stream);
+    case 128: return dispatch_scored_gt<QT, CT, 128>(prm, grid, GT, BS, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
 }  // namespace pa
 
 // One translation unit per (query dtype, cache dtype) pair defines these.
@@ -1926,3 +2017,14 @@ PA_DECLARE_DISPATCH(pa_dispatch_decode_bf16_e4m3);
 PA_DECLARE_DISPATCH(pa_dispatch_decode_f16_e4m3);
 PA_DECLARE_DISPATCH(pa_dispatch_decode_bf16_i8);
 PA_DECLARE_DISPATCH(pa_dispatch_decode_f16_i8);
+#define PA_DECLARE_SCORED(NAME)                                                         \
+  cudaError_t NAME(const pa::DecodeParams& prm, dim3 grid, int D, int GT, int BS, \
+                   cudaStream_t stream)
+PA_DECLARE_SCORED(pa_dispatch_scored_f32_f32);
+PA_DECLARE_SCORED(pa_dispatch_scored_bf16_bf16);
+PA_DECLARE_SCORED(pa_dispatch_scored_f16_f16);
+PA_DECLARE_SCORED(pa_dispatch_scored_f32_e4m3);
+PA_DECLARE_SCORED(pa_dispatch_scored_bf16_e4m3);
+PA_DECLARE_SCORED(pa_dispatch_scored_f16_e4m3);
+PA_DECLARE_SCORED(pa_dispatch_scored_bf16_i8);
+PA_DECLARE_SCORED(pa_dispatch_scored_f16_i8);

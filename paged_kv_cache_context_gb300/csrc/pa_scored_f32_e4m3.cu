@@ -1,0 +1,7 @@
+// pa_scored_f32_e4m3.cu -- scored-decode instantiations for fp32 queries over an
+// FP8 E4M3 cache (one translation unit per pair, so they compile in parallel).
+#include "pa_decode.cuh"
+
+PA_DECLARE_SCORED(pa_dispatch_scored_f32_e4m3) {
+  return pa::dispatch_scored<float, pa::E4M3>(prm, grid, D, GT, BS, stream);
+}

@@ -1,0 +1,58 @@
+// pa_tree.cuh -- attention of trees of drafted tokens over the paged cache:
+// the launchers' parameters, shared by pa_tree.cu (the kernels) and
+// pa_api.cu (the entry points).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace pa {
+
+// Query rows of one tensor-core tile and cached tokens of one staged tile.
+constexpr int kTreeRows = 128;
+constexpr int kTreeTile = 64;
+// Persistent CTAs a workspace is sized for: two per SM of 152, two partial
+// slots each.
+constexpr int kTreeMaxCtas = 152 * 2;
+
+// Sequence s owns query tokens (nodes) [cu_q[s], cu_q[s + 1]); they are the
+// last q_len_s tokens of its cached context of n_s. For kv head g its rows are
+// the q_len_s * G (node, head-in-group) pairs. Work unit: one 64-token tile of
+// one (sequence, kv head, 128-row tile), flattened in that order; CTA c of C
+// takes the equal contiguous share [c P / C, (c + 1) P / C) of the P units.
+struct TreeParams {
+  CUtensorMap tm_k;  // 16-bit caches as [NB Hkv bs rows][D]: boxes of 64 x bs, 128-B swizzle
+  CUtensorMap tm_v;
+  void* out;                    // [T][Hq][D], the query's type
+  const void* query;            // [T][Hq][D]
+  const uint8_t* k_cache;       // 8-bit caches [NB][Hkv][bs][D]
+  const uint8_t* v_cache;
+  const float* k_scales;        // INT8: row scales [NB][Hkv][bs]
+  const float* v_scales;
+  const int32_t* block_tables;  // [S][MB]
+  const int32_t* cu_q;          // [S + 1]
+  const int32_t* context_lens;  // [S]: cached tokens, the nodes among them
+  const unsigned long long* mask;  // [T][mask_words]
+  float4* part_o;               // [C][2][D / 4][128]: cut pieces' un-normalised rows
+  float2* part_ml;              // [C][2][128]: their maximum (log2 units) and sum
+  unsigned* err;
+  int num_seqs, num_heads, num_kv_heads, group, block_size, num_blocks;
+  int num_tokens, max_blocks_per_seq, max_q_len, mask_words;
+  int ctas;          // C
+  float scale_log2;  // scale * log2(e) (* k_scale for an FP8 cache)
+  float v_scale;     // FP8: multiplies the output
+};
+
+// Bytes of the partials (independent of the batch).
+inline size_t tree_workspace_bytes(int D) {
+  const size_t slots = (size_t)kTreeMaxCtas * 2;
+  return slots * kTreeRows * D * 4 + slots * kTreeRows * 8;
+}
+
+// dtype: the query's pa_dtype (PA_BF16, PA_F16); kind: the cache's, 0 = the
+// query's type, 1 = INT8 codes with row scales, 2 = FP8 E4M3 codes. Launches
+// the attention and then the combination of cut segments. p.ctas is set here.
+cudaError_t launch_tree_attention(TreeParams p, int D, int dtype, int kind, cudaStream_t stream);
+
+}  // namespace pa

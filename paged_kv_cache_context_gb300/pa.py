@@ -75,6 +75,19 @@ def lib() -> ctypes.CDLL:
             "pa_prefill": [P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, F, I, P],
             "pa_prefill_int8": [P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, F, I, P],
             "pa_prefill_fp8": [P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, F, F, F, I, P],
+            "pa_tree_workspace_size": [I, I, I],
+            "pa_tree": [P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, F, I, P, Z, P],
+            "pa_tree_int8": [P, P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, F, I, P,
+                             Z, P],
+            "pa_tree_fp8": [P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, F, F, F, I, P,
+                            Z, P],
+            "pa_decode_scored_workspace_size": [I, I, I, I, I, I],
+            "pa_decode_scored": [P, P, P, P, P, P, P, I, I, I, I, I, I, I, F, I, I, F, F, P, Z,
+                                 P],
+            "pa_decode_scored_int8": [P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, F, I, P, Z,
+                                      P],
+            "pa_evict_select": [P, P, P, P, I, I, I, I, I, I, P],
+            "pa_compact": [P, P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, P],
             "pa_decode_static_scratch": [P, P, P, P, P, P, I, I, I, I, I, I, I, F, I, I, I, F,
                                          F, P],
             "pa_get_device_error": [P, P],
@@ -87,6 +100,8 @@ def lib() -> ctypes.CDLL:
             fn.restype = I
         L.pa_decode_workspace_size.restype = Z
         L.pa_decode_cascade_workspace_size.restype = Z
+        L.pa_tree_workspace_size.restype = Z
+        L.pa_decode_scored_workspace_size.restype = Z
         L.pa_block_budget.restype = ctypes.c_int64
         L.pa_status_string.restype = ctypes.c_char_p
         L.pa_test_set_unarmed_page.argtypes = [I]
@@ -511,6 +526,252 @@ def copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, block_pairs: torch
     _check(lib().pa_copy_blocks(_ptr(k_cache), _ptr(v_cache), _ptr(block_pairs),
                                 block_pairs.shape[0], H, D, bs, NB, k_cache.element_size(),
                                 _stream(stream)), "pa_copy_blocks")
+
+
+def _nbytes(t: torch.Tensor) -> int:
+    return t.numel() * t.element_size()
+
+
+def _current_device(t: torch.Tensor, stream):
+    """The library launches on the current device: the tensors and the stream
+    have to be its own."""
+    if not t.is_cuda:
+        return
+    cur = torch.cuda.current_device()
+    if t.device.index != cur:
+        raise ValueError(f"tensors are on {t.device}, the current device is cuda:{cur}")
+    if stream is not None and stream.device.index != cur:
+        raise ValueError(f"the stream is on {stream.device}, the current device is cuda:{cur}")
+
+
+def tree_mask_from_parents(parents, cu_q) -> torch.Tensor:
+    """The tree mask of drafts given as parent indices, on the CPU.
+
+    parents [T]: the node's parent within its own sequence's draft (an earlier
+    node), or -1 for a child of the context's last token; cu_q [S + 1] the
+    drafts' offsets. Returns int64 words [T, W], W = ceil(longest draft / 64):
+    a node sees itself and its ancestors.
+    """
+    par = torch.as_tensor(parents).cpu().tolist()
+    cu = torch.as_tensor(cu_q).cpu().tolist()
+    _need(len(cu) >= 1 and cu[0] == 0 and cu[-1] == len(par) and
+          all(a <= b for a, b in zip(cu, cu[1:])), "cu_q: expected offsets from 0 to len(parents)")
+    words = max([1] + [-(-(b - a) // 64) for a, b in zip(cu, cu[1:])])
+    out = torch.zeros(len(par), words, dtype=torch.int64)
+    for a, b in zip(cu, cu[1:]):
+        seen = []
+        for i in range(b - a):
+            p = par[a + i]
+            _need(-1 <= p < i, f"parents[{a + i}] = {p}: expected -1 or an earlier node of the draft")
+            seen.append((seen[p] if p >= 0 else 0) | 1 << i)
+            for k in range(words):
+                w = seen[i] >> (64 * k) & (1 << 64) - 1
+                out[a + i, k] = w - (1 << 64) if w >> 63 else w
+    return out
+
+
+def tree_workspace_size(num_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    return int(lib().pa_tree_workspace_size(num_heads, num_kv_heads, head_dim))
+
+
+def _check_tree_args(out, query, k_cache, v_cache, block_tables, cu_q, context_lens, tree_mask,
+                     num_kv_heads: int, cache_dtype: torch.dtype, stream):
+    _need(query.dim() == 3, "query: expected [num_tokens, num_heads, head_dim]")
+    _shape("out", out, query.shape)
+    _dtype("out", out, query.dtype)
+    _need(query.dtype in _DTYPE, f"query: unsupported dtype {query.dtype}")
+    _check_caches(k_cache, v_cache, num_kv_heads, query.shape[2], cache_dtype)
+    _need(block_tables.dim() == 2, "block_tables: expected [num_seqs, max_blocks_per_seq]")
+    _dtype("block_tables", block_tables, torch.int32)
+    S = block_tables.shape[0]
+    _shape("cu_q", cu_q, (S + 1,))
+    _dtype("cu_q", cu_q, torch.int32)
+    _shape("context_lens", context_lens, (S,))
+    _dtype("context_lens", context_lens, torch.int32)
+    _need(tree_mask.dim() == 2 and tree_mask.shape[0] == query.shape[0],
+          "tree_mask: expected [num_tokens, mask_words]")
+    _dtype("tree_mask", tree_mask, torch.int64)
+    _current_device(query, stream)
+
+
+def tree_attention(out: torch.Tensor, query: torch.Tensor, k_cache: torch.Tensor,
+                   v_cache: torch.Tensor, block_tables: torch.Tensor, cu_q: torch.Tensor,
+                   context_lens: torch.Tensor, tree_mask: torch.Tensor, num_kv_heads: int,
+                   max_q_len: int, scale: float, workspace: torch.Tensor, stream=None):
+    """pa_tree: attention of drafted nodes query [T, Hq, D] (offsets cu_q [S + 1],
+    the last tokens of each sequence's context) to the context and to the nodes
+    that tree_mask [T, W] (int64 words, see tree_mask_from_parents) names."""
+    _on_device(out=out, query=query, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+               cu_q=cu_q, context_lens=context_lens, tree_mask=tree_mask, workspace=workspace)
+    _check_tree_args(out, query, k_cache, v_cache, block_tables, cu_q, context_lens, tree_mask,
+                     num_kv_heads, query.dtype, stream)
+    T, Hq, D = query.shape
+    NB, _, bs, _ = k_cache.shape
+    S, MB = block_tables.shape
+    _check(lib().pa_tree(_ptr(out), _ptr(query), _ptr(k_cache), _ptr(v_cache),
+                         _ptr(block_tables), _ptr(cu_q), _ptr(context_lens), _ptr(tree_mask), T, S,
+                         Hq, num_kv_heads, D, bs, NB, MB, max_q_len, tree_mask.shape[1], scale,
+                         _DTYPE[query.dtype], _ptr(workspace), _nbytes(workspace),
+                         _stream(stream)), "pa_tree")
+
+
+def tree_attention_int8(out: torch.Tensor, query: torch.Tensor, k_cache: torch.Tensor,
+                        v_cache: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor,
+                        block_tables: torch.Tensor, cu_q: torch.Tensor,
+                        context_lens: torch.Tensor, tree_mask: torch.Tensor, num_kv_heads: int,
+                        max_q_len: int, scale: float, workspace: torch.Tensor, stream=None):
+    """pa_tree_int8: tree_attention over an INT8 cache with per-row scales."""
+    _on_device(out=out, query=query, k_cache=k_cache, v_cache=v_cache, k_scales=k_scales,
+               v_scales=v_scales, block_tables=block_tables, cu_q=cu_q,
+               context_lens=context_lens, tree_mask=tree_mask, workspace=workspace)
+    _check_tree_args(out, query, k_cache, v_cache, block_tables, cu_q, context_lens, tree_mask,
+                     num_kv_heads, torch.int8, stream)
+    _check_scales(k_scales, v_scales, k_cache)
+    T, Hq, D = query.shape
+    NB, _, bs, _ = k_cache.shape
+    S, MB = block_tables.shape
+    _check(lib().pa_tree_int8(_ptr(out), _ptr(query), _ptr(k_cache), _ptr(v_cache),
+                              _ptr(k_scales), _ptr(v_scales), _ptr(block_tables), _ptr(cu_q),
+                              _ptr(context_lens), _ptr(tree_mask), T, S, Hq, num_kv_heads, D, bs,
+                              NB, MB, max_q_len, tree_mask.shape[1], scale, _DTYPE[query.dtype],
+                              _ptr(workspace), _nbytes(workspace), _stream(stream)),
+           "pa_tree_int8")
+
+
+def tree_attention_fp8(out: torch.Tensor, query: torch.Tensor, k_cache: torch.Tensor,
+                       v_cache: torch.Tensor, block_tables: torch.Tensor, cu_q: torch.Tensor,
+                       context_lens: torch.Tensor, tree_mask: torch.Tensor, num_kv_heads: int,
+                       max_q_len: int, scale: float, k_scale: float, v_scale: float,
+                       workspace: torch.Tensor, stream=None):
+    """pa_tree_fp8: tree_attention over an FP8 E4M3 cache (uint8 codes) with
+    per-tensor scales."""
+    _on_device(out=out, query=query, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+               cu_q=cu_q, context_lens=context_lens, tree_mask=tree_mask, workspace=workspace)
+    _check_tree_args(out, query, k_cache, v_cache, block_tables, cu_q, context_lens, tree_mask,
+                     num_kv_heads, torch.uint8, stream)
+    T, Hq, D = query.shape
+    NB, _, bs, _ = k_cache.shape
+    S, MB = block_tables.shape
+    _check(lib().pa_tree_fp8(_ptr(out), _ptr(query), _ptr(k_cache), _ptr(v_cache),
+                             _ptr(block_tables), _ptr(cu_q), _ptr(context_lens), _ptr(tree_mask),
+                             T, S, Hq, num_kv_heads, D, bs, NB, MB, max_q_len,
+                             tree_mask.shape[1], scale, k_scale, v_scale, _DTYPE[query.dtype],
+                             _ptr(workspace), _nbytes(workspace), _stream(stream)), "pa_tree_fp8")
+
+
+def decode_scored_workspace_size(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int,
+                                 block_size: int, max_blocks_per_seq: int) -> int:
+    return int(lib().pa_decode_scored_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim,
+                                                     block_size, max_blocks_per_seq))
+
+
+def _check_scores(scores, num_seqs: int, num_kv_heads: int, length: int):
+    _shape("scores", scores, (num_seqs, num_kv_heads, length))
+    _dtype("scores", scores, torch.float32)
+
+
+def decode_scored(out: torch.Tensor, scores: torch.Tensor, query: torch.Tensor,
+                  k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                  context_lens: torch.Tensor, num_kv_heads: int, scale: float,
+                  workspace: torch.Tensor, kv_dtype: str = "auto", k_scale: float = 1.0,
+                  v_scale: float = 1.0, stream=None):
+    """pa_decode_scored: decode, and scores [S, Hkv, MB * bs] += every token's
+    softmax weight summed over its kv head's query heads."""
+    _on_device(out=out, scores=scores, query=query, k_cache=k_cache, v_cache=v_cache,
+               block_tables=block_tables, context_lens=context_lens, workspace=workspace)
+    _check_decode_args(out, query, k_cache, v_cache, block_tables, context_lens, num_kv_heads,
+                       _CACHE_DTYPE.get(kv_dtype, query.dtype))
+    S, Hq, D = query.shape
+    NB, _, bs, _ = k_cache.shape
+    MB = block_tables.shape[1]
+    _check_scores(scores, S, num_kv_heads, MB * bs)
+    _current_device(query, stream)
+    _check(lib().pa_decode_scored(_ptr(out), _ptr(scores), _ptr(query), _ptr(k_cache),
+                                  _ptr(v_cache), _ptr(block_tables), _ptr(context_lens), S, Hq,
+                                  num_kv_heads, D, bs, NB, MB, scale, _DTYPE[query.dtype],
+                                  _KV[kv_dtype], k_scale, v_scale, _ptr(workspace),
+                                  _nbytes(workspace), _stream(stream)), "pa_decode_scored")
+
+
+def decode_scored_int8(out: torch.Tensor, scores: torch.Tensor, query: torch.Tensor,
+                       k_cache: torch.Tensor, v_cache: torch.Tensor, k_scales: torch.Tensor,
+                       v_scales: torch.Tensor, block_tables: torch.Tensor,
+                       context_lens: torch.Tensor, num_kv_heads: int, scale: float,
+                       workspace: torch.Tensor, stream=None):
+    """pa_decode_scored_int8: decode_scored over an INT8 cache with per-row scales."""
+    _on_device(out=out, scores=scores, query=query, k_cache=k_cache, v_cache=v_cache,
+               k_scales=k_scales, v_scales=v_scales, block_tables=block_tables,
+               context_lens=context_lens, workspace=workspace)
+    _check_decode_args(out, query, k_cache, v_cache, block_tables, context_lens, num_kv_heads,
+                       torch.int8)
+    _check_scales(k_scales, v_scales, k_cache)
+    S, Hq, D = query.shape
+    NB, _, bs, _ = k_cache.shape
+    MB = block_tables.shape[1]
+    _check_scores(scores, S, num_kv_heads, MB * bs)
+    _current_device(query, stream)
+    _check(lib().pa_decode_scored_int8(_ptr(out), _ptr(scores), _ptr(query), _ptr(k_cache),
+                                       _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
+                                       _ptr(block_tables), _ptr(context_lens), S, Hq,
+                                       num_kv_heads, D, bs, NB, MB, scale, _DTYPE[query.dtype],
+                                       _ptr(workspace), _nbytes(workspace), _stream(stream)),
+           "pa_decode_scored_int8")
+
+
+def evict_select(keep: torch.Tensor, new_lens: torch.Tensor, scores: torch.Tensor,
+                 context_lens: torch.Tensor, num_sink: int = 0, num_recent: int = 0, stream=None):
+    """pa_evict_select: keep [S, Hkv, budget] = the ascending positions an
+    eviction to `budget` tokens keeps (-1 past new_lens [S])."""
+    _on_device(keep=keep, new_lens=new_lens, scores=scores, context_lens=context_lens)
+    _need(scores.dim() == 3, "scores: expected [num_seqs, num_kv_heads, length]")
+    S, H, N = scores.shape
+    _dtype("scores", scores, torch.float32)
+    _need(keep.dim() == 3 and keep.shape[:2] == scores.shape[:2],
+          f"keep: expected [{S}, {H}, budget]")
+    _dtype("keep", keep, torch.int32)
+    for name, t in (("new_lens", new_lens), ("context_lens", context_lens)):
+        _shape(name, t, (S,))
+        _dtype(name, t, torch.int32)
+    _current_device(scores, stream)
+    _check(lib().pa_evict_select(_ptr(keep), _ptr(new_lens), _ptr(scores), _ptr(context_lens), S,
+                                 H, N, keep.shape[2], num_sink, num_recent, _stream(stream)),
+           "pa_evict_select")
+
+
+def compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+            context_lens: torch.Tensor, keep: torch.Tensor, keep_lens: torch.Tensor,
+            starts: Optional[torch.Tensor] = None, k_scales: Optional[torch.Tensor] = None,
+            v_scales: Optional[torch.Tensor] = None, scores: Optional[torch.Tensor] = None,
+            stream=None):
+    """pa_compact: row starts[s] + j of sequence s <- row keep[s, g, j] for
+    j < keep_lens[s], in place (keep [S, Hkv or 1, budget])."""
+    _on_device(k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+               context_lens=context_lens, keep=keep, keep_lens=keep_lens, starts=starts,
+               k_scales=k_scales, v_scales=v_scales, scores=scores)
+    _need(k_cache.dim() == 4, "k_cache: expected [num_blocks, num_kv_heads, block_size, D]")
+    _shape("v_cache", v_cache, k_cache.shape)
+    _dtype("v_cache", v_cache, k_cache.dtype)
+    NB, H, bs, D = k_cache.shape
+    _need(block_tables.dim() == 2, "block_tables: expected [num_seqs, max_blocks_per_seq]")
+    _dtype("block_tables", block_tables, torch.int32)
+    S, MB = block_tables.shape
+    _need(keep.dim() == 3 and keep.shape[0] == S and keep.shape[1] in (1, H),
+          f"keep: expected [{S}, {H} or 1, budget]")
+    _dtype("keep", keep, torch.int32)
+    for name, t in (("context_lens", context_lens), ("keep_lens", keep_lens), ("starts", starts)):
+        if t is not None:
+            _shape(name, t, (S,))
+            _dtype(name, t, torch.int32)
+    _need((k_scales is None) == (v_scales is None), "give both row scales or neither")
+    if k_scales is not None:
+        _check_scales(k_scales, v_scales, k_cache)
+    if scores is not None:
+        _check_scores(scores, S, H, MB * bs)
+    _current_device(k_cache, stream)
+    _check(lib().pa_compact(_ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
+                            _ptr(scores), _ptr(block_tables), _ptr(context_lens), _ptr(keep),
+                            _ptr(keep_lens), _ptr(starts), S, H, keep.shape[1], keep.shape[2], D,
+                            bs, NB, MB, k_cache.element_size(), _stream(stream)), "pa_compact")
 
 
 PA_BUDGET_MB, PA_BUDGET_FRACTION, PA_BUDGET_CONTEXT = 0, 1, 2
