@@ -1114,7 +1114,7 @@ static pa_status tree_impl(int kind, void* out, const void* query, const void* k
   if (num_blocks <= 0 || max_blocks_per_seq <= 0 || max_q_len < 1 || max_q_len > num_tokens ||
       mask_words < 1 || (int64_t)mask_words * 64 < max_q_len)
     return PA_ERR_SHAPE;
-  if ((int64_t)max_blocks_per_seq * block_size > INT32_MAX - kTreeTile) return PA_ERR_SHAPE;
+  if ((int64_t)max_blocks_per_seq * block_size > INT32_MAX - kTreeMaxTile) return PA_ERR_SHAPE;
   const int64_t G = num_heads / num_kv_heads;
   if ((max_q_len * G + kTreeRows - 1) / kTreeRows * num_kv_heads > 65535) return PA_ERR_SHAPE;
   const long long cache_rows = (long long)num_blocks * num_kv_heads * block_size;

@@ -25,10 +25,11 @@
 //   warp 4     MMA issue, TMEM allocation
 //   warp 5     copies of K and V tiles into a ring of slots (K and V take
 //              turns, so that K of the next tile arrives early)
-//   warps 6-7  8-bit caches: codes widened exactly to f16
-// S = Q K^T goes to TMEM in two buffers; the weights P go back over their S
-// buffer in TMEM as the A operand of O += P V, so they never pass through
-// shared memory.
+//   four more  8-bit caches: codes widened exactly to f16
+// S = Q K^T goes to TMEM in one buffer, which is free again as soon as the
+// softmax threads hold its logits: the next tile's S runs under their
+// exponentials. The weights P go to TMEM (two buffers) as the A operand of
+// O += P V, so they never pass through shared memory.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -42,31 +43,52 @@ namespace {
 
 enum : int { kT16 = 0, kTI8 = 1, kTE4 = 2 };
 
-template <int D, int KC>
+// QT: 128-row query tiles of a CTA. With one, tiles are 64 tokens, two CTAs
+// share an SM, S has a TMEM buffer and P two, so that the next tile's S runs
+// under this one's exponentials. With two (more rows: the tensor cores are
+// the bound), tiles are 128 tokens, which halves what S = Q K^T costs (a
+// product of 128 x 64 takes the 85 clocks of one of 128 x 128: it waits for A),
+// both query tiles read each staged K and V, P goes back over its S, and one
+// query tile's products run under the other's softmax.
+template <int D, int KC, int QT>
 struct TreeLayout {
   static constexpr bool C8 = KC != kT16;
   static constexpr int KB = D / 64;  // 128-byte column blocks of a 16-bit row
-  static constexpr int MMA_WARP = 4, COPY_WARP = 5, CONV_WARP = 6;
-  static constexpr int CONV = C8 ? 64 : 0;  // widening threads
-  static constexpr int THREADS = 192 + CONV;
-  static constexpr int QBYTES = KB * kTreeRows * 128;  // [KB][128 rows][128 B]
-  static constexpr int SLOT = KB * kTreeTile * 128;    // a K or V tile: [KB][64 tokens][128 B]
-  // slots of 16-bit tiles; 8-bit caches copy into raw slots first
-  static constexpr int SLOTS = C8 ? 3 : (D == 128 ? 5 : 8);
-  static constexpr int RSLOT = kTreeTile * D + (KC == kTI8 ? 2 * kTreeTile * 4 : 0);
-  static constexpr int RSLOTS = C8 ? (D == 128 ? (KC == kTI8 ? 3 : 4) : 6) : 0;
-  static constexpr int SCT = 4;  // INT8: tiles whose row scales are kept
-  static constexpr int OFF_KV = QBYTES;
+  static constexpr int TT = QT == 1 ? 64 : 128;  // tokens of a tile
+  static constexpr bool INPL = QT == 2;          // P over S
+  static constexpr int ROWS = QT * kTreeRows;
+  static constexpr int MMA_WARP = 4 * QT, COPY_WARP = MMA_WARP + 1;
+  static constexpr int CONV_WARP = MMA_WARP + 2;
+  static constexpr int CONV = C8 ? 128 : 0;  // widening threads
+  static constexpr int THREADS = CONV_WARP * 32 + CONV;
+  static constexpr int CTAS = QT == 1 ? 2 : 1;          // per SM
+  static constexpr int QBYTES1 = KB * kTreeRows * 128;  // a query tile: [KB][128 rows][128 B]
+  static constexpr int SLOT = KB * TT * 128;            // a K or V tile: [KB][TT tokens][128 B]
+  static constexpr int SLOTS = D == 128 ? (KC == kTI8 ? 4 : 5) : (C8 ? 6 : 8);
+  // INT8: tiles whose row scales are kept. When K of tile x is copied, slot
+  // 2x - SLOTS is free, so S of tile x - SLOTS / 2 is done, and the weights of
+  // the tile two before that: the tiles from x - SLOTS / 2 - 1 on may be in use.
+  static constexpr int SCT = SLOTS <= 4 ? 4 : 8;
+  static_assert(SCT >= SLOTS / 2 + 2, "row scales in use are not overwritten");
+  // 8-bit codes of a tile, [TT tokens][D], on their way to 16 bits. At D 128
+  // they land in the slot's second column block, where a token's codes take
+  // the very bytes of its second 64 elements: a warp that has read its tokens'
+  // codes may write them widened without asking the other warps. At D 64
+  // they have an area of their own.
+  static constexpr int RAW = C8 && D == 64 ? TT * D : 0;
+  static constexpr int OFF_KV = QT * QBYTES1;
   static constexpr int OFF_RAW = OFF_KV + SLOTS * SLOT;
-  static constexpr int OFF_SC = OFF_RAW + RSLOTS * RSLOT;  // [SCT][K, V][64]
-  static constexpr int OFF_BAR = OFF_SC + (KC == kTI8 ? SCT * 2 * kTreeTile * 4 : 0);
-  static constexpr int NBAR = 2 * SLOTS + 2 * RSLOTS + 7;
-  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int OFF_SC = OFF_RAW + SLOTS * RAW;  // [SCT][K, V][TT]
+  static constexpr int OFF_BAR = OFF_SC + (KC == kTI8 ? SCT * 2 * TT * 4 : 0);
+  static constexpr int NBAR = (C8 ? 3 : 2) * SLOTS + 7 * QT;  // see the kernel
+  static constexpr int OFF_MISC = (OFF_BAR + NBAR * 8 + 15) / 16 * 16;
   static constexpr int SMEM = OFF_MISC + 64;
-  static constexpr uint32_t TMEM_COLS = 256;  // S or P: 2 x 64; O: D at column 128
-  static_assert(OFF_RAW % 16 == 0 && RSLOT % 16 == 0 && OFF_BAR % 16 == 0 && OFF_MISC % 8 == 0,
-                "alignment");
-  static_assert(SMEM <= 113 * 1024, "two CTAs per SM");
+  // TMEM columns: S of query tile q at q TT; (QT 1) P of buffer b at 64 + b 32; O of tile q at
+  // QT 128 + q D
+  static constexpr uint32_t TMEM_COLS = QT == 1 ? 256 : 512;
+  static_assert(QT * (128 + D) <= (int)TMEM_COLS, "TMEM columns");
+  static_assert(OFF_BAR % 16 == 0, "alignment");
+  static_assert(SMEM <= (QT == 1 ? 113 : 227) * 1024, "CTAs per SM");
 };
 
 // A sequence's rows and tiles; T = 0 when it has no work. Impossible offsets
@@ -78,6 +100,7 @@ struct TreeSeq {
 __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int s, bool flag) {
   TreeSeq q{};
   q.q0 = p.cu_q[s];
+  const int n = p.context_lens[s];
   const long long len = (long long)p.cu_q[s + 1] - q.q0;
   if (len < 0 || q.q0 < 0 || q.q0 + len > p.num_tokens || len > p.max_q_len) {
     if (flag) raise_error(p.err, PA_DEVERR_SEQ);
@@ -85,21 +108,23 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int s, bool fla
   }
   q.q_len = static_cast<int>(len);
   if (q.q_len == 0) return q;
-  q.n = p.context_lens[s];
+  q.n = n;
   if (q.n < q.q_len || q.n > (long long)p.max_blocks_per_seq * p.block_size) {
     if (flag) raise_error(p.err, PA_DEVERR_CONTEXT_LEN);
     q.zero = true;
     return q;
   }
-  q.T = (q.n + kTreeTile - 1) / kTreeTile;
-  q.RT = static_cast<int>(((long long)q.q_len * p.group + kTreeRows - 1) / kTreeRows);
+  q.T = (q.n + p.tile_tokens - 1) / p.tile_tokens;
+  q.RT = static_cast<int>(((long long)q.q_len * p.group + p.tile_rows - 1) / p.tile_rows);
   return q;
 }
 
-__device__ __forceinline__ long long tree_lo(long long c, long long P, int C) { return c * P / C; }
-// the CTA whose share holds unit x
-__device__ __forceinline__ int tree_cta(long long x, long long P, int C) {
-  return static_cast<int>(((x + 1) * C - 1) / P);
+// Units of a CTA's share: CTA c takes [c U, min((c + 1) U, P)).
+__device__ __forceinline__ long long tree_div(long long a, long long b) {  // both >= 0
+  return (a | b) >> 32 ? a / b : static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+}
+__device__ __forceinline__ long long tree_share(long long P, int C) {
+  return tree_div(P + C - 1, C);
 }
 
 // Units of all sequences, and where unit `x` lies (one warp; x < 0: none).
@@ -174,17 +199,51 @@ __device__ __forceinline__ void cp_async_wait_all() {
   asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
 }
 
-// D (TMEM) [+]= A (TMEM, 16-bit pairs along K in 32-bit columns) x B (smem).
-__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+// Operand descriptors of 128-byte swizzled tiles, split in words: the high
+// word (stride 1024 bytes, descriptor version, swizzle kind) is the same for
+// all, the low one holds the address and the leading offset in 16-byte units.
+constexpr uint32_t kTreeDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t tree_desc_lo(uint32_t saddr, uint32_t lbo) {
+  return ((saddr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16);
+}
+// One lane of a converged warp. The copy and MMA warps run their loops whole
+// and let one lane issue: addresses and descriptors stay warp-uniform, which
+// the issuing instructions take from uniform registers (a loop inside a
+// one-lane branch moves every operand there first: 86 clocks per product
+// instead of the tensor core's 48 to 64).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+               : "=r"(ok));
+  return ok != 0;
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
+}
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// D (TMEM) [+]= A (smem) x B (smem).
+__device__ __forceinline__ void tree_mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
                                             uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "n"(kTreeDescHi), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+// D (TMEM) [+]= A (TMEM, 16-bit pairs along K in 32-bit columns) x B (smem).
+__device__ __forceinline__ void tree_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
+                                            uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 db, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "n"(kTreeDescHi), "r"(idesc), "r"(accumulate ? 1u : 0u)
       : "memory");
 }
 
-// The tokens of tile [t0, t0 + 64) that a node sees, as bits: context tokens,
+// The tokens [t0, t0 + 64) that a node sees, as bits: context tokens,
 // and nodes by the node's mask words (bits past the sequence's end are off).
 __device__ __forceinline__ unsigned long long tree_seen(const unsigned long long* words, int W,
                                                         int t0, int ctx, int n) {
@@ -199,31 +258,109 @@ __device__ __forceinline__ unsigned long long tree_seen(const unsigned long long
   } else {
     v = ~0ull;
   }
-  const int valid = n - t0;  // >= 1
-  if (valid < 64) v &= (1ull << valid) - 1ull;
+  const int valid = n - t0;
+  if (valid < 64) v &= valid > 0 ? (1ull << valid) - 1ull : 0ull;
   return v;
 }
 
-template <typename QT, int D, int KC>
-__global__ void __launch_bounds__(TreeLayout<D, KC>::THREADS, 2)
+// The largest seen logit (log2 units) of 32 neighbouring tokens. Without row
+// scales and masks the maximum is taken over the raw products: multiplying by
+// a scale that is not negative keeps their order.
+template <bool ROW_SC>
+__device__ __forceinline__ float half_max(const uint32_t (&s)[32], const float* ks, float scale,
+                                          bool masked, uint32_t seen) {
+  float a[4];
+  if (scale >= 0.f && !ROW_SC && !masked) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) a[e] = __uint_as_float(s[e]);
+#pragma unroll
+    for (int e = 4; e < 32; ++e) a[e & 3] = fmaxf(a[e & 3], __uint_as_float(s[e]));
+    return fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])) * scale;
+  }
+  {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) a[e] = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      float x = __uint_as_float(s[e]) * scale;
+      if constexpr (ROW_SC) x *= ks[e];
+      a[e & 3] = fmaxf(a[e & 3], (seen >> e) & 1u ? x : -INFINITY);
+    }
+    return fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
+  }
+}
+
+// The weights 2^(x - mu) of 32 neighbouring tokens, rounded to the MMA type
+// in pairs (INT8: times the V row scale first); `sum` takes them unrounded.
+template <typename T, bool ROW_SC>
+__device__ __forceinline__ void half_weights(const uint32_t (&s)[32], const float* ks,
+                                             const float* vsc, float scale, float mu, bool masked, uint32_t seen, float2& sum,
+                                             uint32_t (&pk)[16]) {
+  const float2 sc2 = make_float2(scale, scale), mu2 = make_float2(-mu, -mu);
+#pragma unroll
+  for (int e = 0; e < 32; e += 2) {
+    float2 x = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+    if constexpr (ROW_SC) x = __fmul2_rn(x, *reinterpret_cast<const float2*>(ks + e));
+    x = __ffma2_rn(x, sc2, mu2);
+    float2 w = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+    if (masked) {
+      w.x = (seen >> e) & 1u ? w.x : 0.f;
+      w.y = (seen >> (e + 1)) & 1u ? w.y : 0.f;
+    }
+    sum = __fadd2_rn(sum, w);
+    if constexpr (ROW_SC) {
+      const float2 vs = *reinterpret_cast<const float2*>(vsc + e);
+      // an unseen token's weight stays zero, whatever its scale
+      if (masked)
+        w = make_float2(w.x == 0.f ? 0.f : w.x * vs.x, w.y == 0.f ? 0.f : w.y * vs.y);
+      else
+        w = __fmul2_rn(w, vs);
+    }
+    pk[e / 2] = Mma<T>::pack(w.x, w.y);
+  }
+}
+
+// 16 consecutive 32-bit columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15])
+      : "memory");
+}
+
+template <typename QT, int D, int KC, int NQ>
+__global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, KC, NQ>::CTAS)
     tree_attention_kernel(const __grid_constant__ TreeParams p) {
-  using Ly = TreeLayout<D, KC>;
+  using Ly = TreeLayout<D, KC, NQ>;
   constexpr bool C8 = Ly::C8, ROW_SC = KC == kTI8;
   using T = typename std::conditional<C8, __half, QT>::type;  // MMA operand type
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-  constexpr int KB = Ly::KB, NS = Ly::SLOTS, RS = Ly::RSLOTS;
+  constexpr int KB = Ly::KB, NS = Ly::SLOTS, ROWS = Ly::ROWS, TT = Ly::TT;
+  constexpr bool INPL = Ly::INPL;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + Ly::OFF_BAR);  // [NS] a tile is in its slot
   uint64_t* empty = full + NS;            // [NS] its MMAs are done
-  uint64_t* s_full = empty + NS;          // [2]
-  uint64_t* p_full = s_full + 2;          // [2]
-  uint64_t* pv_done = p_full + 2;         // [2]
-  uint64_t* q_full = pv_done + 2;         // [1]
-  uint64_t* raw_full = q_full + 1;        // [RS]
-  uint64_t* raw_empty = raw_full + RS;    // [RS]
+  uint64_t* s_full = empty + NS;          // [NQ] S is in TMEM
+  uint64_t* s_free = s_full + NQ;         // [NQ] it has been read
+  uint64_t* p_full = s_free + NQ;         // [NQ][2]
+  uint64_t* pv_done = p_full + 2 * NQ;    // [NQ][2]
+  uint64_t* q_full = pv_done + 2 * NQ;    // [NQ]
+  uint64_t* raw_full = q_full + NQ;       // [NS] 8-bit caches: codes have landed
   int* misc = reinterpret_cast<int*>(smem + Ly::OFF_MISC);            // s, g, rt, tile
-  long long* misc64 = reinterpret_cast<long long*>(smem + Ly::OFF_MISC + 16);  // lo, hi, total
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Ly::OFF_MISC + 40);
+  long long* misc64 = reinterpret_cast<long long*>(smem + Ly::OFF_MISC + 16);  // lo, hi
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Ly::OFF_MISC + 32);
   float* sc = reinterpret_cast<float*>(smem + Ly::OFF_SC);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x, C = p.ctas, S = p.num_seqs;
@@ -235,22 +372,28 @@ __global__ void __launch_bounds__(TreeLayout<D, KC>::THREADS, 2)
   // ---- this CTA's share (copy warp); barriers, TMEM; sequences whose length
   // is impossible get zero rows
   if (warp == Ly::COPY_WARP) {
-    const long long P = tree_total(p, lane);
-    const long long lo = P > 0 ? tree_lo(cta, P, C) : 0, hi = P > 0 ? tree_lo(cta + 1, P, C) : 0;
+    // units of all sequences, lanes taking 32 at a time; a batch of up to 32
+    // keeps them in registers
+    const long long u0 = tree_units(p, lane, lane < S), incl0 = warp_incl(u0, lane);
+    const long long P =
+        S <= 32 ? __shfl_sync(0xffffffffu, incl0, 31) : tree_total(p, lane);
+    const long long U = tree_share(P, C);
+    const long long lo = min(cta * U, P), hi = min(lo + U, P);
     if (lo < hi) {
       long long run = 0;
       for (int b = 0; b < S; b += 32) {
-        const long long u = tree_units(p, b + lane, b + lane < S);
-        const long long incl = warp_incl(u, lane);
+        const long long u = b == 0 ? u0 : tree_units(p, b + lane, b + lane < S);
+        const long long incl = b == 0 ? incl0 : warp_incl(u, lane);
         const unsigned hit = __ballot_sync(0xffffffffu, run + incl > lo);
         if (hit) {
           if (lane == __ffs(hit) - 1) {
             const TreeSeq q = tree_seq(p, b + lane, false);
             const long long rem = lo - (run + incl - u);
+            const long long seg = tree_div(rem, q.T);  // (kv head, row tile)
             misc[0] = b + lane;
-            misc[1] = static_cast<int>(rem / ((long long)q.T * q.RT));
-            misc[2] = static_cast<int>(rem / q.T % q.RT);
-            misc[3] = static_cast<int>(rem % q.T);
+            misc[1] = static_cast<int>(tree_div(seg, q.RT));
+            misc[2] = static_cast<int>(seg - (long long)misc[1] * q.RT);
+            misc[3] = static_cast<int>(rem - seg * q.T);
           }
           break;
         }
@@ -260,7 +403,6 @@ __global__ void __launch_bounds__(TreeLayout<D, KC>::THREADS, 2)
     if (lane == 0) {
       misc64[0] = lo;
       misc64[1] = hi;
-      misc64[2] = P;
     }
   } else if (warp == Ly::MMA_WARP) {
     tmem_alloc(tmem_slot, Ly::TMEM_COLS);
@@ -268,17 +410,17 @@ __global__ void __launch_bounds__(TreeLayout<D, KC>::THREADS, 2)
       for (int i = 0; i < NS; ++i) {
         mbar_init(&full[i], C8 ? Ly::CONV : 1);
         mbar_init(&empty[i], 1);
+        if (C8) mbar_init(&raw_full[i], 1);
       }
-      for (int i = 0; i < RS; ++i) {
-        mbar_init(&raw_full[i], 1);
-        mbar_init(&raw_empty[i], C8 ? Ly::CONV : 1);
-      }
-      for (int i = 0; i < 2; ++i) {
-        mbar_init(&s_full[i], 1);
+      for (int i = 0; i < 2 * NQ; ++i) {
         mbar_init(&p_full[i], kTreeRows);
         mbar_init(&pv_done[i], 1);
       }
-      mbar_init(q_full, kTreeRows);
+      for (int i = 0; i < NQ; ++i) {
+        mbar_init(&s_full[i], 1);
+        mbar_init(&s_free[i], kTreeRows);
+        mbar_init(&q_full[i], kTreeRows);
+      }
       fence_mbar_init();
     }
   } else if (warp < 4) {
@@ -294,7 +436,7 @@ __global__ void __launch_bounds__(TreeLayout<D, KC>::THREADS, 2)
   __syncthreads();
   tc05_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t t_s = tmem, t_o = tmem + 2 * kTreeTile;
+  const uint32_t t_s0 = tmem, t_p0 = INPL ? tmem : tmem + 64, t_o0 = tmem + NQ * 128;
   const long long lo = misc64[0], units = misc64[1] - lo;
   const bool aligned = (smem_u32(smem) & 1023u) == 0;
   if (!aligned && tid == 0) raise_error(err, PA_DEVERR_TIMEOUT);  // never: see __align__ above
@@ -302,389 +444,526 @@ __global__ void __launch_bounds__(TreeLayout<D, KC>::THREADS, 2)
   if (units > 0 && aligned) {
     TreeWalk w;
     w.set(p, misc, units);
+    // query tiles of the current piece that have rows (the first always has)
+    auto live_tiles = [&]() -> int {
+      return NQ == 1 ? 1 : (w.q.q_len * G - w.rt * ROWS > kTreeRows ? 2 : 1);
+    };
     if (warp == Ly::COPY_WARP) {
       // ================================================ copies: K0 V0 K1 V1 ...
-      if (lane == 0) {
-        constexpr int N = C8 ? RS : NS;
-        uint64_t* fb = C8 ? raw_full : full;
-        uint64_t* eb = C8 ? raw_empty : empty;
-        const int rows_end = static_cast<int>(C8 ? 0 : (long long)p.num_blocks * Hkv * bs);
-        const int pages = kTreeTile / bs;
-        long long k = 0;  // slots filled
-        bool ok = true;
-        for (; w.left > 0 && ok; w.next(p)) {
-          const int32_t* table = p.block_tables + (size_t)w.s * p.max_blocks_per_seq;
-          for (int i = 0; i < w.len && ok; ++i) {
-            const int t0 = (w.tile + i) * kTreeTile;
-            int blk[4];  // a page past the end or with a bad id: -1
+      const int sh = 31 - __clz(bs), pages = TT >> sh;  // block_size is a power of two
+      uint64_t* landed = C8 ? raw_full : full;
+      int sl = 0;       // next slot
+      uint32_t ph = 1;  // parity of its last release
+      int filled = 0;   // slots filled (no further than NS)
+      int stile = 0;    // INT8: where the tile's row scales go
+      bool ok = true;
+      // Lane pp looks up page pp of a tile: its index among all (block, kv
+      // head) pages, -1 past the sequence's end, -2 for a bad id.
+      auto lookup = [&](int i) -> int {
+        const int t = (w.tile + i) * TT + (lane << sh);
+        if (lane >= pages || t >= w.q.n) return -1;
+        const int b = __ldg(p.block_tables + (size_t)w.s * p.max_blocks_per_seq + (t >> sh));
+        if (b >= 0 && b < p.num_blocks) return b * Hkv + w.g;
+        raise_error(err, PA_DEVERR_BLOCK_ID);
+        return -2;
+      };
+      int len = uniform(w.len);
+      while (len > 0 && ok) {
+        int y_next = lookup(0);
+        for (int i = 0; i < len && ok; ++i) {
+          const int y_here = y_next;
+          int y[TT / 16];
 #pragma unroll
-            for (int pp = 0; pp < 4; ++pp) {
-              blk[pp] = -1;
-              if (pp < pages && t0 + pp * bs < w.q.n) {
-                const int b = __ldg(table + t0 / bs + pp);
-                if (b >= 0 && b < p.num_blocks)
-                  blk[pp] = b;
-                else
-                  raise_error(err, PA_DEVERR_BLOCK_ID);
-              }
-            }
+          for (int pp = 0; pp < TT / 16; ++pp) y[pp] = __shfl_sync(0xffffffffu, y_here, pp);
+          if (i + 1 < len) y_next = lookup(i + 1);
 #pragma unroll
-            for (int kv = 0; kv < 2; ++kv, ++k) {
-              const int sl = static_cast<int>(k % N);
-              if (k >= N && !mbar_wait_bounded(&eb[sl], static_cast<uint32_t>((k / N - 1) & 1))) {
-                raise_error(err, PA_DEVERR_TIMEOUT);
-                ok = false;
-                break;
-              }
-              if constexpr (!C8) {
-                mbar_arrive_expect_tx(&fb[sl], Ly::SLOT);
-                uint8_t* dst = smem + Ly::OFF_KV + sl * Ly::SLOT;
+          for (int kv = 0; kv < 2; ++kv) {
+            if (filled >= NS) ok = warp_wait(&empty[sl], ph);
+            if (!ok) break;
+            uint8_t* slot = smem + Ly::OFF_KV + sl * Ly::SLOT;
+            if constexpr (!C8) {
+              // a box wholly past the tensor is filled with zeros
+              const int rows_end = static_cast<int>((long long)p.num_blocks * Hkv << sh);
+              if (elect_one()) {
+                mbar_arrive_expect_tx(&landed[sl], Ly::SLOT);
 #pragma unroll
-                for (int pp = 0; pp < 4; ++pp) {
+                for (int pp = 0; pp < TT / 16; ++pp) {
                   if (pp >= pages) break;
-                  // a box wholly past the tensor is filled with zeros
-                  const int y = blk[pp] >= 0 ? (blk[pp] * Hkv + w.g) * bs : rows_end;
 #pragma unroll
                   for (int j = 0; j < KB; ++j)
-                    tma_load_2d(dst + j * (kTreeTile * 128) + pp * bs * 128, kv ? &p.tm_v : &p.tm_k,
-                                64 * j, y, &fb[sl]);
+                    tma_load_2d(slot + j * (TT * 128) + (pp << sh) * 128, kv ? &p.tm_v : &p.tm_k,
+                                64 * j, y[pp] >= 0 ? y[pp] << sh : rows_end, &landed[sl]);
                 }
-              } else {
-                uint8_t* dst = smem + Ly::OFF_RAW + sl * Ly::RSLOT;
-                const bool scales = ROW_SC && kv == 0;  // both kinds come with K
+              }
+            } else {
+              uint8_t* raw = Ly::RAW ? smem + Ly::OFF_RAW + sl * Ly::RAW : slot + Ly::SLOT / 2;
+              float* sct = sc + stile * 2 * TT;  // both kinds come with K
+              // pages past the end are not copied (their K is masked, their V
+              // zeroed with the rows past the end); bad ones become zeros here
+              if (__any_sync(0xffffffffu, y_here == -2)) {
+#pragma unroll
+                for (int pp = 0; pp < TT / 16; ++pp) {
+                  if (pp >= pages || y[pp] != -2) continue;
+                  uint4* z = reinterpret_cast<uint4*>(raw + (pp << sh) * D);
+                  for (int x = lane; x < (D << sh) / 16; x += 32) z[x] = make_uint4(0u, 0u, 0u, 0u);
+                  if (ROW_SC && kv == 0)
+                    for (int x = lane; x < bs; x += 32)
+                      sct[(pp << sh) + x] = sct[TT + (pp << sh) + x] = 0.f;
+                }
+                __syncwarp();
+              }
+              if (elect_one()) {
                 uint32_t bytes = 0;
 #pragma unroll
-                for (int pp = 0; pp < 4; ++pp)
-                  if (blk[pp] >= 0) bytes += bs * D + (scales ? 2 * bs * 4 : 0);
-                mbar_arrive_expect_tx(&fb[sl], bytes);
+                for (int pp = 0; pp < TT / 16; ++pp)
+                  if (pp < pages && y[pp] >= 0) bytes += (D + (ROW_SC && kv == 0 ? 8 : 0)) << sh;
+                mbar_arrive_expect_tx(&landed[sl], bytes);
 #pragma unroll
-                for (int pp = 0; pp < 4; ++pp) {
-                  if (blk[pp] < 0) continue;
-                  const size_t row0 = ((size_t)blk[pp] * Hkv + w.g) * bs;
-                  bulk_g2s(dst + pp * bs * D, (kv ? p.v_cache : p.k_cache) + row0 * D, bs * D,
-                           &fb[sl]);
-                  if (scales) {
-                    uint8_t* sd = dst + kTreeTile * D + pp * bs * 4;
-                    bulk_g2s(sd, p.k_scales + row0, bs * 4, &fb[sl]);
-                    bulk_g2s(sd + kTreeTile * 4, p.v_scales + row0, bs * 4, &fb[sl]);
+                for (int pp = 0; pp < TT / 16; ++pp) {
+                  if (pp >= pages || y[pp] < 0) continue;
+                  const size_t row0 = (size_t)y[pp] << sh;
+                  bulk_g2s(raw + (pp << sh) * D, (kv ? p.v_cache : p.k_cache) + row0 * D, D << sh,
+                           &landed[sl]);
+                  if (ROW_SC && kv == 0) {
+                    bulk_g2s(sct + (pp << sh), p.k_scales + row0, 4 << sh, &landed[sl]);
+                    bulk_g2s(sct + TT + (pp << sh), p.v_scales + row0, 4 << sh, &landed[sl]);
                   }
                 }
               }
             }
+            __syncwarp();
+            if (filled < NS) ++filled;
+            if (++sl == NS) {
+              sl = 0;
+              ph ^= 1;
+            }
           }
-          if (!ok) break;
+          stile = (stile + 1) % Ly::SCT;
         }
-        // never leave with copies in flight
-        for (long long j = k > N ? k - N : 0; j < k; ++j)
-          if (!mbar_wait_bounded(&fb[j % N], static_cast<uint32_t>((j / N) & 1)))
-            raise_error(err, PA_DEVERR_TIMEOUT);
+        w.next(p);
+        len = uniform(w.left > 0 ? w.len : 0);
       }
+      if (!ok && lane == 0) raise_error(err, PA_DEVERR_TIMEOUT);
+      // never leave with copies in flight: the last fill of every slot (a
+      // slot before `sl` was filled in phase ph ^ 1, one from it on in the
+      // phase before)
+      for (int j = 0; j < filled; ++j)
+        if (!warp_wait(&landed[j], (j < sl ? ph ^ 1 : ph) & 1) && lane == 0)
+          raise_error(err, PA_DEVERR_TIMEOUT);
     } else if (warp == Ly::MMA_WARP) {
-      // ================================================ MMA issue (one thread)
-      if (lane == 0) {
-        constexpr uint32_t idesc_s = umma_idesc_f16(kBf16, kTreeRows, kTreeTile, false);
-        constexpr uint32_t idesc_o = umma_idesc_f16(kBf16, kTreeRows, D, true);
-        const uint32_t sq = smem_u32(smem), skv = smem_u32(smem + Ly::OFF_KV);
-        long long c = 0;  // tiles whose S has been issued
-        auto issue_s = [&]() -> bool {
-          const long long k = 2 * c;
-          const int sl = static_cast<int>(k % NS), b = static_cast<int>(c & 1);
-          if (!mbar_wait_bounded(&full[sl], static_cast<uint32_t>((k / NS) & 1))) return false;
-          // the buffer's last weights have been read
-          if (c >= 2 && !mbar_wait_bounded(&pv_done[b], static_cast<uint32_t>(((c >> 1) - 1) & 1)))
+      // ================================================ MMA issue
+      constexpr uint32_t idesc_s = umma_idesc_f16(kBf16, kTreeRows, TT, false);
+      constexpr uint32_t idesc_o = umma_idesc_f16(kBf16, kTreeRows, D, true);
+      // low words of the operands' descriptors: an address adds its 16-byte units
+      const uint32_t dq = tree_desc_lo(smem_u32(smem), 16);
+      const uint32_t dk0 = tree_desc_lo(smem_u32(smem + Ly::OFF_KV), 16);
+      const uint32_t dv0 = tree_desc_lo(smem_u32(smem + Ly::OFF_KV), TT * 128);
+      const uint32_t tb = uniform(tmem);
+      const uint32_t us = tb, up = INPL ? tb : tb + 64, uo = tb + NQ * 128;
+      int ks = 0, vs = 1;         // slots of the next K and V tile
+      uint32_t kph = 0, vph = 0;  // and their phases
+      auto step2 = [&](int& sl, uint32_t& ph) {
+        sl += 2;
+        if (sl >= NS) {
+          sl -= NS;
+          ph ^= 1;
+        }
+      };
+      uint32_t cs[2] = {0, 0};  // tiles whose S has been issued, of query tile q
+      uint32_t cd[2] = {0, 0};  // tiles whose P V has been issued, of query tile q
+      // S of query tile q on the K tile in slot ks; `last`: the slot's last reader
+      auto issue_s = [&](int q, bool last) -> bool {
+        if (!warp_wait(&full[ks], kph)) return false;
+        // S's columns are free: the last tile's logits have been read (P in
+        // buffers of its own), or its weights used (P over S)
+        if (cs[q] >= 1) {
+          const uint32_t x = cs[q] - 1;
+          if (!(INPL ? warp_wait(&pv_done[2 * q + (x & 1)], (x >> 1) & 1)
+                     : warp_wait(&s_free[q], x & 1)))
             return false;
-          tc05_fence_after();
-          const uint32_t kt = skv + sl * Ly::SLOT;
+        }
+        tc05_fence_after();
+        const uint32_t dk = dk0 + ks * (Ly::SLOT >> 4), dqt = dq + q * (Ly::QBYTES1 >> 4);
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            umma_f16(t_s + b * kTreeTile,
-                     umma_sdesc_sw128(sq + (kk >> 2) * (kTreeRows * 128) + (kk & 3) * 32, 16, 1024),
-                     umma_sdesc_sw128(kt + (kk >> 2) * (kTreeTile * 128) + (kk & 3) * 32, 16, 1024),
-                     idesc_s, kk > 0);
-          umma_commit(&s_full[b]);
-          umma_commit(&empty[sl]);
-          ++c;
-          return true;
-        };
-        bool ok = true;
-        long long done = 0;  // tiles whose P V has been issued
-        for (int piece = 0; w.left > 0 && ok; ++piece, w.next(p)) {
-          ok = mbar_wait_bounded(q_full, piece & 1) && issue_s();
-          for (int i = 0; i < w.len && ok; ++i, ++done) {
-            if (i + 1 < w.len) ok = issue_s();
-            const long long k = 2 * done + 1;
-            const int sl = static_cast<int>(k % NS), b = static_cast<int>(done & 1);
-            ok = ok && mbar_wait_bounded(&full[sl], static_cast<uint32_t>((k / NS) & 1)) &&
-                 mbar_wait_bounded(&p_full[b], static_cast<uint32_t>((done >> 1) & 1));
-            if (!ok) break;
-            tc05_fence_after();
-            const uint32_t vt = skv + sl * Ly::SLOT;
+            tree_mma_ss(us + q * TT, dqt + ((kk >> 2) * (kTreeRows * 128) + (kk & 3) * 32) / 16,
+                        dk + ((kk >> 2) * (TT * 128) + (kk & 3) * 32) / 16, idesc_s, kk > 0);
+          umma_commit(&s_full[q]);
+          if (last) umma_commit(&empty[ks]);
+        }
+        __syncwarp();
+        ++cs[q];
+        if (last) step2(ks, kph);
+        return true;
+      };
+      // O += P V of query tile q on the V tile in slot vs
+      auto issue_pv = [&](int q, bool accumulate, bool last) -> bool {
+        const uint32_t b = cd[q] & 1;
+        if (!warp_wait(&full[vs], vph) || !warp_wait(&p_full[2 * q + b], (cd[q] >> 1) & 1))
+          return false;
+        tc05_fence_after();
+        const uint32_t dv = dv0 + vs * (Ly::SLOT >> 4), tp = INPL ? up + q * TT : up + b * 32;
+        if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < kTreeTile / 16; ++kk)
-              umma_f16_ts(t_o, t_s + b * kTreeTile + kk * 8,
-                          umma_sdesc_sw128(vt + kk * 2048, kTreeTile * 128, 1024), idesc_o,
-                          i > 0 || kk > 0);
-            umma_commit(&pv_done[b]);
-            umma_commit(&empty[sl]);
+          for (int kk = 0; kk < TT / 16; ++kk)
+            tree_mma_ts(uo + q * D, tp + kk * 8, dv + kk * (2048 / 16), idesc_o, kk > 0 || accumulate);
+          umma_commit(&pv_done[2 * q + b]);
+          if (last) umma_commit(&empty[vs]);
+        }
+        __syncwarp();
+        ++cd[q];
+        if (last) step2(vs, vph);
+        return true;
+      };
+      bool ok = true;
+      int len = uniform(w.len);
+      for (int piece[2] = {0, 0}; len > 0 && ok;) {
+        const int nq = uniform(live_tiles());
+#pragma unroll
+        for (int q = 0; q < NQ; ++q)
+          if (q < nq) {
+            ok = ok && warp_wait(&q_full[q], piece[q]++ & 1);
+            ok = ok && issue_s(q, q == nq - 1);
+          }
+        for (int i = 0; i < len && ok; ++i) {
+          if constexpr (!INPL) {
+            if (i + 1 < len) ok = issue_s(0, true);
+            ok = ok && issue_pv(0, i > 0, true);
+          } else {
+#pragma unroll
+            for (int q = 0; q < NQ; ++q)
+              if (q < nq) {
+                ok = ok && issue_pv(q, i > 0, q == nq - 1);
+                if (i + 1 < len) ok = ok && issue_s(q, q == nq - 1);
+              }
           }
         }
-        if (!ok) raise_error(err, PA_DEVERR_TIMEOUT);
+        w.next(p);
+        len = uniform(w.left > 0 ? w.len : 0);
       }
+      if (!ok && lane == 0) raise_error(err, PA_DEVERR_TIMEOUT);
     } else if (C8 && warp >= Ly::CONV_WARP) {
       // ================================================ 8-bit codes: widening to f16
+      // A warp takes 16 tokens of each 64, a lane 16 codes of NR of them.
       if constexpr (C8) {
-        const int row = tid - Ly::CONV_WARP * 32;  // a thread widens one token's row
-        long long k = 0;
+        constexpr int LPR = D / 16, RSTEP = 32 / LPR, NR = 16 / RSTEP;
+        const int c16 = lane % LPR, r0 = (warp - Ly::CONV_WARP) * 16 + lane / LPR;
+        // the second column block's lanes store their odd chunk first, so
+        // that the eight lanes of a row (D 128) cover all banks
+        const int sw = (KB == 2 && c16 >= 4) ? 1 : 0;
         bool ok = true;
-        for (; w.left > 0 && ok; w.next(p)) {
-          const int32_t* table = p.block_tables + (size_t)w.s * p.max_blocks_per_seq;
-          for (int i = 0; i < w.len && ok; ++i) {
-            const int t = (w.tile + i) * kTreeTile + row;
-            bool live = t < w.q.n;
-            if (live) {
-              const int b = __ldg(table + t / bs);
-              live = b >= 0 && b < p.num_blocks;
-            }
+        int sl = 0;
+        uint32_t ph = 0;
+        for (long long k = 0; k < 2 * units; ++k) {
+          if (!warp_wait(&raw_full[sl], ph)) {
+            ok = false;
+            break;
+          }
+          uint8_t* dst = smem + Ly::OFF_KV + sl * Ly::SLOT;
+          const uint8_t* raw = Ly::RAW ? smem + Ly::OFF_RAW + sl * Ly::RAW : dst + Ly::SLOT / 2;
 #pragma unroll
-            for (int kv = 0; kv < 2; ++kv, ++k) {
-              const int rs = static_cast<int>(k % RS), sl = static_cast<int>(k % NS);
-              if (!mbar_wait_bounded(&raw_full[rs], static_cast<uint32_t>((k / RS) & 1)) ||
-                  (k >= NS &&
-                   !mbar_wait_bounded(&empty[sl], static_cast<uint32_t>((k / NS - 1) & 1)))) {
-                raise_error(err, PA_DEVERR_TIMEOUT);
-                ok = false;
-                break;
-              }
-              const uint8_t* raw = smem + Ly::OFF_RAW + rs * Ly::RSLOT;
-              uint8_t* dst = smem + Ly::OFF_KV + sl * Ly::SLOT;
+          for (int half = 0; half < TT / 64; ++half) {
+            uint4 src[NR];
 #pragma unroll
-              for (int e = 0; e < KB * 8; ++e) {
-                const int ch = (e + row) & (KB * 8 - 1);  // rotated: a warp's rows hit other banks
-                uint4 o = make_uint4(0u, 0u, 0u, 0u);
-                if (live) {
-                  const uint2 v = *reinterpret_cast<const uint2*>(raw + row * D + 8 * ch);
-                  using Code = typename std::conditional<ROW_SC, I8, E4M3>::type;
-                  widen8<Code>(v.x, o.x, o.y);
-                  widen8<Code>(v.y, o.z, o.w);
-                }
-                *reinterpret_cast<uint4*>(dst + (ch >> 3) * (kTreeTile * 128) + row * 128 +
-                                          (((ch & 7) ^ (row & 7)) << 4)) = o;
+            for (int j = 0; j < NR; ++j)
+              src[j] = *reinterpret_cast<const uint4*>(raw + (half * 64 + r0 + j * RSTEP) * D + 16 * c16);
+            __syncwarp();  // (D 128) the warp's codes are read before their bytes are written
+            using Code = typename std::conditional<ROW_SC, I8, E4M3>::type;
+#pragma unroll
+            for (int j = 0; j < NR; ++j) {
+              const int row = half * 64 + r0 + j * RSTEP;
+              uint4 o[2];
+              widen8<Code>(src[j].x, o[0].x, o[0].y);
+              widen8<Code>(src[j].y, o[0].z, o[0].w);
+              widen8<Code>(src[j].z, o[1].x, o[1].y);
+              widen8<Code>(src[j].w, o[1].z, o[1].w);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int ch = 2 * c16 + (h ^ sw);
+                *reinterpret_cast<uint4*>(dst + (ch >> 3) * (TT * 128) + row * 128 +
+                                          (((ch & 7) ^ (row & 7)) << 4)) = sw ^ h ? o[1] : o[0];
               }
-              if (ROW_SC && kv == 0) {
-                const float* rsc = reinterpret_cast<const float*>(raw + kTreeTile * D);
-                float* sct = sc + ((k >> 1) % Ly::SCT) * 2 * kTreeTile;
-                sct[row] = live ? rsc[row] : 0.f;
-                sct[kTreeTile + row] = live ? rsc[kTreeTile + row] : 0.f;
-              }
-              fence_proxy_async_smem();
-              mbar_arrive(&full[sl]);
-              mbar_arrive(&raw_empty[rs]);
             }
           }
-          if (!ok) break;
+          fence_proxy_async_smem();
+          mbar_arrive(&full[sl]);
+          if (++sl == NS) {
+            sl = 0;
+            ph ^= 1;
+          }
         }
+        if (!ok && lane == 0) raise_error(err, PA_DEVERR_TIMEOUT);
       }
-    } else if (warp < 4) {
+    } else if (warp < Ly::MMA_WARP) {
       // ================================================ softmax, one row per thread
       // (tcgen05.ld / st are warp-wide: every decision that leads to one is
       // taken by the whole warp)
-      const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
-      const uint32_t sq = smem_u32(smem);
+      const int q = warp >> 2;  // query tile
+      const int r1 = tid & 127;  // its row: TMEM lane
+      const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const uint32_t t_s = t_s0 + q * TT + lane_off, t_p = t_p0 + q * TT + lane_off;
+      const uint32_t t_o = t_o0 + q * D + lane_off;
+      uint64_t* pf = p_full + 2 * q;
+      uint64_t* pd = pv_done + 2 * q;
+      uint8_t* qrow = smem + q * Ly::QBYTES1 + r1 * 128;
       constexpr float kLazy = 8.f;  // weights stay <= 2^kLazy
-      long long c = 0;              // tiles taken
+      long long ct = 0;             // tiles of the CTA before the piece
+      long long c = 0;              // tiles this query tile has taken
       bool failed = false;
-      for (int piece = 0; w.left > 0; ++piece, w.next(p)) {
-        const int rows_total = w.q.q_len * G;
-        const int r = w.rt * kTreeRows + tid;
-        const bool live = r < rows_total;
-        const int node = live ? r / G : 0;
-        const size_t orow = ((size_t)(w.q.q0 + node) * Hq + w.g * G + (live ? r % G : 0));
-        // ---- the row's query (every MMA on the last piece's has completed)
+      // the row of the current piece
+      int node = 0, rows_total = 0;
+      size_t orow = 0;
+      bool live = false;
+      auto set_row = [&]() {
+        rows_total = w.q.q_len * G;
+        const int r = w.rt * ROWS + q * kTreeRows + r1;
+        live = r < rows_total;
+        node = live ? r / G : 0;
+        orow = ((size_t)(w.q.q0 + node) * Hq + w.g * G + (live ? r % G : 0));
+      };
+      // the row's query, asynchronously (every S product on the last piece's has completed)
+      auto load_q = [&]() {
         const uint8_t* src = static_cast<const uint8_t*>(p.query) + orow * D * 2;
-        const uint32_t qrow = sq + tid * 128;
 #pragma unroll
         for (int ch = 0; ch < KB * 8; ++ch)
-          cp_async16(qrow + (ch >> 3) * (kTreeRows * 128) + (((ch & 7) ^ (tid & 7)) << 4),
+          cp_async16(smem_u32(qrow) + (ch >> 3) * (kTreeRows * 128) + (((ch & 7) ^ (r1 & 7)) << 4),
                      src + ch * 16, live);
-        cp_async_wait_all();
-        if constexpr (C8 && std::is_same<QT, __nv_bfloat16>::value) {
-          // q is carried in f16 (exact inside f16's range)
+      };
+      set_row();
+      bool work = q < live_tiles();
+      if (work) load_q();
+      for (int piece = 0; w.left > 0; ++piece) {
+        if (work) {
+          cp_async_wait_all();
+          if constexpr (C8 && std::is_same<QT, __nv_bfloat16>::value) {
+            // q is carried in f16 (exact inside f16's range)
 #pragma unroll
-          for (int ch = 0; ch < KB * 8; ++ch) {
-            uint4* q16 = reinterpret_cast<uint4*>(smem + tid * 128 + (ch >> 3) * (kTreeRows * 128) +
-                                                  (ch & 7) * 16);
-            uint4 v = *q16;
-            uint32_t* e = reinterpret_cast<uint32_t*>(&v);
+            for (int ch = 0; ch < KB * 8; ++ch) {
+              uint4* q16 = reinterpret_cast<uint4*>(qrow + (ch >> 3) * (kTreeRows * 128) + (ch & 7) * 16);
+              uint4 v = *q16;
+              uint32_t* e = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const __nv_bfloat162 b = *reinterpret_cast<const __nv_bfloat162*>(&e[j]);
-              const __half2 h = __floats2half2_rn(__low2float(b), __high2float(b));
-              e[j] = *reinterpret_cast<const uint32_t*>(&h);
+              for (int j = 0; j < 4; ++j) {
+                const __nv_bfloat162 b = *reinterpret_cast<const __nv_bfloat162*>(&e[j]);
+                const __half2 h = __floats2half2_rn(__low2float(b), __high2float(b));
+                e[j] = *reinterpret_cast<const uint32_t*>(&h);
+              }
+              *q16 = v;
             }
-            *q16 = v;
           }
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(q_full);
+          fence_proxy_async_smem();
+          mbar_arrive(&q_full[q]);
 
-        const int ctx = w.q.n - w.q.q_len;
-        const unsigned long long* words =
-            p.mask + (size_t)(w.q.q0 + node) * p.mask_words;
-        float m = -INFINITY, l = 0.f;
-        for (int i = 0; i < w.len; ++i, ++c) {
-          const int b = static_cast<int>(c & 1);
-          const uint32_t par = static_cast<uint32_t>((c >> 1) & 1);
-          const int t0 = (w.tile + i) * kTreeTile;
-          // the tile's visible tokens (asked for before the wait)
-          const bool masked = t0 + kTreeTile > ctx;  // CTA-uniform
-          unsigned long long seen = ~0ull;
-          if (masked) seen = live ? tree_seen(words, p.mask_words, t0, ctx, w.q.n) : 0ull;
-          if (__any_sync(0xffffffffu, !mbar_wait_bounded(&s_full[b], par))) {
+          const int ctx = w.q.n - w.q.q_len;
+          // a warp without rows only keeps the barriers' count (its rows of S,
+          // P and O may hold anything: no MMA mixes rows)
+          const bool warp_live = w.rt * ROWS + q * kTreeRows + (warp & 3) * 32 < rows_total;
+          const unsigned long long* words = p.mask + (size_t)(w.q.q0 + node) * p.mask_words;
+          float m = -INFINITY, l = 0.f;
+          for (int i = 0; i < w.len; ++i, ++c) {
+            const int b = static_cast<int>(c & 1);
+            const int t0 = (w.tile + i) * TT;
+            // the tile's visible tokens (asked for before the wait)
+            const bool masked = t0 + TT > ctx;  // CTA-uniform
+            uint32_t seen[TT / 32];
+#pragma unroll
+            for (int h = 0; h < TT / 64; ++h) {
+              unsigned long long v = ~0ull;
+              if (masked) v = live ? tree_seen(words, p.mask_words, t0 + 64 * h, ctx, w.q.n) : 0ull;
+              seen[2 * h] = static_cast<uint32_t>(v);
+              seen[2 * h + 1] = static_cast<uint32_t>(v >> 32);
+            }
+            if (__any_sync(0xffffffffu, !mbar_wait_bounded(&s_full[q], static_cast<uint32_t>(c & 1)))) {
+              failed = true;
+              break;
+            }
+            const long long kv = 2 * (ct + i) + 1;  // V's slot
+            const float* sct = sc + ((ct + i) % Ly::SCT) * 2 * TT;  // INT8 row scales
+            if constexpr (ROW_SC) {
+              // they landed with K's codes, before V's slot was filled (K's may be
+              // on its next phase already)
+              if (__any_sync(0xffffffffu, !mbar_wait_bounded(&full[kv % NS],
+                                                             static_cast<uint32_t>((kv / NS) & 1)))) {
+                failed = true;
+                break;
+              }
+            }
+            if (warp_live) {
+              tc05_fence_after();
+              __syncwarp();
+              // The tile's logits come 32 tokens at a time and, where the
+              // registers do not hold them all (8-bit caches: more threads; 128
+              // tokens), once more for the weights. (Handing the registers out
+              // by warpgroup, so that 8-bit caches hold them too, took 241 us
+              // instead of 206 on 16 sequences over an FP8 cache of 617 MB: the
+              // copying and widening warps spilled.)
+              constexpr int NH = TT / 32;
+              constexpr bool AGAIN = C8 || INPL;
+              uint32_t sr[AGAIN ? 1 : NH][32];
+              float mx = -INFINITY;  // the largest seen logit, log2 units
+              if constexpr (AGAIN) {
+#pragma unroll
+                for (int h = 0; h < NH; ++h) {
+                  tmem_ld32(t_s + 32 * h, sr[0]);
+                  tmem_wait_ld();
+                  mx = fmaxf(mx, half_max<ROW_SC>(sr[0], sct + 32 * h, p.scale_log2, masked, seen[h]));
+                }
+              } else {
+#pragma unroll
+                for (int h = 0; h < NH; ++h) tmem_ld32(t_s + 32 * h, sr[h]);
+                tmem_wait_ld();
+                tc05_fence_before();
+                mbar_arrive(&s_free[q]);
+#pragma unroll
+                for (int h = 0; h < NH; ++h)
+                  mx = fmaxf(mx, half_max<ROW_SC>(sr[h], sct + 32 * h, p.scale_log2, masked, seen[h]));
+              }
+              if (__any_sync(0xffffffffu, mx > m + kLazy)) {
+                const float mn = fmaxf(m, mx);
+                if (i > 0) {
+                  // O holds the tiles so far: scale it by 2^(m - mn) once the last
+                  // P V has landed
+                  const long long cp = c - 1;
+                  if (__any_sync(0xffffffffu,
+                                 !mbar_wait_bounded(&pd[cp & 1],
+                                                    static_cast<uint32_t>((cp >> 1) & 1)))) {
+                    failed = true;
+                    break;
+                  }
+                  tc05_fence_after();
+                  __syncwarp();
+                  const float al = mn == -INFINITY ? 1.f : exp2f(m - mn);
+#pragma unroll
+                  for (int c0 = 0; c0 < D; c0 += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(t_o + c0, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+                    tmem_st16(t_o + c0, o);
+                  }
+                  tmem_wait_st();
+                  l *= al;
+                }
+                m = mn;
+              }
+              // a row that has seen nothing yet keeps weights of zero
+              const float mu = m == -INFINITY ? 0.f : m;
+              float2 sum = make_float2(0.f, 0.f);
+              // the P V before the last has read this buffer
+              if (!INPL && c >= 2 &&
+                  __any_sync(0xffffffffu,
+                             !mbar_wait_bounded(&pd[b], static_cast<uint32_t>(((c >> 1) - 1) & 1)))) {
+                failed = true;
+                break;
+              }
+#pragma unroll
+              for (int h = 0; h < NH; ++h) {
+                if constexpr (AGAIN) {
+                  tmem_ld32(t_s + 32 * h, sr[0]);
+                  tmem_wait_ld();
+                  if (!INPL && h == NH - 1) {
+                    tc05_fence_before();
+                    mbar_arrive(&s_free[q]);
+                  }
+                }
+                uint32_t pk[16];
+                half_weights<T, ROW_SC>(sr[AGAIN ? 0 : h], sct + 32 * h, sct + TT + 32 * h, p.scale_log2,
+                                        mu, masked, seen[h], sum, pk);
+                // (P over S: these columns' logits have been read)
+                tmem_st16(t_p + (INPL ? 0 : b * 32) + 16 * h, pk);
+              }
+              l += sum.x + sum.y;
+              tmem_wait_st();
+            } else if (!INPL) {
+              mbar_arrive(&s_free[q]);
+            }
+            const int valid = w.q.n - t0;
+            if (q == 0 && valid < TT) {  // uniform for the query tile
+              // V rows past the sequence may hold anything, and zero times NaN
+              // is NaN in the MMA: zero them (the first query tile's arrival
+              // comes before either tile's P V is issued)
+              if (__any_sync(0xffffffffu, !mbar_wait_bounded(&full[kv % NS],
+                                                             static_cast<uint32_t>((kv / NS) & 1)))) {
+                failed = true;
+                break;
+              }
+              uint8_t* vt = smem + Ly::OFF_KV + (kv % NS) * Ly::SLOT;
+              for (int z = r1; z < (TT - valid) * KB * 8; z += kTreeRows) {
+                const int row = valid + z / (KB * 8), kb = (z / 8) % KB, ch = z % 8;
+                *reinterpret_cast<uint4*>(vt + kb * (TT * 128) + row * 128 + ch * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+              }
+              fence_proxy_async_smem();
+            }
+            tc05_fence_before();
+            mbar_arrive(&pf[b]);
+          }
+          if (failed) break;
+          // ---- the row's output, or its partial; the next piece's query is on
+          // its way meanwhile (all S products on this one's have completed)
+          const bool whole = w.len == w.q.T, was_live = live;
+          const size_t out_row = orow;
+          ct += w.len;
+          w.next(p);
+          if (w.left > 0) {
+            set_row();
+            work = q < live_tiles();
+            if (work) load_q();
+          }
+          const long long cl = c - 1;
+          if (__any_sync(0xffffffffu,
+                         !mbar_wait_bounded(&pd[cl & 1], static_cast<uint32_t>((cl >> 1) & 1)))) {
             failed = true;
             break;
           }
           tc05_fence_after();
           __syncwarp();
-          uint32_t sr[2][32];
-          tmem_ld32(t_s + b * kTreeTile + lane_off, sr[0]);
-          tmem_ld32(t_s + b * kTreeTile + 32 + lane_off, sr[1]);
-          tmem_wait_ld();
-          const float* sct = sc + (c % Ly::SCT) * 2 * kTreeTile;  // INT8 row scales
-          if constexpr (ROW_SC) {
-            // the widening threads wrote them before they filled V's slot
-            // (K's may be on its next phase already)
-            const long long k = 2 * c + 1;
-            if (__any_sync(0xffffffffu,
-                           !mbar_wait_bounded(&full[k % NS], static_cast<uint32_t>((k / NS) & 1)))) {
-              failed = true;
-              break;
-            }
-          }
-          // logits in log2 units; unseen tokens are -inf
-          float x[kTreeTile];
+          const float inv = (l > 0.f ? 1.f / l : 0.f) * (KC == kTE4 ? p.v_scale : 1.f);
+          const size_t slot = (size_t)cta * 2 + (piece > 0 ? 1 : 0);
+          QT* dst = static_cast<QT*>(p.out) + out_row * D;
+          float4* po = p.part_o + slot * (D / 4) * ROWS + tid;
+          if (warp_live) {
 #pragma unroll
-          for (int e = 0; e < kTreeTile; ++e) {
-            x[e] = __uint_as_float(sr[e >> 5][e & 31]) * p.scale_log2;
-            if constexpr (ROW_SC) x[e] *= sct[e];
-          }
-          if (masked) {
+            for (int c0 = 0; c0 < D; c0 += 32) {
+              uint32_t o[32];
+              tmem_ld32(t_o + c0, o);
+              tmem_wait_ld();
+              if (!was_live) continue;
+              if (whole) {
 #pragma unroll
-            for (int e = 0; e < kTreeTile; ++e) x[e] = (seen >> e) & 1ull ? x[e] : -INFINITY;
-          }
-          float mx = x[0];
+                for (int e = 0; e < 32; e += 8) {
+                  uint4 v;
+                  v.x = Mma<QT>::pack(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+                  v.y = Mma<QT>::pack(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+                  v.z = Mma<QT>::pack(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
+                  v.w = Mma<QT>::pack(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
+                  *reinterpret_cast<uint4*>(dst + c0 + e) = v;
+                }
+              } else {
 #pragma unroll
-          for (int e = 1; e < kTreeTile; ++e) mx = fmaxf(mx, x[e]);
-          if (__any_sync(0xffffffffu, mx > m + kLazy)) {
-            const float mn = fmaxf(m, mx);
-            if (i > 0) {
-              // O holds the tiles so far: scale it by 2^(m - mn) once the last
-              // P V has landed
-              const long long cp = c - 1;
-              if (__any_sync(0xffffffffu, !mbar_wait_bounded(&pv_done[cp & 1],
-                                                             static_cast<uint32_t>((cp >> 1) & 1)))) {
-                failed = true;
-                break;
+                for (int e = 0; e < 32; e += 4)
+                  po[(size_t)((c0 + e) / 4) * ROWS] =
+                      make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
+                                  __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
               }
-              tc05_fence_after();
-              __syncwarp();
-              const float al = mn == -INFINITY ? 1.f : exp2f(m - mn);
-#pragma unroll
-              for (int c0 = 0; c0 < D; c0 += 32) {
-                uint32_t o[32];
-                tmem_ld32(t_o + c0 + lane_off, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
-                tmem_st32(t_o + c0 + lane_off, o);
-              }
-              tmem_wait_st();
-              l *= al;
             }
-            m = mn;
           }
-          // weights rounded to the MMA type (INT8: times the V row scale
-          // first); the running sum takes the fp32 weights. A row that has
-          // seen nothing yet keeps weights of zero.
-          const float mu = m == -INFINITY ? 0.f : m;
-          uint32_t pk[32];
-          float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-          for (int e = 0; e < kTreeTile; e += 2) {
-            const float p0 = ex2_approx(x[e] - mu), p1 = ex2_approx(x[e + 1] - mu);
-            l0 += p0;
-            l1 += p1;
-            if constexpr (ROW_SC)
-              pk[e / 2] = Mma<T>::pack(p0 * sct[kTreeTile + e], p1 * sct[kTreeTile + e + 1]);
-            else
-              pk[e / 2] = Mma<T>::pack(p0, p1);
-          }
-          l += l0 + l1;
-          tmem_st32(t_s + b * kTreeTile + lane_off, pk);
-          tmem_wait_st();
-          const int valid = w.q.n - t0;
-          if (!C8 && valid < kTreeTile) {  // CTA-uniform
-            // V rows past the sequence may hold anything, and zero times NaN
-            // is NaN in the MMA: zero them
-            const long long k = 2 * c + 1;
-            if (__any_sync(0xffffffffu,
-                           !mbar_wait_bounded(&full[k % NS], static_cast<uint32_t>((k / NS) & 1)))) {
-              failed = true;
-              break;
-            }
-            uint8_t* vt = smem + Ly::OFF_KV + (k % NS) * Ly::SLOT;
-            for (int z = tid; z < (kTreeTile - valid) * KB * 8; z += kTreeRows) {
-              const int row = valid + z / (KB * 8), kb = (z / 8) % KB, ch = z % 8;
-              *reinterpret_cast<uint4*>(vt + kb * (kTreeTile * 128) + row * 128 + ch * 16) =
-                  make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async_smem();
-          }
+          if (!whole && was_live) p.part_ml[slot * ROWS + tid] = make_float2(m, l);
+          // the accumulator has been read before the next piece's weights (whose
+          // arrival lets the MMAs overwrite it) are announced
           tc05_fence_before();
-          mbar_arrive(&p_full[b]);
-        }
-        if (failed) break;
-        // ---- the row's output, or its partial
-        const long long cl = c - 1;
-        if (__any_sync(0xffffffffu, !mbar_wait_bounded(&pv_done[cl & 1],
-                                                       static_cast<uint32_t>((cl >> 1) & 1)))) {
-          failed = true;
-          break;
-        }
-        tc05_fence_after();
-        __syncwarp();
-        const bool whole = w.len == w.q.T;
-        const float inv = (l > 0.f ? 1.f / l : 0.f) * (KC == kTE4 ? p.v_scale : 1.f);
-        const size_t slot = (size_t)cta * 2 + (piece > 0 ? 1 : 0);
-        QT* dst = static_cast<QT*>(p.out) + orow * D;
-        float4* po = p.part_o + slot * (D / 4) * kTreeRows + tid;
-#pragma unroll
-        for (int c0 = 0; c0 < D; c0 += 32) {
-          uint32_t o[32];
-          tmem_ld32(t_o + c0 + lane_off, o);
-          tmem_wait_ld();
-          if (!live) continue;
-          if (whole) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              uint4 v;
-              v.x = Mma<QT>::pack(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
-              v.y = Mma<QT>::pack(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-              v.z = Mma<QT>::pack(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
-              v.w = Mma<QT>::pack(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
-              *reinterpret_cast<uint4*>(dst + c0 + e) = v;
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              po[(size_t)((c0 + e) / 4) * kTreeRows] =
-                  make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
-                              __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+        } else {
+          // no rows for this query tile in the piece
+          ct += w.len;
+          w.next(p);
+          if (w.left > 0) {
+            set_row();
+            work = q < live_tiles();
+            if (work) load_q();
           }
         }
-        if (!whole && live) p.part_ml[slot * kTreeRows + tid] = make_float2(m, l);
-        // the accumulator has been read before the next piece's weights (whose
-        // arrival lets the MMAs overwrite it) are announced
-        tc05_fence_before();
       }
       if (failed) raise_error(err, PA_DEVERR_TIMEOUT);
     }
@@ -701,19 +980,23 @@ __global__ void __launch_bounds__(TreeLayout<D, KC>::THREADS, 2)
 
 // Joins the partial rows of cut (sequence, kv head, row tile) segments:
 // with M the largest maximum, out = sum_j 2^(m_j - M) o_j / sum_j 2^(m_j - M) l_j.
-// CTA (row slice of 16, (kv head, row tile), sequence), 128 threads: thread
-// (column group, row) with rows fastest, as the partials are stored.
-constexpr int kJoinRows = 16, kJoinThreads = 128;
+// CTA (slice of 8 rows, (kv head, row tile), sequence): the factors of the
+// slice's pieces go to shared memory first, so that the loads of the partial
+// rows do not wait for one another. Thread (column group, row) with rows
+// fastest, as the partials are stored.
+constexpr int kJoinRows = 8, kJoinThreads = 128, kJoinGroups = kJoinThreads / kJoinRows;
 template <typename QT, int D>
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ TreeParams p,
                                                                 float out_scale) {
+  __shared__ float fac[kTreeMaxCtas][kJoinRows];  // 2^(m_j - M), zero where l_j is
+  __shared__ float inv[kJoinRows];
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, lane = tid & 31, s = blockIdx.z, C = p.ctas;
+  const int tid = threadIdx.x, lane = tid & 31, s = blockIdx.z;
   const int g = blockIdx.y % p.num_kv_heads, rt = blockIdx.y / p.num_kv_heads;
   const TreeSeq q = tree_seq(p, s, false);
   const int rows_total = q.q_len * p.group;
-  const int r0 = rt * kTreeRows + blockIdx.x * kJoinRows;
+  const int R = p.tile_rows, r0 = rt * R + blockIdx.x * kJoinRows;
   if (q.T == 0 || r0 >= rows_total) return;
   // units before this sequence, and of all (every warp the same)
   long long before = 0, P = 0;
@@ -727,64 +1010,85 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
     P += __shfl_xor_sync(0xffffffffu, P, off);
     before += __shfl_xor_sync(0xffffffffu, before, off);
   }
-  const long long seg0 = before + ((long long)g * q.RT + rt) * q.T, seg1 = seg0 + q.T;
-  const int c0 = tree_cta(seg0, P, C), c1 = tree_cta(seg1 - 1, P, C);
-  if (c0 == c1) return;  // not cut
-  const int rr = tid % kJoinRows, r = r0 + rr;
-  if (r >= rows_total) return;
-  const int lr = r % kTreeRows;  // row of the tile
-  // with P < C most CTAs hold at most one unit and some none
-  auto slot_of = [&](int c) -> long long {
-    const long long a = tree_lo(c, P, C);
-    if (tree_lo(c + 1, P, C) <= a) return -1;
-    return (long long)c * 2 + (a < seg0 ? 1 : 0);
-  };
-  float M = -INFINITY;
-  for (int c = c0; c <= c1; ++c) {
-    const long long sl = slot_of(c);
-    if (sl < 0) continue;
-    const float2 ml = p.part_ml[sl * kTreeRows + lr];
-    if (ml.y > 0.f) M = fmaxf(M, ml.x);
+  const long long U = tree_share(P, p.ctas);
+  const long long seg0 = before + ((long long)g * q.RT + rt) * q.T;
+  const int c0 = static_cast<int>(tree_div(seg0, U));
+  const int n = static_cast<int>(tree_div(seg0 + q.T - 1, U)) - c0 + 1;
+  if (n == 1) return;  // not cut
+  // piece j sits in CTA c0 + j: in its first slot unless it began the segment
+  // after other work
+  const int first = seg0 != c0 * U ? 1 : 0;
+  const int rr = tid % kJoinRows, lr0 = r0 % R;
+  const float2* ml = p.part_ml + (size_t)c0 * 2 * R + lr0;
+  for (int i = tid; i < n * kJoinRows; i += kJoinThreads) {
+    const int j = i / kJoinRows;
+    const float2 v = ml[(size_t)(2 * j + (j == 0 ? first : 0)) * R + i % kJoinRows];
+    fac[j][i % kJoinRows] = v.y > 0.f ? v.x : -INFINITY;
   }
-  constexpr int NC = D / 4 / (kJoinThreads / kJoinRows);  // column groups per thread
+  __syncthreads();
+  const int cg = tid / kJoinRows;
+  float M = -INFINITY;
+  for (int j = 0; j < n; ++j) M = fmaxf(M, fac[j][rr]);
+  __syncthreads();
+  if (M == -INFINITY) M = 0.f;  // nothing seen in any piece: every factor is zero
+  for (int j = cg; j < n; j += kJoinGroups) fac[j][rr] = exp2f(fac[j][rr] - M);
+  __syncthreads();
+  if (tid < kJoinRows) {
+    float l = 0.f;
+    for (int j = 0; j < n; ++j)
+      l = fmaf(fac[j][rr], ml[(size_t)(2 * j + (j == 0 ? first : 0)) * R + rr].y, l);
+    inv[rr] = (l > 0.f ? 1.f / l : 0.f) * out_scale;
+  }
+  constexpr int NC = D / 4 / kJoinGroups;  // column groups per thread
+  const float4* po = p.part_o + (size_t)c0 * 2 * (D / 4) * R + lr0 + rr;
   float4 acc[NC];
 #pragma unroll
-  for (int j = 0; j < NC; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-  for (int c = c0; c <= c1; ++c) {
-    const long long sl = slot_of(c);
-    if (sl < 0) continue;
-    const float2 ml = p.part_ml[sl * kTreeRows + lr];
-    if (!(ml.y > 0.f)) continue;
-    const float f = exp2f(ml.x - M);
-    l += f * ml.y;
+  for (int k = 0; k < NC; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int J = 8;  // pieces whose loads are in flight together
+  for (int j0 = 0; j0 < n; j0 += J) {
+    float4 v[J][NC];
+    float f[J];
 #pragma unroll
-    for (int j = 0; j < NC; ++j) {
-      const int c4 = tid / kJoinRows + j * (kJoinThreads / kJoinRows);
-      const float4 v = p.part_o[(sl * (D / 4) + c4) * kTreeRows + lr];
-      acc[j].x = fmaf(f, v.x, acc[j].x);
-      acc[j].y = fmaf(f, v.y, acc[j].y);
-      acc[j].z = fmaf(f, v.z, acc[j].z);
-      acc[j].w = fmaf(f, v.w, acc[j].w);
+    for (int u = 0; u < J; ++u) {
+      const int j = j0 + u;
+      f[u] = j < n ? fac[j][rr] : 0.f;
+#pragma unroll
+      for (int k = 0; k < NC; ++k) {
+        v[u][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (f[u] > 0.f)
+          v[u][k] = __ldcg(po + ((size_t)(2 * j + (j == 0 ? first : 0)) * (D / 4) + cg +
+                                 k * kJoinGroups) * R);
+      }
     }
+#pragma unroll
+    for (int u = 0; u < J; ++u)
+#pragma unroll
+      for (int k = 0; k < NC; ++k) {
+        acc[k].x = fmaf(f[u], v[u][k].x, acc[k].x);
+        acc[k].y = fmaf(f[u], v[u][k].y, acc[k].y);
+        acc[k].z = fmaf(f[u], v[u][k].z, acc[k].z);
+        acc[k].w = fmaf(f[u], v[u][k].w, acc[k].w);
+      }
   }
-  const float inv = (l > 0.f ? 1.f / l : 0.f) * out_scale;
+  __syncthreads();
+  const int r = r0 + rr;
+  if (r >= rows_total) return;
+  const float sc = inv[rr];
   QT* dst = static_cast<QT*>(p.out) +
             ((size_t)(q.q0 + r / p.group) * p.num_heads + g * p.group + r % p.group) * D;
 #pragma unroll
-  for (int j = 0; j < NC; ++j) {
-    const int c4 = tid / kJoinRows + j * (kJoinThreads / kJoinRows);
+  for (int k = 0; k < NC; ++k) {
     uint2 v;
-    v.x = Mma<QT>::pack(acc[j].x * inv, acc[j].y * inv);
-    v.y = Mma<QT>::pack(acc[j].z * inv, acc[j].w * inv);
-    *reinterpret_cast<uint2*>(dst + 4 * c4) = v;
+    v.x = Mma<QT>::pack(acc[k].x * sc, acc[k].y * sc);
+    v.y = Mma<QT>::pack(acc[k].z * sc, acc[k].w * sc);
+    *reinterpret_cast<uint2*>(dst + 4 * (cg + k * kJoinGroups)) = v;
   }
 }
 
-template <typename QT, int D, int KC>
-cudaError_t launch_tree(TreeParams& p, cudaStream_t st) {
-  using Ly = TreeLayout<D, KC>;
-  auto kern = tree_attention_kernel<QT, D, KC>;
+template <typename QT, int D, int KC, int NQ>
+cudaError_t launch_tree_nq(TreeParams& p, cudaStream_t st) {
+  using Ly = TreeLayout<D, KC, NQ>;
+  auto kern = tree_attention_kernel<QT, D, KC, NQ>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Ly::SMEM);
   if (e != cudaSuccess) return e;
   int dev = 0, sms = 0;
@@ -792,15 +1096,25 @@ cudaError_t launch_tree(TreeParams& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  p.ctas = sms * 2 < kTreeMaxCtas ? sms * 2 : kTreeMaxCtas;
+  // (the workspace holds kTreeMaxCtas CTAs of 128 rows)
+  p.ctas = (sms * 2 < kTreeMaxCtas ? sms * 2 : kTreeMaxCtas) / NQ;
+  p.tile_rows = Ly::ROWS;
+  p.tile_tokens = Ly::TT;
   e = launch_pdl(kern, dim3(p.ctas), dim3(Ly::THREADS), Ly::SMEM, st, p);
   if (e != cudaSuccess) return e;
   const long long rows = (long long)p.max_q_len * p.group;
-  const long long rts = (rows + kTreeRows - 1) / kTreeRows;
-  const int slices = static_cast<int>(((rows < kTreeRows ? rows : kTreeRows) + kJoinRows - 1) / kJoinRows);
+  const long long rts = (rows + Ly::ROWS - 1) / Ly::ROWS;
+  const int slices =
+      static_cast<int>(((rows < Ly::ROWS ? rows : Ly::ROWS) + kJoinRows - 1) / kJoinRows);
   const dim3 grid(slices, static_cast<unsigned>(rts * p.num_kv_heads), p.num_seqs);
   return launch_pdl(tree_join_kernel<QT, D>, grid, dim3(kJoinThreads), 0, st, p,
                     KC == kTE4 ? p.v_scale : 1.f);
+}
+
+template <typename QT, int D, int KC>
+cudaError_t launch_tree(TreeParams& p, cudaStream_t st) {
+  return (long long)p.max_q_len * p.group > kTreeRows ? launch_tree_nq<QT, D, KC, 2>(p, st)
+                                                      : launch_tree_nq<QT, D, KC, 1>(p, st);
 }
 
 }  // namespace

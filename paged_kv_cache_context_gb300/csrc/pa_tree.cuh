@@ -9,18 +9,18 @@
 
 namespace pa {
 
-// Query rows of one tensor-core tile and cached tokens of one staged tile.
+// Query rows of one tensor-core tile, and the most cached tokens of a staged tile.
 constexpr int kTreeRows = 128;
-constexpr int kTreeTile = 64;
-// Persistent CTAs a workspace is sized for: two per SM of 152, two partial
-// slots each.
+constexpr int kTreeMaxTile = 128;
+// Persistent CTAs a workspace is sized for: two per SM of 152 (or one of twice
+// the rows), two partial slots each.
 constexpr int kTreeMaxCtas = 152 * 2;
 
 // Sequence s owns query tokens (nodes) [cu_q[s], cu_q[s + 1]); they are the
 // last q_len_s tokens of its cached context of n_s. For kv head g its rows are
-// the q_len_s * G (node, head-in-group) pairs. Work unit: one 64-token tile of
-// one (sequence, kv head, 128-row tile), flattened in that order; CTA c of C
-// takes the equal contiguous share [c P / C, (c + 1) P / C) of the P units.
+// the q_len_s * G (node, head-in-group) pairs. Work unit: one tile of 64
+// or 128 tokens of one (sequence, kv head, 128-row tile), flattened in that order; CTA c of C
+// takes the equal contiguous share [c U, (c + 1) U) of the P units, U = ceil(P / C).
 struct TreeParams {
   CUtensorMap tm_k;  // 16-bit caches as [NB Hkv bs rows][D]: boxes of 64 x bs, 128-B swizzle
   CUtensorMap tm_v;
@@ -34,12 +34,14 @@ struct TreeParams {
   const int32_t* cu_q;          // [S + 1]
   const int32_t* context_lens;  // [S]: cached tokens, the nodes among them
   const unsigned long long* mask;  // [T][mask_words]
-  float4* part_o;               // [C][2][D / 4][128]: cut pieces' un-normalised rows
-  float2* part_ml;              // [C][2][128]: their maximum (log2 units) and sum
+  float4* part_o;               // [C][2][D / 4][tile_rows]: cut pieces' un-normalised rows
+  float2* part_ml;              // [C][2][tile_rows]: their maximum (log2 units) and sum
   unsigned* err;
   int num_seqs, num_heads, num_kv_heads, group, block_size, num_blocks;
   int num_tokens, max_blocks_per_seq, max_q_len, mask_words;
   int ctas;          // C
+  int tile_rows;     // rows of a CTA's query tiles: 128 or 256
+  int tile_tokens;   // 64 or 128
   float scale_log2;  // scale * log2(e) (* k_scale for an FP8 cache)
   float v_scale;     // FP8: multiplies the output
 };
@@ -52,7 +54,7 @@ inline size_t tree_workspace_bytes(int D) {
 
 // dtype: the query's pa_dtype (PA_BF16, PA_F16); kind: the cache's, 0 = the
 // query's type, 1 = INT8 codes with row scales, 2 = FP8 E4M3 codes. Launches
-// the attention and then the combination of cut segments. p.ctas is set here.
+// the attention and then the join of cut segments; sets p.ctas and p.tile_rows.
 cudaError_t launch_tree_attention(TreeParams p, int D, int dtype, int kind, cudaStream_t stream);
 
 }  // namespace pa

@@ -258,14 +258,6 @@ def test_mask_helper_refuses_what_is_no_tree():
 
 
 # ---------------------------------------------------------------- shares of the tree kernel
-def tree_lo(c, P, C):
-    return c * P // C
-
-
-def tree_cta(x, P, C):
-    return ((x + 1) * C - 1) // P
-
-
 @pytest.mark.parametrize("seed", range(30))
 def test_tree_shares_cover_and_the_join_finds_every_piece(seed):
     """The join's enumeration of a cut segment's partial slots against what the walk writes."""
@@ -279,9 +271,11 @@ def test_tree_shares_cover_and_the_join_finds_every_piece(seed):
             P += T
     if P == 0:
         return
+    U = -(-P // C)
     wrote, units = {}, 0
     for c in range(C):
-        a, b = tree_lo(c, P, C), tree_lo(c + 1, P, C)
+        a = min(c * U, P)
+        b = min(a + U, P)
         piece = 0
         for i, (x, T) in enumerate(segs):
             lo, hi = max(a, x), min(b, x + T)
@@ -296,11 +290,10 @@ def test_tree_shares_cover_and_the_join_finds_every_piece(seed):
     assert units == P
     found = {}
     for i, (x, T) in enumerate(segs):
-        c0, c1 = tree_cta(x, P, C), tree_cta(x + T - 1, P, C)
-        assert tree_lo(c0, P, C) <= x < tree_lo(c0 + 1, P, C)
-        if c0 == c1:
+        c0 = x // U
+        n = (x + T - 1) // U - c0 + 1
+        if n == 1:
             continue
-        for c in range(c0, c1 + 1):
-            if tree_lo(c + 1, P, C) > tree_lo(c, P, C):
-                found[(c, 1 if tree_lo(c, P, C) < x else 0)] = i
+        for j in range(n):
+            found[(c0 + j, 1 if j == 0 and x != c0 * U else 0)] = i
     assert found == wrote
