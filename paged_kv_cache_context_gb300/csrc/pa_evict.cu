@@ -58,9 +58,11 @@ __global__ void __launch_bounds__(kScoreThreads) scores_kernel(const __grid_cons
 // One CTA per (sequence, kv head). Scores become unsigned keys in their
 // order (NaN lowest, -0 as +0); the first `sink` and last `recent` tokens get
 // the highest key. A radix search over 11, 11 and 10 bits with histograms in
-// shared memory finds the budget-th largest key; a pass in token order then
-// writes the tokens above it and the first ones equal to it.
-constexpr int kSelThreads = 1024, kSelWarps = 32, kSelBins = 2048;
+// shared memory finds the budget-th largest key; then each warp turns its
+// tokens into words of 32 bits (kept or not), lane i holding word i, and every
+// lane writes the positions of its own word's bits. The bytes are few (4 per
+// score): the bound is the chain of passes of the longest row.
+constexpr int kSelBins = 2048;
 
 __device__ __forceinline__ unsigned score_key(float x) {
   if (x != x) return 0u;
@@ -68,13 +70,34 @@ __device__ __forceinline__ unsigned score_key(float x) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-// ITEMS > 0: the CTA's keys stay in registers (ITEMS per thread); 0: they are
-// read again in every pass.
-template <int ITEMS>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_constant__ SelectParams p) {
+__device__ __forceinline__ unsigned lanes_incl(unsigned v, int lane) {
+#pragma unroll
+  for (int off = 1; off < 32; off *= 2) {
+    const unsigned u = __shfl_up_sync(0xffffffffu, v, off);
+    if (lane >= off) v += u;
+  }
+  return v;
+}
+// Sum of the values of all threads before this one (each warp scans the warp totals itself).
+template <int WARPS>
+__device__ __forceinline__ unsigned block_before(unsigned v, unsigned* wsum, int warp, int lane) {
+  const unsigned incl = lanes_incl(v, lane);
+  if (lane == 31) wsum[warp] = incl;
+  __syncthreads();
+  const unsigned t = lane < WARPS ? wsum[lane] : 0u;
+  const unsigned upto = lanes_incl(t, lane);
+  const unsigned before = __shfl_sync(0xffffffffu, upto - t, warp);
+  return before + incl - v;
+}
+
+// THREADS * ITEMS tokens at most stay in registers, ITEMS <= 32 per thread;
+// ITEMS 0: any number, in rounds of 32 per thread that are read again in every pass.
+template <int THREADS, int ITEMS>
+__global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__ SelectParams p) {
+  constexpr int WARPS = THREADS / 32, PER = ITEMS > 0 ? ITEMS : 32;
   __shared__ unsigned hist[kSelBins];
-  __shared__ unsigned wsum[kSelWarps], wsum2[kSelWarps];
-  __shared__ unsigned s_bin, s_above;
+  __shared__ unsigned wsum[3][WARPS];
+  __shared__ unsigned s_bin, s_above, s_count;
   pdl_wait();
   pdl_trigger();
   const int g = blockIdx.x, s = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -88,129 +111,130 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
   const size_t row = (size_t)s * p.num_kv_heads + g;
   int32_t* out = p.keep + row * B;
   if (g == 0 && tid == 0) p.new_lens[s] = kept;
-  for (int i = kept + tid; i < B; i += kSelThreads) out[i] = -1;
+  for (int i = kept + tid; i < B; i += THREADS) out[i] = -1;
   if (n <= B) {
-    for (int i = tid; i < n; i += kSelThreads) out[i] = i;
+    for (int i = tid; i < n; i += THREADS) out[i] = i;
     return;
   }
-  // warp w takes the tokens [w * per, (w + 1) * per), lane by lane
   const float* sc = p.scores + row * p.cap;
-  const int per = ITEMS > 0 ? ITEMS * 32 : ((n + kSelThreads - 1) / kSelThreads) * 32;
-  const int items = per / 32, base = warp * per;
   const int last = n - p.recent;
-  auto key_at = [&](int t) -> unsigned {
-    return (t < p.sink || t >= last) ? 0xFFFFFFFFu : score_key(__ldg(sc + t));
-  };
-  unsigned keys[ITEMS > 0 ? ITEMS : 1];
-  if constexpr (ITEMS > 0) {
+  const int rounds = ITEMS > 0 ? 1 : (n + THREADS * PER - 1) / (THREADS * PER);
+  // the keys of round r: warp w takes PER * 32 tokens, lane by lane; a place
+  // past the sequence holds key 0 and is left out by its position
+  unsigned keys[PER];
+  auto base_of = [&](int r) { return (r * WARPS + warp) * PER * 32; };
+  auto load = [&](int r) {
+    const int base = base_of(r) + lane;
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      const int t = base + i * 32 + lane;
-      keys[i] = t < n ? key_at(t) : 0u;
-    }
-  }
-  // f(i, t, key) for every token of this thread
-  auto each = [&](auto&& f) {
-    if constexpr (ITEMS > 0) {
-#pragma unroll
-      for (int i = 0; i < ITEMS; ++i) {
-        const int t = base + i * 32 + lane;
-        f(t, keys[i], t < n);
-      }
-    } else {
-      for (int i = 0; i < items; ++i) {
-        const int t = base + i * 32 + lane;
-        f(t, t < n ? key_at(t) : 0u, t < n);
-      }
+    for (int i = 0; i < PER; ++i) {
+      const int t = base + i * 32;
+      const float x = t < n ? __ldg(sc + t) : 0.f;
+      keys[i] = t >= n ? 0u : (t < p.sink || t >= last) ? 0xFFFFFFFFu : score_key(x);
     }
   };
+  if (ITEMS > 0) load(0);
   // the budget-th largest key, digit by digit
   unsigned prefix = 0u, mask = 0u, want = static_cast<unsigned>(kept);  // want-th among the prefix's
 #pragma unroll
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
     const unsigned bins = pass == 2 ? 1024u : 2048u;
-    for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0u;
+    for (int i = tid; i < kSelBins; i += THREADS) hist[i] = 0u;
     __syncthreads();
-    each([&](int, unsigned k, bool ok) {
-      if (ok && (k & mask) == prefix) atomicAdd(&hist[(k >> shift) & (bins - 1u)], 1u);
-    });
-    __syncthreads();
-    // bins from the highest down: thread t takes two
-    const unsigned hi = hist[kSelBins - 1 - 2 * tid], lo2 = hist[kSelBins - 2 - 2 * tid];
-    unsigned incl = hi + lo2;
+    for (int r = 0; r < rounds; ++r) {
+      if (ITEMS == 0) load(r);
+      const int left = n - base_of(r) - lane;  // > 32 i: inside the sequence
 #pragma unroll
-    for (int off = 1; off < 32; off *= 2) {
-      const unsigned v = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += v;
+      for (int i = 0; i < PER; ++i)
+        if (left > 32 * i && (keys[i] & mask) == prefix)
+          atomicAdd(&hist[(keys[i] >> shift) & (bins - 1u)], 1u);
     }
-    if (lane == 31) wsum[warp] = incl;
     __syncthreads();
-    if (warp == 0) {
-      unsigned v = wsum[lane];
+    // bins from the highest down, BPT a thread
+    constexpr int BPT = kSelBins / THREADS;
+    unsigned mine[BPT], sum = 0u;
 #pragma unroll
-      for (int off = 1; off < 32; off *= 2) {
-        const unsigned u = __shfl_up_sync(0xffffffffu, v, off);
-        if (lane >= off) v += u;
+    for (int b = 0; b < BPT; ++b) {
+      mine[b] = hist[kSelBins - 1 - (BPT * tid + b)];
+      sum += mine[b];
+    }
+    unsigned before = block_before<WARPS>(sum, wsum[pass], warp, lane);
+#pragma unroll
+    for (int b = 0; b < BPT; ++b) {
+      if (before < want && want <= before + mine[b]) {
+        s_bin = kSelBins - 1 - (BPT * tid + b);
+        s_above = before;
+        s_count = mine[b];
       }
-      wsum[lane] = v;
-    }
-    __syncthreads();
-    const unsigned before = (warp ? wsum[warp - 1] : 0u) + incl - hi - lo2;
-    if (before < want && want <= before + hi) {
-      s_bin = kSelBins - 1 - 2 * tid;
-      s_above = before;
-    } else if (before + hi < want && want <= before + hi + lo2) {
-      s_bin = kSelBins - 2 - 2 * tid;
-      s_above = before + hi;
+      before += mine[b];
     }
     __syncthreads();
     prefix |= s_bin << shift;
     mask |= (bins - 1u) << shift;
     want -= s_above;
-    __syncthreads();
   }
-  // prefix is the budget-th largest key; `want` of its equals are kept, the
-  // first ones. Counts per warp, then positions in token order.
-  unsigned above = 0u, equal = 0u;
-  each([&](int, unsigned k, bool ok) {
-    above += __popc(__ballot_sync(0xffffffffu, ok && k > prefix));
-    equal += __popc(__ballot_sync(0xffffffffu, ok && k == prefix));
-  });
-  if (lane == 0) {
-    wsum[warp] = above;
-    wsum2[warp] = equal;
-  }
+  // prefix is the budget-th largest key: all larger ones are kept, and the
+  // first `want` of its s_count equals
+  const bool ties = s_count != want;
   __syncthreads();
-  unsigned a0 = 0u, e0 = 0u;
-  for (int w = 0; w < warp; ++w) {
-    a0 += wsum[w];
-    e0 += wsum2[w];
+  unsigned done = 0u, done_eq = 0u;  // kept, and equals met, in earlier rounds
+  for (int r = 0; r < rounds; ++r) {
+    if (ITEMS == 0) load(r);
+    const int left = n - base_of(r) - lane;
+    unsigned word = 0u, equal = 0u;  // of the 32 tokens from base + 32 lane on
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const bool in = left > 32 * i;
+      const unsigned w =
+          __ballot_sync(0xffffffffu, in && (ties ? keys[i] > prefix : keys[i] >= prefix));
+      if (lane == i) word = w;
+    }
+    if (ties) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const unsigned w = __ballot_sync(0xffffffffu, left > 32 * i && keys[i] == prefix);
+        if (lane == i) equal = w;
+      }
+      unsigned seen = done_eq + block_before<WARPS>(__popc(equal), wsum[1], warp, lane);
+      for (; equal && seen < want; ++seen) {  // the first of them, in order
+        word |= equal & (0u - equal);
+        equal &= equal - 1u;
+      }
+      if (rounds > 1) {
+        // equals of this round, for the next one
+        unsigned total = 0u;
+        for (int w = 0; w < WARPS; ++w) total += wsum[1][w];
+        done_eq += total;
+        __syncthreads();
+      }
+    }
+    unsigned at = done + block_before<WARPS>(__popc(word), wsum[2], warp, lane);
+    if (rounds > 1) {
+      unsigned total = 0u;
+      for (int w = 0; w < WARPS; ++w) total += wsum[2][w];
+      done += total;
+      __syncthreads();
+    }
+    const int t0 = base_of(r) + 32 * lane;
+    for (; word; word &= word - 1u) out[at++] = t0 + __ffs(word) - 1;
   }
-  const unsigned below = (1u << lane) - 1u;
-  each([&](int t, unsigned k, bool ok) {
-    const unsigned ba = __ballot_sync(0xffffffffu, ok && k > prefix);
-    const unsigned be = __ballot_sync(0xffffffffu, ok && k == prefix);
-    const unsigned ea = e0 + __popc(be & below), aa = a0 + __popc(ba & below);
-    if (ok && (k > prefix || (k == prefix && ea < want)))
-      out[aa + (ea < want ? ea : want)] = t;
-    a0 += __popc(ba);
-    e0 += __popc(be);
-  });
 }
 
 // ================================================================ compaction
 // CTA (array and column slice, kv head, sequence) moves its columns of every
-// kept row. Rows are taken in chunks: a chunk is read whole, then (after a
-// barrier) written. keep[j] >= start + j, so a chunk's writes only reach rows
-// before every later chunk's sources, and earlier chunks have been read.
-constexpr int kMoveThreads = 256, kMoveUnroll = 4;
+// kept row. Rows are taken in batches: a batch is read whole into registers,
+// then (after a barrier) written, and the next batch's reads are issued before
+// that. keep[j] >= start + j, so a batch's writes only reach rows before every
+// later batch's sources, and every earlier batch has been read when they are
+// made. Where the rows are is worked out first, a chunk of them at a time, so
+// that the reads of a batch do not wait for indexes.
+// The bound is reading and writing the moved rows once.
+constexpr int kMoveThreads = 256, kMoveChunk = 1024;
 
 // Physical row of position t, or -1 with the error raised.
 __device__ __forceinline__ long long compact_row(const CompactParams& p, const int32_t* table, int g,
                                                  int t) {
-  const int page = t / p.block_size;
-  const int b = table[page];
+  const int b = __ldg(table + t / p.block_size);
   if (b < 0 || b >= p.num_blocks) {
     raise_error(p.err, PA_DEVERR_BLOCK_ID);
     return -1;
@@ -233,80 +257,90 @@ __device__ __forceinline__ bool compact_seq(const CompactParams& p, int s, bool 
   return true;
 }
 
-// VEC: the elements moved (uint4: 16-byte pieces of K / V rows; float: row scales).
-template <typename VEC>
-__device__ __forceinline__ void move_rows(const CompactParams& p, VEC* cache, int row_vecs, int v0,
-                                          int nv, const int32_t* table, const int32_t* keep, int g,
-                                          int start, int kept, int n) {
-  const int rows = kMoveThreads / nv;  // rows taken at once by one unroll step
-  const int r = threadIdx.x / nv, c = v0 + threadIdx.x % nv;
-  for (int j0 = 0; j0 < kept; j0 += rows * kMoveUnroll) {
-    VEC val[kMoveUnroll];
-    long long dst[kMoveUnroll];
-#pragma unroll
-    for (int u = 0; u < kMoveUnroll; ++u) {
-      const int j = j0 + u * rows + r;
-      dst[u] = -1;
-      if (r < rows && j < kept) {
-        const int from = keep[j], to = start + j;
-        if (from < to || from >= n) {
-          raise_error(p.err, PA_DEVERR_SLOT);
-        } else if (from != to) {
-          const long long a = compact_row(p, table, g, from), b = compact_row(p, table, g, to);
-          if (a >= 0 && b >= 0) {
-            val[u] = cache[a * row_vecs + c];
-            dst[u] = b * row_vecs + c;
-          }
-        }
-      }
-    }
+// VEC: the elements moved (uint4: 16-byte pieces of K / V rows; float: row
+// scales and scores); columns [v0, v0 + nv) of row_vecs. locate(j): the
+// physical source and destination rows of entry j, source -1 where nothing moves.
+template <typename VEC, int U, typename Locate>
+__device__ __forceinline__ void move_rows(VEC* cache, int row_vecs, int v0, int nv, int kept,
+                                          longlong2* where, Locate locate) {
+  const int rows = kMoveThreads / nv;  // rows one unroll step takes
+  const int r = threadIdx.x / nv, c = v0 + threadIdx.x % nv, batch = rows * U;
+  for (int j0 = 0; j0 < kept; j0 += kMoveChunk) {
+    const int n = min(kMoveChunk, kept - j0);
+    __syncthreads();  // the last chunk's places have been used
+    for (int i = threadIdx.x; i < n; i += kMoveThreads) where[i] = locate(j0 + i);
     __syncthreads();
+    VEC val[2][U];
+    auto load = [&](int i0, VEC (&dst)[U]) {
 #pragma unroll
-    for (int u = 0; u < kMoveUnroll; ++u)
-      if (dst[u] >= 0) cache[dst[u]] = val[u];
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * rows + r;
+        if (r < rows && i < n && where[i].x >= 0) dst[u] = cache[where[i].x * row_vecs + c];
+      }
+    };
+    auto store = [&](int i0, const VEC (&src)[U]) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * rows + r;
+        if (r < rows && i < n && where[i].x >= 0) cache[where[i].y * row_vecs + c] = src[u];
+      }
+    };
+    load(0, val[0]);
+    for (int i0 = 0; i0 < n; i0 += 2 * batch) {
+      load(i0 + batch, val[1]);
+      __syncthreads();
+      store(i0, val[0]);
+      load(i0 + 2 * batch, val[0]);
+      __syncthreads();
+      store(i0 + batch, val[1]);
+    }
   }
 }
 
-__global__ void __launch_bounds__(kMoveThreads)
+__global__ void __launch_bounds__(kMoveThreads, 3)
     compact_kernel(const __grid_constant__ CompactParams p, int slices) {
+  __shared__ longlong2 where[kMoveChunk];
   pdl_wait();
   pdl_trigger();
-  const int g = blockIdx.y, s = blockIdx.z, a = blockIdx.x;
+  // the 4-byte arrays first: their many small moves take as long as a slice's
+  const int g = blockIdx.y, s = blockIdx.z;
+  const int extras = (p.k_scales ? 2 : 0) + (p.scores ? 1 : 0);
+  const int a = static_cast<int>(blockIdx.x) - extras;
   int start, kept, n;
-  if (!compact_seq(p, s, a == 0 && g == 0 && threadIdx.x == 0, &start, &kept, &n)) return;
+  if (!compact_seq(p, s, blockIdx.x == 0 && g == 0 && threadIdx.x == 0, &start, &kept, &n)) return;
   const int32_t* table = p.block_tables + (size_t)s * p.max_blocks_per_seq;
   const int32_t* keep =
       p.keep + ((size_t)s * p.keep_heads + (p.keep_heads > 1 ? g : 0)) * p.budget;
-  if (a < 2 * slices) {  // K or V: row_bytes / 16 pieces a row, cut into slices
+  auto entry = [&](int j) -> int {  // source position of entry j, or -1
+    const int from = __ldg(keep + j);
+    if (from < start + j || from >= n) {
+      raise_error(p.err, PA_DEVERR_SLOT);
+      return -1;
+    }
+    return from;
+  };
+  auto locate = [&](int j) -> longlong2 {
+    const int from = entry(j), to = start + j;
+    if (from < 0 || from == to) return make_longlong2(-1, -1);
+    const long long x = compact_row(p, table, g, from), y = compact_row(p, table, g, to);
+    return make_longlong2(y >= 0 ? x : -1, y);
+  };
+  if (a >= 0) {  // K or V: row_bytes / 16 pieces a row, cut into slices
     const int vecs = p.row_bytes / 16, nv = vecs / slices;
     uint4* cache = reinterpret_cast<uint4*>(a < slices ? p.k_cache : p.v_cache);
-    move_rows<uint4>(p, cache, vecs, (a % slices) * nv, nv, table, keep, g, start, kept, n);
-    return;
-  }
-  const int extra = a - 2 * slices;
-  if (p.k_scales && extra < 2) {
-    move_rows<float>(p, extra ? p.v_scales : p.k_scales, 1, 0, 1, table, keep, g, start, kept, n);
-    return;
-  }
-  // scores: their row is in token order; entries past the kept ones become 0
-  float* sc = p.scores +
-              ((size_t)s * p.num_kv_heads + g) * p.max_blocks_per_seq * p.block_size;
-  for (int j0 = 0; j0 < kept; j0 += kMoveThreads) {
-    const int j = j0 + threadIdx.x;
-    float v = 0.f;
-    int from = -1;
-    if (j < kept) {
-      from = keep[j];
-      if (from < start + j || from >= n)
-        from = -1;
-      else
-        v = sc[from];
-    }
+    move_rows<uint4, 6>(cache, vecs, (a % slices) * nv, nv, kept, where, locate);
+  } else if (p.k_scales && a >= -2) {
+    move_rows<float, 4>(a == -1 ? p.v_scales : p.k_scales, 1, 0, 1, kept, where, locate);
+  } else {
+    // scores: their row is in token order; entries past the kept ones become 0
+    float* sc = p.scores +
+                ((size_t)s * p.num_kv_heads + g) * p.max_blocks_per_seq * p.block_size;
+    move_rows<float, 4>(sc, 1, 0, 1, kept, where, [&](int j) -> longlong2 {
+      return make_longlong2(entry(j), start + j);
+    });
     __syncthreads();
-    if (from >= 0) sc[start + j] = v;
+    for (int j = start + kept + threadIdx.x; j < n; j += kMoveThreads) sc[j] = 0.f;
   }
-  __syncthreads();
-  for (int j = start + kept + threadIdx.x; j < n; j += kMoveThreads) sc[j] = 0.f;
 }
 
 }  // namespace
@@ -319,11 +353,13 @@ cudaError_t launch_scores(const ScoresParams& p, cudaStream_t st) {
 }
 
 cudaError_t launch_select(const SelectParams& p, cudaStream_t st) {
-  const dim3 grid(p.num_kv_heads, p.num_seqs), block(kSelThreads);
-  if (p.cap <= 4 * kSelThreads) return launch_pdl(select_kernel<4>, grid, block, 0, st, p);
-  if (p.cap <= 16 * kSelThreads) return launch_pdl(select_kernel<16>, grid, block, 0, st, p);
-  if (p.cap <= 32 * kSelThreads) return launch_pdl(select_kernel<32>, grid, block, 0, st, p);
-  return launch_pdl(select_kernel<0>, grid, block, 0, st, p);
+  // as few threads as hold the row (fewer warps meet at each barrier sooner)
+  const dim3 grid(p.num_kv_heads, p.num_seqs);
+  if (p.cap <= 256 * 4) return launch_pdl(select_kernel<256, 4>, grid, dim3(256), 0, st, p);
+  if (p.cap <= 512 * 8) return launch_pdl(select_kernel<512, 8>, grid, dim3(512), 0, st, p);
+  if (p.cap <= 1024 * 16) return launch_pdl(select_kernel<1024, 16>, grid, dim3(1024), 0, st, p);
+  if (p.cap <= 1024 * 32) return launch_pdl(select_kernel<1024, 32>, grid, dim3(1024), 0, st, p);
+  return launch_pdl(select_kernel<512, 0>, grid, dim3(512), 0, st, p);
 }
 
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t st) {

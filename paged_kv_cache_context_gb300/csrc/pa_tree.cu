@@ -1089,13 +1089,23 @@ template <typename QT, int D, int KC, int NQ>
 cudaError_t launch_tree_nq(TreeParams& p, cudaStream_t st) {
   using Ly = TreeLayout<D, KC, NQ>;
   auto kern = tree_attention_kernel<QT, D, KC, NQ>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Ly::SMEM);
-  if (e != cudaSuccess) return e;
+  static int configured_devices = 0;  // bit per device id < 32
+  static int device_sms[32] = {};
   int dev = 0, sms = 0;
-  e = cudaGetDevice(&dev);
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
+  if (dev < 32 && (__atomic_load_n(&configured_devices, __ATOMIC_ACQUIRE) & (1 << dev))) {
+    sms = device_sms[dev];
+  } else {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Ly::SMEM);
+    if (e != cudaSuccess) return e;
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 32) {
+      __atomic_store_n(&device_sms[dev], sms, __ATOMIC_RELAXED);
+      __atomic_fetch_or(&configured_devices, 1 << dev, __ATOMIC_RELEASE);
+    }
+  }
   // (the workspace holds kTreeMaxCtas CTAs of 128 rows)
   p.ctas = (sms * 2 < kTreeMaxCtas ? sms * 2 : kTreeMaxCtas) / NQ;
   p.tile_rows = Ly::ROWS;

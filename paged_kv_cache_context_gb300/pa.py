@@ -194,9 +194,16 @@ def _check_decode_args(out, query, k_cache, v_cache, block_tables, context_lens,
     _dtype("context_lens", context_lens, torch.int32)
 
 
+# the current stream's handle without a Stream object around it (3 us less per call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream: Optional[torch.cuda.Stream]) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _check(rc: int, what: str):
@@ -532,16 +539,27 @@ def _nbytes(t: torch.Tensor) -> int:
     return t.numel() * t.element_size()
 
 
-def _current_device(t: torch.Tensor, stream):
-    """The library launches on the current device: the tensors and the stream
-    have to be its own."""
-    if not t.is_cuda:
+def _here(stream, **named):
+    """Every tensor argument (None where optional) and the stream are on the
+    current device, which is the one the library launches on."""
+    ok = stream is None
+    if ok:
+        cur = torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+        for t in named.values():
+            if t is not None and not (isinstance(t, torch.Tensor) and t.get_device() == cur and
+                                      cur >= 0):
+                ok = False
+                break
+    if ok:
         return
-    cur = torch.cuda.current_device()
-    if t.device.index != cur:
-        raise ValueError(f"tensors are on {t.device}, the current device is cuda:{cur}")
-    if stream is not None and stream.device.index != cur:
-        raise ValueError(f"the stream is on {stream.device}, the current device is cuda:{cur}")
+    _on_device(**named)
+    for t in named.values():
+        if t is not None and t.is_cuda and t.device.index != torch.cuda.current_device():
+            raise ValueError(f"tensors are on {t.device}, the current device is "
+                             f"cuda:{torch.cuda.current_device()}")
+    if stream is not None and stream.device.index != torch.cuda.current_device():
+        raise ValueError(f"the stream is on {stream.device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
 
 
 def tree_mask_from_parents(parents, cu_q) -> torch.Tensor:
@@ -575,7 +593,7 @@ def tree_workspace_size(num_heads: int, num_kv_heads: int, head_dim: int) -> int
 
 
 def _check_tree_args(out, query, k_cache, v_cache, block_tables, cu_q, context_lens, tree_mask,
-                     num_kv_heads: int, cache_dtype: torch.dtype, stream):
+                     num_kv_heads: int, cache_dtype: torch.dtype):
     _need(query.dim() == 3, "query: expected [num_tokens, num_heads, head_dim]")
     _shape("out", out, query.shape)
     _dtype("out", out, query.dtype)
@@ -591,7 +609,6 @@ def _check_tree_args(out, query, k_cache, v_cache, block_tables, cu_q, context_l
     _need(tree_mask.dim() == 2 and tree_mask.shape[0] == query.shape[0],
           "tree_mask: expected [num_tokens, mask_words]")
     _dtype("tree_mask", tree_mask, torch.int64)
-    _current_device(query, stream)
 
 
 def tree_attention(out: torch.Tensor, query: torch.Tensor, k_cache: torch.Tensor,
@@ -601,10 +618,11 @@ def tree_attention(out: torch.Tensor, query: torch.Tensor, k_cache: torch.Tensor
     """pa_tree: attention of drafted nodes query [T, Hq, D] (offsets cu_q [S + 1],
     the last tokens of each sequence's context) to the context and to the nodes
     that tree_mask [T, W] (int64 words, see tree_mask_from_parents) names."""
-    _on_device(out=out, query=query, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
-               cu_q=cu_q, context_lens=context_lens, tree_mask=tree_mask, workspace=workspace)
+    _here(stream, out=out, query=query, k_cache=k_cache, v_cache=v_cache,
+          block_tables=block_tables, cu_q=cu_q, context_lens=context_lens, tree_mask=tree_mask,
+          workspace=workspace)
     _check_tree_args(out, query, k_cache, v_cache, block_tables, cu_q, context_lens, tree_mask,
-                     num_kv_heads, query.dtype, stream)
+                     num_kv_heads, query.dtype)
     T, Hq, D = query.shape
     NB, _, bs, _ = k_cache.shape
     S, MB = block_tables.shape
@@ -621,11 +639,11 @@ def tree_attention_int8(out: torch.Tensor, query: torch.Tensor, k_cache: torch.T
                         context_lens: torch.Tensor, tree_mask: torch.Tensor, num_kv_heads: int,
                         max_q_len: int, scale: float, workspace: torch.Tensor, stream=None):
     """pa_tree_int8: tree_attention over an INT8 cache with per-row scales."""
-    _on_device(out=out, query=query, k_cache=k_cache, v_cache=v_cache, k_scales=k_scales,
-               v_scales=v_scales, block_tables=block_tables, cu_q=cu_q,
-               context_lens=context_lens, tree_mask=tree_mask, workspace=workspace)
+    _here(stream, out=out, query=query, k_cache=k_cache, v_cache=v_cache, k_scales=k_scales,
+          v_scales=v_scales, block_tables=block_tables, cu_q=cu_q, context_lens=context_lens,
+          tree_mask=tree_mask, workspace=workspace)
     _check_tree_args(out, query, k_cache, v_cache, block_tables, cu_q, context_lens, tree_mask,
-                     num_kv_heads, torch.int8, stream)
+                     num_kv_heads, torch.int8)
     _check_scales(k_scales, v_scales, k_cache)
     T, Hq, D = query.shape
     NB, _, bs, _ = k_cache.shape
@@ -645,10 +663,11 @@ def tree_attention_fp8(out: torch.Tensor, query: torch.Tensor, k_cache: torch.Te
                        workspace: torch.Tensor, stream=None):
     """pa_tree_fp8: tree_attention over an FP8 E4M3 cache (uint8 codes) with
     per-tensor scales."""
-    _on_device(out=out, query=query, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
-               cu_q=cu_q, context_lens=context_lens, tree_mask=tree_mask, workspace=workspace)
+    _here(stream, out=out, query=query, k_cache=k_cache, v_cache=v_cache,
+          block_tables=block_tables, cu_q=cu_q, context_lens=context_lens, tree_mask=tree_mask,
+          workspace=workspace)
     _check_tree_args(out, query, k_cache, v_cache, block_tables, cu_q, context_lens, tree_mask,
-                     num_kv_heads, torch.uint8, stream)
+                     num_kv_heads, torch.uint8)
     T, Hq, D = query.shape
     NB, _, bs, _ = k_cache.shape
     S, MB = block_tables.shape
@@ -677,15 +696,14 @@ def decode_scored(out: torch.Tensor, scores: torch.Tensor, query: torch.Tensor,
                   v_scale: float = 1.0, stream=None):
     """pa_decode_scored: decode, and scores [S, Hkv, MB * bs] += every token's
     softmax weight summed over its kv head's query heads."""
-    _on_device(out=out, scores=scores, query=query, k_cache=k_cache, v_cache=v_cache,
-               block_tables=block_tables, context_lens=context_lens, workspace=workspace)
+    _here(stream, out=out, scores=scores, query=query, k_cache=k_cache, v_cache=v_cache,
+          block_tables=block_tables, context_lens=context_lens, workspace=workspace)
     _check_decode_args(out, query, k_cache, v_cache, block_tables, context_lens, num_kv_heads,
                        _CACHE_DTYPE.get(kv_dtype, query.dtype))
     S, Hq, D = query.shape
     NB, _, bs, _ = k_cache.shape
     MB = block_tables.shape[1]
     _check_scores(scores, S, num_kv_heads, MB * bs)
-    _current_device(query, stream)
     _check(lib().pa_decode_scored(_ptr(out), _ptr(scores), _ptr(query), _ptr(k_cache),
                                   _ptr(v_cache), _ptr(block_tables), _ptr(context_lens), S, Hq,
                                   num_kv_heads, D, bs, NB, MB, scale, _DTYPE[query.dtype],
@@ -699,9 +717,9 @@ def decode_scored_int8(out: torch.Tensor, scores: torch.Tensor, query: torch.Ten
                        context_lens: torch.Tensor, num_kv_heads: int, scale: float,
                        workspace: torch.Tensor, stream=None):
     """pa_decode_scored_int8: decode_scored over an INT8 cache with per-row scales."""
-    _on_device(out=out, scores=scores, query=query, k_cache=k_cache, v_cache=v_cache,
-               k_scales=k_scales, v_scales=v_scales, block_tables=block_tables,
-               context_lens=context_lens, workspace=workspace)
+    _here(stream, out=out, scores=scores, query=query, k_cache=k_cache, v_cache=v_cache,
+          k_scales=k_scales, v_scales=v_scales, block_tables=block_tables,
+          context_lens=context_lens, workspace=workspace)
     _check_decode_args(out, query, k_cache, v_cache, block_tables, context_lens, num_kv_heads,
                        torch.int8)
     _check_scales(k_scales, v_scales, k_cache)
@@ -709,7 +727,6 @@ def decode_scored_int8(out: torch.Tensor, scores: torch.Tensor, query: torch.Ten
     NB, _, bs, _ = k_cache.shape
     MB = block_tables.shape[1]
     _check_scores(scores, S, num_kv_heads, MB * bs)
-    _current_device(query, stream)
     _check(lib().pa_decode_scored_int8(_ptr(out), _ptr(scores), _ptr(query), _ptr(k_cache),
                                        _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
                                        _ptr(block_tables), _ptr(context_lens), S, Hq,
@@ -722,7 +739,7 @@ def evict_select(keep: torch.Tensor, new_lens: torch.Tensor, scores: torch.Tenso
                  context_lens: torch.Tensor, num_sink: int = 0, num_recent: int = 0, stream=None):
     """pa_evict_select: keep [S, Hkv, budget] = the ascending positions an
     eviction to `budget` tokens keeps (-1 past new_lens [S])."""
-    _on_device(keep=keep, new_lens=new_lens, scores=scores, context_lens=context_lens)
+    _here(stream, keep=keep, new_lens=new_lens, scores=scores, context_lens=context_lens)
     _need(scores.dim() == 3, "scores: expected [num_seqs, num_kv_heads, length]")
     S, H, N = scores.shape
     _dtype("scores", scores, torch.float32)
@@ -732,7 +749,6 @@ def evict_select(keep: torch.Tensor, new_lens: torch.Tensor, scores: torch.Tenso
     for name, t in (("new_lens", new_lens), ("context_lens", context_lens)):
         _shape(name, t, (S,))
         _dtype(name, t, torch.int32)
-    _current_device(scores, stream)
     _check(lib().pa_evict_select(_ptr(keep), _ptr(new_lens), _ptr(scores), _ptr(context_lens), S,
                                  H, N, keep.shape[2], num_sink, num_recent, _stream(stream)),
            "pa_evict_select")
@@ -745,9 +761,9 @@ def compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Te
             stream=None):
     """pa_compact: row starts[s] + j of sequence s <- row keep[s, g, j] for
     j < keep_lens[s], in place (keep [S, Hkv or 1, budget])."""
-    _on_device(k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
-               context_lens=context_lens, keep=keep, keep_lens=keep_lens, starts=starts,
-               k_scales=k_scales, v_scales=v_scales, scores=scores)
+    _here(stream, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+          context_lens=context_lens, keep=keep, keep_lens=keep_lens, starts=starts,
+          k_scales=k_scales, v_scales=v_scales, scores=scores)
     _need(k_cache.dim() == 4, "k_cache: expected [num_blocks, num_kv_heads, block_size, D]")
     _shape("v_cache", v_cache, k_cache.shape)
     _dtype("v_cache", v_cache, k_cache.dtype)
@@ -767,7 +783,6 @@ def compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Te
         _check_scales(k_scales, v_scales, k_cache)
     if scores is not None:
         _check_scores(scores, S, H, MB * bs)
-    _current_device(k_cache, stream)
     _check(lib().pa_compact(_ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
                             _ptr(scores), _ptr(block_tables), _ptr(context_lens), _ptr(keep),
                             _ptr(keep_lens), _ptr(starts), S, H, keep.shape[1], keep.shape[2], D,
