@@ -1158,8 +1158,9 @@ static pa_status tree_impl(int kind, void* out, const void* query, const void* k
   p.mask_words = mask_words;
   p.scale_log2 = scale * kLog2e * (kind == 2 ? k_scale : 1.f);
   p.v_scale = kind == 2 ? v_scale : 1.f;
-  return launch_tree_attention(p, head_dim, q_dtype, kind,
-                               reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return (q_dtype == PA_BF16 ? launch_tree_bf16 : launch_tree_f16)(p, head_dim, kind, st) ==
+                 cudaSuccess
              ? PA_OK
              : PA_ERR_CUDA;
 }

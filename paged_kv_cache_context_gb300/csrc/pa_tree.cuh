@@ -1,5 +1,5 @@
 // pa_tree.cuh -- attention of trees of drafted tokens over the paged cache:
-// the launchers' parameters, shared by pa_tree.cu (the kernels) and
+// the launchers' parameters, shared by pa_tree_impl.cuh (the kernels) and
 // pa_api.cu (the entry points).
 #pragma once
 
@@ -52,9 +52,10 @@ inline size_t tree_workspace_bytes(int D) {
   return slots * kTreeRows * D * 4 + slots * kTreeRows * 8;
 }
 
-// dtype: the query's pa_dtype (PA_BF16, PA_F16); kind: the cache's, 0 = the
-// query's type, 1 = INT8 codes with row scales, 2 = FP8 E4M3 codes. Launches
-// the attention and then the join of cut segments; sets p.ctas and p.tile_rows.
-cudaError_t launch_tree_attention(TreeParams p, int D, int dtype, int kind, cudaStream_t stream);
+// Launches the attention and then the join of cut segments (p.ctas, p.tile_rows
+// and p.tile_tokens are set on the way). D 64 or 128; kind: the cache's, 0 =
+// the query's type, 1 = INT8 codes with row scales, 2 = FP8 E4M3 codes.
+cudaError_t launch_tree_bf16(TreeParams p, int D, int kind, cudaStream_t stream);
+cudaError_t launch_tree_f16(TreeParams p, int D, int kind, cudaStream_t stream);
 
 }  // namespace pa

@@ -1,5 +1,6 @@
-// pa_tree.cu -- attention of trees of drafted tokens over the paged cache, on
-// the fifth-generation tensor cores.
+// pa_tree_impl.cuh -- attention of trees of drafted tokens over the paged
+// cache, on the fifth-generation tensor cores (instantiated per query type by
+// pa_tree_bf16.cu and pa_tree_f16.cu, which build in parallel).
 //
 // Mathematics. Node i of a sequence (of q_len nodes, the last q_len of its n
 // cached tokens) sees every context token j < n - q_len and the nodes k whose
@@ -30,6 +31,8 @@
 // softmax threads hold its logits: the next tile's S runs under their
 // exponentials. The weights P go to TMEM (two buffers) as the A operand of
 // O += P V, so they never pass through shared memory.
+#pragma once
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -64,27 +67,28 @@ struct TreeLayout {
   static constexpr int CTAS = QT == 1 ? 2 : 1;          // per SM
   static constexpr int QBYTES1 = KB * kTreeRows * 128;  // a query tile: [KB][128 rows][128 B]
   static constexpr int SLOT = KB * TT * 128;            // a K or V tile: [KB][TT tokens][128 B]
-  static constexpr int SLOTS = D == 128 ? (KC == kTI8 ? 4 : 5) : (C8 ? 6 : 8);
-  // INT8: tiles whose row scales are kept. When K of tile x is copied, slot
-  // 2x - SLOTS is free, so S of tile x - SLOTS / 2 is done, and the weights of
-  // the tile two before that: the tiles from x - SLOTS / 2 - 1 on may be in use.
-  static constexpr int SCT = SLOTS <= 4 ? 4 : 8;
-  static_assert(SCT >= SLOTS / 2 + 2, "row scales in use are not overwritten");
-  // 8-bit codes of a tile, [TT tokens][D], on their way to 16 bits. At D 128
-  // they land in the slot's second column block, where a token's codes take
-  // the very bytes of its second 64 elements: a warp that has read its tokens'
-  // codes may write them widened without asking the other warps. At D 64
-  // they have an area of their own.
-  static constexpr int RAW = C8 && D == 64 ? TT * D : 0;
+  // 16-bit tiles, and 8-bit codes on their way to them (a raw slot is in
+  // flight until its codes land, a 16-bit one from then on until its products
+  // are done; codes copied into the 16-bit slots themselves left too little in
+  // flight: 206 us against the time in the launcher's comment)
+  static constexpr int SLOTS = C8 ? (D == 128 ? 3 : 4) : (D == 128 ? 5 : 8);
+  static constexpr int RSLOTS = !C8 ? 0 : D == 64 ? 8 : KC == kTI8 ? 3 : 4;
+  static constexpr int RAW = TT * D;  // [TT tokens][D]
+  // INT8: tiles whose row scales are kept. K of tile x is copied when the raw
+  // slot of half tile 2x - RSLOTS has been read, for which 16-bit slot 2x -
+  // RSLOTS - SLOTS was free; the weights of the tile two before that half
+  // tile's are done, and those from then on may be in use.
+  static constexpr int SCT = 8;
+  static_assert(SCT >= (RSLOTS + SLOTS + 1) / 2 + 2, "row scales in use are not overwritten");
   static constexpr int OFF_KV = QT * QBYTES1;
   static constexpr int OFF_RAW = OFF_KV + SLOTS * SLOT;
-  static constexpr int OFF_SC = OFF_RAW + SLOTS * RAW;  // [SCT][K, V][TT]
+  static constexpr int OFF_SC = OFF_RAW + RSLOTS * RAW;  // [SCT][K, V][TT]
   static constexpr int OFF_BAR = OFF_SC + (KC == kTI8 ? SCT * 2 * TT * 4 : 0);
-  static constexpr int NBAR = (C8 ? 3 : 2) * SLOTS + 7 * QT;  // see the kernel
+  static constexpr int NBAR = 2 * SLOTS + 2 * RSLOTS + 7 * QT;  // see the kernel
   static constexpr int OFF_MISC = (OFF_BAR + NBAR * 8 + 15) / 16 * 16;
   static constexpr int SMEM = OFF_MISC + 64;
-  // TMEM columns: S of query tile q at q TT; (QT 1) P of buffer b at 64 + b 32; O of tile q at
-  // QT 128 + q D
+  // TMEM columns: S of query tile q at q TT; P at 64 + b 32 (buffer b; with two
+  // query tiles at q 128 + 64, over the second half of S); O of tile q at QT 128 + q D
   static constexpr uint32_t TMEM_COLS = QT == 1 ? 256 : 512;
   static_assert(QT * (128 + D) <= (int)TMEM_COLS, "TMEM columns");
   static_assert(OFF_BAR % 16 == 0, "alignment");
@@ -263,42 +267,40 @@ __device__ __forceinline__ unsigned long long tree_seen(const unsigned long long
   return v;
 }
 
-// The largest seen logit (log2 units) of 32 neighbouring tokens. Without row
+// The largest seen logit (log2 units) of N neighbouring tokens. Without row
 // scales and masks the maximum is taken over the raw products: multiplying by
 // a scale that is not negative keeps their order.
-template <bool ROW_SC>
-__device__ __forceinline__ float half_max(const uint32_t (&s)[32], const float* ks, float scale,
+template <bool ROW_SC, int N>
+__device__ __forceinline__ float part_max(const uint32_t (&s)[N], const float* ks, float scale,
                                           bool masked, uint32_t seen) {
   float a[4];
   if (scale >= 0.f && !ROW_SC && !masked) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) a[e] = __uint_as_float(s[e]);
 #pragma unroll
-    for (int e = 4; e < 32; ++e) a[e & 3] = fmaxf(a[e & 3], __uint_as_float(s[e]));
+    for (int e = 4; e < N; ++e) a[e & 3] = fmaxf(a[e & 3], __uint_as_float(s[e]));
     return fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])) * scale;
   }
-  {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) a[e] = -INFINITY;
+  for (int e = 0; e < 4; ++e) a[e] = -INFINITY;
 #pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      float x = __uint_as_float(s[e]) * scale;
-      if constexpr (ROW_SC) x *= ks[e];
-      a[e & 3] = fmaxf(a[e & 3], (seen >> e) & 1u ? x : -INFINITY);
-    }
-    return fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
+  for (int e = 0; e < N; ++e) {
+    float x = __uint_as_float(s[e]) * scale;
+    if constexpr (ROW_SC) x *= ks[e];
+    a[e & 3] = fmaxf(a[e & 3], (seen >> e) & 1u ? x : -INFINITY);
   }
+  return fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
 }
 
-// The weights 2^(x - mu) of 32 neighbouring tokens, rounded to the MMA type
+// The weights 2^(x - mu) of N neighbouring tokens, rounded to the MMA type
 // in pairs (INT8: times the V row scale first); `sum` takes them unrounded.
-template <typename T, bool ROW_SC>
-__device__ __forceinline__ void half_weights(const uint32_t (&s)[32], const float* ks,
-                                             const float* vsc, float scale, float mu, bool masked, uint32_t seen, float2& sum,
-                                             uint32_t (&pk)[16]) {
+template <typename T, bool ROW_SC, int N>
+__device__ __forceinline__ void part_weights(const uint32_t (&s)[N], const float* ks,
+                                             const float* vsc, float scale, float mu, bool masked,
+                                             uint32_t seen, float2& sum, uint32_t (&pk)[N / 2]) {
   const float2 sc2 = make_float2(scale, scale), mu2 = make_float2(-mu, -mu);
 #pragma unroll
-  for (int e = 0; e < 32; e += 2) {
+  for (int e = 0; e < N; e += 2) {
     float2 x = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
     if constexpr (ROW_SC) x = __fmul2_rn(x, *reinterpret_cast<const float2*>(ks + e));
     x = __ffma2_rn(x, sc2, mu2);
@@ -340,6 +342,9 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 
+// 16 or 32 columns.
+__device__ __forceinline__ void tmem_ld_n(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
+__device__ __forceinline__ void tmem_ld_n(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16(taddr, r); }
 template <typename QT, int D, int KC, int NQ>
 __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, KC, NQ>::CTAS)
     tree_attention_kernel(const __grid_constant__ TreeParams p) {
@@ -357,7 +362,8 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
   uint64_t* p_full = s_free + NQ;         // [NQ][2]
   uint64_t* pv_done = p_full + 2 * NQ;    // [NQ][2]
   uint64_t* q_full = pv_done + 2 * NQ;    // [NQ]
-  uint64_t* raw_full = q_full + NQ;       // [NS] 8-bit caches: codes have landed
+  uint64_t* raw_full = q_full + NQ;       // [RS] 8-bit caches: codes have landed
+  uint64_t* raw_empty = raw_full + Ly::RSLOTS;  // [RS] and have been read
   int* misc = reinterpret_cast<int*>(smem + Ly::OFF_MISC);            // s, g, rt, tile
   long long* misc64 = reinterpret_cast<long long*>(smem + Ly::OFF_MISC + 16);  // lo, hi
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Ly::OFF_MISC + 32);
@@ -410,7 +416,10 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
       for (int i = 0; i < NS; ++i) {
         mbar_init(&full[i], C8 ? Ly::CONV : 1);
         mbar_init(&empty[i], 1);
-        if (C8) mbar_init(&raw_full[i], 1);
+      }
+      for (int i = 0; i < Ly::RSLOTS; ++i) {
+        mbar_init(&raw_full[i], 1);
+        mbar_init(&raw_empty[i], Ly::CONV / 32);
       }
       for (int i = 0; i < 2 * NQ; ++i) {
         mbar_init(&p_full[i], kTreeRows);
@@ -436,7 +445,7 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
   __syncthreads();
   tc05_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t t_s0 = tmem, t_p0 = INPL ? tmem : tmem + 64, t_o0 = tmem + NQ * 128;
+  const uint32_t t_s0 = tmem, t_p0 = tmem + 64, t_o0 = tmem + NQ * 128;
   const long long lo = misc64[0], units = misc64[1] - lo;
   const bool aligned = (smem_u32(smem) & 1023u) == 0;
   if (!aligned && tid == 0) raise_error(err, PA_DEVERR_TIMEOUT);  // never: see __align__ above
@@ -451,10 +460,12 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
     if (warp == Ly::COPY_WARP) {
       // ================================================ copies: K0 V0 K1 V1 ...
       const int sh = 31 - __clz(bs), pages = TT >> sh;  // block_size is a power of two
+      constexpr int NL = C8 ? Ly::RSLOTS : NS;  // slots copied into
       uint64_t* landed = C8 ? raw_full : full;
+      uint64_t* freed = C8 ? raw_empty : empty;
       int sl = 0;       // next slot
       uint32_t ph = 1;  // parity of its last release
-      int filled = 0;   // slots filled (no further than NS)
+      int filled = 0;   // slots filled (no further than NL)
       int stile = 0;    // INT8: where the tile's row scales go
       bool ok = true;
       // Lane pp looks up page pp of a tile: its index among all (block, kv
@@ -478,10 +489,10 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
           if (i + 1 < len) y_next = lookup(i + 1);
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
-            if (filled >= NS) ok = warp_wait(&empty[sl], ph);
+            if (filled >= NL) ok = warp_wait(&freed[sl], ph);
             if (!ok) break;
-            uint8_t* slot = smem + Ly::OFF_KV + sl * Ly::SLOT;
             if constexpr (!C8) {
+              uint8_t* slot = smem + Ly::OFF_KV + sl * Ly::SLOT;
               // a box wholly past the tensor is filled with zeros
               const int rows_end = static_cast<int>((long long)p.num_blocks * Hkv << sh);
               if (elect_one()) {
@@ -496,7 +507,7 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
                 }
               }
             } else {
-              uint8_t* raw = Ly::RAW ? smem + Ly::OFF_RAW + sl * Ly::RAW : slot + Ly::SLOT / 2;
+              uint8_t* raw = smem + Ly::OFF_RAW + sl * Ly::RAW;
               float* sct = sc + stile * 2 * TT;  // both kinds come with K
               // pages past the end are not copied (their K is masked, their V
               // zeroed with the rows past the end); bad ones become zeros here
@@ -532,8 +543,8 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
               }
             }
             __syncwarp();
-            if (filled < NS) ++filled;
-            if (++sl == NS) {
+            if (filled < NL) ++filled;
+            if (++sl == NL) {
               sl = 0;
               ph ^= 1;
             }
@@ -559,7 +570,7 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
       const uint32_t dk0 = tree_desc_lo(smem_u32(smem + Ly::OFF_KV), 16);
       const uint32_t dv0 = tree_desc_lo(smem_u32(smem + Ly::OFF_KV), TT * 128);
       const uint32_t tb = uniform(tmem);
-      const uint32_t us = tb, up = INPL ? tb : tb + 64, uo = tb + NQ * 128;
+      const uint32_t us = tb, up = tb + 64, uo = tb + NQ * 128;
       int ks = 0, vs = 1;         // slots of the next K and V tile
       uint32_t kph = 0, vph = 0;  // and their phases
       auto step2 = [&](int& sl, uint32_t& ph) {
@@ -653,22 +664,24 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
         // that the eight lanes of a row (D 128) cover all banks
         const int sw = (KB == 2 && c16 >= 4) ? 1 : 0;
         bool ok = true;
-        int sl = 0;
-        uint32_t ph = 0;
-        for (long long k = 0; k < 2 * units; ++k) {
-          if (!warp_wait(&raw_full[sl], ph)) {
-            ok = false;
-            break;
-          }
+        int sl = 0, rs = 0, filled = 0;
+        uint32_t ph = 1, rph = 0;
+        for (long long k = 0; k < 2 * units && ok; ++k) {
+          ok = warp_wait(&raw_full[rs], rph);
+          if (ok && filled >= NS) ok = warp_wait(&empty[sl], ph);
+          if (!ok) break;
           uint8_t* dst = smem + Ly::OFF_KV + sl * Ly::SLOT;
-          const uint8_t* raw = Ly::RAW ? smem + Ly::OFF_RAW + sl * Ly::RAW : dst + Ly::SLOT / 2;
+          const uint8_t* raw = smem + Ly::OFF_RAW + rs * Ly::RAW;
 #pragma unroll
           for (int half = 0; half < TT / 64; ++half) {
             uint4 src[NR];
 #pragma unroll
             for (int j = 0; j < NR; ++j)
               src[j] = *reinterpret_cast<const uint4*>(raw + (half * 64 + r0 + j * RSTEP) * D + 16 * c16);
-            __syncwarp();  // (D 128) the warp's codes are read before their bytes are written
+            if (half == TT / 64 - 1) {
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&raw_empty[rs]);
+            }
             using Code = typename std::conditional<ROW_SC, I8, E4M3>::type;
 #pragma unroll
             for (int j = 0; j < NR; ++j) {
@@ -688,9 +701,14 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
           }
           fence_proxy_async_smem();
           mbar_arrive(&full[sl]);
+          if (filled < NS) ++filled;
           if (++sl == NS) {
             sl = 0;
             ph ^= 1;
+          }
+          if (++rs == Ly::RSLOTS) {
+            rs = 0;
+            rph ^= 1;
           }
         }
         if (!ok && lane == 0) raise_error(err, PA_DEVERR_TIMEOUT);
@@ -792,87 +810,135 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
             if (warp_live) {
               tc05_fence_after();
               __syncwarp();
-              // The tile's logits come 32 tokens at a time and, where the
-              // registers do not hold them all (8-bit caches: more threads; 128
-              // tokens), once more for the weights. (Handing the registers out
-              // by warpgroup, so that 8-bit caches hold them too, took 241 us
-              // instead of 206 on 16 sequences over an FP8 cache of 617 MB: the
-              // copying and widening warps spilled.)
-              constexpr int NH = TT / 32;
-              constexpr bool AGAIN = C8 || INPL;
-              uint32_t sr[AGAIN ? 1 : NH][32];
               float mx = -INFINITY;  // the largest seen logit, log2 units
-              if constexpr (AGAIN) {
+              float mu = 0.f;
+              float2 sum = make_float2(0.f, 0.f);
+              auto s_read = [&]() {  // S's columns may be overwritten
+                if (!INPL) {
+                  tc05_fence_before();
+                  mbar_arrive(&s_free[q]);
+                }
+              };
+              // Moves the running maximum if `mx` clears it, sets mu, and waits
+              // for the weights' buffer. False after a timeout.
+              auto settle = [&]() -> bool {
+                if (__any_sync(0xffffffffu, mx > m + kLazy)) {
+                  const float mn = fmaxf(m, mx);
+                  if (i > 0) {
+                    // O holds the tiles so far: scale it by 2^(m - mn) once the
+                    // last P V has landed
+                    const long long cp = c - 1;
+                    if (__any_sync(0xffffffffu,
+                                   !mbar_wait_bounded(&pd[cp & 1],
+                                                      static_cast<uint32_t>((cp >> 1) & 1))))
+                      return false;
+                    tc05_fence_after();
+                    __syncwarp();
+                    const float al = mn == -INFINITY ? 1.f : exp2f(m - mn);
 #pragma unroll
-                for (int h = 0; h < NH; ++h) {
-                  tmem_ld32(t_s + 32 * h, sr[0]);
+                    for (int c0 = 0; c0 < D; c0 += 16) {
+                      uint32_t o[16];
+                      tmem_ld16(t_o + c0, o);
+                      tmem_wait_ld();
+#pragma unroll
+                      for (int e = 0; e < 16; ++e)
+                        o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+                      tmem_st16(t_o + c0, o);
+                    }
+                    tmem_wait_st();
+                    l *= al;
+                  }
+                  m = mn;
+                }
+                mu = m == -INFINITY ? 0.f : m;  // nothing seen yet: weights of zero
+                // the P V before the last has read the buffer
+                return INPL || c < 2 ||
+                       !__any_sync(0xffffffffu,
+                                   !mbar_wait_bounded(&pd[b],
+                                                      static_cast<uint32_t>(((c >> 1) - 1) & 1)));
+              };
+              const float sl2 = p.scale_log2;
+              auto maxi = [&](auto& sr, int e0, uint32_t bits) {
+                mx = fmaxf(mx, part_max<ROW_SC>(sr, sct + e0, sl2, masked, bits));
+              };
+              auto weigh = [&](auto& sr, int e0, uint32_t bits, auto& pk) {
+                part_weights<T, ROW_SC>(sr, sct + e0, sct + TT + e0, sl2, mu, masked, bits, sum, pk);
+              };
+              if constexpr (INPL) {
+                // 128 tokens, XH * 32 at a time: the last part stays in registers and
+                // is weighed first, its weights going over logits of its own
+                // or of parts that have been weighed; the others are read again
+                constexpr int XH = C8 ? 1 : 2;
+                uint32_t sr[XH][32], pk[16];
+#pragma unroll
+                for (int h = 0; h < 4; h += XH) {
+#pragma unroll
+                  for (int x = 0; x < XH; ++x) tmem_ld32(t_s + 32 * (h + x), sr[x]);
                   tmem_wait_ld();
-                  mx = fmaxf(mx, half_max<ROW_SC>(sr[0], sct + 32 * h, p.scale_log2, masked, seen[h]));
+#pragma unroll
+                  for (int x = 0; x < XH; ++x) maxi(sr[x], 32 * (h + x), seen[h + x]);
+                }
+                if (!settle()) {
+                  failed = true;
+                  break;
+                }
+#pragma unroll
+                for (int h = 4 - XH; h >= 0; h -= XH) {
+                  if (h < 4 - XH) {
+#pragma unroll
+                    for (int x = 0; x < XH; ++x) tmem_ld32(t_s + 32 * (h + x), sr[x]);
+                    tmem_wait_ld();
+                  }
+#pragma unroll
+                  for (int x = 0; x < XH; ++x) {
+                    weigh(sr[x], 32 * (h + x), seen[h + x], pk);
+                    tmem_st16(t_p + 16 * (h + x), pk);
+                  }
                 }
               } else {
+                const uint32_t tpb = t_p + b * 32;
+                if constexpr (C8) {
+                  // (more threads, fewer registers: each half is read twice.
+                  // Handing the registers out by warpgroup, so that they
+                  // hold both, took 241 us instead of 206 on 16 sequences over
+                  // an FP8 cache of 617 MB: the other warps spilled.)
+                  uint32_t sr[32], pk[16];
 #pragma unroll
-                for (int h = 0; h < NH; ++h) tmem_ld32(t_s + 32 * h, sr[h]);
-                tmem_wait_ld();
-                tc05_fence_before();
-                mbar_arrive(&s_free[q]);
-#pragma unroll
-                for (int h = 0; h < NH; ++h)
-                  mx = fmaxf(mx, half_max<ROW_SC>(sr[h], sct + 32 * h, p.scale_log2, masked, seen[h]));
-              }
-              if (__any_sync(0xffffffffu, mx > m + kLazy)) {
-                const float mn = fmaxf(m, mx);
-                if (i > 0) {
-                  // O holds the tiles so far: scale it by 2^(m - mn) once the last
-                  // P V has landed
-                  const long long cp = c - 1;
-                  if (__any_sync(0xffffffffu,
-                                 !mbar_wait_bounded(&pd[cp & 1],
-                                                    static_cast<uint32_t>((cp >> 1) & 1)))) {
+                  for (int h = 0; h < 2; ++h) {
+                    tmem_ld32(t_s + 32 * h, sr);
+                    tmem_wait_ld();
+                    maxi(sr, 32 * h, seen[h]);
+                  }
+                  if (!settle()) {
                     failed = true;
                     break;
                   }
-                  tc05_fence_after();
-                  __syncwarp();
-                  const float al = mn == -INFINITY ? 1.f : exp2f(m - mn);
 #pragma unroll
-                  for (int c0 = 0; c0 < D; c0 += 16) {
-                    uint32_t o[16];
-                    tmem_ld16(t_o + c0, o);
+                  for (int h = 0; h < 2; ++h) {
+                    tmem_ld32(t_s + 32 * h, sr);
                     tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
-                    tmem_st16(t_o + c0, o);
+                    if (h == 1) s_read();
+                    weigh(sr, 32 * h, seen[h], pk);
+                    tmem_st16(tpb + 16 * h, pk);
                   }
-                  tmem_wait_st();
-                  l *= al;
-                }
-                m = mn;
-              }
-              // a row that has seen nothing yet keeps weights of zero
-              const float mu = m == -INFINITY ? 0.f : m;
-              float2 sum = make_float2(0.f, 0.f);
-              // the P V before the last has read this buffer
-              if (!INPL && c >= 2 &&
-                  __any_sync(0xffffffffu,
-                             !mbar_wait_bounded(&pd[b], static_cast<uint32_t>(((c >> 1) - 1) & 1)))) {
-                failed = true;
-                break;
-              }
-#pragma unroll
-              for (int h = 0; h < NH; ++h) {
-                if constexpr (AGAIN) {
-                  tmem_ld32(t_s + 32 * h, sr[0]);
+                } else {
+                  uint32_t sr[2][32], pk[16];
+                  tmem_ld32(t_s, sr[0]);
+                  tmem_ld32(t_s + 32, sr[1]);
                   tmem_wait_ld();
-                  if (!INPL && h == NH - 1) {
-                    tc05_fence_before();
-                    mbar_arrive(&s_free[q]);
+                  s_read();
+                  maxi(sr[0], 0, seen[0]);
+                  maxi(sr[1], 32, seen[1]);
+                  if (!settle()) {
+                    failed = true;
+                    break;
+                  }
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) {
+                    weigh(sr[h], 32 * h, seen[h], pk);
+                    tmem_st16(tpb + 16 * h, pk);
                   }
                 }
-                uint32_t pk[16];
-                half_weights<T, ROW_SC>(sr[AGAIN ? 0 : h], sct + 32 * h, sct + TT + 32 * h, p.scale_log2,
-                                        mu, masked, seen[h], sum, pk);
-                // (P over S: these columns' logits have been read)
-                tmem_st16(t_p + (INPL ? 0 : b * 32) + 16 * h, pk);
               }
               l += sum.x + sum.y;
               tmem_wait_st();
@@ -901,10 +967,11 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
             mbar_arrive(&pf[b]);
           }
           if (failed) break;
-          // ---- the row's output, or its partial; the next piece's query is on
-          // its way meanwhile (all S products on this one's have completed)
+          // ---- the row's output, or its partial
           const bool whole = w.len == w.q.T, was_live = live;
           const size_t out_row = orow;
+          // the next piece's query is on its way meanwhile (all S products on
+          // this one's have completed)
           ct += w.len;
           w.next(p);
           if (w.left > 0) {
@@ -925,15 +992,16 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
           QT* dst = static_cast<QT*>(p.out) + out_row * D;
           float4* po = p.part_o + slot * (D / 4) * ROWS + tid;
           if (warp_live) {
+            constexpr int EC = C8 ? 16 : 32;  // columns held at once
 #pragma unroll
-            for (int c0 = 0; c0 < D; c0 += 32) {
-              uint32_t o[32];
-              tmem_ld32(t_o + c0, o);
+            for (int c0 = 0; c0 < D; c0 += EC) {
+              uint32_t o[EC];
+              tmem_ld_n(t_o + c0, o);
               tmem_wait_ld();
               if (!was_live) continue;
               if (whole) {
 #pragma unroll
-                for (int e = 0; e < 32; e += 8) {
+                for (int e = 0; e < EC; e += 8) {
                   uint4 v;
                   v.x = Mma<QT>::pack(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
                   v.y = Mma<QT>::pack(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
@@ -943,7 +1011,7 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
                 }
               } else {
 #pragma unroll
-                for (int e = 0; e < 32; e += 4)
+                for (int e = 0; e < EC; e += 4)
                   po[(size_t)((c0 + e) / 4) * ROWS] =
                       make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
                                   __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
@@ -978,26 +1046,24 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
   }
 }
 
-// Joins the partial rows of cut (sequence, kv head, row tile) segments:
-// with M the largest maximum, out = sum_j 2^(m_j - M) o_j / sum_j 2^(m_j - M) l_j.
-// CTA (slice of 8 rows, (kv head, row tile), sequence): the factors of the
-// slice's pieces go to shared memory first, so that the loads of the partial
-// rows do not wait for one another. Thread (column group, row) with rows
-// fastest, as the partials are stored.
-constexpr int kJoinRows = 8, kJoinThreads = 128, kJoinGroups = kJoinThreads / kJoinRows;
-template <typename QT, int D>
+// Joins the partial rows of cut (sequence, kv head, row tile) segments: with a
+// running maximum M over the pieces, out = sum_j 2^(m_j - M) o_j / sum_j 2^(m_j - M) l_j.
+// CTA (slice of columns, (kv head, row tile), sequence); a thread takes NC
+// neighbouring groups of four columns of one row, rows fastest, as the
+// partials are stored. NC 8 where there are many segments (few, wide loads);
+// 1 where there are few, whose pieces are then many. It is bound by the
+// latency of three dependent loads (lengths, pieces, output) and, on large
+// batches, by reading the partials from L2.
+constexpr int kJoinThreads = 256;
+template <typename QT, int D, int NC>
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ TreeParams p,
                                                                 float out_scale) {
-  __shared__ float fac[kTreeMaxCtas][kJoinRows];  // 2^(m_j - M), zero where l_j is
-  __shared__ float inv[kJoinRows];
-  pdl_wait();
-  pdl_trigger();
+  // The offsets and lengths are inputs that were complete before the
+  // attention kernel let this launch start (it had waited for all before it):
+  // reading them does not have to wait for its end.
   const int tid = threadIdx.x, lane = tid & 31, s = blockIdx.z;
   const int g = blockIdx.y % p.num_kv_heads, rt = blockIdx.y / p.num_kv_heads;
   const TreeSeq q = tree_seq(p, s, false);
-  const int rows_total = q.q_len * p.group;
-  const int R = p.tile_rows, r0 = rt * R + blockIdx.x * kJoinRows;
-  if (q.T == 0 || r0 >= rows_total) return;
   // units before this sequence, and of all (every warp the same)
   long long before = 0, P = 0;
   for (int b = 0; b < p.num_seqs; b += 32) {
@@ -1010,78 +1076,72 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
     P += __shfl_xor_sync(0xffffffffu, P, off);
     before += __shfl_xor_sync(0xffffffffu, before, off);
   }
-  const long long U = tree_share(P, p.ctas);
-  const long long seg0 = before + ((long long)g * q.RT + rt) * q.T;
-  const int c0 = static_cast<int>(tree_div(seg0, U));
-  const int n = static_cast<int>(tree_div(seg0 + q.T - 1, U)) - c0 + 1;
-  if (n == 1) return;  // not cut
-  // piece j sits in CTA c0 + j: in its first slot unless it began the segment
-  // after other work
-  const int first = seg0 != c0 * U ? 1 : 0;
-  const int rr = tid % kJoinRows, lr0 = r0 % R;
-  const float2* ml = p.part_ml + (size_t)c0 * 2 * R + lr0;
-  for (int i = tid; i < n * kJoinRows; i += kJoinThreads) {
-    const int j = i / kJoinRows;
-    const float2 v = ml[(size_t)(2 * j + (j == 0 ? first : 0)) * R + i % kJoinRows];
-    fac[j][i % kJoinRows] = v.y > 0.f ? v.x : -INFINITY;
+  const int R = p.tile_rows, rows_total = q.q_len * p.group, lr = tid % R, r = rt * R + lr;
+  int c0 = 0, n = 0, first = 0;
+  if (q.T > 0 && rt < q.RT) {
+    const long long U = tree_share(P, p.ctas);
+    const long long seg0 = before + ((long long)g * q.RT + rt) * q.T;
+    c0 = static_cast<int>(tree_div(seg0, U));
+    n = static_cast<int>(tree_div(seg0 + q.T - 1, U)) - c0 + 1;
+    // piece j sits in CTA c0 + j: in its first slot unless it began the segment
+    // after other work
+    first = seg0 != c0 * U ? 1 : 0;
   }
-  __syncthreads();
-  const int cg = tid / kJoinRows;
-  float M = -INFINITY;
-  for (int j = 0; j < n; ++j) M = fmaxf(M, fac[j][rr]);
-  __syncthreads();
-  if (M == -INFINITY) M = 0.f;  // nothing seen in any piece: every factor is zero
-  for (int j = cg; j < n; j += kJoinGroups) fac[j][rr] = exp2f(fac[j][rr] - M);
-  __syncthreads();
-  if (tid < kJoinRows) {
-    float l = 0.f;
-    for (int j = 0; j < n; ++j)
-      l = fmaf(fac[j][rr], ml[(size_t)(2 * j + (j == 0 ? first : 0)) * R + rr].y, l);
-    inv[rr] = (l > 0.f ? 1.f / l : 0.f) * out_scale;
-  }
-  constexpr int NC = D / 4 / kJoinGroups;  // column groups per thread
-  const float4* po = p.part_o + (size_t)c0 * 2 * (D / 4) * R + lr0 + rr;
+  pdl_wait();
+  pdl_trigger();
+  if (n <= 1 || r >= rows_total) return;  // not cut
+  const int c4 = (blockIdx.x * (kJoinThreads / R) + tid / R) * NC;
+  const float2* ml = p.part_ml + (size_t)c0 * 2 * R + lr;
+  const float4* po = p.part_o + ((size_t)c0 * 2 * (D / 4) + c4) * R + lr;
+  constexpr int J = NC == 1 ? 8 : 2;  // pieces whose loads are in flight together
   float4 acc[NC];
 #pragma unroll
   for (int k = 0; k < NC; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int J = 8;  // pieces whose loads are in flight together
+  float M = -INFINITY, l = 0.f;
   for (int j0 = 0; j0 < n; j0 += J) {
+    float2 h[J];
     float4 v[J][NC];
-    float f[J];
 #pragma unroll
     for (int u = 0; u < J; ++u) {
-      const int j = j0 + u;
-      f[u] = j < n ? fac[j][rr] : 0.f;
+      const int j = j0 + u, sl = 2 * j + (j == 0 ? first : 0);
+      h[u] = make_float2(-INFINITY, 0.f);
+      if (j < n) {
+        h[u] = __ldcg(ml + (size_t)sl * R);
 #pragma unroll
-      for (int k = 0; k < NC; ++k) {
-        v[u][k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (f[u] > 0.f)
-          v[u][k] = __ldcg(po + ((size_t)(2 * j + (j == 0 ? first : 0)) * (D / 4) + cg +
-                                 k * kJoinGroups) * R);
+        for (int k = 0; k < NC; ++k) v[u][k] = __ldcg(po + ((size_t)sl * (D / 4) + k) * R);
       }
     }
 #pragma unroll
-    for (int u = 0; u < J; ++u)
+    for (int u = 0; u < J; ++u) {
+      if (!(h[u].y > 0.f)) continue;  // nothing seen in the piece
+      if (h[u].x > M) {
+        const float f = exp2f(M - h[u].x);
+        l *= f;
+#pragma unroll
+        for (int k = 0; k < NC; ++k)
+          acc[k] = make_float4(acc[k].x * f, acc[k].y * f, acc[k].z * f, acc[k].w * f);
+        M = h[u].x;
+      }
+      const float f = exp2f(h[u].x - M);
+      l = fmaf(f, h[u].y, l);
 #pragma unroll
       for (int k = 0; k < NC; ++k) {
-        acc[k].x = fmaf(f[u], v[u][k].x, acc[k].x);
-        acc[k].y = fmaf(f[u], v[u][k].y, acc[k].y);
-        acc[k].z = fmaf(f[u], v[u][k].z, acc[k].z);
-        acc[k].w = fmaf(f[u], v[u][k].w, acc[k].w);
+        acc[k].x = fmaf(f, v[u][k].x, acc[k].x);
+        acc[k].y = fmaf(f, v[u][k].y, acc[k].y);
+        acc[k].z = fmaf(f, v[u][k].z, acc[k].z);
+        acc[k].w = fmaf(f, v[u][k].w, acc[k].w);
       }
+    }
   }
-  __syncthreads();
-  const int r = r0 + rr;
-  if (r >= rows_total) return;
-  const float sc = inv[rr];
+  const float inv = (l > 0.f ? 1.f / l : 0.f) * out_scale;
   QT* dst = static_cast<QT*>(p.out) +
-            ((size_t)(q.q0 + r / p.group) * p.num_heads + g * p.group + r % p.group) * D;
+            ((size_t)(q.q0 + r / p.group) * p.num_heads + g * p.group + r % p.group) * D + 4 * c4;
 #pragma unroll
   for (int k = 0; k < NC; ++k) {
     uint2 v;
-    v.x = Mma<QT>::pack(acc[k].x * sc, acc[k].y * sc);
-    v.y = Mma<QT>::pack(acc[k].z * sc, acc[k].w * sc);
-    *reinterpret_cast<uint2*>(dst + 4 * (cg + k * kJoinGroups)) = v;
+    v.x = Mma<QT>::pack(acc[k].x * inv, acc[k].y * inv);
+    v.y = Mma<QT>::pack(acc[k].z * inv, acc[k].w * inv);
+    *reinterpret_cast<uint2*>(dst + 4 * k) = v;
   }
 }
 
@@ -1114,11 +1174,17 @@ cudaError_t launch_tree_nq(TreeParams& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const long long rows = (long long)p.max_q_len * p.group;
   const long long rts = (rows + Ly::ROWS - 1) / Ly::ROWS;
-  const int slices =
-      static_cast<int>(((rows < Ly::ROWS ? rows : Ly::ROWS) + kJoinRows - 1) / kJoinRows);
-  const dim3 grid(slices, static_cast<unsigned>(rts * p.num_kv_heads), p.num_seqs);
-  return launch_pdl(tree_join_kernel<QT, D>, grid, dim3(kJoinThreads), 0, st, p,
-                    KC == kTE4 ? p.v_scale : 1.f);
+  const long long segments = rts * p.num_kv_heads * p.num_seqs;
+  constexpr int NG = kJoinThreads / Ly::ROWS;  // column groups a CTA takes side by side
+  const float out_scale = KC == kTE4 ? p.v_scale : 1.f;
+  // with a quarter as many segments as CTAs or more, a segment has some five
+  // pieces at most
+  const dim3 wide(D / 4 / 8 / NG > 0 ? D / 4 / 8 / NG : 1, static_cast<unsigned>(rts * p.num_kv_heads),
+                  p.num_seqs);
+  const dim3 narrow(D / 4 / NG, wide.y, wide.z);
+  return 4 * segments >= p.ctas
+             ? launch_pdl(tree_join_kernel<QT, D, 8>, wide, dim3(kJoinThreads), 0, st, p, out_scale)
+             : launch_pdl(tree_join_kernel<QT, D, 1>, narrow, dim3(kJoinThreads), 0, st, p, out_scale);
 }
 
 template <typename QT, int D, int KC>
@@ -1127,25 +1193,18 @@ cudaError_t launch_tree(TreeParams& p, cudaStream_t st) {
                                                       : launch_tree_nq<QT, D, KC, 1>(p, st);
 }
 
-}  // namespace
-
-cudaError_t launch_tree_attention(TreeParams p, int D, int dtype, int kind, cudaStream_t st) {
-  if ((D != 64 && D != 128) || (dtype != PA_BF16 && dtype != PA_F16) || kind < 0 || kind > 2)
-    return cudaErrorInvalidValue;
-  switch ((dtype == PA_BF16 ? 0 : 6) + (D == 64 ? 0 : 3) + kind) {
-    case 0: return launch_tree<__nv_bfloat16, 64, kT16>(p, st);
-    case 1: return launch_tree<__nv_bfloat16, 64, kTI8>(p, st);
-    case 2: return launch_tree<__nv_bfloat16, 64, kTE4>(p, st);
-    case 3: return launch_tree<__nv_bfloat16, 128, kT16>(p, st);
-    case 4: return launch_tree<__nv_bfloat16, 128, kTI8>(p, st);
-    case 5: return launch_tree<__nv_bfloat16, 128, kTE4>(p, st);
-    case 6: return launch_tree<__half, 64, kT16>(p, st);
-    case 7: return launch_tree<__half, 64, kTI8>(p, st);
-    case 8: return launch_tree<__half, 64, kTE4>(p, st);
-    case 9: return launch_tree<__half, 128, kT16>(p, st);
-    case 10: return launch_tree<__half, 128, kTI8>(p, st);
-    default: return launch_tree<__half, 128, kTE4>(p, st);
+// kind: the cache's, as launch_tree_attention.
+template <typename QT>
+cudaError_t launch_tree_kind(TreeParams& p, int D, int kind, cudaStream_t st) {
+  switch ((D == 64 ? 0 : 3) + kind) {
+    case 0: return launch_tree<QT, 64, kT16>(p, st);
+    case 1: return launch_tree<QT, 64, kTI8>(p, st);
+    case 2: return launch_tree<QT, 64, kTE4>(p, st);
+    case 3: return launch_tree<QT, 128, kT16>(p, st);
+    case 4: return launch_tree<QT, 128, kTI8>(p, st);
+    default: return launch_tree<QT, 128, kTE4>(p, st);
   }
 }
 
+}  // namespace
 }  // namespace pa

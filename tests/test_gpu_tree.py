@@ -100,6 +100,11 @@ CASES = [
     ("int8", torch.bfloat16, 128, 2, 4, 32, [333, 65, 128], [13, 31, 2]),
     ("int8", torch.float16, 64, 1, 2, 64, [70, 700, 16], [64, 65, 16]),
     ("int8", torch.bfloat16, 128, 1, 5, 16, [2100], [7]),
+    # 32, 33, 64, 65, 128, 129 rows: one row tile holds them four, two times, once; two tiles
+    ("auto", torch.bfloat16, 128, 2, 1, 32, [333, 1000, 70, 65, 640, 129], [32, 33, 64, 65, 128, 129]),
+    ("auto", torch.float16, 64, 2, 2, 16, [900, 77, 350], [16, 17, 32]),
+    ("fp8_e4m3", torch.bfloat16, 64, 1, 4, 64, [700, 99], [8, 16]),
+    ("int8", torch.float16, 128, 2, 1, 32, [500, 80], [40, 33]),
 ]
 
 
