@@ -34,14 +34,14 @@ struct TreeParams {
   const int32_t* cu_q;          // [S + 1]
   const int32_t* context_lens;  // [S]: cached tokens, the nodes among them
   const unsigned long long* mask;  // [T][mask_words]
-  float4* part_o;               // [C][2][D / 4][tile_rows]: cut pieces' un-normalised rows
-  float2* part_ml;              // [C][2][tile_rows]: their maximum (log2 units) and sum
+  float4* part_o;               // [C][2][D / 4][rows of a CTA]: cut pieces' un-normalised rows
+  float2* part_ml;              // [C][2][rows of a CTA]: their maximum (log2 units) and sum
   unsigned* err;
   int num_seqs, num_heads, num_kv_heads, group, block_size, num_blocks;
   int num_tokens, max_blocks_per_seq, max_q_len, mask_words;
   int ctas;          // C
-  int tile_rows;     // rows of a CTA's query tiles: 128 or 256
-  int tile_tokens;   // 64 or 128
+  int row_bits;      // a CTA's query tiles have 2^row_bits rows: 128 or 256
+  int token_bits;    // a K/V tile 2^token_bits tokens: 64 or 128
   float scale_log2;  // scale * log2(e) (* k_scale for an FP8 cache)
   float v_scale;     // FP8: multiplies the output
 };
@@ -52,8 +52,8 @@ inline size_t tree_workspace_bytes(int D) {
   return slots * kTreeRows * D * 4 + slots * kTreeRows * 8;
 }
 
-// Launches the attention and then the join of cut segments (p.ctas, p.tile_rows
-// and p.tile_tokens are set on the way). D 64 or 128; kind: the cache's, 0 =
+// Launches the attention and then the join of cut segments (p.ctas, p.row_bits
+// and p.token_bits are set on the way). D 64 or 128; kind: the cache's, 0 =
 // the query's type, 1 = INT8 codes with row scales, 2 = FP8 E4M3 codes.
 cudaError_t launch_tree_bf16(TreeParams p, int D, int kind, cudaStream_t stream);
 cudaError_t launch_tree_f16(TreeParams p, int D, int kind, cudaStream_t stream);

@@ -118,8 +118,8 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int s, bool fla
     q.zero = true;
     return q;
   }
-  q.T = (q.n + p.tile_tokens - 1) / p.tile_tokens;
-  q.RT = static_cast<int>(((long long)q.q_len * p.group + p.tile_rows - 1) / p.tile_rows);
+  q.T = (q.n + (1 << p.token_bits) - 1) >> p.token_bits;
+  q.RT = static_cast<int>(((long long)q.q_len * p.group + (1 << p.row_bits) - 1) >> p.row_bits);
   return q;
 }
 
@@ -1076,7 +1076,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
     P += __shfl_xor_sync(0xffffffffu, P, off);
     before += __shfl_xor_sync(0xffffffffu, before, off);
   }
-  const int R = p.tile_rows, rows_total = q.q_len * p.group, lr = tid % R, r = rt * R + lr;
+  const int R = 1 << p.row_bits, rows_total = q.q_len * p.group, lr = tid & (R - 1), r = rt * R + lr;
   int c0 = 0, n = 0, first = 0;
   if (q.T > 0 && rt < q.RT) {
     const long long U = tree_share(P, p.ctas);
@@ -1089,8 +1089,10 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
   }
   pdl_wait();
   pdl_trigger();
-  if (n <= 1 || r >= rows_total) return;  // not cut
-  const int c4 = (blockIdx.x * (kJoinThreads / R) + tid / R) * NC;
+  if (n <= 1) return;  // not cut
+  if (r - lane >= rows_total) return;  // (a warp's rows are neighbours)
+  const bool live = r < rows_total;
+  const int c4 = (blockIdx.x * (kJoinThreads >> p.row_bits) + (tid >> p.row_bits)) * NC;
   const float2* ml = p.part_ml + (size_t)c0 * 2 * R + lr;
   const float4* po = p.part_o + ((size_t)c0 * 2 * (D / 4) + c4) * R + lr;
   constexpr int J = NC == 1 ? 8 : 2;  // pieces whose loads are in flight together
@@ -1106,9 +1108,10 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
       const int j = j0 + u, sl = 2 * j + (j == 0 ? first : 0);
       h[u] = make_float2(-INFINITY, 0.f);
       if (j < n) {
-        h[u] = __ldcg(ml + (size_t)sl * R);
+        if (live) h[u] = __ldcg(ml + (size_t)sl * R);
 #pragma unroll
-        for (int k = 0; k < NC; ++k) v[u][k] = __ldcg(po + ((size_t)sl * (D / 4) + k) * R);
+        for (int k = 0; k < NC; ++k)
+          if (live) v[u][k] = __ldcg(po + ((size_t)sl * (D / 4) + k) * R);
       }
     }
 #pragma unroll
@@ -1134,14 +1137,33 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
     }
   }
   const float inv = (l > 0.f ? 1.f / l : 0.f) * out_scale;
-  QT* dst = static_cast<QT*>(p.out) +
-            ((size_t)(q.q0 + r / p.group) * p.num_heads + g * p.group + r % p.group) * D + 4 * c4;
+  const long long at =
+      live ? ((long long)(q.q0 + r / p.group) * p.num_heads + g * p.group + r % p.group) * D + 4 * c4
+           : -1;
+  QT* out = static_cast<QT*>(p.out);
+  if constexpr (NC == 1) {
+    if (live)
+      *reinterpret_cast<uint2*>(out + at) =
+          make_uint2(Mma<QT>::pack(acc[0].x * inv, acc[0].y * inv),
+                     Mma<QT>::pack(acc[0].z * inv, acc[0].w * inv));
+  } else {
+    // through shared memory (80 bytes a row: no two lanes of a quarter warp in
+    // a bank), so that whole sectors are written: 4 lanes store a row's 64 bytes
+    __shared__ uint4 turn[kJoinThreads / 32][32][5];
+    uint4(*t)[5] = turn[tid / 32];
 #pragma unroll
-  for (int k = 0; k < NC; ++k) {
-    uint2 v;
-    v.x = Mma<QT>::pack(acc[k].x * inv, acc[k].y * inv);
-    v.y = Mma<QT>::pack(acc[k].z * inv, acc[k].w * inv);
-    *reinterpret_cast<uint2*>(dst + 4 * k) = v;
+    for (int k = 0; k < NC; k += 2)
+      t[lane][k / 2] = make_uint4(Mma<QT>::pack(acc[k].x * inv, acc[k].y * inv),
+                                  Mma<QT>::pack(acc[k].z * inv, acc[k].w * inv),
+                                  Mma<QT>::pack(acc[k + 1].x * inv, acc[k + 1].y * inv),
+                                  Mma<QT>::pack(acc[k + 1].z * inv, acc[k + 1].w * inv));
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int row = 8 * k + lane / 4;
+      const long long a = __shfl_sync(0xffffffffu, at, row);
+      if (a >= 0) *reinterpret_cast<uint4*>(out + a + 8 * (lane % 4)) = t[row][lane % 4];
+    }
   }
 }
 
@@ -1168,8 +1190,10 @@ cudaError_t launch_tree_nq(TreeParams& p, cudaStream_t st) {
   }
   // (the workspace holds kTreeMaxCtas CTAs of 128 rows)
   p.ctas = (sms * 2 < kTreeMaxCtas ? sms * 2 : kTreeMaxCtas) / NQ;
-  p.tile_rows = Ly::ROWS;
-  p.tile_tokens = Ly::TT;
+  p.row_bits = NQ == 1 ? 7 : 8;
+  p.token_bits = NQ == 1 ? 6 : 7;
+  static_assert(Ly::ROWS == (NQ == 1 ? 1 << 7 : 1 << 8) && Ly::TT == (NQ == 1 ? 1 << 6 : 1 << 7),
+                "the shifts that replace divisions");
   e = launch_pdl(kern, dim3(p.ctas), dim3(Ly::THREADS), Ly::SMEM, st, p);
   if (e != cudaSuccess) return e;
   const long long rows = (long long)p.max_q_len * p.group;
