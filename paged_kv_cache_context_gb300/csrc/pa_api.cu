@@ -1143,8 +1143,10 @@ static pa_status tree_impl(int kind, void* out, const void* query, const void* k
   p.context_lens = context_lens;
   p.mask = reinterpret_cast<const unsigned long long*>(tree_mask);
   p.part_o = static_cast<float4*>(workspace);
-  p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) +
-                                        (size_t)kTreeMaxCtas * 2 * kTreeRows * head_dim * 4);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.part_ml = reinterpret_cast<float2*>(ws + (size_t)kTreeMaxCtas * 2 * kTreeRows * head_dim * 4);
+  p.seq_units = reinterpret_cast<long long*>(
+      ws + (size_t)kTreeMaxCtas * 2 * kTreeRows * (head_dim * 4 + 8));
   p.err = error_word();
   p.num_seqs = num_seqs;
   p.num_heads = num_heads;
@@ -1207,11 +1209,14 @@ PA_API pa_status pa_tree_fp8(void* out, const void* query, const uint8_t* k_cach
 }
 
 // ================================================================ eviction by attention weight
-// Workspace of a scored decode: the balanced mode's, every row's statistics,
-// then the logits.
+// Workspace of a scored decode: the balanced mode's (its counters are not
+// used), every row's statistics, the sequences' page counts, then the logits.
 static size_t scored_stats_offset(int GT, int D) { return align256(balanced_bytes(GT, D)); }
-static size_t scored_logits_offset(int GT, int D, int S, int Hq) {
+static size_t scored_pages_offset(int GT, int D, int S, int Hq) {
   return scored_stats_offset(GT, D) + align256((size_t)S * Hq * sizeof(float2));
+}
+static size_t scored_logits_offset(int GT, int D, int S, int Hq) {
+  return scored_pages_offset(GT, D, S, Hq) + align256(((size_t)S + 1) * sizeof(long long));
 }
 
 PA_API size_t pa_decode_scored_workspace_size(int num_seqs, int num_heads, int num_kv_heads,
@@ -1225,7 +1230,8 @@ PA_API size_t pa_decode_scored_workspace_size(int num_seqs, int num_heads, int n
          (size_t)num_seqs * num_heads * max_blocks_per_seq * block_size * sizeof(float);
 }
 
-static cudaError_t run_scored(const DecodeParams& prm_in, const DecodeShape& a, cudaStream_t st) {
+static cudaError_t run_scored(const DecodeParams& prm_in, const DecodeShape& a, int* ctas,
+                              cudaStream_t st) {
   const int GT = group_bucket(a.Hq / a.Hkv);
   const dim3 grid(0, 1, 1);
   DecodeParams prm = prm_in;
@@ -1238,18 +1244,18 @@ static cudaError_t run_scored(const DecodeParams& prm_in, const DecodeShape& a, 
   }
   if (a.kv_dtype == PA_KV_AUTO) {
     switch (a.q_dtype) {
-      case PA_F32: return pa_dispatch_scored_f32_f32(prm, grid, a.D, GT, a.bs, st);
-      case PA_BF16: return pa_dispatch_scored_bf16_bf16(prm, grid, a.D, GT, a.bs, st);
-      default: return pa_dispatch_scored_f16_f16(prm, grid, a.D, GT, a.bs, st);
+      case PA_F32: return pa_dispatch_scored_f32_f32(prm, grid, a.D, GT, a.bs, ctas, st);
+      case PA_BF16: return pa_dispatch_scored_bf16_bf16(prm, grid, a.D, GT, a.bs, ctas, st);
+      default: return pa_dispatch_scored_f16_f16(prm, grid, a.D, GT, a.bs, ctas, st);
     }
   }
   if (a.kv_dtype == PA_KV_INT8)
-    return a.q_dtype == PA_BF16 ? pa_dispatch_scored_bf16_i8(prm, grid, a.D, GT, a.bs, st)
-                                : pa_dispatch_scored_f16_i8(prm, grid, a.D, GT, a.bs, st);
+    return a.q_dtype == PA_BF16 ? pa_dispatch_scored_bf16_i8(prm, grid, a.D, GT, a.bs, ctas, st)
+                                : pa_dispatch_scored_f16_i8(prm, grid, a.D, GT, a.bs, ctas, st);
   switch (a.q_dtype) {
-    case PA_F32: return pa_dispatch_scored_f32_e4m3(prm, grid, a.D, GT, a.bs, st);
-    case PA_BF16: return pa_dispatch_scored_bf16_e4m3(prm, grid, a.D, GT, a.bs, st);
-    default: return pa_dispatch_scored_f16_e4m3(prm, grid, a.D, GT, a.bs, st);
+    case PA_F32: return pa_dispatch_scored_f32_e4m3(prm, grid, a.D, GT, a.bs, ctas, st);
+    case PA_BF16: return pa_dispatch_scored_bf16_e4m3(prm, grid, a.D, GT, a.bs, ctas, st);
+    default: return pa_dispatch_scored_f16_e4m3(prm, grid, a.D, GT, a.bs, ctas, st);
   }
 }
 
@@ -1259,7 +1265,7 @@ static pa_status scored_impl(const DecodeShape& a, void* out, float* scores, con
                              const int32_t* context_lens, float scale, void* workspace,
                              size_t workspace_bytes, pa_stream_t stream) {
   if (!scores || !workspace) return PA_ERR_NULL;
-  if ((int64_t)a.MB * a.bs > INT32_MAX - 4 * 256) return PA_ERR_SHAPE;
+  if ((int64_t)a.MB * a.bs > INT32_MAX - 16 * 1024) return PA_ERR_SHAPE;
   if (workspace_bytes <
       pa_decode_scored_workspace_size(a.S, a.Hq, a.Hkv, a.D, a.bs, a.MB))
     return PA_ERR_WORKSPACE;
@@ -1278,14 +1284,32 @@ static pa_status scored_impl(const DecodeShape& a, void* out, float* scores, con
   p.num_splits = 1;
   p.pages_per_split = 1;
   p.row_stats = reinterpret_cast<float2*>(ws + scored_stats_offset(GT, a.D));
+  p.seq_pages = reinterpret_cast<long long*>(ws + scored_pages_offset(GT, a.D, a.S, a.Hq));
   p.logits = reinterpret_cast<float*>(ws + scored_logits_offset(GT, a.D, a.S, a.Hq));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const pa_status rc = pa_decode_workspace_clear(workspace, workspace_bytes, stream);
-  if (rc != PA_OK) return rc;
-  if (run_scored(p, a, st) != cudaSuccess) return PA_ERR_CUDA;
-  ScoresParams sp{scores, p.logits, p.row_stats, block_tables, context_lens, a.S,
-                  a.Hq,   a.Hkv,    a.Hq / a.Hkv, a.bs,        a.NB,         a.MB};
-  return launch_scores(sp, st) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  int ctas = 0;
+  if (run_scored(p, a, &ctas, st) != cudaSuccess) return PA_ERR_CUDA;
+  ScoresParams sp{};
+  sp.out = out;
+  sp.scores = scores;
+  sp.logits = p.logits;
+  sp.stats = p.row_stats;
+  sp.seq_pages = p.seq_pages;
+  sp.piece_o = w.piece_o;
+  sp.piece_ml = reinterpret_cast<const float2*>(w.piece_ml);
+  sp.block_tables = block_tables;
+  sp.context_lens = context_lens;
+  sp.num_seqs = a.S;
+  sp.num_heads = a.Hq;
+  sp.num_kv_heads = a.Hkv;
+  sp.group = a.Hq / a.Hkv;
+  sp.group_slots = GT;
+  sp.head_dim = a.D;
+  sp.block_size = a.bs;
+  sp.num_blocks = a.NB;
+  sp.max_blocks_per_seq = a.MB;
+  sp.ctas = ctas;
+  return launch_scores(sp, a.q_dtype, st) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 PA_API pa_status pa_decode_scored(void* out, float* scores, const void* query, const void* k_cache,

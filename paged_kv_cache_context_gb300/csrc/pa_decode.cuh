@@ -129,9 +129,10 @@ namespace pa {
 #define PA_TC8_MAX_STAGES 16
 #endif
 
-// Scored mode is the balanced mode that also leaves every attended slot's
-// logit and every row's largest logit and sum, from which a second launch
-// adds the softmax weights to running scores. Its running sums take the
+// Scored mode streams as the balanced mode does and also leaves every attended
+// slot's logit and every whole segment's largest logits and sums; a second
+// launch (scores_kernel) combines the cut segments, so nothing is counted here,
+// and adds the softmax weights to running scores. Its running sums take the
 // weights before they are rounded for the MMAs (the scores are held in 32
 // bits and want the exact normaliser).
 enum : int { kModeSplit = 0, kModeBalanced = 1, kModeScored = 2 };
@@ -227,7 +228,9 @@ struct DecodeParams {
   int* arrived;         // [C]: pages of a cut segment whose pieces are published,
                         // at the CTA holding the segment's last page (zero at launch)
   float* logits;        // scored mode: [S][Hq][MB * bs], log2 units
-  float2* row_stats;    // scored mode: [S][Hq]: largest logit (log2 units), sum relative to it
+  long long* seq_pages; // scored mode: [S + 1]: attended pages of the sequences before each
+  float2* row_stats;    // scored mode, whole segments: [S][Hq]: largest logit (log2 units),
+                        // sum relative to it
   // inputs
   const void* query;    // [S][Hq][D] of QT
   const uint8_t* k_cache;
@@ -1361,14 +1364,13 @@ __device__ __forceinline__ void combine_segment(const DecodeParams& p, QT* out, 
       for (int u = 0; u < U; ++u) {
         if (ml[u].y > 0.f) {
           if (ml[u].x > M) {
-            const float f = Ly::SCORED ? exp2f(M - ml[u].x) : expf(M - ml[u].x);
+            const float f = expf(M - ml[u].x);
             lsum *= f;
 #pragma unroll
             for (int t = 0; t < DPL; ++t) acc[t] *= f;
             M = ml[u].x;
           }
-          const float w =
-              ml[u].y * (Ly::SCORED ? exp2f(ml[u].x - M) : expf(ml[u].x - M));
+          const float w = ml[u].y * expf(ml[u].x - M);
           lsum += w;
 #pragma unroll
           for (int t = 0; t < DPL; ++t) acc[t] = fmaf(w, o[u][t], acc[t]);
@@ -1378,10 +1380,6 @@ __device__ __forceinline__ void combine_segment(const DecodeParams& p, QT* out, 
     const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
 #pragma unroll
     for (int t = 0; t < DPL; ++t) out[h * D + lane + 32 * t] = Elem<QT>::from_f32(acc[t] * inv);
-    if constexpr (Ly::SCORED) {
-      if (lane == 0)
-        p.row_stats[(out - static_cast<const QT*>(p.out)) / D + h] = make_float2(M, lsum);
-    }
   }
 }
 
@@ -1493,6 +1491,24 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p) {
         const int pg = s < S ? (attended_len(p, s, BS, false) + BS - 1) / BS : 0;
         total += warp_sum_int(pg);
       }
+      if constexpr (Ly::SCORED) {
+        if (cta == 0) {  // for the second launch
+          long long run = 0;
+          for (int b = 0; b < S; b += 32) {
+            const int s = b + lane;
+            const int pg = s < S ? (attended_len(p, s, BS, false) + BS - 1) / BS : 0;
+            int incl = pg;
+#pragma unroll
+            for (int off = 1; off < 32; off *= 2) {
+              const int v = __shfl_up_sync(0xffffffffu, incl, off);
+              if (lane >= off) incl += v;
+            }
+            if (s < S) p.seq_pages[s] = run + incl - pg;
+            run += __shfl_sync(0xffffffffu, incl, 31);
+          }
+          if (lane == 0) p.seq_pages[S] = total;
+        }
+      }
       const long long P = total * Hkv;
       const long long lo = range_lo(cta, P, C), hi = range_lo(cta + 1, P, C);
       int ls0 = 0, lg0 = 0, lpg0 = 0;
@@ -1586,7 +1602,7 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p) {
         piece_end = k + len - 1;
         piece_flags = (pg == 0 ? kSegFirst : 0) | (pg + len == pages ? kSegLast : 0) |
                       (k > 0 ? kSlot1 : 0);
-        if constexpr (MODE != kModeSplit) {
+        if constexpr (MODE == kModeBalanced) {
           if (pg != 0 || pg + len != pages) {  // cut
             const bool tail = k + len == npages;
             if (!tail) {
@@ -1652,7 +1668,7 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p) {
         }
       }
       if (__shfl_sync(0xffffffffu, aborted ? 1 : 0, 0)) break;
-      if constexpr (MODE != kModeSplit) {
+      if constexpr (MODE == kModeBalanced) {
         // the wait above saw the head piece's last stage released: count it
         // now, with this iteration's copies already in flight
         if (h_on && k == h_k + STAGES) {
@@ -1687,7 +1703,7 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p) {
         if (!mbar_wait_bounded(&full[k % STAGES], (k / STAGES) & 1))
           raise_error(p.err, PA_DEVERR_TIMEOUT);
     }
-    if constexpr (MODE != kModeSplit) {
+    if constexpr (MODE == kModeBalanced) {
       // a head piece whose last stage was not reused: wait for the consumers
       // to release it, then count it (skipped after any timeout)
       if (h_on && __shfl_sync(0xffffffffu, aborted ? 0 : 1, 0)) {
@@ -1853,7 +1869,7 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p) {
     k += n_here;
     if (last_flags & kCtaLast) break;
   }
-  if constexpr (MODE != kModeSplit) {
+  if constexpr (MODE == kModeBalanced) {
     if (tail_cut) {
       // The tail piece, counted here. If every other piece of its segment
       // has been counted already, it completes the segment and needs no
@@ -1973,32 +1989,33 @@ cudaError_t dispatch_decode(const DecodeParams& prm, dim3 grid, int D, int GT, i
 }
 
 template <typename QT, typename CT, int D, int GT>
-cudaError_t dispatch_scored_bs(const DecodeParams& prm, dim3 grid, int BS, cudaStream_t stream) {
+cudaError_t dispatch_scored_bs(const DecodeParams& prm, dim3 grid, int BS, int* ctas,
+                               cudaStream_t stream) {
   switch (BS) {
-    case 16: return launch_decode<QT, CT, D, GT, 16, kModeScored>(prm, grid, nullptr, stream);
-    case 32: return launch_decode<QT, CT, D, GT, 32, kModeScored>(prm, grid, nullptr, stream);
-    case 64: return launch_decode<QT, CT, D, GT, 64, kModeScored>(prm, grid, nullptr, stream);
+    case 16: return launch_decode<QT, CT, D, GT, 16, kModeScored>(prm, grid, ctas, stream);
+    case 32: return launch_decode<QT, CT, D, GT, 32, kModeScored>(prm, grid, ctas, stream);
+    case 64: return launch_decode<QT, CT, D, GT, 64, kModeScored>(prm, grid, ctas, stream);
     default: return cudaErrorInvalidValue;
   }
 }
 template <typename QT, typename CT, int D>
-cudaError_t dispatch_scored_gt(const DecodeParams& prm, dim3 grid, int GT, int BS,
+cudaError_t dispatch_scored_gt(const DecodeParams& prm, dim3 grid, int GT, int BS, int* ctas,
                                cudaStream_t stream) {
   switch (GT) {
-    case 1: return dispatch_scored_bs<QT, CT, D, 1>(prm, grid, BS, stream);
-    case 2: return dispatch_scored_bs<QT, CT, D, 2>(prm, grid, BS, stream);
-    case 4: return dispatch_scored_bs<QT, CT, D, 4>(prm, grid, BS, stream);
-    case 8: return dispatch_scored_bs<QT, CT, D, 8>(prm, grid, BS, stream);
+    case 1: return dispatch_scored_bs<QT, CT, D, 1>(prm, grid, BS, ctas, stream);
+    case 2: return dispatch_scored_bs<QT, CT, D, 2>(prm, grid, BS, ctas, stream);
+    case 4: return dispatch_scored_bs<QT, CT, D, 4>(prm, grid, BS, ctas, stream);
+    case 8: return dispatch_scored_bs<QT, CT, D, 8>(prm, grid, BS, ctas, stream);
     default: return cudaErrorInvalidValue;
   }
 }
 template <typename QT, typename CT>
-cudaError_t dispatch_scored(const DecodeParams& prm, dim3 grid, int D, int GT, int BS,
+cudaError_t dispatch_scored(const DecodeParams& prm, dim3 grid, int D, int GT, int BS, int* ctas,
                             cudaStream_t stream) {
   switch (D) {
-    case 64: return dispatch_scored_gt<QT, CT, 64>(prm, grid, GT, BS, stream);
-    case 96: return dispatch_scored_gt<QT, CT, 96>(prm, grid, GT, BS, stream);
-    case 128: return dispatch_scored_gt<QT, CT, 128>(prm, grid, GT, BS, stream);
+    case 64: return dispatch_scored_gt<QT, CT, 64>(prm, grid, GT, BS, ctas, stream);
+    case 96: return dispatch_scored_gt<QT, CT, 96>(prm, grid, GT, BS, ctas, stream);
+    case 128: return dispatch_scored_gt<QT, CT, 128>(prm, grid, GT, BS, ctas, stream);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -2019,7 +2036,7 @@ PA_DECLARE_DISPATCH(pa_dispatch_decode_bf16_i8);
 PA_DECLARE_DISPATCH(pa_dispatch_decode_f16_i8);
 #define PA_DECLARE_SCORED(NAME)                                                         \
   cudaError_t NAME(const pa::DecodeParams& prm, dim3 grid, int D, int GT, int BS, \
-                   cudaStream_t stream)
+                   int* ctas, cudaStream_t stream)
 PA_DECLARE_SCORED(pa_dispatch_scored_f32_f32);
 PA_DECLARE_SCORED(pa_dispatch_scored_bf16_bf16);
 PA_DECLARE_SCORED(pa_dispatch_scored_f16_f16);

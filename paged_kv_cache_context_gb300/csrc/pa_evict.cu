@@ -3,6 +3,7 @@
 // to keep, and the move of the kept rows to the front.
 #include <cuda_runtime.h>
 
+#include "pa_decode.cuh"
 #include "pa_device.cuh"
 #include "pa_evict.cuh"
 
@@ -10,48 +11,168 @@ namespace pa {
 namespace {
 
 // ================================================================ scores
-// One thread takes four neighbouring tokens of a (sequence, kv head): the
-// group's logits are read once (they are in L2 from the decode that wrote
-// them), the scores read and written once.
-constexpr int kScoreThreads = 256;
+// CTA (tokens, kv head, sequence). Segments that the decode's shares cut
+// are combined here: warp h finds head h's largest logit and sum from the
+// pieces, and the CTAs of a segment share its output elements. Then a thread
+// takes four neighbouring tokens: the group's logits are read once (they are
+// in L2 from the decode that wrote them), the scores read and written once.
+// It is bound by those 4 G + 8 bytes per token and kv head.
+constexpr int kScoreThreads = 256, kScoreTokens = 4 * kScoreThreads;
+
+// The decode's shares (range_lo and cta_of of the balanced mode), with 32-bit
+// divisions where the operands allow: the 64-bit ones took a fifth of this kernel.
+__device__ __forceinline__ long long score_div(long long a, long long b) {  // both >= 0
+  return (a | b) >> 32 ? a / b : static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+}
+__device__ __forceinline__ int score_cta(long long x, long long P, int C) {
+  return static_cast<int>(score_div((x + 1) * C - 1, P));
+}
+
+__device__ __forceinline__ int scored_len(const ScoresParams& p, int s) {
+  const int n = p.context_lens[s], cap = p.max_blocks_per_seq * p.block_size;
+  return n < 0 ? 0 : n > cap ? cap : n;
+}
+
+// R: rounds of kScoreTokens tokens a CTA takes. The
+// loads that do not depend on the statistics (old scores, the first heads'
+// logits) are issued before those are worked out.
+template <typename QT, int R>
 __global__ void __launch_bounds__(kScoreThreads) scores_kernel(const __grid_constant__ ScoresParams p) {
+  __shared__ float2 stat[8];  // largest logit, one over the sum (0: nothing attended)
+  const int s = blockIdx.z, g = blockIdx.y, G = p.group, tid = threadIdx.x;
+  const int warp = tid >> 5, lane = tid & 31, D = p.head_dim;
+  const int n = scored_len(p, s), sh = 31 - __clz(p.block_size);
+  constexpr int kSpan = R * kScoreTokens;
+  const int tb = blockIdx.x * kSpan + 4 * tid;  // this thread's first tokens
+  // (the length was complete before the decode let this launch start)
   pdl_wait();
   pdl_trigger();
-  const int s = blockIdx.z, g = blockIdx.y, G = p.group;
+  if (static_cast<int>(blockIdx.x) * kSpan >= n) return;
   const size_t cap = (size_t)p.max_blocks_per_seq * p.block_size;
-  const long long n0 = p.context_lens[s];
-  const long long n = n0 < 0 ? 0 : n0 > (long long)cap ? (long long)cap : n0;
-  const long long t = ((long long)blockIdx.x * kScoreThreads + threadIdx.x) * 4;
-  if (t >= n) return;
-  // four tokens lie in one page (pages are multiples of 16 tokens); a page
-  // with a bad block id holds no tokens
-  const int b = p.block_tables[(size_t)s * p.max_blocks_per_seq + t / p.block_size];
-  if (b < 0 || b >= p.num_blocks) return;
   const size_t row0 = (size_t)s * p.num_heads + (size_t)g * G;
-  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int h = 0; h < G; ++h) {
-    const float2 st = p.stats[row0 + h];
-    if (!(st.y > 0.f)) continue;
-    const float inv = 1.f / st.y;
-    const float4 x = __ldcg(reinterpret_cast<const float4*>(p.logits + (row0 + h) * cap + t));
-    sum.x = fmaf(exp2f(x.x - st.x), inv, sum.x);
-    sum.y = fmaf(exp2f(x.y - st.x), inv, sum.y);
-    sum.z = fmaf(exp2f(x.z - st.x), inv, sum.z);
-    sum.w = fmaf(exp2f(x.w - st.x), inv, sum.w);
+  const float* logits = p.logits + row0 * cap;
+  float* scores = p.scores + ((size_t)s * p.num_kv_heads + g) * cap;
+  const long long before = __ldcg(p.seq_pages + s), total = __ldcg(p.seq_pages + p.num_seqs);
+  // ---- loads ahead: four tokens lie in one page (pages are multiples of 16
+  // tokens); a page with a bad block id holds no tokens
+  constexpr int PH = 4 / R;  // heads whose logits are loaded ahead
+  bool ok[R];
+  float4 old[R], x[PH][R];
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    const int t = tb + k * kScoreTokens;
+    ok[k] = t < n;
+    if (ok[k]) {
+      const int b = __ldg(p.block_tables + (size_t)s * p.max_blocks_per_seq + (t >> sh));
+      old[k] = *reinterpret_cast<const float4*>(scores + t);
+#pragma unroll
+      for (int h = 0; h < PH; ++h)
+        if (h < G) x[h][k] = __ldcg(reinterpret_cast<const float4*>(logits + h * cap + t));
+      ok[k] = b >= 0 && b < p.num_blocks;
+    }
   }
-  float* dst = p.scores + ((size_t)s * p.num_kv_heads + g) * cap + t;
-  if (t + 3 < n) {
-    float4 v = *reinterpret_cast<float4*>(dst);
-    v.x += sum.x;
-    v.y += sum.y;
-    v.z += sum.z;
-    v.w += sum.w;
-    *reinterpret_cast<float4*>(dst) = v;
-  } else {
-    dst[0] += sum.x;
-    if (t + 1 < n) dst[1] += sum.y;
-    if (t + 2 < n) dst[2] += sum.z;
+  // ---- the rows' statistics
+  const int pages = (n + p.block_size - 1) >> sh, C = p.ctas;
+  const long long P = total * p.num_kv_heads, seg0 = before * p.num_kv_heads + (long long)g * pages;
+  const int c_first = score_cta(seg0, P, C);
+  const bool in_slot1 = seg0 != score_div(c_first * P, C);
+  // as the balanced decode's: with fewer pages than CTAs a piece is a page
+  const int pieces = P >= C ? score_cta(seg0 + pages - 1, P, C) - c_first + 1 : pages;
+  // where piece j lies: its CTA's second slot if the CTA began with other work
+  auto piece = [&](int j) -> size_t {
+    const int c = P >= C ? c_first + j : score_cta(seg0 + j, P, C);
+    return (size_t)c * kPieceSlots + (j == 0 && in_slot1 ? 1 : 0);
+  };
+  if (pieces == 1) {
+    if (tid < G) {
+      const float2 st = p.stats[row0 + tid];
+      stat[tid] = make_float2(st.x, st.y > 0.f ? 1.f / st.y : 0.f);
+    }
+  } else if (warp < G) {
+    float M = -INFINITY, l = 0.f;
+    for (int j = lane; j < pieces; j += 32) {
+      const float2 ml = __ldcg(p.piece_ml + piece(j) * p.group_slots + warp);
+      if (!(ml.y > 0.f)) continue;
+      const float m = fmaxf(M, ml.x);
+      l = l * exp2f(M - m) + ml.y * exp2f(ml.x - m);
+      M = m;
+    }
+    float top = M;
+#pragma unroll
+    for (int off = 16; off >= 1; off /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    l = M == -INFINITY ? 0.f : l * exp2f(M - top);
+#pragma unroll
+    for (int off = 16; off >= 1; off /= 2) l += __shfl_xor_sync(0xffffffffu, l, off);
+    if (lane == 0) stat[warp] = make_float2(top, l > 0.f ? 1.f / l : 0.f);
   }
+  __syncthreads();
+  // ---- the weights
+  float4 sum[R];
+#pragma unroll
+  for (int k = 0; k < R; ++k) sum[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](float4& to, const float4& v, const float2& st) {
+    to.x = fmaf(exp2f(v.x - st.x), st.y, to.x);
+    to.y = fmaf(exp2f(v.y - st.x), st.y, to.y);
+    to.z = fmaf(exp2f(v.z - st.x), st.y, to.z);
+    to.w = fmaf(exp2f(v.w - st.x), st.y, to.w);
+  };
+#pragma unroll
+  for (int h = 0; h < PH; ++h) {
+    if (h >= G || !(stat[h].y > 0.f)) continue;
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+      if (ok[k]) add(sum[k], x[h][k], stat[h]);
+  }
+  for (int h = PH; h < G; ++h) {
+    if (!(stat[h].y > 0.f)) continue;
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+      if (ok[k])
+        add(sum[k], __ldcg(reinterpret_cast<const float4*>(logits + h * cap + tb + k * kScoreTokens)),
+            stat[h]);
+  }
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    const int t = tb + k * kScoreTokens;
+    if (!ok[k]) continue;
+    const float4 v = make_float4(old[k].x + sum[k].x, old[k].y + sum[k].y, old[k].z + sum[k].z,
+                                 old[k].w + sum[k].w);
+    if (t + 3 < n) {
+      *reinterpret_cast<float4*>(scores + t) = v;
+    } else {  // entries past the length stay as they are
+      scores[t] = v.x;
+      if (t + 1 < n) scores[t + 1] = v.y;
+      if (t + 2 < n) scores[t + 2] = v.z;
+    }
+  }
+  // ---- a cut segment's output, shared by its CTAs
+  if (pieces > 1) {
+    const int here = (n + kSpan - 1) / kSpan;
+    for (int e = blockIdx.x * kScoreThreads + tid; e < G * D; e += here * kScoreThreads) {
+      const int h = e / D, d = e % D;
+      const float M = stat[h].x;
+      float acc = 0.f;
+#pragma unroll 4
+      for (int j = 0; j < pieces; ++j) {
+        const size_t b = piece(j) * p.group_slots + h;
+        const float2 ml = __ldcg(p.piece_ml + b);
+        const float o = __ldcg(p.piece_o + b * D + d);
+        if (ml.y > 0.f) acc = fmaf(ml.y * exp2f(ml.x - M), o, acc);
+      }
+      static_cast<QT*>(p.out)[row0 * D + e] = Elem<QT>::from_f32(acc * stat[h].y);
+    }
+  }
+}
+
+template <int R>
+cudaError_t launch_scores_r(const ScoresParams& p, int dtype, cudaStream_t st) {
+  const long long cap = (long long)p.max_blocks_per_seq * p.block_size;
+  const dim3 grid(static_cast<unsigned>((cap + R * kScoreTokens - 1) / (R * kScoreTokens)),
+                  p.num_kv_heads, p.num_seqs);
+  const auto kern = dtype == PA_F32    ? scores_kernel<float, R>
+                    : dtype == PA_BF16 ? scores_kernel<__nv_bfloat16, R>
+                                       : scores_kernel<__half, R>;
+  return launch_pdl(kern, grid, dim3(kScoreThreads), 0, st, p);
 }
 
 // ================================================================ choice
@@ -345,11 +466,13 @@ __global__ void __launch_bounds__(kMoveThreads, 3)
 
 }  // namespace
 
-cudaError_t launch_scores(const ScoresParams& p, cudaStream_t st) {
+cudaError_t launch_scores(const ScoresParams& p, int dtype, cudaStream_t st) {
+  // four rounds of tokens a CTA where that leaves several CTAs per SM
   const long long cap = (long long)p.max_blocks_per_seq * p.block_size;
-  const long long blocks = (cap + 4 * kScoreThreads - 1) / (4 * kScoreThreads);
-  return launch_pdl(scores_kernel, dim3(static_cast<unsigned>(blocks), p.num_kv_heads, p.num_seqs),
-                    dim3(kScoreThreads), 0, st, p);
+  const long long rows = (long long)p.num_kv_heads * p.num_seqs;
+  return rows * ((cap + 4 * kScoreTokens - 1) / (4 * kScoreTokens)) >= 152 * 4
+             ? launch_scores_r<4>(p, dtype, st)
+             : launch_scores_r<1>(p, dtype, st);
 }
 
 cudaError_t launch_select(const SelectParams& p, cudaStream_t st) {

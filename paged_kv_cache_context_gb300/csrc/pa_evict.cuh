@@ -8,16 +8,24 @@
 namespace pa {
 
 // scores[s][g][j] += sum over the group's heads of 2^(x - m) / l for every
-// attended slot j, x the logits that the scored decode left (log2 units).
+// attended slot j, x the logits that the scored decode left (log2 units); and
+// the outputs of the segments that its CTAs' shares cut, from their pieces.
 struct ScoresParams {
-  float* scores;                // [S][Hkv][cap]
-  const float* logits;          // [S][Hq][cap]
-  const float2* stats;          // [S][Hq]: largest logit (log2 units), sum relative to it
+  void* out;                    // [S][Hq][D]
+  float* scores;                // [S][Hkv][MB * bs]
+  const float* logits;          // [S][Hq][MB * bs]
+  const long long* seq_pages;   // [S + 1]: attended pages of the sequences before each
+  const float2* stats;          // whole segments: [S][Hq]: largest logit (log2 units), sum
+  const float* piece_o;         // [C][2][group_slots][D]: a piece's normalised output rows
+  const float2* piece_ml;       // [C][2][group_slots]: their largest logit (log2 units), sum
   const int32_t* block_tables;  // [S][MB]
   const int32_t* context_lens;  // [S]
-  int num_seqs, num_heads, num_kv_heads, group, block_size, num_blocks, max_blocks_per_seq;
+  int num_seqs, num_heads, num_kv_heads, group, group_slots, head_dim;
+  int block_size, num_blocks, max_blocks_per_seq;
+  int ctas;  // C
 };
-cudaError_t launch_scores(const ScoresParams& p, cudaStream_t stream);
+// dtype: out's pa_dtype.
+cudaError_t launch_scores(const ScoresParams& p, int dtype, cudaStream_t stream);
 
 // The tokens an eviction to `budget` keeps.
 struct SelectParams {

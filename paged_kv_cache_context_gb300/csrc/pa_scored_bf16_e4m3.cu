@@ -3,5 +3,5 @@
 #include "pa_decode.cuh"
 
 PA_DECLARE_SCORED(pa_dispatch_scored_bf16_e4m3) {
-  return pa::dispatch_scored<__nv_bfloat16, pa::E4M3>(prm, grid, D, GT, BS, stream);
+  return pa::dispatch_scored<__nv_bfloat16, pa::E4M3>(prm, grid, D, GT, BS, ctas, stream);
 }

@@ -3,5 +3,5 @@
 #include "pa_decode.cuh"
 
 PA_DECLARE_SCORED(pa_dispatch_scored_f16_f16) {
-  return pa::dispatch_scored<__half, __half>(prm, grid, D, GT, BS, stream);
+  return pa::dispatch_scored<__half, __half>(prm, grid, D, GT, BS, ctas, stream);
 }

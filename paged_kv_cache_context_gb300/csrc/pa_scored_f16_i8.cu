@@ -3,5 +3,5 @@
 #include "pa_decode.cuh"
 
 PA_DECLARE_SCORED(pa_dispatch_scored_f16_i8) {
-  return pa::dispatch_scored<__half, pa::I8>(prm, grid, D, GT, BS, stream);
+  return pa::dispatch_scored<__half, pa::I8>(prm, grid, D, GT, BS, ctas, stream);
 }

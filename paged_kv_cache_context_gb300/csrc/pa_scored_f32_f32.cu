@@ -3,5 +3,5 @@
 #include "pa_decode.cuh"
 
 PA_DECLARE_SCORED(pa_dispatch_scored_f32_f32) {
-  return pa::dispatch_scored<float, float>(prm, grid, D, GT, BS, stream);
+  return pa::dispatch_scored<float, float>(prm, grid, D, GT, BS, ctas, stream);
 }

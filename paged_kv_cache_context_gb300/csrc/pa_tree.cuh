@@ -36,6 +36,7 @@ struct TreeParams {
   const unsigned long long* mask;  // [T][mask_words]
   float4* part_o;               // [C][2][D / 4][rows of a CTA]: cut pieces' un-normalised rows
   float2* part_ml;              // [C][2][rows of a CTA]: their maximum (log2 units) and sum
+  long long* seq_units;         // [S + 1]: units of the sequences before each (written by CTA 0)
   unsigned* err;
   int num_seqs, num_heads, num_kv_heads, group, block_size, num_blocks;
   int num_tokens, max_blocks_per_seq, max_q_len, mask_words;
@@ -49,7 +50,7 @@ struct TreeParams {
 // Bytes of the partials (independent of the batch).
 inline size_t tree_workspace_bytes(int D) {
   const size_t slots = (size_t)kTreeMaxCtas * 2;
-  return slots * kTreeRows * D * 4 + slots * kTreeRows * 8;
+  return slots * kTreeRows * D * 4 + slots * kTreeRows * 8 + 65536 * sizeof(long long);
 }
 
 // Launches the attention and then the join of cut segments (p.ctas, p.row_bits

@@ -152,6 +152,7 @@ __device__ __forceinline__ long long tree_units(const TreeParams& p, int s, int 
 }
 __device__ __forceinline__ long long tree_total(const TreeParams& p, int lane) {
   long long v = 0;
+#pragma unroll 4
   for (int b = 0; b < p.num_seqs; b += 32) v += tree_units(p, b + lane, b + lane < p.num_seqs);
 #pragma unroll
   for (int off = 16; off >= 1; off /= 2) v += __shfl_xor_sync(0xffffffffu, v, off);
@@ -385,12 +386,15 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
         S <= 32 ? __shfl_sync(0xffffffffu, incl0, 31) : tree_total(p, lane);
     const long long U = tree_share(P, C);
     const long long lo = min(cta * U, P), hi = min(lo + U, P);
+    // (CTA 0 goes on to the end: the join wants every sequence's place)
     if (lo < hi) {
       long long run = 0;
-      for (int b = 0; b < S; b += 32) {
+      bool found = false;
+      for (int b = 0; b < S && (!found || cta == 0); b += 32) {
         const long long u = b == 0 ? u0 : tree_units(p, b + lane, b + lane < S);
         const long long incl = b == 0 ? incl0 : warp_incl(u, lane);
-        const unsigned hit = __ballot_sync(0xffffffffu, run + incl > lo);
+        if (cta == 0 && b + lane < S) p.seq_units[b + lane] = run + incl - u;
+        const unsigned hit = found ? 0u : __ballot_sync(0xffffffffu, run + incl > lo);
         if (hit) {
           if (lane == __ffs(hit) - 1) {
             const TreeSeq q = tree_seq(p, b + lane, false);
@@ -401,7 +405,7 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
             misc[2] = static_cast<int>(seg - (long long)misc[1] * q.RT);
             misc[3] = static_cast<int>(rem - seg * q.T);
           }
-          break;
+          found = true;
         }
         run += __shfl_sync(0xffffffffu, incl, 31);
       }
@@ -409,6 +413,7 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
     if (lane == 0) {
       misc64[0] = lo;
       misc64[1] = hi;
+      if (cta == 0) p.seq_units[S] = P;
     }
   } else if (warp == Ly::MMA_WARP) {
     tmem_alloc(tmem_slot, Ly::TMEM_COLS);
@@ -1058,24 +1063,15 @@ constexpr int kJoinThreads = 256;
 template <typename QT, int D, int NC>
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ TreeParams p,
                                                                 float out_scale) {
-  // The offsets and lengths are inputs that were complete before the
+  // The sequence's offsets and length are inputs that were complete before the
   // attention kernel let this launch start (it had waited for all before it):
   // reading them does not have to wait for its end.
   const int tid = threadIdx.x, lane = tid & 31, s = blockIdx.z;
   const int g = blockIdx.y % p.num_kv_heads, rt = blockIdx.y / p.num_kv_heads;
   const TreeSeq q = tree_seq(p, s, false);
-  // units before this sequence, and of all (every warp the same)
-  long long before = 0, P = 0;
-  for (int b = 0; b < p.num_seqs; b += 32) {
-    const long long u = tree_units(p, b + lane, b + lane < p.num_seqs);
-    P += u;
-    if (b + lane < s) before += u;
-  }
-#pragma unroll
-  for (int off = 16; off >= 1; off /= 2) {
-    P += __shfl_xor_sync(0xffffffffu, P, off);
-    before += __shfl_xor_sync(0xffffffffu, before, off);
-  }
+  pdl_wait();
+  pdl_trigger();
+  const long long before = __ldcg(p.seq_units + s), P = __ldcg(p.seq_units + p.num_seqs);
   const int R = 1 << p.row_bits, rows_total = q.q_len * p.group, lr = tid & (R - 1), r = rt * R + lr;
   int c0 = 0, n = 0, first = 0;
   if (q.T > 0 && rt < q.RT) {
@@ -1087,8 +1083,6 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
     // after other work
     first = seg0 != c0 * U ? 1 : 0;
   }
-  pdl_wait();
-  pdl_trigger();
   if (n <= 1) return;  // not cut
   if (r - lane >= rows_total) return;  // (a warp's rows are neighbours)
   const bool live = r < rows_total;

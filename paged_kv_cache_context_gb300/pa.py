@@ -539,27 +539,30 @@ def _nbytes(t: torch.Tensor) -> int:
     return t.numel() * t.element_size()
 
 
-def _here(stream, **named):
-    """Every tensor argument (None where optional) and the stream are on the
-    current device, which is the one the library launches on."""
-    ok = stream is None
-    if ok:
-        cur = torch.cuda.current_device() if torch.cuda.is_initialized() else -1
-        for t in named.values():
-            if t is not None and not (isinstance(t, torch.Tensor) and t.get_device() == cur and
-                                      cur >= 0):
-                ok = False
-                break
-    if ok:
-        return
-    _on_device(**named)
-    for t in named.values():
+def _pointers(stream, names: str, *tensors):
+    """Device pointers of contiguous tensors on the current device, which is the
+    one the library launches on (None where an optional one is missing). The
+    names are for what is raised; they are not looked at otherwise."""
+    cur = torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+    out = []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+        elif isinstance(t, torch.Tensor) and t.get_device() == cur >= 0 and t.is_contiguous():
+            out.append(t.data_ptr())
+        else:
+            break
+    if len(out) == len(tensors) and (stream is None or stream.device.index == cur):
+        return out
+    _on_device(**dict(zip(names.split(), tensors)))
+    for t in tensors:
         if t is not None and t.is_cuda and t.device.index != torch.cuda.current_device():
             raise ValueError(f"tensors are on {t.device}, the current device is "
                              f"cuda:{torch.cuda.current_device()}")
     if stream is not None and stream.device.index != torch.cuda.current_device():
         raise ValueError(f"the stream is on {stream.device}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
+    return [_ptr(t) for t in tensors]
 
 
 def tree_mask_from_parents(parents, cu_q) -> torch.Tensor:
@@ -594,6 +597,16 @@ def tree_workspace_size(num_heads: int, num_kv_heads: int, head_dim: int) -> int
 
 def _check_tree_args(out, query, k_cache, v_cache, block_tables, cu_q, context_lens, tree_mask,
                      num_kv_heads: int, cache_dtype: torch.dtype):
+    """Sizes (T, S, Hq, Hkv, D, bs, NB, MB) of consistent arguments; raises on others."""
+    q, k, bt = query.shape, k_cache.shape, block_tables.shape
+    if (len(q) == 3 and len(k) == 4 and len(bt) == 2 and out.shape == q and v_cache.shape == k and
+            k[1] == num_kv_heads and k[3] == q[2] and cu_q.shape == (bt[0] + 1,) and
+            context_lens.shape == (bt[0],) and tree_mask.dim() == 2 and
+            tree_mask.shape[0] == q[0] and query.dtype in _DTYPE and
+            out.dtype == query.dtype and k_cache.dtype == v_cache.dtype == cache_dtype and
+            block_tables.dtype == cu_q.dtype == context_lens.dtype == torch.int32 and
+            tree_mask.dtype == torch.int64):
+        return q[0], bt[0], q[1], num_kv_heads, q[2], k[2], k[0], bt[1]
     _need(query.dim() == 3, "query: expected [num_tokens, num_heads, head_dim]")
     _shape("out", out, query.shape)
     _dtype("out", out, query.dtype)
@@ -609,6 +622,10 @@ def _check_tree_args(out, query, k_cache, v_cache, block_tables, cu_q, context_l
     _need(tree_mask.dim() == 2 and tree_mask.shape[0] == query.shape[0],
           "tree_mask: expected [num_tokens, mask_words]")
     _dtype("tree_mask", tree_mask, torch.int64)
+    raise ValueError("inconsistent arguments")
+
+
+_TREE = "out query k_cache v_cache block_tables cu_q context_lens tree_mask workspace"
 
 
 def tree_attention(out: torch.Tensor, query: torch.Tensor, k_cache: torch.Tensor,
@@ -618,19 +635,12 @@ def tree_attention(out: torch.Tensor, query: torch.Tensor, k_cache: torch.Tensor
     """pa_tree: attention of drafted nodes query [T, Hq, D] (offsets cu_q [S + 1],
     the last tokens of each sequence's context) to the context and to the nodes
     that tree_mask [T, W] (int64 words, see tree_mask_from_parents) names."""
-    _here(stream, out=out, query=query, k_cache=k_cache, v_cache=v_cache,
-          block_tables=block_tables, cu_q=cu_q, context_lens=context_lens, tree_mask=tree_mask,
-          workspace=workspace)
-    _check_tree_args(out, query, k_cache, v_cache, block_tables, cu_q, context_lens, tree_mask,
-                     num_kv_heads, query.dtype)
-    T, Hq, D = query.shape
-    NB, _, bs, _ = k_cache.shape
-    S, MB = block_tables.shape
-    _check(lib().pa_tree(_ptr(out), _ptr(query), _ptr(k_cache), _ptr(v_cache),
-                         _ptr(block_tables), _ptr(cu_q), _ptr(context_lens), _ptr(tree_mask), T, S,
-                         Hq, num_kv_heads, D, bs, NB, MB, max_q_len, tree_mask.shape[1], scale,
-                         _DTYPE[query.dtype], _ptr(workspace), _nbytes(workspace),
-                         _stream(stream)), "pa_tree")
+    *ptrs, ws = _pointers(stream, _TREE, out, query, k_cache, v_cache, block_tables, cu_q,
+                          context_lens, tree_mask, workspace)
+    sizes = _check_tree_args(out, query, k_cache, v_cache, block_tables, cu_q, context_lens,
+                             tree_mask, num_kv_heads, query.dtype)
+    _check(lib().pa_tree(*ptrs, *sizes, max_q_len, tree_mask.shape[1], scale,
+                         _DTYPE[query.dtype], ws, _nbytes(workspace), _stream(stream)), "pa_tree")
 
 
 def tree_attention_int8(out: torch.Tensor, query: torch.Tensor, k_cache: torch.Tensor,
@@ -639,20 +649,15 @@ def tree_attention_int8(out: torch.Tensor, query: torch.Tensor, k_cache: torch.T
                         context_lens: torch.Tensor, tree_mask: torch.Tensor, num_kv_heads: int,
                         max_q_len: int, scale: float, workspace: torch.Tensor, stream=None):
     """pa_tree_int8: tree_attention over an INT8 cache with per-row scales."""
-    _here(stream, out=out, query=query, k_cache=k_cache, v_cache=v_cache, k_scales=k_scales,
-          v_scales=v_scales, block_tables=block_tables, cu_q=cu_q, context_lens=context_lens,
-          tree_mask=tree_mask, workspace=workspace)
-    _check_tree_args(out, query, k_cache, v_cache, block_tables, cu_q, context_lens, tree_mask,
-                     num_kv_heads, torch.int8)
+    *ptrs, ws = _pointers(stream, "out query k_cache v_cache k_scales v_scales block_tables cu_q "
+                          "context_lens tree_mask workspace", out, query, k_cache, v_cache,
+                          k_scales, v_scales, block_tables, cu_q, context_lens, tree_mask,
+                          workspace)
+    sizes = _check_tree_args(out, query, k_cache, v_cache, block_tables, cu_q, context_lens,
+                             tree_mask, num_kv_heads, torch.int8)
     _check_scales(k_scales, v_scales, k_cache)
-    T, Hq, D = query.shape
-    NB, _, bs, _ = k_cache.shape
-    S, MB = block_tables.shape
-    _check(lib().pa_tree_int8(_ptr(out), _ptr(query), _ptr(k_cache), _ptr(v_cache),
-                              _ptr(k_scales), _ptr(v_scales), _ptr(block_tables), _ptr(cu_q),
-                              _ptr(context_lens), _ptr(tree_mask), T, S, Hq, num_kv_heads, D, bs,
-                              NB, MB, max_q_len, tree_mask.shape[1], scale, _DTYPE[query.dtype],
-                              _ptr(workspace), _nbytes(workspace), _stream(stream)),
+    _check(lib().pa_tree_int8(*ptrs, *sizes, max_q_len, tree_mask.shape[1], scale,
+                              _DTYPE[query.dtype], ws, _nbytes(workspace), _stream(stream)),
            "pa_tree_int8")
 
 
@@ -663,19 +668,13 @@ def tree_attention_fp8(out: torch.Tensor, query: torch.Tensor, k_cache: torch.Te
                        workspace: torch.Tensor, stream=None):
     """pa_tree_fp8: tree_attention over an FP8 E4M3 cache (uint8 codes) with
     per-tensor scales."""
-    _here(stream, out=out, query=query, k_cache=k_cache, v_cache=v_cache,
-          block_tables=block_tables, cu_q=cu_q, context_lens=context_lens, tree_mask=tree_mask,
-          workspace=workspace)
-    _check_tree_args(out, query, k_cache, v_cache, block_tables, cu_q, context_lens, tree_mask,
-                     num_kv_heads, torch.uint8)
-    T, Hq, D = query.shape
-    NB, _, bs, _ = k_cache.shape
-    S, MB = block_tables.shape
-    _check(lib().pa_tree_fp8(_ptr(out), _ptr(query), _ptr(k_cache), _ptr(v_cache),
-                             _ptr(block_tables), _ptr(cu_q), _ptr(context_lens), _ptr(tree_mask),
-                             T, S, Hq, num_kv_heads, D, bs, NB, MB, max_q_len,
-                             tree_mask.shape[1], scale, k_scale, v_scale, _DTYPE[query.dtype],
-                             _ptr(workspace), _nbytes(workspace), _stream(stream)), "pa_tree_fp8")
+    *ptrs, ws = _pointers(stream, _TREE, out, query, k_cache, v_cache, block_tables, cu_q,
+                          context_lens, tree_mask, workspace)
+    sizes = _check_tree_args(out, query, k_cache, v_cache, block_tables, cu_q, context_lens,
+                             tree_mask, num_kv_heads, torch.uint8)
+    _check(lib().pa_tree_fp8(*ptrs, *sizes, max_q_len, tree_mask.shape[1], scale, k_scale, v_scale,
+                             _DTYPE[query.dtype], ws, _nbytes(workspace), _stream(stream)),
+           "pa_tree_fp8")
 
 
 def decode_scored_workspace_size(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int,
@@ -689,6 +688,25 @@ def _check_scores(scores, num_seqs: int, num_kv_heads: int, length: int):
     _dtype("scores", scores, torch.float32)
 
 
+def _check_scored_args(out, scores, query, k_cache, v_cache, block_tables, context_lens,
+                       num_kv_heads: int, cache_dtype: torch.dtype):
+    """Sizes (S, Hq, Hkv, D, bs, NB, MB) of consistent arguments; raises on others."""
+    q, k, bt = query.shape, k_cache.shape, block_tables.shape
+    if (len(q) == 3 and len(k) == 4 and len(bt) == 2 and out.shape == q and v_cache.shape == k and
+            k[1] == num_kv_heads and k[3] == q[2] and bt[0] == q[0] and
+            context_lens.shape == (q[0],) and scores.shape == (q[0], k[1], bt[1] * k[2]) and
+            scores.dtype == torch.float32 and query.dtype in _DTYPE and
+            out.dtype == query.dtype and
+            k_cache.dtype == v_cache.dtype == cache_dtype and
+            block_tables.dtype == context_lens.dtype == torch.int32):
+        return q[0], q[1], num_kv_heads, q[2], k[2], k[0], bt[1]
+    _check_decode_args(out, query, k_cache, v_cache, block_tables, context_lens, num_kv_heads,
+                       cache_dtype)
+    _check_scores(scores, q[0], num_kv_heads, bt[1] * k[2])
+    _need(query.dtype in _DTYPE, f"query: unsupported dtype {query.dtype}")
+    raise ValueError("inconsistent arguments")
+
+
 def decode_scored(out: torch.Tensor, scores: torch.Tensor, query: torch.Tensor,
                   k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
                   context_lens: torch.Tensor, num_kv_heads: int, scale: float,
@@ -696,19 +714,14 @@ def decode_scored(out: torch.Tensor, scores: torch.Tensor, query: torch.Tensor,
                   v_scale: float = 1.0, stream=None):
     """pa_decode_scored: decode, and scores [S, Hkv, MB * bs] += every token's
     softmax weight summed over its kv head's query heads."""
-    _here(stream, out=out, scores=scores, query=query, k_cache=k_cache, v_cache=v_cache,
-          block_tables=block_tables, context_lens=context_lens, workspace=workspace)
-    _check_decode_args(out, query, k_cache, v_cache, block_tables, context_lens, num_kv_heads,
-                       _CACHE_DTYPE.get(kv_dtype, query.dtype))
-    S, Hq, D = query.shape
-    NB, _, bs, _ = k_cache.shape
-    MB = block_tables.shape[1]
-    _check_scores(scores, S, num_kv_heads, MB * bs)
-    _check(lib().pa_decode_scored(_ptr(out), _ptr(scores), _ptr(query), _ptr(k_cache),
-                                  _ptr(v_cache), _ptr(block_tables), _ptr(context_lens), S, Hq,
-                                  num_kv_heads, D, bs, NB, MB, scale, _DTYPE[query.dtype],
-                                  _KV[kv_dtype], k_scale, v_scale, _ptr(workspace),
-                                  _nbytes(workspace), _stream(stream)), "pa_decode_scored")
+    *ptrs, ws = _pointers(stream, "out scores query k_cache v_cache block_tables context_lens "
+                          "workspace", out, scores, query, k_cache, v_cache, block_tables,
+                          context_lens, workspace)
+    sizes = _check_scored_args(out, scores, query, k_cache, v_cache, block_tables, context_lens,
+                               num_kv_heads, _CACHE_DTYPE.get(kv_dtype, query.dtype))
+    _check(lib().pa_decode_scored(*ptrs, *sizes, scale, _DTYPE[query.dtype], _KV[kv_dtype],
+                                  k_scale, v_scale, ws, _nbytes(workspace), _stream(stream)),
+           "pa_decode_scored")
 
 
 def decode_scored_int8(out: torch.Tensor, scores: torch.Tensor, query: torch.Tensor,
@@ -717,21 +730,14 @@ def decode_scored_int8(out: torch.Tensor, scores: torch.Tensor, query: torch.Ten
                        context_lens: torch.Tensor, num_kv_heads: int, scale: float,
                        workspace: torch.Tensor, stream=None):
     """pa_decode_scored_int8: decode_scored over an INT8 cache with per-row scales."""
-    _here(stream, out=out, scores=scores, query=query, k_cache=k_cache, v_cache=v_cache,
-          k_scales=k_scales, v_scales=v_scales, block_tables=block_tables,
-          context_lens=context_lens, workspace=workspace)
-    _check_decode_args(out, query, k_cache, v_cache, block_tables, context_lens, num_kv_heads,
-                       torch.int8)
+    *ptrs, ws = _pointers(stream, "out scores query k_cache v_cache k_scales v_scales "
+                          "block_tables context_lens workspace", out, scores, query, k_cache,
+                          v_cache, k_scales, v_scales, block_tables, context_lens, workspace)
+    sizes = _check_scored_args(out, scores, query, k_cache, v_cache, block_tables, context_lens,
+                               num_kv_heads, torch.int8)
     _check_scales(k_scales, v_scales, k_cache)
-    S, Hq, D = query.shape
-    NB, _, bs, _ = k_cache.shape
-    MB = block_tables.shape[1]
-    _check_scores(scores, S, num_kv_heads, MB * bs)
-    _check(lib().pa_decode_scored_int8(_ptr(out), _ptr(scores), _ptr(query), _ptr(k_cache),
-                                       _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
-                                       _ptr(block_tables), _ptr(context_lens), S, Hq,
-                                       num_kv_heads, D, bs, NB, MB, scale, _DTYPE[query.dtype],
-                                       _ptr(workspace), _nbytes(workspace), _stream(stream)),
+    _check(lib().pa_decode_scored_int8(*ptrs, *sizes, scale, _DTYPE[query.dtype], ws,
+                                       _nbytes(workspace), _stream(stream)),
            "pa_decode_scored_int8")
 
 
@@ -739,18 +745,17 @@ def evict_select(keep: torch.Tensor, new_lens: torch.Tensor, scores: torch.Tenso
                  context_lens: torch.Tensor, num_sink: int = 0, num_recent: int = 0, stream=None):
     """pa_evict_select: keep [S, Hkv, budget] = the ascending positions an
     eviction to `budget` tokens keeps (-1 past new_lens [S])."""
-    _here(stream, keep=keep, new_lens=new_lens, scores=scores, context_lens=context_lens)
-    _need(scores.dim() == 3, "scores: expected [num_seqs, num_kv_heads, length]")
-    S, H, N = scores.shape
+    ptrs = _pointers(stream, "keep new_lens scores context_lens", keep, new_lens, scores,
+                     context_lens)
+    sc, kp = scores.shape, keep.shape
+    _need(len(sc) == 3, "scores: expected [num_seqs, num_kv_heads, length]")
     _dtype("scores", scores, torch.float32)
-    _need(keep.dim() == 3 and keep.shape[:2] == scores.shape[:2],
-          f"keep: expected [{S}, {H}, budget]")
+    _need(len(kp) == 3 and kp[:2] == sc[:2], "keep: expected [num_seqs, num_kv_heads, budget]")
     _dtype("keep", keep, torch.int32)
     for name, t in (("new_lens", new_lens), ("context_lens", context_lens)):
-        _shape(name, t, (S,))
+        _shape(name, t, sc[:1])
         _dtype(name, t, torch.int32)
-    _check(lib().pa_evict_select(_ptr(keep), _ptr(new_lens), _ptr(scores), _ptr(context_lens), S,
-                                 H, N, keep.shape[2], num_sink, num_recent, _stream(stream)),
+    _check(lib().pa_evict_select(*ptrs, *sc, kp[2], num_sink, num_recent, _stream(stream)),
            "pa_evict_select")
 
 
@@ -761,32 +766,37 @@ def compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Te
             stream=None):
     """pa_compact: row starts[s] + j of sequence s <- row keep[s, g, j] for
     j < keep_lens[s], in place (keep [S, Hkv or 1, budget])."""
-    _here(stream, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
-          context_lens=context_lens, keep=keep, keep_lens=keep_lens, starts=starts,
-          k_scales=k_scales, v_scales=v_scales, scores=scores)
-    _need(k_cache.dim() == 4, "k_cache: expected [num_blocks, num_kv_heads, block_size, D]")
-    _shape("v_cache", v_cache, k_cache.shape)
-    _dtype("v_cache", v_cache, k_cache.dtype)
-    NB, H, bs, D = k_cache.shape
-    _need(block_tables.dim() == 2, "block_tables: expected [num_seqs, max_blocks_per_seq]")
-    _dtype("block_tables", block_tables, torch.int32)
-    S, MB = block_tables.shape
-    _need(keep.dim() == 3 and keep.shape[0] == S and keep.shape[1] in (1, H),
-          f"keep: expected [{S}, {H} or 1, budget]")
-    _dtype("keep", keep, torch.int32)
-    for name, t in (("context_lens", context_lens), ("keep_lens", keep_lens), ("starts", starts)):
-        if t is not None:
-            _shape(name, t, (S,))
-            _dtype(name, t, torch.int32)
+    ptrs = _pointers(stream, "k_cache v_cache k_scales v_scales scores block_tables context_lens "
+                     "keep keep_lens starts", k_cache, v_cache, k_scales, v_scales, scores,
+                     block_tables, context_lens, keep, keep_lens, starts)
+    k, bt, kp = k_cache.shape, block_tables.shape, keep.shape
+    if not (len(k) == 4 and len(bt) == 2 and len(kp) == 3 and v_cache.shape == k and
+            v_cache.dtype == k_cache.dtype and kp[0] == bt[0] and kp[1] in (1, k[1]) and
+            context_lens.shape == keep_lens.shape == bt[:1] and
+            (starts is None or starts.shape == bt[:1] and starts.dtype == torch.int32) and
+            block_tables.dtype == keep.dtype == context_lens.dtype == keep_lens.dtype ==
+            torch.int32):
+        _need(len(k) == 4, "k_cache: expected [num_blocks, num_kv_heads, block_size, D]")
+        _shape("v_cache", v_cache, k)
+        _dtype("v_cache", v_cache, k_cache.dtype)
+        _need(len(bt) == 2, "block_tables: expected [num_seqs, max_blocks_per_seq]")
+        _dtype("block_tables", block_tables, torch.int32)
+        _need(len(kp) == 3 and kp[0] == bt[0] and kp[1] in (1, k[1]),
+              f"keep: expected [{bt[0]}, {k[1]} or 1, budget]")
+        _dtype("keep", keep, torch.int32)
+        for name, t in (("context_lens", context_lens), ("keep_lens", keep_lens),
+                        ("starts", starts)):
+            if t is not None:
+                _shape(name, t, bt[:1])
+                _dtype(name, t, torch.int32)
+        raise ValueError("inconsistent arguments")
     _need((k_scales is None) == (v_scales is None), "give both row scales or neither")
     if k_scales is not None:
         _check_scales(k_scales, v_scales, k_cache)
     if scores is not None:
-        _check_scores(scores, S, H, MB * bs)
-    _check(lib().pa_compact(_ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
-                            _ptr(scores), _ptr(block_tables), _ptr(context_lens), _ptr(keep),
-                            _ptr(keep_lens), _ptr(starts), S, H, keep.shape[1], keep.shape[2], D,
-                            bs, NB, MB, k_cache.element_size(), _stream(stream)), "pa_compact")
+        _check_scores(scores, bt[0], k[1], bt[1] * k[2])
+    _check(lib().pa_compact(*ptrs, bt[0], k[1], kp[1], kp[2], k[3], k[2], k[0], bt[1],
+                            k_cache.element_size(), _stream(stream)), "pa_compact")
 
 
 PA_BUDGET_MB, PA_BUDGET_FRACTION, PA_BUDGET_CONTEXT = 0, 1, 2
