@@ -1406,7 +1406,8 @@ PA_API pa_status pa_compact(void* k_cache, void* v_cache, float* k_scales, float
                   head_dim * elem_bytes,
                   block_size,
                   num_blocks,
-                  max_blocks_per_seq};
+                  max_blocks_per_seq,
+                  (block_size & (block_size - 1)) == 0 ? __builtin_ctz(block_size) : -1};
   return launch_compact(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
                                                                                   : PA_ERR_CUDA;
 }

@@ -348,19 +348,23 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
 // that. keep[j] >= start + j, so a batch's writes only reach rows before every
 // later batch's sources, and every earlier batch has been read when they are
 // made. Where the rows are is worked out first, a chunk of them at a time, so
-// that the reads of a batch do not wait for indexes.
-// The bound is reading and writing the moved rows once.
-constexpr int kMoveThreads = 256, kMoveChunk = 1024;
+// that the reads of a batch do not wait for indexes. The bound is reading and
+// writing the moved rows once. 512 threads with two rows in flight each and as
+// many again moved 238 MB (32 sequences to 1024 rows of 256 bytes, 8 kv heads)
+// in 47 us; 256 threads with 4: 50, with 6: 56, 128 with 6: 69 us.
+constexpr int kMoveThreads = 512, kMoveUnroll = 2, kMoveCtas = 3, kMoveChunk = 512;
 
 // Physical row of position t, or -1 with the error raised.
 __device__ __forceinline__ long long compact_row(const CompactParams& p, const int32_t* table, int g,
                                                  int t) {
-  const int b = __ldg(table + t / p.block_size);
+  // (a shift where the block size is a power of two)
+  const int page = p.block_bits >= 0 ? t >> p.block_bits : t / p.block_size;
+  const int b = __ldg(table + page);
   if (b < 0 || b >= p.num_blocks) {
     raise_error(p.err, PA_DEVERR_BLOCK_ID);
     return -1;
   }
-  return ((long long)b * p.num_kv_heads + g) * p.block_size + t % p.block_size;
+  return ((long long)b * p.num_kv_heads + g) * p.block_size + (t - page * p.block_size);
 }
 
 // Sequence s's range: `start`, kept entries and old length; false when there is nothing to do.
@@ -378,28 +382,28 @@ __device__ __forceinline__ bool compact_seq(const CompactParams& p, int s, bool 
   return true;
 }
 
-// VEC: the elements moved (uint4: 16-byte pieces of K / V rows; float: row
-// scales and scores); columns [v0, v0 + nv) of row_vecs. locate(j): the
-// physical source and destination rows of entry j, source -1 where nothing moves.
-template <typename VEC, int U, typename Locate>
-__device__ __forceinline__ void move_rows(VEC* cache, int row_vecs, int v0, int nv, int kept,
-                                          longlong2* where, Locate locate) {
+// Columns [v0, v0 + nv) of row_vecs 16-byte pieces of every row, U rows a
+// thread and batch. locate(from, j): the physical source and destination rows
+// of entry j, source -1 where nothing moves.
+template <int U, typename Source, typename Locate>
+__device__ __forceinline__ void move_rows(uint4* cache, int row_vecs, int v0, int nv, int kept,
+                                          longlong2* where, Source source, Locate locate) {
   const int rows = kMoveThreads / nv;  // rows one unroll step takes
   const int r = threadIdx.x / nv, c = v0 + threadIdx.x % nv, batch = rows * U;
   for (int j0 = 0; j0 < kept; j0 += kMoveChunk) {
     const int n = min(kMoveChunk, kept - j0);
     __syncthreads();  // the last chunk's places have been used
-    for (int i = threadIdx.x; i < n; i += kMoveThreads) where[i] = locate(j0 + i);
+    for (int i = threadIdx.x; i < n; i += kMoveThreads) where[i] = locate(source(j0 + i), j0 + i);
     __syncthreads();
-    VEC val[2][U];
-    auto load = [&](int i0, VEC (&dst)[U]) {
+    uint4 val[2][U];
+    auto load = [&](int i0, uint4 (&dst)[U]) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int i = i0 + u * rows + r;
         if (r < rows && i < n && where[i].x >= 0) dst[u] = cache[where[i].x * row_vecs + c];
       }
     };
-    auto store = [&](int i0, const VEC (&src)[U]) {
+    auto store = [&](int i0, const uint4 (&src)[U]) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int i = i0 + u * rows + r;
@@ -418,12 +422,36 @@ __device__ __forceinline__ void move_rows(VEC* cache, int row_vecs, int v0, int 
   }
 }
 
-__global__ void __launch_bounds__(kMoveThreads, 3)
+// The same for arrays of one word a row (row scales, scores), four entries a thread.
+template <typename Source, typename Locate>
+__device__ __forceinline__ void move_words(float* words, int kept, Source source, Locate locate) {
+  for (int j0 = 0; j0 < kept; j0 += 4 * kMoveThreads) {
+    int from[4];
+    longlong2 w[4];
+    float val[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int j = j0 + u * kMoveThreads + threadIdx.x;
+      from[u] = j < kept ? source(j) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) w[u] = locate(from[u], j0 + u * kMoveThreads + threadIdx.x);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (w[u].x >= 0) val[u] = words[w[u].x];
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (w[u].x >= 0) words[w[u].y] = val[u];
+  }
+}
+
+__global__ void __launch_bounds__(kMoveThreads, kMoveCtas)
     compact_kernel(const __grid_constant__ CompactParams p, int slices) {
   __shared__ longlong2 where[kMoveChunk];
   pdl_wait();
   pdl_trigger();
-  // the 4-byte arrays first: their many small moves take as long as a slice's
+  // the arrays of one word a row first: their many small moves take as long as a slice's
   const int g = blockIdx.y, s = blockIdx.z;
   const int extras = (p.k_scales ? 2 : 0) + (p.scores ? 1 : 0);
   const int a = static_cast<int>(blockIdx.x) - extras;
@@ -432,7 +460,7 @@ __global__ void __launch_bounds__(kMoveThreads, 3)
   const int32_t* table = p.block_tables + (size_t)s * p.max_blocks_per_seq;
   const int32_t* keep =
       p.keep + ((size_t)s * p.keep_heads + (p.keep_heads > 1 ? g : 0)) * p.budget;
-  auto entry = [&](int j) -> int {  // source position of entry j, or -1
+  auto source = [&](int j) -> int {  // source position of entry j, or -1
     const int from = __ldg(keep + j);
     if (from < start + j || from >= n) {
       raise_error(p.err, PA_DEVERR_SLOT);
@@ -440,8 +468,8 @@ __global__ void __launch_bounds__(kMoveThreads, 3)
     }
     return from;
   };
-  auto locate = [&](int j) -> longlong2 {
-    const int from = entry(j), to = start + j;
+  auto locate = [&](int from, int j) -> longlong2 {
+    const int to = start + j;
     if (from < 0 || from == to) return make_longlong2(-1, -1);
     const long long x = compact_row(p, table, g, from), y = compact_row(p, table, g, to);
     return make_longlong2(y >= 0 ? x : -1, y);
@@ -449,16 +477,15 @@ __global__ void __launch_bounds__(kMoveThreads, 3)
   if (a >= 0) {  // K or V: row_bytes / 16 pieces a row, cut into slices
     const int vecs = p.row_bytes / 16, nv = vecs / slices;
     uint4* cache = reinterpret_cast<uint4*>(a < slices ? p.k_cache : p.v_cache);
-    move_rows<uint4, 6>(cache, vecs, (a % slices) * nv, nv, kept, where, locate);
+    move_rows<kMoveUnroll>(cache, vecs, (a % slices) * nv, nv, kept, where, source, locate);
   } else if (p.k_scales && a >= -2) {
-    move_rows<float, 4>(a == -1 ? p.v_scales : p.k_scales, 1, 0, 1, kept, where, locate);
+    move_words(a == -1 ? p.v_scales : p.k_scales, kept, source, locate);
   } else {
     // scores: their row is in token order; entries past the kept ones become 0
     float* sc = p.scores +
                 ((size_t)s * p.num_kv_heads + g) * p.max_blocks_per_seq * p.block_size;
-    move_rows<float, 4>(sc, 1, 0, 1, kept, where, [&](int j) -> longlong2 {
-      return make_longlong2(entry(j), start + j);
-    });
+    move_words(sc, kept, source,
+               [&](int from, int j) -> longlong2 { return make_longlong2(from, start + j); });
     __syncthreads();
     for (int j = start + kept + threadIdx.x; j < n; j += kMoveThreads) sc[j] = 0.f;
   }

@@ -53,6 +53,7 @@ struct CompactParams {
   unsigned* err;
   int num_seqs, num_kv_heads, keep_heads, budget, row_bytes, block_size, num_blocks;
   int max_blocks_per_seq;
+  int block_bits;  // log2 of block_size, -1 where that is no whole number
 };
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream);
 
