@@ -69,8 +69,7 @@ struct TreeLayout {
   static constexpr int SLOT = KB * TT * 128;            // a K or V tile: [KB][TT tokens][128 B]
   // 16-bit tiles, and 8-bit codes on their way to them (a raw slot is in
   // flight until its codes land, a 16-bit one from then on until its products
-  // are done; codes copied into the 16-bit slots themselves left too little in
-  // flight: 206 us against the time in the launcher's comment)
+  // are done)
   static constexpr int SLOTS = C8 ? (D == 128 ? 3 : 4) : (D == 128 ? 5 : 8);
   static constexpr int RSLOTS = !C8 ? 0 : D == 64 ? 8 : KC == kTI8 ? 3 : 4;
   static constexpr int RAW = TT * D;  // [TT tokens][D]
@@ -683,10 +682,6 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
 #pragma unroll
             for (int j = 0; j < NR; ++j)
               src[j] = *reinterpret_cast<const uint4*>(raw + (half * 64 + r0 + j * RSTEP) * D + 16 * c16);
-            if (half == TT / 64 - 1) {
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&raw_empty[rs]);
-            }
             using Code = typename std::conditional<ROW_SC, I8, E4M3>::type;
 #pragma unroll
             for (int j = 0; j < NR; ++j) {
@@ -706,6 +701,10 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
           }
           fence_proxy_async_smem();
           mbar_arrive(&full[sl]);
+          // the codes have been used, not only asked for: the copies of the
+          // next ones may overwrite them
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&raw_empty[rs]);
           if (filled < NS) ++filled;
           if (++sl == NS) {
             sl = 0;

@@ -119,6 +119,34 @@ def test_matches_the_definition(kv, dtype, D, Hkv, G, bs, lens, nodes):
     check(cache, nodes, G, q, mask, out, scale)
 
 
+# kv, dtype, D, G: with 24 sequences of up to 1500 tokens and 8 kv heads a CTA's
+# share is several tiles long and holds whole segments, so that every ring of
+# buffers goes round many times and pieces follow one another
+LONG_SHARES = [
+    ("auto", torch.bfloat16, 128, 1), ("auto", torch.float16, 64, 2), ("auto", torch.bfloat16, 128, 8),
+    ("fp8_e4m3", torch.bfloat16, 128, 1), ("fp8_e4m3", torch.float16, 128, 2),
+    ("fp8_e4m3", torch.bfloat16, 64, 1), ("fp8_e4m3", torch.bfloat16, 128, 8),
+    ("int8", torch.bfloat16, 128, 1), ("int8", torch.float16, 128, 3), ("int8", torch.float16, 64, 1),
+    ("int8", torch.float16, 128, 8),
+]
+
+
+@pytest.mark.parametrize("kv,dtype,D,G", LONG_SHARES)
+def test_shares_of_many_tiles(kv, dtype, D, G):
+    pa.get_device_error()
+    lens = [40 + (977 * s) % (1460 if s % 3 == 0 else 300) for s in range(24)]
+    nodes = [1 + s % (5 if G < 8 else 20) for s in range(24)]  # 8 rows a node: two query tiles a CTA
+    cache = Cache(lens, 8, D, 32, kv, dtype, seed=D + G)
+    q, cu, mask = inputs(cache, nodes, G, dtype, 11)
+    args = (q.cuda(), cu.cuda(), mask.cuda(), max(nodes), default_scale(D))
+    out = run(cache, *args)
+    assert pa.get_device_error() == 0
+    check(cache, nodes, G, q, mask, out, default_scale(D), heads=None if G <= 3 else [0, 5])
+    ws = torch.zeros(pa.tree_workspace_size(8 * G, 8, D), dtype=torch.uint8, device="cuda")
+    for _ in range(30):
+        assert torch.equal(run(cache, *args, ws=ws), out)
+
+
 def test_a_chain_is_causal_prefill():
     cache = Cache([333, 70], 2, 128, 32, seed=5)
     nodes, G = [20, 64], 4
