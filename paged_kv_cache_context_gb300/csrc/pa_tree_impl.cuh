@@ -60,7 +60,13 @@ struct TreeLayout {
   static constexpr int TT = QT == 1 ? 64 : 128;  // tokens of a tile
   static constexpr bool INPL = QT == 2;          // P over S
   static constexpr int ROWS = QT * kTreeRows;
-  static constexpr int MMA_WARP = 4 * QT, COPY_WARP = MMA_WARP + 1;
+  // Threads of a row. With two query tiles the products of one wait for the other's
+  // softmax, whose length counts: two threads take half of a row's tokens each (tree of
+  // 47 to 96 nodes, 32 heads, 90,000 cached tokens: 127 us, one thread a row 136).
+  // With one query tile two threads a row have too few registers (211 us against 204
+  // on the FP8 batch of the launcher's comment).
+  static constexpr int HV = QT;
+  static constexpr int MMA_WARP = 4 * QT * HV, COPY_WARP = MMA_WARP + 1;
   static constexpr int CONV_WARP = MMA_WARP + 2;
   static constexpr int CONV = C8 ? 128 : 0;  // widening threads
   static constexpr int THREADS = CONV_WARP * 32 + CONV;
@@ -83,11 +89,12 @@ struct TreeLayout {
   static constexpr int OFF_RAW = OFF_KV + SLOTS * SLOT;
   static constexpr int OFF_SC = OFF_RAW + RSLOTS * RAW;  // [SCT][K, V][TT]
   static constexpr int OFF_BAR = OFF_SC + (KC == kTI8 ? SCT * 2 * TT * 4 : 0);
-  static constexpr int NBAR = 2 * SLOTS + 2 * RSLOTS + 7 * QT;  // see the kernel
-  static constexpr int OFF_MISC = (OFF_BAR + NBAR * 8 + 15) / 16 * 16;
+  static constexpr int NBAR = 2 * SLOTS + 2 * RSLOTS + 11 * QT;  // see the kernel
+  static constexpr int OFF_X = (OFF_BAR + NBAR * 8 + 15) / 16 * 16;  // [QT][2 halves][128 rows]
+  static constexpr int OFF_MISC = OFF_X + (HV == 2 ? QT * 2 * kTreeRows * 4 : 0);
   static constexpr int SMEM = OFF_MISC + 64;
   // TMEM columns: S of query tile q at q TT; P at 64 + b 32 (buffer b; with two
-  // query tiles at q 128 + 64, over the second half of S); O of tile q at QT 128 + q D
+  // query tiles over S: tokens 0-63 in its first 32 columns, 64-127 in its last); O of tile q at QT 128 + q D
   static constexpr uint32_t TMEM_COLS = QT == 1 ? 256 : 512;
   static_assert(QT * (128 + D) <= (int)TMEM_COLS, "TMEM columns");
   static_assert(OFF_BAR % 16 == 0, "alignment");
@@ -221,8 +228,12 @@ __device__ __forceinline__ bool elect_one() {
                : "=r"(ok));
   return ok != 0;
 }
+// Polls without the clock first: reading it takes longer than most waits here.
+__device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity) {
+  return mbar_wait_bounded(bar, parity);
+}
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
+  return __all_sync(0xffffffffu, tree_wait(bar, parity));
 }
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
@@ -294,9 +305,9 @@ __device__ __forceinline__ float part_max(const uint32_t (&s)[N], const float* k
 
 // The weights 2^(x - mu) of N neighbouring tokens, rounded to the MMA type
 // in pairs (INT8: times the V row scale first); `sum` takes them unrounded.
-template <typename T, bool ROW_SC, int N>
+template <typename T, bool ROW_SC, bool masked, int N>
 __device__ __forceinline__ void part_weights(const uint32_t (&s)[N], const float* ks,
-                                             const float* vsc, float scale, float mu, bool masked,
+                                             const float* vsc, float scale, float mu,
                                              uint32_t seen, float2& sum, uint32_t (&pk)[N / 2]) {
   const float2 sc2 = make_float2(scale, scale), mu2 = make_float2(-mu, -mu);
 #pragma unroll
@@ -354,6 +365,7 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr int KB = Ly::KB, NS = Ly::SLOTS, ROWS = Ly::ROWS, TT = Ly::TT;
   constexpr bool INPL = Ly::INPL;
+  constexpr int HV = Ly::HV;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + Ly::OFF_BAR);  // [NS] a tile is in its slot
   uint64_t* empty = full + NS;            // [NS] its MMAs are done
@@ -362,7 +374,8 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
   uint64_t* p_full = s_free + NQ;         // [NQ][2]
   uint64_t* pv_done = p_full + 2 * NQ;    // [NQ][2]
   uint64_t* q_full = pv_done + 2 * NQ;    // [NQ]
-  uint64_t* raw_full = q_full + NQ;       // [RS] 8-bit caches: codes have landed
+  uint64_t* paired = q_full + NQ;         // [NQ][4] both warps of 32 rows have given a value
+  uint64_t* raw_full = paired + 4 * NQ;   // [RS] 8-bit caches: codes have landed
   uint64_t* raw_empty = raw_full + Ly::RSLOTS;  // [RS] and have been read
   int* misc = reinterpret_cast<int*>(smem + Ly::OFF_MISC);            // s, g, rt, tile
   long long* misc64 = reinterpret_cast<long long*>(smem + Ly::OFF_MISC + 16);  // lo, hi
@@ -426,13 +439,14 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
         mbar_init(&raw_empty[i], Ly::CONV / 32);
       }
       for (int i = 0; i < 2 * NQ; ++i) {
-        mbar_init(&p_full[i], kTreeRows);
+        mbar_init(&p_full[i], HV * kTreeRows);
         mbar_init(&pv_done[i], 1);
       }
       for (int i = 0; i < NQ; ++i) {
         mbar_init(&s_full[i], 1);
-        mbar_init(&s_free[i], kTreeRows);
-        mbar_init(&q_full[i], kTreeRows);
+        mbar_init(&s_free[i], HV * kTreeRows);
+        mbar_init(&q_full[i], HV * kTreeRows);
+        for (int j = 0; j < 4; ++j) mbar_init(&paired[4 * i + j], 2);
       }
       fence_mbar_init();
     }
@@ -618,11 +632,12 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
         if (!warp_wait(&full[vs], vph) || !warp_wait(&p_full[2 * q + b], (cd[q] >> 1) & 1))
           return false;
         tc05_fence_after();
-        const uint32_t dv = dv0 + vs * (Ly::SLOT >> 4), tp = INPL ? up + q * TT : up + b * 32;
+        const uint32_t dv = dv0 + vs * (Ly::SLOT >> 4), tp = INPL ? us + q * TT : up + b * 32;
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < TT / 16; ++kk)
-            tree_mma_ts(uo + q * D, tp + kk * 8, dv + kk * (2048 / 16), idesc_o, kk > 0 || accumulate);
+            tree_mma_ts(uo + q * D, tp + kk * 8 + (INPL && kk >= 4 ? 64 : 0), dv + kk * (2048 / 16),
+                        idesc_o, kk > 0 || accumulate);
           umma_commit(&pv_done[2 * q + b]);
           if (last) umma_commit(&empty[vs]);
         }
@@ -721,34 +736,52 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
       // ================================================ softmax, one row per thread
       // (tcgen05.ld / st are warp-wide: every decision that leads to one is
       // taken by the whole warp)
-      const int q = warp >> 2;  // query tile
+      const int q = warp / (4 * HV);  // query tile
+      const int hf = HV == 2 ? (warp >> 2) & 1 : 0;  // the thread's half of the tile's tokens
       const int r1 = tid & 127;  // its row: TMEM lane
       const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-      const uint32_t t_s = t_s0 + q * TT + lane_off, t_p = t_p0 + q * TT + lane_off;
+      const uint32_t t_s = t_s0 + q * TT + lane_off;
       const uint32_t t_o = t_o0 + q * D + lane_off;
       uint64_t* pf = p_full + 2 * q;
       uint64_t* pd = pv_done + 2 * q;
       uint8_t* qrow = smem + q * Ly::QBYTES1 + r1 * 128;
       constexpr float kLazy = 8.f;  // weights stay <= 2^kLazy
-      long long ct = 0;             // tiles of the CTA before the piece
-      long long c = 0;              // tiles this query tile has taken
+      // (a CTA's share is less than 2^31 tiles: that many would take it a quarter of an hour)
+      uint32_t ct = 0;  // tiles of the CTA before the piece
+      uint32_t c = 0;   // tiles this query tile has taken
       bool failed = false;
       // the row of the current piece
       int node = 0, rows_total = 0;
-      size_t orow = 0;
+      uint32_t orow = 0;  // (a row is 128 bytes or more: 32 bits hold any that fits the memory)
       bool live = false;
+      uint32_t xph = 0;
+      float* xmine = reinterpret_cast<float*>(smem + Ly::OFF_X) + (q * 2 + hf) * kTreeRows + r1;
+      const float* xother = reinterpret_cast<const float*>(smem + Ly::OFF_X) +
+                            (q * 2 + (hf ^ 1)) * kTreeRows + r1;
+      // The value of the row's other thread for this one's; false after a timeout.
+      auto exchange = [&](float mine, float& other) -> bool {
+        *xmine = mine;
+        __syncwarp();
+        uint64_t* bar = paired + 4 * q + (warp & 3);
+        if (lane == 0) mbar_arrive(bar);
+        if (!warp_wait(bar, xph)) return false;
+        xph ^= 1;
+        other = *xother;
+        return true;
+      };
       auto set_row = [&]() {
         rows_total = w.q.q_len * G;
         const int r = w.rt * ROWS + q * kTreeRows + r1;
         live = r < rows_total;
         node = live ? r / G : 0;
-        orow = ((size_t)(w.q.q0 + node) * Hq + w.g * G + (live ? r % G : 0));
+        orow = static_cast<uint32_t>(w.q.q0 + node) * Hq + w.g * G + (live ? r % G : 0);
       };
       // the row's query, asynchronously (every S product on the last piece's has completed)
+      constexpr int QCH = KB * 8 / HV;  // 16-byte chunks of it per thread
       auto load_q = [&]() {
-        const uint8_t* src = static_cast<const uint8_t*>(p.query) + orow * D * 2;
+        const uint8_t* src = static_cast<const uint8_t*>(p.query) + (size_t)orow * D * 2;
 #pragma unroll
-        for (int ch = 0; ch < KB * 8; ++ch)
+        for (int x = 0, ch = hf * QCH; x < QCH; ++x, ++ch)
           cp_async16(smem_u32(qrow) + (ch >> 3) * (kTreeRows * 128) + (((ch & 7) ^ (r1 & 7)) << 4),
                      src + ch * 16, live);
       };
@@ -761,8 +794,9 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
           if constexpr (C8 && std::is_same<QT, __nv_bfloat16>::value) {
             // q is carried in f16 (exact inside f16's range)
 #pragma unroll
-            for (int ch = 0; ch < KB * 8; ++ch) {
-              uint4* q16 = reinterpret_cast<uint4*>(qrow + (ch >> 3) * (kTreeRows * 128) + (ch & 7) * 16);
+            for (int x = 0, ch = hf * QCH; x < QCH; ++x, ++ch) {
+              uint4* q16 = reinterpret_cast<uint4*>(qrow + (ch >> 3) * (kTreeRows * 128) +
+                                                    (((ch & 7) ^ (r1 & 7)) << 4));
               uint4 v = *q16;
               uint32_t* e = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
@@ -781,31 +815,32 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
           // a warp without rows only keeps the barriers' count (its rows of S,
           // P and O may hold anything: no MMA mixes rows)
           const bool warp_live = w.rt * ROWS + q * kTreeRows + (warp & 3) * 32 < rows_total;
-          const unsigned long long* words = p.mask + (size_t)(w.q.q0 + node) * p.mask_words;
           float m = -INFINITY, l = 0.f;
           for (int i = 0; i < w.len; ++i, ++c) {
             const int b = static_cast<int>(c & 1);
             const int t0 = (w.tile + i) * TT;
             // the tile's visible tokens (asked for before the wait)
             const bool masked = t0 + TT > ctx;  // CTA-uniform
-            uint32_t seen[TT / 32];
+            constexpr int TH = TT / HV;  // the thread's tokens: 32, 64 or 128
+            uint32_t seen[(TH + 63) / 64 * 2];
 #pragma unroll
-            for (int h = 0; h < TT / 64; ++h) {
+            for (int h = 0; h < (TH + 63) / 64; ++h) {
               unsigned long long v = ~0ull;
-              if (masked) v = live ? tree_seen(words, p.mask_words, t0 + 64 * h, ctx, w.q.n) : 0ull;
+              if (masked)
+                v = live ? tree_seen(p.mask + (size_t)(w.q.q0 + node) * p.mask_words, p.mask_words, t0 + hf * TH + 64 * h, ctx, w.q.n) : 0ull;
               seen[2 * h] = static_cast<uint32_t>(v);
               seen[2 * h + 1] = static_cast<uint32_t>(v >> 32);
             }
-            if (__any_sync(0xffffffffu, !mbar_wait_bounded(&s_full[q], static_cast<uint32_t>(c & 1)))) {
+            if (__any_sync(0xffffffffu, !tree_wait(&s_full[q], static_cast<uint32_t>(c & 1)))) {
               failed = true;
               break;
             }
-            const long long kv = 2 * (ct + i) + 1;  // V's slot
-            const float* sct = sc + ((ct + i) % Ly::SCT) * 2 * TT;  // INT8 row scales
+            const uint32_t kv = 2 * (ct + i) + 1;  // V's slot
+            const float* sct = sc + ((ct + i) % Ly::SCT) * 2 * TT + hf * TH;  // INT8 row scales
             if constexpr (ROW_SC) {
               // they landed with K's codes, before V's slot was filled (K's may be
               // on its next phase already)
-              if (__any_sync(0xffffffffu, !mbar_wait_bounded(&full[kv % NS],
+              if (__any_sync(0xffffffffu, !tree_wait(&full[kv % NS],
                                                              static_cast<uint32_t>((kv / NS) & 1)))) {
                 failed = true;
                 break;
@@ -825,22 +860,27 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
               };
               // Moves the running maximum if `mx` clears it, sets mu, and waits
               // for the weights' buffer. False after a timeout.
-              auto settle = [&]() -> bool {
+              auto settle = [&](auto reload) -> bool {
+                if constexpr (HV == 2) {
+                  float other;
+                  if (!exchange(mx, other)) return false;
+                  mx = fmaxf(mx, other);
+                }
                 if (__any_sync(0xffffffffu, mx > m + kLazy)) {
                   const float mn = fmaxf(m, mx);
                   if (i > 0) {
                     // O holds the tiles so far: scale it by 2^(m - mn) once the
                     // last P V has landed
-                    const long long cp = c - 1;
+                    const uint32_t cp = c - 1;
                     if (__any_sync(0xffffffffu,
-                                   !mbar_wait_bounded(&pd[cp & 1],
+                                   !tree_wait(&pd[cp & 1],
                                                       static_cast<uint32_t>((cp >> 1) & 1))))
                       return false;
                     tc05_fence_after();
                     __syncwarp();
                     const float al = mn == -INFINITY ? 1.f : exp2f(m - mn);
 #pragma unroll
-                    for (int c0 = 0; c0 < D; c0 += 16) {
+                    for (int c0 = hf * (D / HV); c0 < (hf + 1) * (D / HV); c0 += 16) {
                       uint32_t o[16];
                       tmem_ld16(t_o + c0, o);
                       tmem_wait_ld();
@@ -851,6 +891,7 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
                     }
                     tmem_wait_st();
                     l *= al;
+                    reload();  // (held logits: their registers are free for the scaling)
                   }
                   m = mn;
                 }
@@ -858,7 +899,7 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
                 // the P V before the last has read the buffer
                 return INPL || c < 2 ||
                        !__any_sync(0xffffffffu,
-                                   !mbar_wait_bounded(&pd[b],
+                                   !tree_wait(&pd[b],
                                                       static_cast<uint32_t>(((c >> 1) - 1) & 1)));
               };
               const float sl2 = p.scale_log2;
@@ -866,82 +907,79 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
                 mx = fmaxf(mx, part_max<ROW_SC>(sr, sct + e0, sl2, masked, bits));
               };
               auto weigh = [&](auto& sr, int e0, uint32_t bits, auto& pk) {
-                part_weights<T, ROW_SC>(sr, sct + e0, sct + TT + e0, sl2, mu, masked, bits, sum, pk);
+                if (masked)
+                  part_weights<T, ROW_SC, true>(sr, sct + e0, sct + TT + e0, sl2, mu, bits, sum, pk);
+                else
+                  part_weights<T, ROW_SC, false>(sr, sct + e0, sct + TT + e0, sl2, mu, bits, sum, pk);
               };
               if constexpr (INPL) {
-                // 128 tokens, XH * 32 at a time: the last part stays in registers and
-                // is weighed first, its weights going over logits of its own
-                // or of parts that have been weighed; the others are read again
-                constexpr int XH = C8 ? 1 : 2;
-                uint32_t sr[XH][32], pk[16];
-#pragma unroll
-                for (int h = 0; h < 4; h += XH) {
-#pragma unroll
-                  for (int x = 0; x < XH; ++x) tmem_ld32(t_s + 32 * (h + x), sr[x]);
-                  tmem_wait_ld();
-#pragma unroll
-                  for (int x = 0; x < XH; ++x) maxi(sr[x], 32 * (h + x), seen[h + x]);
+                // 64 tokens of 128, 32 at a time: the 32 read last stay in registers and
+                // are weighed first, their weights going over logits of their own; the
+                // others are read again. Half 0 holds its first 32 tokens (weights in
+                // columns 0 to 31 of S), half 1 its last ones (columns 96 to 127).
+                const int kp = hf, ot = hf ^ 1;
+                const uint32_t t_own = t_s + 64 * hf, t_p = t_own + 32 * hf;
+                uint32_t sr[32], pk[16];
+                tmem_ld32(t_own + 32 * ot, sr);
+                tmem_wait_ld();
+                maxi(sr, 32 * ot, seen[ot]);
+                tmem_ld32(t_own + 32 * kp, sr);
+                tmem_wait_ld();
+                maxi(sr, 32 * kp, seen[kp]);
+                if (!settle([&]() {
+                      tmem_ld32(t_own + 32 * kp, sr);
+                      tmem_wait_ld();
+                    })) {
+                  failed = true;
+                  break;
                 }
-                if (!settle()) {
+                weigh(sr, 32 * kp, seen[kp], pk);
+                tmem_st16(t_p + 16 * kp, pk);
+                tmem_ld32(t_own + 32 * ot, sr);
+                tmem_wait_ld();
+                weigh(sr, 32 * ot, seen[ot], pk);
+                tmem_st16(t_p + 16 * ot, pk);
+              } else if constexpr (C8) {
+                // (more threads, fewer registers: each half is read twice.
+                // Handing the registers out by warpgroup, so that these threads
+                // hold both, was slower: the other warps spilled.)
+                const uint32_t t_p = t_p0 + lane_off + b * 32;
+                uint32_t sr[32], pk[16];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  tmem_ld32(t_s + 32 * h, sr);
+                  tmem_wait_ld();
+                  maxi(sr, 32 * h, seen[h]);
+                }
+                if (!settle([]() {})) {
                   failed = true;
                   break;
                 }
 #pragma unroll
-                for (int h = 4 - XH; h >= 0; h -= XH) {
-                  if (h < 4 - XH) {
-#pragma unroll
-                    for (int x = 0; x < XH; ++x) tmem_ld32(t_s + 32 * (h + x), sr[x]);
-                    tmem_wait_ld();
-                  }
-#pragma unroll
-                  for (int x = 0; x < XH; ++x) {
-                    weigh(sr[x], 32 * (h + x), seen[h + x], pk);
-                    tmem_st16(t_p + 16 * (h + x), pk);
-                  }
+                for (int h = 0; h < 2; ++h) {
+                  tmem_ld32(t_s + 32 * h, sr);
+                  tmem_wait_ld();
+                  if (h == 1) s_read();
+                  weigh(sr, 32 * h, seen[h], pk);
+                  tmem_st16(t_p + 16 * h, pk);
                 }
               } else {
-                const uint32_t tpb = t_p + b * 32;
-                if constexpr (C8) {
-                  // (more threads, fewer registers: each half is read twice.
-                  // Handing the registers out by warpgroup, so that they
-                  // hold both, took 241 us instead of 206 on 16 sequences over
-                  // an FP8 cache of 617 MB: the other warps spilled.)
-                  uint32_t sr[32], pk[16];
+                const uint32_t t_p = t_p0 + lane_off + b * 32;
+                uint32_t sr[2][32], pk[16];
+                tmem_ld32(t_s, sr[0]);
+                tmem_ld32(t_s + 32, sr[1]);
+                tmem_wait_ld();
+                s_read();
+                maxi(sr[0], 0, seen[0]);
+                maxi(sr[1], 32, seen[1]);
+                if (!settle([]() {})) {
+                  failed = true;
+                  break;
+                }
 #pragma unroll
-                  for (int h = 0; h < 2; ++h) {
-                    tmem_ld32(t_s + 32 * h, sr);
-                    tmem_wait_ld();
-                    maxi(sr, 32 * h, seen[h]);
-                  }
-                  if (!settle()) {
-                    failed = true;
-                    break;
-                  }
-#pragma unroll
-                  for (int h = 0; h < 2; ++h) {
-                    tmem_ld32(t_s + 32 * h, sr);
-                    tmem_wait_ld();
-                    if (h == 1) s_read();
-                    weigh(sr, 32 * h, seen[h], pk);
-                    tmem_st16(tpb + 16 * h, pk);
-                  }
-                } else {
-                  uint32_t sr[2][32], pk[16];
-                  tmem_ld32(t_s, sr[0]);
-                  tmem_ld32(t_s + 32, sr[1]);
-                  tmem_wait_ld();
-                  s_read();
-                  maxi(sr[0], 0, seen[0]);
-                  maxi(sr[1], 32, seen[1]);
-                  if (!settle()) {
-                    failed = true;
-                    break;
-                  }
-#pragma unroll
-                  for (int h = 0; h < 2; ++h) {
-                    weigh(sr[h], 32 * h, seen[h], pk);
-                    tmem_st16(tpb + 16 * h, pk);
-                  }
+                for (int h = 0; h < 2; ++h) {
+                  weigh(sr[h], 32 * h, seen[h], pk);
+                  tmem_st16(t_p + 16 * h, pk);
                 }
               }
               l += sum.x + sum.y;
@@ -954,13 +992,13 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
               // V rows past the sequence may hold anything, and zero times NaN
               // is NaN in the MMA: zero them (the first query tile's arrival
               // comes before either tile's P V is issued)
-              if (__any_sync(0xffffffffu, !mbar_wait_bounded(&full[kv % NS],
+              if (__any_sync(0xffffffffu, !tree_wait(&full[kv % NS],
                                                              static_cast<uint32_t>((kv / NS) & 1)))) {
                 failed = true;
                 break;
               }
               uint8_t* vt = smem + Ly::OFF_KV + (kv % NS) * Ly::SLOT;
-              for (int z = r1; z < (TT - valid) * KB * 8; z += kTreeRows) {
+              for (int z = hf * kTreeRows + r1; z < (TT - valid) * KB * 8; z += HV * kTreeRows) {
                 const int row = valid + z / (KB * 8), kb = (z / 8) % KB, ch = z % 8;
                 *reinterpret_cast<uint4*>(vt + kb * (TT * 128) + row * 128 + ch * 16) =
                     make_uint4(0u, 0u, 0u, 0u);
@@ -973,7 +1011,7 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
           if (failed) break;
           // ---- the row's output, or its partial
           const bool whole = w.len == w.q.T, was_live = live;
-          const size_t out_row = orow;
+          const uint32_t out_row = orow;
           // the next piece's query is on its way meanwhile (all S products on
           // this one's have completed)
           ct += w.len;
@@ -983,22 +1021,31 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
             work = q < live_tiles();
             if (work) load_q();
           }
-          const long long cl = c - 1;
+          const uint32_t cl = c - 1;
           if (__any_sync(0xffffffffu,
-                         !mbar_wait_bounded(&pd[cl & 1], static_cast<uint32_t>((cl >> 1) & 1)))) {
+                         !tree_wait(&pd[cl & 1], static_cast<uint32_t>((cl >> 1) & 1)))) {
             failed = true;
             break;
           }
           tc05_fence_after();
           __syncwarp();
+          if constexpr (HV == 2) {
+            float other = 0.f;
+            if (warp_live && !exchange(l, other)) {
+              failed = true;
+              break;
+            }
+            l += other;
+          }
           const float inv = (l > 0.f ? 1.f / l : 0.f) * (KC == kTE4 ? p.v_scale : 1.f);
           const size_t slot = (size_t)cta * 2 + (piece > 0 ? 1 : 0);
-          QT* dst = static_cast<QT*>(p.out) + out_row * D;
-          float4* po = p.part_o + slot * (D / 4) * ROWS + tid;
+          QT* dst = static_cast<QT*>(p.out) + (size_t)out_row * D;
+          float4* po = p.part_o + slot * (D / 4) * ROWS + q * kTreeRows + r1;
           if (warp_live) {
-            constexpr int EC = C8 ? 16 : 32;  // columns held at once
+            constexpr int EC = C8 || HV == 2 ? 16 : 32;  // columns held at once
 #pragma unroll
-            for (int c0 = 0; c0 < D; c0 += EC) {
+            for (int x = 0; x < D / HV; x += EC) {
+              const int c0 = hf * (D / HV) + x;
               uint32_t o[EC];
               tmem_ld_n(t_o + c0, o);
               tmem_wait_ld();
@@ -1022,7 +1069,8 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
               }
             }
           }
-          if (!whole && was_live) p.part_ml[slot * ROWS + tid] = make_float2(m, l);
+          if (!whole && was_live && hf == 0)
+            p.part_ml[slot * ROWS + q * kTreeRows + r1] = make_float2(m, l);
           // the accumulator has been read before the next piece's weights (whose
           // arrival lets the MMAs overwrite it) are announced
           tc05_fence_before();
