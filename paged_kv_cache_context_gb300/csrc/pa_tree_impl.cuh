@@ -278,22 +278,25 @@ __device__ __forceinline__ unsigned long long tree_seen(const unsigned long long
   return v;
 }
 
-// The largest seen logit (log2 units) of N neighbouring tokens. Without row
-// scales and masks the maximum is taken over the raw products: multiplying by
-// a scale that is not negative keeps their order.
+// The largest seen logit (log2 units) of N neighbouring tokens. Without masks
+// the maximum is taken before the scale: multiplying by one that is not
+// negative keeps the order.
 template <bool ROW_SC, int N>
 __device__ __forceinline__ float part_max(const uint32_t (&s)[N], const float* ks, float scale,
                                           bool masked, uint32_t seen) {
-  float a[4];
-  if (scale >= 0.f && !ROW_SC && !masked) {
+  float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  if (scale >= 0.f && !masked) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) a[e] = __uint_as_float(s[e]);
-#pragma unroll
-    for (int e = 4; e < N; ++e) a[e & 3] = fmaxf(a[e & 3], __uint_as_float(s[e]));
+    for (int e = 0; e < N; e += 4) {
+      float4 k = make_float4(1.f, 1.f, 1.f, 1.f);
+      if constexpr (ROW_SC) k = *reinterpret_cast<const float4*>(ks + e);
+      a[0] = fmaxf(a[0], __uint_as_float(s[e]) * k.x);
+      a[1] = fmaxf(a[1], __uint_as_float(s[e + 1]) * k.y);
+      a[2] = fmaxf(a[2], __uint_as_float(s[e + 2]) * k.z);
+      a[3] = fmaxf(a[3], __uint_as_float(s[e + 3]) * k.w);
+    }
     return fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])) * scale;
   }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) a[e] = -INFINITY;
 #pragma unroll
   for (int e = 0; e < N; ++e) {
     float x = __uint_as_float(s[e]) * scale;
@@ -310,10 +313,17 @@ __device__ __forceinline__ void part_weights(const uint32_t (&s)[N], const float
                                              const float* vsc, float scale, float mu,
                                              uint32_t seen, float2& sum, uint32_t (&pk)[N / 2]) {
   const float2 sc2 = make_float2(scale, scale), mu2 = make_float2(-mu, -mu);
+  float4 k4 = {}, v4 = {};  // row scales of four tokens
 #pragma unroll
   for (int e = 0; e < N; e += 2) {
     float2 x = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-    if constexpr (ROW_SC) x = __fmul2_rn(x, *reinterpret_cast<const float2*>(ks + e));
+    if constexpr (ROW_SC) {
+      if (e % 4 == 0) {
+        k4 = *reinterpret_cast<const float4*>(ks + e);
+        v4 = *reinterpret_cast<const float4*>(vsc + e);
+      }
+      x = __fmul2_rn(x, e % 4 ? make_float2(k4.z, k4.w) : make_float2(k4.x, k4.y));
+    }
     x = __ffma2_rn(x, sc2, mu2);
     float2 w = make_float2(ex2_approx(x.x), ex2_approx(x.y));
     if (masked) {
@@ -322,7 +332,7 @@ __device__ __forceinline__ void part_weights(const uint32_t (&s)[N], const float
     }
     sum = __fadd2_rn(sum, w);
     if constexpr (ROW_SC) {
-      const float2 vs = *reinterpret_cast<const float2*>(vsc + e);
+      const float2 vs = e % 4 ? make_float2(v4.z, v4.w) : make_float2(v4.x, v4.y);
       // an unseen token's weight stays zero, whatever its scale
       if (masked)
         w = make_float2(w.x == 0.f ? 0.f : w.x * vs.x, w.y == 0.f ? 0.f : w.y * vs.y);
