@@ -606,8 +606,9 @@ pa_status pa_decode_scored_int8(void* out, float* scores, const void* query,
  * new_lens  : out, int32 [S] = min(n_s, budget).
  * scores    : in, fp32 [S][Hkv][score_len].  context_lens : int32 [S].
  * 1 <= budget, 0 <= num_sink, 0 <= num_recent, num_sink + num_recent <= budget,
- * 1 <= score_len, S and Hkv <= 65535 (else PA_ERR_SHAPE). n_s outside [0, score_len] sets
- * PA_DEVERR_CONTEXT_LEN and is clamped. S == 0 is a no-op.
+ * 1 <= score_len, budget and score_len < 2^31 - 2^16, S and Hkv <= 65535 (else PA_ERR_SHAPE).
+ * n_s outside [0, score_len] sets PA_DEVERR_CONTEXT_LEN and is clamped.
+ * S == 0 is a no-op.
  */
 pa_status pa_evict_select(int32_t* keep, int32_t* new_lens, const float* scores,
                           const int32_t* context_lens, int num_seqs, int num_kv_heads,

@@ -1358,6 +1358,8 @@ PA_API pa_status pa_evict_select(int32_t* keep, int32_t* new_lens, const float* 
   if (num_kv_heads <= 0 || num_kv_heads > 65535 || score_len < 1 || budget < 1 || num_sink < 0 ||
       num_recent < 0 || (int64_t)num_sink + num_recent > budget)
     return PA_ERR_SHAPE;
+  // (positions are counted in 32 bits, up to a block's tokens past the end)
+  if (score_len > INT32_MAX - 64 * 1024 || budget > INT32_MAX - 64 * 1024) return PA_ERR_SHAPE;
   SelectParams p{keep,     new_lens,     scores,    context_lens, error_word(),
                  num_seqs, num_kv_heads, score_len, budget,       num_sink,     num_recent};
   return launch_select(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK

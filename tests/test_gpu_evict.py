@@ -77,6 +77,16 @@ def test_select_ties_signs_infinities_and_nan():
     check_select(tiny, [N], 5, 0, 0)
 
 
+def test_select_ties_past_the_registers_of_one_block():
+    """Equal scores spread over several rounds of a row: the first of them, counted across rounds."""
+    N = 40003
+    g = torch.Generator().manual_seed(2)
+    few = torch.randint(0, 3, (1, 2, N), generator=g).float()
+    few[0, 1] = 2.0
+    for B, sink, recent in ((20000, 4, 100), (39000, 0, 0), (17, 1, 0)):
+        check_select(few, [N], B, sink, recent)
+
+
 def test_select_clamps_bad_lengths():
     pa.get_device_error()
     scores = torch.rand(2, 1, 64)
@@ -154,6 +164,22 @@ def test_compact_moves_the_kept_rows(kv, dtype, D, H, bs, lens, B, heads, from_s
         assert torch.equal(bits(got[x]), bits(want[x])), x
     if with_scores:
         assert torch.equal(got_s.cpu(), want_s)
+
+
+@pytest.mark.parametrize("dtype,D,bs", [(torch.bfloat16, 8, 24), (torch.float32, 256, 1),
+                                         (torch.float16, 40, 100)])
+def test_compact_of_other_page_and_row_sizes(dtype, D, bs):
+    """The moves read no page structure: any block size and whole 16-byte pieces of a row."""
+    pa.get_device_error()
+    cache = Cache([130, 700, 1], 3, D, bs, "auto", dtype, seed=6)
+    kept = [100, 600, 1]
+    keep = ascending(cache.lens, 3, 600, kept, None, 9)
+    scores = torch.rand(3, 3, cache.MB * bs)
+    want, want_s = moved(cache, keep, kept, None, scores)
+    got, got_s = compact(cache, keep, kept, None, scores)
+    assert pa.get_device_error() == 0
+    assert torch.equal(bits(got["k"]), bits(want["k"])) and torch.equal(bits(got["v"]), bits(want["v"]))
+    assert torch.equal(got_s.cpu(), want_s)
 
 
 def test_compact_takes_any_source_at_or_after_its_place():

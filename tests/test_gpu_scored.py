@@ -90,6 +90,26 @@ def test_matches_the_definition(kv, dtype, D, Hkv, G, bs, lens):
     check(cache, G, q, before, out, scores, default_scale(D))
 
 
+@pytest.mark.parametrize("kv,dtype,D,G,bs", [
+    ("auto", torch.bfloat16, 128, 4, 32), ("auto", torch.float32, 64, 1, 16),
+    ("fp8_e4m3", torch.float16, 96, 1, 32), ("int8", torch.bfloat16, 128, 2, 16)])
+def test_shares_of_many_pages(kv, dtype, D, G, bs):
+    """More sequences than a warp has lanes and more pages than CTAs: shares that hold whole
+    segments, begin and end inside one, and skip empty sequences."""
+    pa.get_device_error()
+    lens = [(379 * s) % 1021 if s % 5 else 0 for s in range(70)] + [2500]
+    cache = Cache(lens, 3, D, bs, kv, dtype, seed=D + G)
+    q, before = inputs(cache, G, dtype, 5)
+    scores = before.cuda()
+    out = run(cache, q.cuda(), scores, default_scale(D))
+    assert pa.get_device_error() == 0
+    check(cache, G, q, before, out, scores, default_scale(D))
+    for _ in range(20):
+        again = before.cuda()
+        assert torch.equal(run(cache, q.cuda(), again, default_scale(D)), out)
+        assert torch.equal(again, scores)
+
+
 @pytest.mark.parametrize("scale,qmul", [(-0.2, 1.0), (0.0, 1.0), (1.0, 10.0)])
 def test_other_scales_and_large_logits(scale, qmul):
     cache = Cache([200, 77], 2, 128, 32, seed=9)

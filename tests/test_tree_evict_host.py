@@ -95,6 +95,8 @@ def test_scored_kinds_reject_their_own(L):
     (dict(keep=None), -1), (dict(sc=None), -1), (dict(S=-1), -3), (dict(S=70000), -3),
     (dict(H=0), -3), (dict(N=0), -3), (dict(B=0), -3), (dict(sink=-1), -3), (dict(recent=-1), -3),
     (dict(sink=9, recent=8), -3), (dict(sink=2 ** 31 - 1, recent=2 ** 31 - 1), -3),
+    # 32-bit positions would run over
+    (dict(N=2 ** 31 - 1), -3), (dict(B=2 ** 31 - 1), -3),
 ])
 def test_select_rejects_bad_arguments_on_host(L, kw, code):
     a = dict(keep=P, new=P, sc=P, cl=P, S=2, H=2, N=64, B=16, sink=1, recent=4)
