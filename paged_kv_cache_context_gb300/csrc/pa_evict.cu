@@ -179,10 +179,11 @@ cudaError_t launch_scores_r(const ScoresParams& p, int dtype, cudaStream_t st) {
 // One CTA per (sequence, kv head). Scores become unsigned keys in their
 // order (NaN lowest, -0 as +0); the first `sink` and last `recent` tokens get
 // the highest key. A radix search over 11, 11 and 10 bits with histograms in
-// shared memory finds the budget-th largest key; then each warp turns its
-// tokens into words of 32 bits (kept or not), lane i holding word i, and every
-// lane writes the positions of its own word's bits. The bytes are few (4 per
-// score): the bound is the chain of passes of the longest row.
+// shared memory finds the budget-th largest key (it ends early where a whole
+// bin is kept); then each thread turns a run of tokens into the bits of a word
+// and writes their positions. The bytes are few (4 per score): the bound is
+// the chain of passes over the longest row, of which the first, with the
+// loads, takes a third.
 constexpr int kSelBins = 2048;
 
 __device__ __forceinline__ unsigned score_key(float x) {
@@ -211,11 +212,16 @@ __device__ __forceinline__ unsigned block_before(unsigned v, unsigned* wsum, int
   return before + incl - v;
 }
 
-// THREADS * ITEMS tokens at most stay in registers, ITEMS <= 32 per thread;
-// ITEMS 0: any number, in rounds of 32 per thread that are read again in every pass.
-template <int THREADS, int ITEMS>
+// STAGED: the row's keys are kept in shared memory; otherwise every pass reads
+// the scores again. The loops are short and rolled on purpose: with the keys in
+// registers, 32 a thread, fetching the unrolled code took most of the time
+// (128 rows of up to 32768 scores: 17.4 us, as it is now 12.0; one sequence of
+// 700, 8 rows: 5.6 and 4.7). Four histograms side by side in the first pass, so
+// that equal digits of a warp meet less often, were no faster (12.9 us).
+template <int THREADS, bool STAGED>
 __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__ SelectParams p) {
-  constexpr int WARPS = THREADS / 32, PER = ITEMS > 0 ? ITEMS : 32;
+  constexpr int WARPS = THREADS / 32;
+  extern __shared__ uint4 keys4[];  // [cap / 4], rounded up to eights
   __shared__ unsigned hist[kSelBins];
   __shared__ unsigned wsum[3][WARPS];
   __shared__ unsigned s_bin, s_above, s_count;
@@ -238,45 +244,75 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
     return;
   }
   const float* sc = p.scores + row * p.cap;
-  const int last = n - p.recent;
-  const int rounds = ITEMS > 0 ? 1 : (n + THREADS * PER - 1) / (THREADS * PER);
-  // the keys of round r: warp w takes PER * 32 tokens, lane by lane; a place
-  // past the sequence holds key 0 and is left out by its position
-  unsigned keys[PER];
-  auto base_of = [&](int r) { return (r * WARPS + warp) * PER * 32; };
-  auto load = [&](int r) {
-    const int base = base_of(r) + lane;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int t = base + i * 32;
-      const float x = t < n ? __ldg(sc + t) : 0.f;
-      keys[i] = t >= n ? 0u : (t < p.sink || t >= last) ? 0xFFFFFFFFu : score_key(x);
-    }
+  const bool vec = (reinterpret_cast<uintptr_t>(sc) & 15u) == 0;
+  const int sink = p.sink, last = n - p.recent;
+  // the scores of tokens [t, t + 4), zeros past the end, and their keys
+  auto read = [&](int t) -> float4 {
+    if (vec && t + 3 < n) return __ldg(reinterpret_cast<const float4*>(sc + t));
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (t < n) x.x = __ldg(sc + t);
+    if (t + 1 < n) x.y = __ldg(sc + t + 1);
+    if (t + 2 < n) x.z = __ldg(sc + t + 2);
+    if (t + 3 < n) x.w = __ldg(sc + t + 3);
+    return x;
   };
-  if (ITEMS > 0) load(0);
+  auto make = [&](const float4& x, int t) -> uint4 {
+    uint4 k = make_uint4(score_key(x.x), score_key(x.y), score_key(x.z), score_key(x.w));
+    if (t < sink || t + 3 >= last) {
+      if (t < sink || t >= last) k.x = 0xFFFFFFFFu;
+      if (t + 1 < sink || t + 1 >= last) k.y = 0xFFFFFFFFu;
+      if (t + 2 < sink || t + 2 >= last) k.z = 0xFFFFFFFFu;
+      if (t + 3 < sink || t + 3 >= last) k.w = 0xFFFFFFFFu;
+    }
+    return k;
+  };
+  // where tokens [t, t + 4) are kept: neighbouring lanes read neighbouring
+  // groups, or runs of two, four or eight, without bank conflicts
+  auto place = [](int t) -> int { return (t >> 2) ^ ((t >> 5) & 7); };
+  for (int i = tid; i < kSelBins; i += THREADS) hist[i] = 0u;
+  __syncthreads();
   // the budget-th largest key, digit by digit
-  unsigned prefix = 0u, mask = 0u, want = static_cast<unsigned>(kept);  // want-th among the prefix's
+  unsigned prefix = 0u, want = static_cast<unsigned>(kept);  // want-th among the prefix's
 #pragma unroll
   for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;  // of the digit; above it the prefix
     const unsigned bins = pass == 2 ? 1024u : 2048u;
-    for (int i = tid; i < kSelBins; i += THREADS) hist[i] = 0u;
-    __syncthreads();
-    for (int r = 0; r < rounds; ++r) {
-      if (ITEMS == 0) load(r);
-      const int left = n - base_of(r) - lane;  // > 32 i: inside the sequence
+    constexpr int U = THREADS == 256 ? 1 : 4;  // groups of tokens in flight
+    for (int t0 = 4 * tid; t0 < n; t0 += 4 * U * THREADS) {
+      uint4 k[U];
+      if (!STAGED || pass == 0) {
+        float4 x[U];
 #pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (left > 32 * i && (keys[i] & mask) == prefix)
-          atomicAdd(&hist[(keys[i] >> shift) & (bins - 1u)], 1u);
+        for (int u = 0; u < U; ++u) x[u] = read(t0 + 4 * u * THREADS);
+#pragma unroll
+        for (int u = 0; u < U; ++u) k[u] = make(x[u], t0 + 4 * u * THREADS);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int t = t0 + 4 * u * THREADS;
+        if (t >= n) break;
+        if (STAGED) {
+          if (pass == 0)
+            keys4[place(t)] = k[u];
+          else
+            k[u] = keys4[place(t)];
+        }
+        const unsigned e[4] = {k[u].x, k[u].y, k[u].z, k[u].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (t + i < n && (pass == 0 || ((e[i] ^ prefix) >> (pass == 1 ? 21 : 10)) == 0u))
+            atomicAdd(&hist[(e[i] >> shift) & (bins - 1u)], 1u);
+      }
     }
     __syncthreads();
-    // bins from the highest down, BPT a thread
+    // bins from the highest down, BPT a thread; they are cleared for the next pass
     constexpr int BPT = kSelBins / THREADS;
     unsigned mine[BPT], sum = 0u;
 #pragma unroll
     for (int b = 0; b < BPT; ++b) {
-      mine[b] = hist[kSelBins - 1 - (BPT * tid + b)];
+      const int bin = kSelBins - 1 - (BPT * tid + b);
+      mine[b] = hist[bin];
+      hist[bin] = 0u;
       sum += mine[b];
     }
     unsigned before = block_before<WARPS>(sum, wsum[pass], warp, lane);
@@ -291,31 +327,35 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
     }
     __syncthreads();
     prefix |= s_bin << shift;
-    mask |= (bins - 1u) << shift;
     want -= s_above;
+    if (s_count == want) break;  // the whole bin is kept: no digit below matters
   }
-  // prefix is the budget-th largest key: all larger ones are kept, and the
-  // first `want` of its s_count equals
+  // all keys above the prefix's bin are kept, and the first `want` of the
+  // s_count in it (more than that only where they are equal)
   const bool ties = s_count != want;
   __syncthreads();
   unsigned done = 0u, done_eq = 0u;  // kept, and equals met, in earlier rounds
+  // a thread turns runs of 4 to 32 tokens into the bits of a word: as few
+  // as leave every thread one
+  int run = 4;
+  while (run < 32 && run * THREADS < n) run *= 2;
+  const int rounds = (n + run * THREADS - 1) / (run * THREADS);
   for (int r = 0; r < rounds; ++r) {
-    if (ITEMS == 0) load(r);
-    const int left = n - base_of(r) - lane;
-    unsigned word = 0u, equal = 0u;  // of the 32 tokens from base + 32 lane on
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const bool in = left > 32 * i;
-      const unsigned w =
-          __ballot_sync(0xffffffffu, in && (ties ? keys[i] > prefix : keys[i] >= prefix));
-      if (lane == i) word = w;
+    const int t0 = (r * THREADS + tid) * run;
+    unsigned word = 0u, equal = 0u;
+    for (int i = 0; i < run && t0 + i < n; i += 4) {
+      const int t = t0 + i;
+      const uint4 k = STAGED ? keys4[place(t)] : make(read(t), t);
+      const unsigned in = t + 3 < n ? 15u : (1u << (n - t)) - 1u;
+      const unsigned ge = (k.x >= prefix) | (k.y >= prefix) << 1 | (k.z >= prefix) << 2 |
+                          (k.w >= prefix) << 3;
+      unsigned eq = 0u;
+      if (ties)
+        eq = (k.x == prefix) | (k.y == prefix) << 1 | (k.z == prefix) << 2 | (k.w == prefix) << 3;
+      word |= (ge & ~eq & in) << i;
+      equal |= (eq & in) << i;
     }
     if (ties) {
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const unsigned w = __ballot_sync(0xffffffffu, left > 32 * i && keys[i] == prefix);
-        if (lane == i) equal = w;
-      }
       unsigned seen = done_eq + block_before<WARPS>(__popc(equal), wsum[1], warp, lane);
       for (; equal && seen < want; ++seen) {  // the first of them, in order
         word |= equal & (0u - equal);
@@ -336,7 +376,6 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
       done += total;
       __syncthreads();
     }
-    const int t0 = base_of(r) + 32 * lane;
     for (; word; word &= word - 1u) out[at++] = t0 + __ffs(word) - 1;
   }
 }
@@ -502,14 +541,24 @@ cudaError_t launch_scores(const ScoresParams& p, int dtype, cudaStream_t st) {
              : launch_scores_r<1>(p, dtype, st);
 }
 
+template <int THREADS>
+static cudaError_t launch_select_staged(const SelectParams& p, cudaStream_t st) {
+  const auto kern = select_kernel<THREADS, true>;
+  const int smem = (p.cap + 31) / 32 * 128;  // whole runs of eight groups
+  if (smem > 32 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(kern, dim3(p.num_kv_heads, p.num_seqs), dim3(THREADS), smem, st, p);
+}
+
 cudaError_t launch_select(const SelectParams& p, cudaStream_t st) {
-  // as few threads as hold the row (fewer warps meet at each barrier sooner)
-  const dim3 grid(p.num_kv_heads, p.num_seqs);
-  if (p.cap <= 256 * 4) return launch_pdl(select_kernel<256, 4>, grid, dim3(256), 0, st, p);
-  if (p.cap <= 512 * 8) return launch_pdl(select_kernel<512, 8>, grid, dim3(512), 0, st, p);
-  if (p.cap <= 1024 * 16) return launch_pdl(select_kernel<1024, 16>, grid, dim3(1024), 0, st, p);
-  if (p.cap <= 1024 * 32) return launch_pdl(select_kernel<1024, 32>, grid, dim3(1024), 0, st, p);
-  return launch_pdl(select_kernel<512, 0>, grid, dim3(512), 0, st, p);
+  // few threads for short rows (fewer warps meet at each barrier sooner); rows
+  // whose keys do not fit an SM's shared memory beside the histogram are read in every pass
+  if (p.cap <= 1024) return launch_select_staged<256>(p, st);
+  if (p.cap <= 4096) return launch_select_staged<512>(p, st);
+  if (p.cap <= 52 * 1024) return launch_select_staged<1024>(p, st);
+  return launch_pdl(select_kernel<1024, false>, dim3(p.num_kv_heads, p.num_seqs), dim3(1024), 0, st, p);
 }
 
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t st) {
