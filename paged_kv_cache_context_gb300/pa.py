@@ -194,15 +194,17 @@ def _check_decode_args(out, query, k_cache, v_cache, block_tables, context_lens,
     _dtype("context_lens", context_lens, torch.int32)
 
 
-# the current stream's handle without a Stream object around it (3 us less per call)
+# the current device, and the current stream's handle without a Stream object around
+# it (3 us less per call)
+_raw_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream: Optional[torch.cuda.Stream]) -> int:
     if stream is not None:
         return stream.cuda_stream
-    if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+    if _raw_stream is not None and torch.cuda.is_initialized():
+        return _raw_stream(_raw_device())
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -543,7 +545,7 @@ def _pointers(stream, names: str, *tensors):
     """Device pointers of contiguous tensors on the current device, which is the
     one the library launches on (None where an optional one is missing). The
     names are for what is raised; they are not looked at otherwise."""
-    cur = torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+    cur = _raw_device() if torch.cuda.is_initialized() else -1
     out = []
     for t in tensors:
         if t is None:
@@ -748,13 +750,17 @@ def evict_select(keep: torch.Tensor, new_lens: torch.Tensor, scores: torch.Tenso
     ptrs = _pointers(stream, "keep new_lens scores context_lens", keep, new_lens, scores,
                      context_lens)
     sc, kp = scores.shape, keep.shape
-    _need(len(sc) == 3, "scores: expected [num_seqs, num_kv_heads, length]")
-    _dtype("scores", scores, torch.float32)
-    _need(len(kp) == 3 and kp[:2] == sc[:2], "keep: expected [num_seqs, num_kv_heads, budget]")
-    _dtype("keep", keep, torch.int32)
-    for name, t in (("new_lens", new_lens), ("context_lens", context_lens)):
-        _shape(name, t, sc[:1])
-        _dtype(name, t, torch.int32)
+    if not (len(sc) == len(kp) == 3 and kp[0] == sc[0] and kp[1] == sc[1] and
+            new_lens.shape == context_lens.shape == sc[:1] and scores.dtype == torch.float32 and
+            keep.dtype == new_lens.dtype == context_lens.dtype == torch.int32):
+        _need(len(sc) == 3, "scores: expected [num_seqs, num_kv_heads, length]")
+        _dtype("scores", scores, torch.float32)
+        _need(len(kp) == 3 and kp[:2] == sc[:2], "keep: expected [num_seqs, num_kv_heads, budget]")
+        _dtype("keep", keep, torch.int32)
+        for name, t in (("new_lens", new_lens), ("context_lens", context_lens)):
+            _shape(name, t, sc[:1])
+            _dtype(name, t, torch.int32)
+        raise ValueError("inconsistent arguments")
     _check(lib().pa_evict_select(*ptrs, *sc, kp[2], num_sink, num_recent, _stream(stream)),
            "pa_evict_select")
 
