@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;  // of the digit; above it the prefix
     const unsigned bins = pass == 2 ? 1024u : 2048u;
-    constexpr int U = THREADS == 256 ? 1 : 4;  // groups of tokens in flight
+    constexpr int U = 4;  // groups of tokens in flight
     for (int t0 = 4 * tid; t0 < n; t0 += 4 * U * THREADS) {
       uint4 k[U];
       if (!STAGED || pass == 0) {
@@ -533,7 +533,10 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtas)
 }  // namespace
 
 cudaError_t launch_scores(const ScoresParams& p, int dtype, cudaStream_t st) {
-  // four rounds of tokens a CTA where that leaves several CTAs per SM
+  // four rounds of tokens a CTA where that leaves several CTAs per SM (64
+  // sequences of up to 8192, 32 kv heads: 374 us with the decode, one round
+  // 389; where it does not, 32 sequences of up to 4096, 8 kv heads: 70 us
+  // with four, 64 with one)
   const long long cap = (long long)p.max_blocks_per_seq * p.block_size;
   const long long rows = (long long)p.num_kv_heads * p.num_seqs;
   return rows * ((cap + 4 * kScoreTokens - 1) / (4 * kScoreTokens)) >= 152 * 4
@@ -553,21 +556,29 @@ static cudaError_t launch_select_staged(const SelectParams& p, cudaStream_t st) 
 }
 
 cudaError_t launch_select(const SelectParams& p, cudaStream_t st) {
-  // few threads for short rows (fewer warps meet at each barrier sooner); rows
-  // whose keys do not fit an SM's shared memory beside the histogram are read in every pass
-  if (p.cap <= 1024) return launch_select_staged<256>(p, st);
+  // fewer threads for short rows, so that an SM holds more of them (512 rows of
+  // 4000: 13.2 us, with 1024 threads 19.7; 128 rows of up to 32768: 14.5 and
+  // 12.0); rows whose keys do not fit an SM's shared memory beside the
+  // histogram are read in every pass
   if (p.cap <= 4096) return launch_select_staged<512>(p, st);
   if (p.cap <= 52 * 1024) return launch_select_staged<1024>(p, st);
   return launch_pdl(select_kernel<1024, false>, dim3(p.num_kv_heads, p.num_seqs), dim3(1024), 0, st, p);
 }
 
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t st) {
-  // column slices until about two CTAs per SM, at least two pieces (32 bytes) a slice
+  // column slices: of 64 bytes or more up to two CTAs per SM, of 32 only while
+  // the CTAs stay fewer than the SMs (rows of 256 bytes, 8 kv heads, 1024 of
+  // 4096 tokens kept. One sequence: 8 slices 5.4 us, 4 slices 6.0, one 11.8;
+  // two: 4 slices 6.0, 8 slices 8.9; four: 2 slices 12.5, 4 10.5, 8 14.2; eight:
+  // one slice 24.0, two 18.7; sixteen: one 31.0, two 33.7)
   const int vecs = p.row_bytes / 16;
   int slices = 1;
-  while (vecs % (2 * slices) == 0 && vecs / (2 * slices) >= 2 &&
-         (long long)p.num_seqs * p.num_kv_heads * 2 * slices < 2 * 152)
-    slices *= 2;
+  for (;;) {
+    const int next = 2 * slices;
+    const long long ctas = (long long)p.num_seqs * p.num_kv_heads * 2 * next;
+    if (vecs % next != 0 || vecs / next < 2 || ctas > (vecs / next >= 4 ? 2 * 152 : 152)) break;
+    slices = next;
+  }
   const int arrays = 2 * slices + (p.k_scales ? 2 : 0) + (p.scores ? 1 : 0);
   return launch_pdl(compact_kernel, dim3(arrays, p.num_kv_heads, p.num_seqs), dim3(kMoveThreads), 0,
                     st, p, slices);

@@ -11,20 +11,26 @@
 // What bounds it. A kv head's q_len G rows share its K and V: 4 D q_len G
 // operations per 2 D elements read, so up to about 290 rows over a 16-bit cache
 // (the ratio of the measured tensor and HBM rates) the bound is reading K and
-// V once. One 128-row tile of tcgen05 products costs about 0.35 us of tensor
-// time per 64 tokens of an SM's share, against 0.73 us to read them.
+// V once. Measured (GB300, both launches): 32 sequences of 512 to 4096 tokens, 64 to
+// 128 rows a kv head, bf16: 70 us, 4.6 TB/s (the floor is 47 us at the
+// measured copy rate; 9 of the 70 are the join); 4 of 9001 to 32768 tokens,
+// 188 to 384 rows, f16: 128 us, 880 TFLOP/s, bound by the chain of a query
+// tile's S, softmax and P V; 16 of 1024 to 8192, FP8, 13 to 61 rows: 193 us, 3.2 TB/s,
+// bound by the tensor cores, which take as long for 13 rows as for 128.
 //
 // Work. Units are 64-token tiles of (sequence, kv head, 128-row tile) in that
-// order; every CTA takes an equal contiguous share, so ragged batches and
+// order (128 tokens by 256 rows where there are more than 128 rows); every CTA takes an equal contiguous share, so ragged batches and
 // single long sequences fill the GPU alike. A (sequence, kv head, row tile)
 // that lies inside one share is finished there; one that is cut leaves
 // un-normalised partial rows with their maximum and sum, which a second
 // launch joins in order (no atomics: the same inputs give the same bits).
 //
-// CTA (two per SM, so that one's piece ends hide behind the other's tiles):
-//   warps 0-3  softmax, thread t owns row t (TMEM lane t)
-//   warp 4     MMA issue, TMEM allocation
-//   warp 5     copies of K and V tiles into a ring of slots (K and V take
+// CTA (two per SM, so that one's piece ends hide behind the other's tiles;
+// one with two query tiles, which hide behind one another):
+//   four warps a query tile   softmax, thread t owns row t (TMEM lane t);
+//              with two query tiles eight, two threads a row
+//   one warp   MMA issue, TMEM allocation
+//   one warp   copies of K and V tiles into a ring of slots (K and V take
 //              turns, so that K of the next tile arrives early)
 //   four more  8-bit caches: codes widened exactly to f16
 // S = Q K^T goes to TMEM in one buffer, which is free again as soon as the
@@ -60,11 +66,10 @@ struct TreeLayout {
   static constexpr int TT = QT == 1 ? 64 : 128;  // tokens of a tile
   static constexpr bool INPL = QT == 2;          // P over S
   static constexpr int ROWS = QT * kTreeRows;
-  // Threads of a row. With two query tiles the products of one wait for the other's
-  // softmax, whose length counts: two threads take half of a row's tokens each (tree of
-  // 47 to 96 nodes, 32 heads, 90,000 cached tokens: 127 us, one thread a row 136).
-  // With one query tile two threads a row have too few registers (211 us against 204
-  // on the FP8 batch of the launcher's comment).
+  // Threads of a row. With two query tiles a tile's products wait for its softmax,
+  // whose length counts: two threads take half of a row's tokens each (128 us
+  // on the launcher's 384 rows, one thread a row 136). With one query tile two
+  // threads a row have too few registers (211 us against 204 on its FP8 batch).
   static constexpr int HV = QT;
   static constexpr int MMA_WARP = 4 * QT * HV, COPY_WARP = MMA_WARP + 1;
   static constexpr int CONV_WARP = MMA_WARP + 2;
@@ -1253,7 +1258,8 @@ cudaError_t launch_tree_nq(TreeParams& p, cudaStream_t st) {
   constexpr int NG = kJoinThreads / Ly::ROWS;  // column groups a CTA takes side by side
   const float out_scale = KC == kTE4 ? p.v_scale : 1.f;
   // with a quarter as many segments as CTAs or more, a segment has some five
-  // pieces at most
+  // pieces at most (256 segments: narrow 85 us in all, wide 70; 8 segments of 8
+  // pieces: wide 11.7 us, narrow 10.2)
   const dim3 wide(D / 4 / 8 / NG > 0 ? D / 4 / 8 / NG : 1, static_cast<unsigned>(rts * p.num_kv_heads),
                   p.num_seqs);
   const dim3 narrow(D / 4 / NG, wide.y, wide.z);
@@ -1264,6 +1270,9 @@ cudaError_t launch_tree_nq(TreeParams& p, cudaStream_t st) {
 
 template <typename QT, int D, int KC>
 cudaError_t launch_tree(TreeParams& p, cudaStream_t st) {
+  // (188 to 384 rows a kv head, f16, 90,000 cached tokens: two query tiles 128 us,
+  // one 158; 64 to 128 rows, bf16, 70,000 tokens: two 84 us, one 70; 13 to 61
+  // rows over FP8, 75,000 tokens of 32 kv heads: two 321 us, one 193)
   return (long long)p.max_q_len * p.group > kTreeRows ? launch_tree_nq<QT, D, KC, 2>(p, st)
                                                       : launch_tree_nq<QT, D, KC, 1>(p, st);
 }
