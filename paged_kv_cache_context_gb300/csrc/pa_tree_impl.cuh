@@ -16,7 +16,8 @@
 // measured copy rate; 9 of the 70 are the join); 4 of 9001 to 32768 tokens,
 // 188 to 384 rows, f16: 128 us, 880 TFLOP/s, bound by the chain of a query
 // tile's S, softmax and P V; 16 of 1024 to 8192, FP8, 13 to 61 rows: 193 us, 3.2 TB/s,
-// bound by the tensor cores, which take as long for 13 rows as for 128.
+// bound by shared memory: a product S waits 85 clocks for its operands (32 of
+// them compute) whatever the number of rows, beside the widening's traffic.
 //
 // Work. Units are 64-token tiles of (sequence, kv head, 128-row tile) in that
 // order (128 tokens by 256 rows where there are more than 128 rows); every CTA takes an equal contiguous share, so ragged batches and
