@@ -187,7 +187,7 @@ cudaError_t launch_scores_r(const ScoresParams& p, int dtype, cudaStream_t st) {
 // and writes their positions. The bytes are few (4 per score): the bound is
 // the chain of passes over the longest row, of which the first, with the
 // loads, takes a third.
-constexpr int kSelBins = 2048;
+constexpr int kSelBins = 2048, kSelStaged = 52 * 1024;  // digits; longest row kept on chip
 
 __device__ __forceinline__ unsigned score_key(float x) {
   if (x != x) return 0u;
@@ -552,7 +552,9 @@ static cudaError_t launch_select_staged(const SelectParams& p, cudaStream_t st) 
   const auto kern = select_kernel<THREADS, true>;
   const int smem = (p.cap + 31) / 32 * 128;  // whole runs of eight groups
   if (smem > 32 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // (always the same limit: host threads may be here with rows of different lengths)
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kSelStaged * 4);
     if (e != cudaSuccess) return e;
   }
   return launch_pdl(kern, dim3(p.num_kv_heads, p.num_seqs), dim3(THREADS), smem, st, p);
@@ -564,7 +566,7 @@ cudaError_t launch_select(const SelectParams& p, cudaStream_t st) {
   // 12.0); rows whose keys do not fit an SM's shared memory beside the
   // histogram are read in every pass
   if (p.cap <= 4096) return launch_select_staged<512>(p, st);
-  if (p.cap <= 52 * 1024) return launch_select_staged<1024>(p, st);
+  if (p.cap <= kSelStaged) return launch_select_staged<1024>(p, st);
   return launch_pdl(select_kernel<1024, false>, dim3(p.num_kv_heads, p.num_seqs), dim3(1024), 0, st, p);
 }
 

@@ -87,6 +87,39 @@ def test_select_ties_past_the_registers_of_one_block():
         check_select(few, [N], B, sink, recent)
 
 
+def test_select_from_two_host_threads():
+    """Rows of different lengths, which want different amounts of shared memory, at once."""
+    import threading
+    made, failed = {}, []
+    for i, N in enumerate((9000, 50001, 30000)):
+        g = torch.Generator().manual_seed(i)
+        sc = torch.rand(1, 1, N, generator=g)
+        made[N] = (sc.cuda(), torch.tensor([N], dtype=torch.int32).cuda(),
+                   choose(sc[0, 0].tolist(), N, 500, 4, 50), torch.cuda.Stream())
+    torch.cuda.synchronize()
+
+    def work(N):
+        sc, n, want, stream = made[N]
+        try:
+            for _ in range(100):
+                keep = torch.empty(1, 1, 500, dtype=torch.int32, device="cuda")
+                new = torch.empty(1, dtype=torch.int32, device="cuda")
+                torch.cuda.current_stream().synchronize()
+                pa.evict_select(keep, new, sc, n, 4, 50, stream=stream)
+                stream.synchronize()
+                if keep[0, 0].tolist() != want:
+                    failed.append((N, "other tokens"))
+        except Exception as e:  # reported by the main thread
+            failed.append((N, repr(e)))
+
+    threads = [threading.Thread(target=work, args=(N,)) for N in made]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed[:3]
+
+
 def test_select_clamps_bad_lengths():
     pa.get_device_error()
     scores = torch.rand(2, 1, 64)
