@@ -147,6 +147,25 @@ def test_shares_of_many_tiles(kv, dtype, D, G):
         assert torch.equal(run(cache, *args, ws=ws), out)
 
 
+@pytest.mark.parametrize("kv,dtype,D", [("auto", torch.float16, 128), ("fp8_e4m3", torch.bfloat16, 128),
+                                        ("fp8_e4m3", torch.float16, 64), ("int8", torch.bfloat16, 64),
+                                        ("int8", torch.float16, 128)])
+def test_two_row_tiles_and_a_bound_above_every_draft(kv, dtype, D):
+    """320 rows a kv head (256 and 64 of them in a tile), next to sequences of one node; then
+    a max_q_len that asks for wide tiles where no draft has more than a few rows."""
+    pa.get_device_error()
+    cache = Cache([700, 41, 300], 2, D, 32, kv, dtype, seed=D)
+    for nodes, max_q in (([40, 1, 17], 40), ([3, 1, 2], 100)):
+        q, cu, mask = inputs(cache, nodes, 8, dtype, 13, words=2)
+        q = torch.cat([q] * -(-max_q // q.shape[0]))      # with rows past the last sequence
+        mask = torch.cat([mask, torch.zeros(q.shape[0] - mask.shape[0], 2, dtype=torch.int64)])
+        out = torch.full_like(q, 7.0).cuda()
+        run(cache, q.cuda(), cu.cuda(), mask.cuda(), max_q, default_scale(D), out=out)
+        assert pa.get_device_error() == 0
+        check(cache, nodes, 8, q, mask, out, default_scale(D))
+        assert out[sum(nodes):].eq(7.0).all()
+
+
 def test_a_chain_is_causal_prefill():
     cache = Cache([333, 70], 2, 128, 32, seed=5)
     nodes, G = [20, 64], 4
