@@ -100,7 +100,8 @@ struct TreeLayout {
   static constexpr int OFF_MISC = OFF_X + (HV == 2 ? QT * 2 * kTreeRows * 4 : 0);
   static constexpr int SMEM = OFF_MISC + 64;
   // TMEM columns: S of query tile q at q TT; P at 64 + b 32 (buffer b; with two
-  // query tiles over S: tokens 0-63 in its first 32 columns, 64-127 in its last); O of tile q at QT 128 + q D
+  // query tiles over S: tokens 0-63 in its first 32 columns, 64-127 in its
+  // last); O of tile q at QT 128 + q D
   static constexpr uint32_t TMEM_COLS = QT == 1 ? 256 : 512;
   static_assert(QT * (128 + D) <= (int)TMEM_COLS, "TMEM columns");
   static_assert(OFF_BAR % 16 == 0, "alignment");
@@ -234,12 +235,8 @@ __device__ __forceinline__ bool elect_one() {
                : "=r"(ok));
   return ok != 0;
 }
-// Polls without the clock first: reading it takes longer than most waits here.
-__device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity) {
-  return mbar_wait_bounded(bar, parity);
-}
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, tree_wait(bar, parity));
+  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
 }
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
@@ -749,7 +746,7 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
         if (!ok && lane == 0) raise_error(err, PA_DEVERR_TIMEOUT);
       }
     } else if (warp < Ly::MMA_WARP) {
-      // ================================================ softmax, one row per thread
+      // ================================================ softmax, a row (or half of one) per thread
       // (tcgen05.ld / st are warp-wide: every decision that leads to one is
       // taken by the whole warp)
       const int q = warp / (4 * HV);  // query tile
@@ -835,29 +832,31 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
           for (int i = 0; i < w.len; ++i, ++c) {
             const int b = static_cast<int>(c & 1);
             const int t0 = (w.tile + i) * TT;
-            // the tile's visible tokens (asked for before the wait)
+            // the tile's visible tokens (asked for before the wait; without the
+            // loop around it the compiler's order cost 4 % on an FP8 cache)
             const bool masked = t0 + TT > ctx;  // CTA-uniform
-            constexpr int TH = TT / HV;  // the thread's tokens: 32, 64 or 128
-            uint32_t seen[(TH + 63) / 64 * 2];
+            constexpr int TH = TT / HV;  // the thread's tokens: 64
+            uint32_t seen[TH / 32];
 #pragma unroll
-            for (int h = 0; h < (TH + 63) / 64; ++h) {
+            for (int h = 0; h < TH / 64; ++h) {
               unsigned long long v = ~0ull;
               if (masked)
-                v = live ? tree_seen(p.mask + (size_t)(w.q.q0 + node) * p.mask_words, p.mask_words, t0 + hf * TH + 64 * h, ctx, w.q.n) : 0ull;
+                v = live ? tree_seen(p.mask + (size_t)(w.q.q0 + node) * p.mask_words, p.mask_words,
+                                     t0 + hf * TH + 64 * h, ctx, w.q.n)
+                         : 0ull;
               seen[2 * h] = static_cast<uint32_t>(v);
               seen[2 * h + 1] = static_cast<uint32_t>(v >> 32);
             }
-            if (__any_sync(0xffffffffu, !tree_wait(&s_full[q], static_cast<uint32_t>(c & 1)))) {
+            if (!warp_wait(&s_full[q], c & 1)) {
               failed = true;
               break;
             }
             const uint32_t kv = 2 * (ct + i) + 1;  // V's slot
-            const float* sct = sc + ((ct + i) % Ly::SCT) * 2 * TT + hf * TH;  // INT8 row scales
+            const float* sct = sc + ((ct + i) % Ly::SCT) * 2 * TT + 64 * hf;  // INT8 row scales
             if constexpr (ROW_SC) {
               // they landed with K's codes, before V's slot was filled (K's may be
               // on its next phase already)
-              if (__any_sync(0xffffffffu, !tree_wait(&full[kv % NS],
-                                                             static_cast<uint32_t>((kv / NS) & 1)))) {
+              if (!warp_wait(&full[kv % NS], (kv / NS) & 1)) {
                 failed = true;
                 break;
               }
@@ -888,10 +887,7 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
                     // O holds the tiles so far: scale it by 2^(m - mn) once the
                     // last P V has landed
                     const uint32_t cp = c - 1;
-                    if (__any_sync(0xffffffffu,
-                                   !tree_wait(&pd[cp & 1],
-                                                      static_cast<uint32_t>((cp >> 1) & 1))))
-                      return false;
+                    if (!warp_wait(&pd[cp & 1], (cp >> 1) & 1)) return false;
                     tc05_fence_after();
                     __syncwarp();
                     const float al = mn == -INFINITY ? 1.f : exp2f(m - mn);
@@ -914,9 +910,7 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
                 mu = m == -INFINITY ? 0.f : m;  // nothing seen yet: weights of zero
                 // the P V before the last has read the buffer
                 return INPL || c < 2 ||
-                       !__any_sync(0xffffffffu,
-                                   !tree_wait(&pd[b],
-                                                      static_cast<uint32_t>(((c >> 1) - 1) & 1)));
+                       warp_wait(&pd[b], ((c >> 1) - 1) & 1);
               };
               const float sl2 = p.scale_log2;
               auto maxi = [&](auto& sr, int e0, uint32_t bits) {
@@ -1008,8 +1002,7 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
               // V rows past the sequence may hold anything, and zero times NaN
               // is NaN in the MMA: zero them (the first query tile's arrival
               // comes before either tile's P V is issued)
-              if (__any_sync(0xffffffffu, !tree_wait(&full[kv % NS],
-                                                             static_cast<uint32_t>((kv / NS) & 1)))) {
+              if (!warp_wait(&full[kv % NS], (kv / NS) & 1)) {
                 failed = true;
                 break;
               }
@@ -1038,8 +1031,7 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
             if (work) load_q();
           }
           const uint32_t cl = c - 1;
-          if (__any_sync(0xffffffffu,
-                         !tree_wait(&pd[cl & 1], static_cast<uint32_t>((cl >> 1) & 1)))) {
+          if (!warp_wait(&pd[cl & 1], (cl >> 1) & 1)) {
             failed = true;
             break;
           }
