@@ -35,7 +35,7 @@ struct TreeParams {
   const int32_t* context_lens;  // [S]: cached tokens, the nodes among them
   const unsigned long long* mask;  // [T][mask_words]
   float4* part_o;               // [C][2][D / 4][rows of a CTA]: cut pieces' un-normalised rows
-  float2* part_ml;              // [C][2][rows of a CTA]: their maximum (log2 units) and sum
+  float2* part_ml;              // [C][2][rows of a CTA]: their reference (log2 units) and sum
   long long* seq_units;         // [S + 1]: units of the sequences before each (written by CTA 0)
   unsigned* err;
   int num_seqs, num_heads, num_kv_heads, group, block_size, num_blocks;
