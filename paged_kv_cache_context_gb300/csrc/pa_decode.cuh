@@ -134,8 +134,13 @@ namespace pa {
 // launch (scores_kernel) combines the cut segments, so nothing is counted here,
 // and adds the softmax weights to running scores. Its running sums take the
 // weights before they are rounded for the MMAs (the scores are held in 32
-// bits and want the exact normaliser).
+// bits and want the exact normaliser). Weights that are rounded to f16 are held
+// kScoredTop = 7 above the reference of the other modes, over an INT8 cache
+// less the exponent of the slices' largest V scale: the products that the MMA
+// takes reach 2^15 at most and keep f16's precision down to 2^-21 of the largest,
+// whatever the scales' size (sum and output are in the same units).
 enum : int { kModeSplit = 0, kModeBalanced = 1, kModeScored = 2 };
+constexpr float kScoredTop = 7.f;
 
 // Which consumers a (query type, cache type, head_dim, group bucket, block
 // size) instantiation runs, asked with the C ABI's type codes so that the
@@ -739,6 +744,7 @@ __device__ __forceinline__ void process_tc(TcState<D>& st, const uint8_t* const 
   tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 1));
   tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 2));
   st.s_top = fmaxf(st.s_top, tm);
+  if constexpr (Ly::SCORED && std::is_same<QT, __half>::value) tm -= kScoredTop;
   if (__any_sync(0xffffffffu, tm > st.m_run + kLazy)) {
     const float mn = fmaxf(st.m_run, tm);
     const float al = mn == -INFINITY ? 1.f : exp2f(st.m_run - mn);
@@ -1029,6 +1035,27 @@ __device__ __forceinline__ void process_tc8(Tc8State<D>& st, const uint8_t* cons
   }
   st.s_top[0] = fmaxf(st.s_top[0], tm0);
   st.s_top[1] = fmaxf(st.s_top[1], tm1);
+  if constexpr (Ly::SCORED) {
+    float top = kScoredTop;
+    if constexpr (Ly::ROW_SCALES) {
+      // the largest V scale of the attended rows is below 2^e (the bits of numbers that
+      // are not negative are in their order; infinities and NaN are left out); held to
+      // [-60, 60], so that the sums stay inside 32 bits
+      uint32_t most = 0;
+#pragma unroll
+      for (int j = 0; j < SW; ++j)
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+          if (kr + 8 * half < lim[j]) {
+            const uint32_t b = __float_as_uint(vsc[j][r0[j] + 8 * half + kr]) & 0x7FFFFFFFu;
+            if (b < 0x7F800000u) most = max(most, b);
+          }
+      most = __reduce_max_sync(0xffffffffu, most);
+      top -= static_cast<float>(min(max(static_cast<int>(most >> 23) - 126, -60), 60));
+    }
+    tm0 -= top;
+    tm1 -= top;
+  }
   if (__any_sync(0xffffffffu, tm0 > st.m_run[0] + kLazy || tm1 > st.m_run[1] + kLazy)) {
     const float mn0 = fmaxf(st.m_run[0], tm0), mn1 = fmaxf(st.m_run[1], tm1);
     const float al0 = mn0 == -INFINITY ? 1.f : exp2f(st.m_run[0] - mn0);
