@@ -396,11 +396,15 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
 // in 47 us; 256 threads with 4: 50, with 6: 56, 128 with 6: 69 us.
 constexpr int kMoveThreads = 512, kMoveUnroll = 2, kMoveCtas = 3, kMoveChunk = 512;
 
+// The page of position t (a shift where the block size is a power of two).
+__device__ __forceinline__ int page_of(const CompactParams& p, int t) {
+  return p.block_bits >= 0 ? t >> p.block_bits : t / p.block_size;
+}
+
 // Physical row of position t, or -1 with the error raised.
 __device__ __forceinline__ long long compact_row(const CompactParams& p, const int32_t* table, int g,
                                                  int t) {
-  // (a shift where the block size is a power of two)
-  const int page = p.block_bits >= 0 ? t >> p.block_bits : t / p.block_size;
+  const int page = page_of(p, t);
   const int b = __ldg(table + page);
   if (b < 0 || b >= p.num_blocks) {
     raise_error(p.err, PA_DEVERR_BLOCK_ID);
@@ -464,7 +468,8 @@ __device__ __forceinline__ void move_rows(uint4* cache, int row_vecs, int v0, in
   }
 }
 
-// The same for arrays of one word a row (row scales, scores), four entries a thread.
+// The same for arrays of one word a row (row scales, scores), four entries a
+// thread; an entry of destination -1 is not stored either.
 template <typename Source, typename Locate>
 __device__ __forceinline__ void move_words(float* words, int kept, Source source, Locate locate) {
   for (int j0 = 0; j0 < kept; j0 += 4 * kMoveThreads) {
@@ -484,7 +489,7 @@ __device__ __forceinline__ void move_words(float* words, int kept, Source source
     __syncthreads();
 #pragma unroll
     for (int u = 0; u < 4; ++u)
-      if (w[u].x >= 0) words[w[u].y] = val[u];
+      if (w[u].x >= 0 && w[u].y >= 0) words[w[u].y] = val[u];
   }
 }
 
@@ -523,11 +528,19 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtas)
   } else if (p.k_scales && a >= -2) {
     move_words(a == -1 ? p.v_scales : p.k_scales, kept, source, locate);
   } else {
-    // scores: their row is in token order; entries past the kept ones become 0
+    // scores: their row is in token order; an entry moves only if its row does, which
+    // is so if both blocks are good (the rows' CTAs flag bad ones; here only the
+    // store waits for the table: looked up first, it took 48.7 us, so 48.0). Entries past
+    // the kept ones become 0
     float* sc = p.scores +
                 ((size_t)s * p.num_kv_heads + g) * p.max_blocks_per_seq * p.block_size;
-    move_words(sc, kept, source,
-               [&](int from, int j) -> longlong2 { return make_longlong2(from, start + j); });
+    move_words(sc, kept, source, [&](int from, int j) -> longlong2 {
+      const int to = start + j;
+      if (from < 0 || from == to) return make_longlong2(-1, -1);
+      const unsigned a = __ldg(table + page_of(p, from)), b = __ldg(table + page_of(p, to));
+      const unsigned nb = p.num_blocks;
+      return make_longlong2(from, a < nb && b < nb ? to : -1);
+    });
     __syncthreads();
     for (int j = start + kept + threadIdx.x; j < n; j += kMoveThreads) sc[j] = 0.f;
   }
