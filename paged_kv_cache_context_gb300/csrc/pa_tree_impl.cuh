@@ -1201,7 +1201,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
     }
 #pragma unroll
     for (int u = 0; u < J; ++u) {
-      if (!(h[u].y > 0.f)) continue;  // nothing seen in the piece
+      if (h[u].y == 0.f) continue;  // nothing seen in the piece (a NaN stays one)
       if (h[u].x > M) {
         const float f = exp2f(M - h[u].x);
         l *= f;
@@ -1221,7 +1221,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
       }
     }
   }
-  const float inv = (l > 0.f ? 1.f / l : 0.f) * out_scale;
+  const float inv = (l == 0.f ? 0.f : 1.f / l) * out_scale;
   const long long at =
       live ? ((long long)(q.q0 + r / p.group) * p.num_heads + g * p.group + r % p.group) * D + 4 * c4
            : -1;
