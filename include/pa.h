@@ -233,7 +233,10 @@ pa_status pa_reshape_and_cache_int8(const void* key, const void* value,
  *   K_j[d] = k_cache[blk][g][row][d] * k_scales[blk][g][row]
  * and V_j likewise (one binary32 multiply each; the kernel applies the K scale
  * to the dot product and the V scale to the softmax weight, which is the same
- * value up to fp32 rounding). k_scales / v_scales : in, fp32 [NB][Hkv][bs].
+ * value up to fp32 rounding, and on the tensor cores up to the rounding of that
+ * product to f16: it loses bits where it is below 2^-14, so V row scales (largest
+ * |V| / 127) much below 1e-3 cost accuracy, and overflows for scales past 255).
+ * k_scales / v_scales : in, fp32 [NB][Hkv][bs].
  * Supported: q_dtype BF16 or F16 (else PA_ERR_DTYPE); D, bs, G and window as
  * pa_decode. Pointers 16-byte aligned.
  */
@@ -296,7 +299,8 @@ pa_status pa_prefill(void* out, const void* query,
  * k_scales, v_scales: fp32 [NB][Hkv][bs]. On the tensor cores the codes are
  * widened exactly to f16, q is carried in f16 (exact for a bf16 query inside
  * f16's range), the K row scale multiplies the logit and the V row scale the
- * softmax weight before it is rounded to f16; fp32 accumulation. Pages are
+ * softmax weight before it is rounded to f16 (as pa_decode_int8: V row scales
+ * much below 1e-3 cost accuracy); fp32 accumulation. Pages are
  * moved by 1-D bulk copies (no limit on the cache's rows). NULL scales ->
  * PA_ERR_NULL; scales not 16-byte aligned -> PA_ERR_ALIGN.
  */
@@ -442,7 +446,8 @@ pa_status pa_decode_cascade(void* out, const void* query,
  * carried in f16 (exact for a bf16 query inside f16's range); FP8: k_scale
  * multiplies the logit scale and v_scale the output; INT8: the K row scale
  * multiplies the logit and the V row scale the weight before it is rounded
- * to f16. The sequences' own pages go through the decode of that cache kind.
+ * to f16 (as pa_prefill_int8). The sequences' own pages go through the decode
+ * of that cache kind.
  * k_scale or v_scale not finite and positive -> PA_ERR_SCALE; NULL row scales
  * -> PA_ERR_NULL, not 16-byte aligned -> PA_ERR_ALIGN.
  */
@@ -495,10 +500,12 @@ pa_status pa_copy_blocks(void* k_cache, void* v_cache, const int32_t* block_pair
  *   out[cu_q[s] + i][h][:] = sum_j softmax_j seen(scale * q . K_j) V_j,
  * kv head h / G; a zero row where nothing is seen. fp32 accumulation; the
  * weights are rounded to the input type before P.V (tensor cores), the running
- * sum takes them unrounded; output rounded to q_dtype. No window. The cached
- * rows of a sequence's n_s tokens must be finite for every node to be
- * (an unseen token's weight is zero, and zero times infinity is NaN); rows past n_s may
- * hold anything.
+ * sum takes them unrounded; output rounded to q_dtype. f16 weights keep their
+ * precision down to 2^-21 of a row's largest, smaller ones lose bits. No
+ * window. NaN in a seen K row or in the query makes a node's row NaN, in a seen
+ * V row that element of it. The V rows of a sequence's n_s tokens must be finite
+ * for every node to be, seen or not (an unseen token's weight is zero, and zero
+ * times infinity is NaN); K of unseen nodes and rows past n_s may hold anything.
  *
  * out, query   : [T][Hq][D] of q_dtype (BF16 or F16, else PA_ERR_DTYPE).
  * k_cache,
@@ -516,7 +523,11 @@ pa_status pa_copy_blocks(void* k_cache, void* v_cache, const int32_t* block_pair
  * max_q_len set PA_DEVERR_SEQ and that sequence is not written; n_s < q_len_s
  * or n_s > MB * bs sets PA_DEVERR_CONTEXT_LEN and its rows are zero; a block
  * id outside [0, NB) sets PA_DEVERR_BLOCK_ID and reads as zeros. T == 0 or
- * S == 0 is a no-op. Two launches: the attention on equal shares of the work,
+ * S == 0 is a no-op. max_q_len is a bound for the batch that also chooses how
+ * the work is cut: past 128 rows (max_q_len * G) tiles are laid out for
+ * long drafts, which costs drafts of up to 128 rows a fifth (16-bit caches) to
+ * two thirds (8-bit) more time; pass the longest draft's length where it is
+ * known. Two launches: the attention on equal shares of the work,
  * then the join of the rows that the shares cut, in a fixed order (the same
  * inputs give the same bits on the same device).
  */
@@ -534,7 +545,10 @@ pa_status pa_tree(void* out, const void* query, const void* k_cache, const void*
  * scales or an FP8 E4M3 cache with per-tensor scales. Same computation,
  * arguments and errors, with the dequantisation, the f16 operands and the
  * additional errors of pa_prefill_int8 / pa_prefill_fp8; pages are moved by
- * 1-D bulk copies (no limit on the cache's rows).
+ * 1-D bulk copies (no limit on the cache's rows). INT8: V row scales of any
+ * size from 2^-60 to 2^60 are held to the precision above, relative to the
+ * largest product of weight and scale (a power of two of the scales is carried
+ * apart from the f16 product).
  */
 pa_status pa_tree_int8(void* out, const void* query, const int8_t* k_cache,
                        const int8_t* v_cache, const float* k_scales, const float* v_scales,
@@ -560,7 +574,12 @@ pa_status pa_tree_fp8(void* out, const void* query, const uint8_t* k_cache,
  * Sources: the decode of "PagedAttention in mistral.rs", whose cache is a pool
  * of fixed size; "Rolling buffer cache" bounds a cache by age, these calls with
  * pa_evict_select and pa_compact bound it by use.
- *   out            as pa_decode / pa_decode_int8,
+ *   out            as pa_decode / pa_decode_int8 up to rounding: the weights
+ *                  that the tensor cores take are rounded as there, but they
+ *                  are divided by the sum of the unrounded ones, so out is not
+ *                  the same bits; and f16 weights keep their precision down
+ *                  to 2^-21 of a row's largest, over INT8 for V row scales of
+ *                  any size from 2^-60 to 2^60,
  *   scores[s][g][j] += sum over the G heads h of kv head g of softmax(logit_h)_j
  * for j in [0, n_s); other entries are left as they are. scores: in/out, fp32
  * [S][Hkv][MB * bs], in the sequence's own token order (not by block, so
@@ -623,6 +642,7 @@ pa_status pa_evict_select(int32_t* keep, int32_t* new_lens, const float* scores,
  * of a tree becomes the sequence's next tokens. For every sequence s, kv head g and j <
  * keep_lens[s], with a = starts ? starts[s] : 0 and n_s = context_lens[s]:
  *   row a + j of (s, g)  <-  row keep[s][keep_heads == 1 ? 0 : g][j]
+ * (one entry moves everywhere or nowhere)
  * for K, V, the row scales (k_scales, v_scales: both or neither) and the
  * scores (may be NULL), whose entries [a + keep_lens[s], n_s) become zero. The
  * result is as if every row were read before any is written. The sequence's
@@ -640,8 +660,8 @@ pa_status pa_evict_select(int32_t* keep, int32_t* new_lens, const float* scores,
  * 0 <= keep_lens[s] <= budget, a + keep_lens[s] <= n_s <= MB * bs) set
  * PA_DEVERR_CONTEXT_LEN and the sequence is left as it is; an entry keep[j]
  * outside [a + j, n_s) sets PA_DEVERR_SLOT, a block id outside [0, NB)
- * PA_DEVERR_BLOCK_ID, and that row is not moved. block_size >= 1, S and Hkv
- * <= 65535. Pointers 16-byte aligned. S == 0 is a no-op.
+ * PA_DEVERR_BLOCK_ID, and that row and its score are not moved. block_size >= 1,
+ * S and Hkv <= 65535. Pointers 16-byte aligned. S == 0 is a no-op.
  */
 pa_status pa_compact(void* k_cache, void* v_cache, float* k_scales, float* v_scales,
                      float* scores, const int32_t* block_tables, const int32_t* context_lens,

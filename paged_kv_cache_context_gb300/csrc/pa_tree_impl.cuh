@@ -6,7 +6,8 @@
 // cached tokens) sees every context token j < n - q_len and the nodes k whose
 // bit is set in its mask: out = sum_j p_j V_j with p the softmax of
 // scale q.K_j over the seen j (a zero row when there is none). It is computed
-// in one pass over the cache with a running maximum and sum in 32 bits.
+// in one pass over the cache with a running reference (see the weights' range
+// below) and sum in 32 bits.
 //
 // What bounds it. A kv head's q_len G rows share its K and V: 4 D q_len G
 // operations per 2 D elements read, so up to about 290 rows over a 16-bit cache
@@ -20,10 +21,11 @@
 // them compute) whatever the number of rows, beside the widening's traffic.
 //
 // Work. Units are 64-token tiles of (sequence, kv head, 128-row tile) in that
-// order (128 tokens by 256 rows where there are more than 128 rows); every CTA takes an equal contiguous share, so ragged batches and
+// order (128 tokens by 256 rows where there are more than 128 rows); every CTA
+// takes an equal contiguous share, so ragged batches and
 // single long sequences fill the GPU alike. A (sequence, kv head, row tile)
 // that lies inside one share is finished there; one that is cut leaves
-// un-normalised partial rows with their maximum and sum, which a second
+// un-normalised partial rows with their reference and sum, which a second
 // launch joins in order (no atomics: the same inputs give the same bits).
 //
 // CTA (two per SM, so that one's piece ends hide behind the other's tiles;
@@ -401,6 +403,7 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 // 16 or 32 columns.
 __device__ __forceinline__ void tmem_ld_n(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
 __device__ __forceinline__ void tmem_ld_n(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16(taddr, r); }
+
 template <typename QT, int D, int KC, int NQ>
 __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, KC, NQ>::CTAS)
     tree_attention_kernel(const __grid_constant__ TreeParams p) {
@@ -1143,7 +1146,8 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
 }
 
 // Joins the partial rows of cut (sequence, kv head, row tile) segments: with a
-// running maximum M over the pieces, out = sum_j 2^(m_j - M) o_j / sum_j 2^(m_j - M) l_j.
+// running maximum M of the pieces' references m_j,
+// out = sum_j 2^(m_j - M) o_j / sum_j 2^(m_j - M) l_j.
 // CTA (slice of columns, (kv head, row tile), sequence); a thread takes NC
 // neighbouring groups of four columns of one row, rows fastest, as the
 // partials are stored. NC 8 where there are many segments (few, wide loads);
@@ -1300,13 +1304,16 @@ cudaError_t launch_tree_nq(TreeParams& p, cudaStream_t st) {
 template <typename QT, int D, int KC>
 cudaError_t launch_tree(TreeParams& p, cudaStream_t st) {
   // (188 to 384 rows a kv head, f16, 90,000 cached tokens: two query tiles 128 us,
-  // one 158; 64 to 128 rows, bf16, 70,000 tokens: two 84 us, one 70; 13 to 61
-  // rows over FP8, 75,000 tokens of 32 kv heads: two 321 us, one 193)
+  // one 158; 64 to 128 rows, bf16, 70,000 tokens: two 84 us, one 70. 75,000 tokens of
+  // 32 kv heads over FP8, 13 to 61 rows: two 321 us, one 193; 52 to 244 rows: two
+  // 377, one 294, and over INT8 538 and 451: there the rule is not yet the faster
+  // side, since the 8-bit kernels of two tiles spill at 80 registers a thread and
+  // widen for both tiles with 128 threads)
   return (long long)p.max_q_len * p.group > kTreeRows ? launch_tree_nq<QT, D, KC, 2>(p, st)
                                                       : launch_tree_nq<QT, D, KC, 1>(p, st);
 }
 
-// kind: the cache's, as launch_tree_attention.
+// kind: the cache's (0 the query's type, 1 INT8, 2 FP8 E4M3).
 template <typename QT>
 cudaError_t launch_tree_kind(TreeParams& p, int D, int kind, cudaStream_t st) {
   switch ((D == 64 ? 0 : 3) + kind) {

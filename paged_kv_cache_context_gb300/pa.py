@@ -636,7 +636,9 @@ def tree_attention(out: torch.Tensor, query: torch.Tensor, k_cache: torch.Tensor
                    max_q_len: int, scale: float, workspace: torch.Tensor, stream=None):
     """pa_tree: attention of drafted nodes query [T, Hq, D] (offsets cu_q [S + 1],
     the last tokens of each sequence's context) to the context and to the nodes
-    that tree_mask [T, W] (int64 words, see tree_mask_from_parents) names."""
+    that tree_mask [T, W] (int64 words, see tree_mask_from_parents) names. max_q_len:
+    the longest draft; a bound above it is allowed, but past 128 / (Hq / Hkv) nodes it
+    chooses tiles that short drafts pay for."""
     *ptrs, ws = _pointers(stream, _TREE, out, query, k_cache, v_cache, block_tables, cu_q,
                           context_lens, tree_mask, workspace)
     sizes = _check_tree_args(out, query, k_cache, v_cache, block_tables, cu_q, context_lens,
@@ -714,8 +716,9 @@ def decode_scored(out: torch.Tensor, scores: torch.Tensor, query: torch.Tensor,
                   context_lens: torch.Tensor, num_kv_heads: int, scale: float,
                   workspace: torch.Tensor, kv_dtype: str = "auto", k_scale: float = 1.0,
                   v_scale: float = 1.0, stream=None):
-    """pa_decode_scored: decode, and scores [S, Hkv, MB * bs] += every token's
-    softmax weight summed over its kv head's query heads."""
+    """pa_decode_scored: decode (up to rounding: the sum takes unrounded weights), and
+    scores [S, Hkv, MB * bs] += every token's softmax weight summed over its kv head's
+    query heads."""
     *ptrs, ws = _pointers(stream, "out scores query k_cache v_cache block_tables context_lens "
                           "workspace", out, scores, query, k_cache, v_cache, block_tables,
                           context_lens, workspace)
