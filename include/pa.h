@@ -39,7 +39,9 @@
  *    (block, kv head) is bs*D contiguous elements ("head-major pages").
  *    Element type: the input dtype for PA_KV_AUTO, one byte (E4M3) for
  *    PA_KV_FP8_E4M3, one signed byte for PA_KV_INT8 (whose calls take, beside
- *    each cache, fp32 row scales [NB][Hkv][bs]: one per token and kv head).
+ *    each cache, fp32 row scales [NB][Hkv][bs]: one per token and kv head), one
+ *    byte (E4M3) for PA_KV_FP8_BLOCK (whose calls, the _fp8_block ones, take beside
+ *    each cache fp32 scales [NB][Hkv]: one per page).
  */
 #ifndef PA_H
 #define PA_H
@@ -75,7 +77,12 @@ typedef enum {
 typedef enum { PA_F32 = 0, PA_BF16 = 1, PA_F16 = 2 } pa_dtype;
 
 /* Cache storage type ("auto" and "f8e4m3" of "KV Cache Quantization"). */
-typedef enum { PA_KV_AUTO = 0, PA_KV_FP8_E4M3 = 1, PA_KV_INT8 = 2 } pa_kv_dtype;
+typedef enum {
+    PA_KV_AUTO = 0,
+    PA_KV_FP8_E4M3 = 1,
+    PA_KV_INT8 = 2,
+    PA_KV_FP8_BLOCK = 3
+} pa_kv_dtype;
 
 /* Bits of the per-device error word (see pa_get_device_error). */
 enum {
@@ -671,6 +678,138 @@ pa_status pa_compact(void* k_cache, void* v_cache, float* k_scales, float* v_sca
                      pa_stream_t stream);
 
 /*
+ * pa_norm_rope -- the norm of every query and key head and the rotation by its
+ * token's position, in one pass.
+ *
+ * Source: "PagedAttention in mistral.rs" (the models whose queries and keys the
+ * cache serves turn them by position before they are cached; vision models are in
+ * the feature list: positions with several axes). For a head x of D elements:
+ *   y = x * weight / sqrt(mean(x^2) + eps)       (y = x where the weight is NULL)
+ *   theta_i = 2 pi frac(sum_a positions[a][t] * turns[a][i] / 2^64), i < R / 2
+ *   (u, v) = (y_i, y_{i + R/2}), interleaved: (y_{2i}, y_{2i+1})
+ *   (u, v) <- (u cos theta_i - v sin theta_i, v cos theta_i + u sin theta_i)
+ * and elements from R on are y. Everything is computed in binary32 and rounded
+ * once. The sum is taken modulo 2^64, so angles are exact to 2^-31 of a turn for
+ * every position (negative ones too).
+ *
+ * query, key   : in, [T][Hq][D] and [T][Hkv][D] of dtype, heads dense, tokens
+ *                q_stride / k_stride elements apart (>= Hq D / Hkv D: views of one
+ *                projection's output will do).
+ * q_out, k_out : out, likewise with their own strides. Each may be its input (the same
+ *                pointer and stride); they may not overlap otherwise.
+ * q_weight,
+ * k_weight     : fp32 [D], or NULL.
+ * turns        : 64-bit [A][R / 2], the fraction of a turn that pair i makes per
+ *                position of axis a, in units of 2^-64 (a frequency of f radians:
+ *                round(f / (2 pi) 2^64) modulo 2^64; 0 where the axis does not turn
+ *                the pair). NULL where R == 0.
+ * positions    : int32 [A][T].
+ * Supported: D a multiple of 16 from 16 to 256 (else PA_ERR_HEAD_DIM); R a multiple
+ * of 16 from 0 to D, A 1..8, strides that are multiples of 16 bytes and not below a
+ * token's heads, eps finite and >= 0 (else PA_ERR_SHAPE); any group size.
+ * Pointers 16-byte aligned (turns 8, positions 4: PA_ERR_ALIGN). T == 0 is a no-op.
+ */
+pa_status pa_norm_rope(void* q_out, void* k_out, const void* query, const void* key,
+                       const float* q_weight, const float* k_weight, const uint64_t* turns,
+                       const int32_t* positions, int num_tokens, int num_heads,
+                       int num_kv_heads, int head_dim, int rot_dim, int num_axes,
+                       int64_t q_out_stride, int64_t k_out_stride, int64_t q_stride,
+                       int64_t k_stride, float eps, int interleaved, pa_dtype dtype,
+                       pa_stream_t stream);
+
+/*
+ * pa_norm_rope_and_cache -- pa_norm_rope whose keys go, with the values, straight
+ * to their cache slots: bit for bit what pa_norm_rope followed by
+ * pa_reshape_and_cache leaves in q_out and the caches, without the keys' way through
+ * memory.
+ *
+ * Source: "Optimization plans" (reshape_and_cache) after the rotation of
+ * pa_norm_rope. value: in, [T][Hkv][D] of dtype, tokens v_stride elements apart. Caches,
+ * slot_mapping, kv_dtype (AUTO or FP8_E4M3, else PA_ERR_DTYPE), k_scale, v_scale
+ * and their errors as pa_reshape_and_cache (block_size 1..1024); other arguments and
+ * errors as pa_norm_rope. A token whose slot is negative has its query turned and
+ * nothing cached. q_out may be query.
+ */
+pa_status pa_norm_rope_and_cache(void* q_out, const void* query, const void* key,
+                                 const void* value, void* k_cache, void* v_cache,
+                                 const int64_t* slot_mapping, const float* q_weight,
+                                 const float* k_weight, const uint64_t* turns,
+                                 const int32_t* positions, int num_tokens, int num_heads,
+                                 int num_kv_heads, int head_dim, int rot_dim, int num_axes,
+                                 int block_size, int num_blocks, int64_t q_out_stride,
+                                 int64_t q_stride, int64_t k_stride, int64_t v_stride, float eps,
+                                 int interleaved, pa_dtype dtype, pa_kv_dtype kv_dtype,
+                                 float k_scale, float v_scale, pa_stream_t stream);
+
+/*
+ * pa_append_fp8_block -- write the K/V of new tokens to an FP8 E4M3 cache with
+ * one scale per (block, kv head) for K and one for V.
+ *
+ * Sources: "KV Cache Quantization" (the F8E4M3 cache), with the scales between its one
+ * per tensor and the one per token and head of "libmir-metal trace/kv.rs": an outlier costs
+ * one page its range, and a scale costs 4 bytes a page. Because a scale belongs to
+ * all rows of a page, tokens come by sequence as in pa_prefill, not by slot: tokens
+ * [cu_q[s], cu_q[s+1]) are the last q_len_s of sequence s's n_s = context_lens[s], and
+ * are written to their positions. For each page that gets rows, K and V apart:
+ *   A = the largest finite |x| of the new rows,
+ *   p = the smallest power of two >= 2^-126 with A <= 448 p (0 where A is 0),
+ *   scale = p where the page's first row is among the new ones, else max(scale, p)
+ *   new rows: code = E4M3(x / scale) (0 over 0 is 0), round to nearest even, +-inf
+ *     and finite overflow to +-448, NaN to a NaN code;
+ *   where an old scale grew, the rows that the page had: code = E4M3(code old / scale)
+ * (exact but for codes below 2^-6; 2^-9 scale at most in all, however often it grows).
+ * Only the scale, the rows before the new ones (of a page whose scale grew) and the new
+ * rows are written; rows at or past n_s stay.
+ *
+ * key, value   : in, [T][Hkv][D] of in_dtype, heads dense, tokens key_stride /
+ *                value_stride elements apart (>= Hkv D).
+ * k_cache,
+ * v_cache      : in/out, E4M3 bytes [NB][Hkv][bs][D].
+ * k_scales,
+ * v_scales     : in/out, fp32 [NB][Hkv]; what a page's scale held before its first row is
+ *                written does not matter.
+ * block_tables : int32 [S][MB].  cu_q : int32 [S + 1].  context_lens : int32 [S].
+ * Precondition: the blocks written belong to one sequence only (pa_copy_blocks first where
+ * the last block is shared; its scales are copied by the caller).
+ * Supported: D 64, 96 or 128 (PA_ERR_HEAD_DIM); bs 16, 32 or 64 (PA_ERR_BLOCK_SIZE); strides
+ * that are multiples of 16 bytes (PA_ERR_SHAPE). Device-side checks: offsets that do not fit
+ * [0, T] set PA_DEVERR_SEQ, n_s < q_len_s or n_s > MB * bs PA_DEVERR_CONTEXT_LEN, and nothing
+ * of that sequence is written; a block id outside [0, NB) sets PA_DEVERR_BLOCK_ID and
+ * that page is not written. Pointers 16-byte aligned (scales 4). T == 0 or S == 0 is a
+ * no-op. The same inputs give the same bits.
+ */
+pa_status pa_append_fp8_block(const void* key, const void* value, uint8_t* k_cache,
+                              uint8_t* v_cache, float* k_scales, float* v_scales,
+                              const int32_t* block_tables, const int32_t* cu_q,
+                              const int32_t* context_lens, int num_tokens, int num_seqs,
+                              int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                              int max_blocks_per_seq, int64_t key_stride, int64_t value_stride,
+                              pa_dtype in_dtype, pa_stream_t stream);
+
+/*
+ * pa_decode_fp8_block -- pa_decode (window 0) over the cache of pa_append_fp8_block.
+ *
+ * Source: "PagedAttention in mistral.rs", "KV Cache Quantization". Same computation,
+ * arguments, errors and device-side checks as pa_decode, with
+ *   K_j[d] = e4m3(k_cache[blk][g][row][d]) * k_scales[blk][g]
+ * and V_j likewise. The K scale multiplies the fp32 logit; the V scale the weight, which
+ * is then rounded to f16 and keeps its precision down to 2^-21 of the row's largest
+ * product for V scales from 2^-60 to 2^60; the running sum takes the weights
+ * unrounded; q is carried in f16 (exact for a bf16 query inside f16's range).
+ * Supported: q_dtype BF16 or F16 (else PA_ERR_DTYPE). workspace: at least
+ * pa_decode_workspace_size() bytes (PA_ERR_NULL / PA_ERR_WORKSPACE), 16-byte aligned;
+ * contents on entry do not matter; calls that may overlap on the GPU need one each.
+ * Scales 4-byte aligned. Head_dim 128: NB * Hkv * bs <= 2^31 - 1 (PA_ERR_SHAPE).
+ */
+pa_status pa_decode_fp8_block(void* out, const void* query, const uint8_t* k_cache,
+                              const uint8_t* v_cache, const float* k_scales,
+                              const float* v_scales, const int32_t* block_tables,
+                              const int32_t* context_lens, int num_seqs, int num_heads,
+                              int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                              int max_blocks_per_seq, float scale, pa_dtype q_dtype,
+                              void* workspace, size_t workspace_bytes, pa_stream_t stream);
+
+/*
  * pa_decode_partials -- the split phase of pa_decode with an explicit plan.
  *
  * For split i of (s, h) (slots [i*P*bs, (i+1)*P*bs) intersected with
@@ -761,7 +900,8 @@ pa_status pa_decode_static_scratch(void* out, const void* query,
  * layer:  block_bytes = num_layers * 2 * num_kv_heads * block_size * row_bytes,
  *         row_bytes = head_dim * element size (4 for F32, 2 for BF16/F16, 1
  *                     for an FP8 E4M3 or INT8 cache), plus 4 for the fp32
- *                     row scale of an INT8 cache.
+ *                     row scale of an INT8 cache (a block-scaled FP8 cache: 4
+ *                     per block and head instead, for K and for V).
  *   PA_BUDGET_MB:       amount = MB (2^20 bytes) for the cache;
  *                       blocks = floor(amount * 2^20 / block_bytes).
  *   PA_BUDGET_FRACTION: amount in (0, 1] of available_bytes (the caller's

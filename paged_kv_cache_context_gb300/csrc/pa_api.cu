@@ -11,10 +11,12 @@
 #include <cmath>
 #include <mutex>
 
+#include "pa_append.cuh"
 #include "pa_cascade.cuh"
 #include "pa_decode.cuh"
 #include "pa_device.cuh"
 #include "pa_evict.cuh"
+#include "pa_rope.cuh"
 #include "pa_tree.cuh"
 
 #define PA_API extern "C" __attribute__((visibility("default")))
@@ -508,6 +510,9 @@ static cudaError_t run_decode(const DecodeParams& prm_in, const DecodeShape& a, 
       default: return pa_dispatch_decode_f16_f16(prm, grid, a.D, GT, a.bs, mode, ctas, st);
     }
   }
+  if (a.kv_dtype == PA_KV_FP8_BLOCK)
+    return a.q_dtype == PA_BF16 ? pa_dispatch_block_bf16(prm, grid, a.D, GT, a.bs, st)
+                                : pa_dispatch_block_f16(prm, grid, a.D, GT, a.bs, st);
   if (a.kv_dtype == PA_KV_INT8) {
     return a.q_dtype == PA_BF16
                ? pa_dispatch_decode_bf16_i8(prm, grid, a.D, GT, a.bs, mode, ctas, st)
@@ -1627,6 +1632,227 @@ PA_API pa_status pa_copy_blocks(void* k_cache, void* v_cache, const int32_t* blo
              : PA_ERR_CUDA;
 }
 
+// ================================================================ norms and rotation
+static bool aligned_to(const void* p, uintptr_t bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
+}
+// A token stride that the vector accesses can take: whole 16-byte steps, a token's heads or more.
+static bool token_stride_ok(int64_t stride, int64_t heads, int D, int dtype) {
+  return stride >= heads * D && stride <= (INT64_MAX >> 36) &&
+         stride * dtype_bytes(dtype) % 16 == 0;
+}
+
+// The checks that both entry points share; what is stored where has been filled in.
+static pa_status rope_impl(RopeParams& p, int store, int dtype, cudaStream_t st) {
+  if (!valid_dtype(dtype)) return PA_ERR_DTYPE;
+  if (p.heads <= 0 || p.kv_heads <= 0 || p.heads > 65535 || p.kv_heads > 65535)
+    return PA_ERR_SHAPE;
+  if (p.head_dim < 16 || p.head_dim > 256 || p.head_dim % 16 != 0) return PA_ERR_HEAD_DIM;
+  if (p.rot_dim < 0 || p.rot_dim > p.head_dim || p.rot_dim % 16 != 0 || p.axes < 1 ||
+      p.axes > 8 || !(p.eps >= 0.f) || !isfinite(p.eps))
+    return PA_ERR_SHAPE;
+  if (!p.turns && p.rot_dim > 0) return PA_ERR_NULL;
+  if (!token_stride_ok(p.q_stride, p.heads, p.head_dim, dtype) ||
+      !token_stride_ok(p.k_stride, p.kv_heads, p.head_dim, dtype) ||
+      !token_stride_ok(p.q_out_stride, p.heads, p.head_dim, dtype) ||
+      (store == kRopeRows && !token_stride_ok(p.k_out_stride, p.kv_heads, p.head_dim, dtype)) ||
+      (store != kRopeRows && !token_stride_ok(p.v_stride, p.kv_heads, p.head_dim, dtype)))
+    return PA_ERR_SHAPE;
+  if (!aligned16(p.q) || !aligned16(p.k) || !aligned16(p.v) || !aligned16(p.q_out) ||
+      !aligned16(p.k_out) || !aligned16(p.k_cache) || !aligned16(p.v_cache) ||
+      !aligned16(p.q_weight) || !aligned16(p.k_weight) || !aligned_to(p.turns, 8) ||
+      !aligned_to(p.positions, 4) || !aligned_to(p.slots, 8))
+    return PA_ERR_ALIGN;
+  p.err = error_word();
+  const cudaError_t e = dtype == PA_F32    ? launch_rope_f32(p, store, st)
+                        : dtype == PA_BF16 ? launch_rope_bf16(p, store, st)
+                                           : launch_rope_f16(p, store, st);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+PA_API pa_status pa_norm_rope(void* q_out, void* k_out, const void* query, const void* key,
+                              const float* q_weight, const float* k_weight,
+                              const uint64_t* turns, const int32_t* positions, int num_tokens,
+                              int num_heads, int num_kv_heads, int head_dim, int rot_dim,
+                              int num_axes, int64_t q_out_stride, int64_t k_out_stride,
+                              int64_t q_stride, int64_t k_stride, float eps, int interleaved,
+                              pa_dtype dtype, pa_stream_t stream) {
+  if (num_tokens < 0) return PA_ERR_SHAPE;
+  if (num_tokens == 0) return PA_OK;
+  if (!q_out || !k_out || !query || !key || !positions) return PA_ERR_NULL;
+  RopeParams p{};
+  p.q = query;
+  p.k = key;
+  p.q_out = q_out;
+  p.k_out = k_out;
+  p.q_weight = q_weight;
+  p.k_weight = k_weight;
+  p.turns = turns;
+  p.positions = positions;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.q_out_stride = q_out_stride;
+  p.k_out_stride = k_out_stride;
+  p.tokens = num_tokens;
+  p.heads = num_heads;
+  p.kv_heads = num_kv_heads;
+  p.head_dim = head_dim;
+  p.rot_dim = rot_dim;
+  p.axes = num_axes;
+  p.block_size = 1;
+  p.interleaved = interleaved != 0;
+  p.eps = eps;
+  return rope_impl(p, kRopeRows, dtype, reinterpret_cast<cudaStream_t>(stream));
+}
+
+PA_API pa_status pa_norm_rope_and_cache(
+    void* q_out, const void* query, const void* key, const void* value, void* k_cache,
+    void* v_cache, const int64_t* slot_mapping, const float* q_weight, const float* k_weight,
+    const uint64_t* turns, const int32_t* positions, int num_tokens, int num_heads,
+    int num_kv_heads, int head_dim, int rot_dim, int num_axes, int block_size, int num_blocks,
+    int64_t q_out_stride, int64_t q_stride, int64_t k_stride, int64_t v_stride, float eps,
+    int interleaved, pa_dtype dtype, pa_kv_dtype kv_dtype, float k_scale, float v_scale,
+    pa_stream_t stream) {
+  if (num_tokens < 0) return PA_ERR_SHAPE;
+  if (num_tokens == 0) return PA_OK;
+  if (!q_out || !query || !key || !value || !k_cache || !v_cache || !slot_mapping || !positions)
+    return PA_ERR_NULL;
+  if (kv_dtype != PA_KV_AUTO && kv_dtype != PA_KV_FP8_E4M3) return PA_ERR_DTYPE;
+  if (num_blocks <= 0) return PA_ERR_SHAPE;
+  if (block_size <= 0 || block_size > 1024) return PA_ERR_BLOCK_SIZE;
+  if (kv_dtype == PA_KV_FP8_E4M3 &&
+      !(isfinite(k_scale) && k_scale > 0.f && isfinite(v_scale) && v_scale > 0.f))
+    return PA_ERR_SCALE;
+  RopeParams p{};
+  p.q = query;
+  p.k = key;
+  p.v = value;
+  p.q_out = q_out;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.slots = slot_mapping;
+  p.q_weight = q_weight;
+  p.k_weight = k_weight;
+  p.turns = turns;
+  p.positions = positions;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.q_out_stride = q_out_stride;
+  p.capacity = (int64_t)num_blocks * block_size;
+  p.tokens = num_tokens;
+  p.heads = num_heads;
+  p.kv_heads = num_kv_heads;
+  p.head_dim = head_dim;
+  p.rot_dim = rot_dim;
+  p.axes = num_axes;
+  p.block_size = block_size;
+  p.interleaved = interleaved != 0;
+  p.eps = eps;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  return rope_impl(p, kv_dtype == PA_KV_AUTO ? kRopeCache : kRopeFp8, dtype,
+                   reinterpret_cast<cudaStream_t>(stream));
+}
+
+// ================================================================ block-scaled FP8 cache
+PA_API pa_status pa_append_fp8_block(const void* key, const void* value, uint8_t* k_cache,
+                                     uint8_t* v_cache, float* k_scales, float* v_scales,
+                                     const int32_t* block_tables, const int32_t* cu_q,
+                                     const int32_t* context_lens, int num_tokens, int num_seqs,
+                                     int num_kv_heads, int head_dim, int block_size,
+                                     int num_blocks, int max_blocks_per_seq, int64_t key_stride,
+                                     int64_t value_stride, pa_dtype in_dtype,
+                                     pa_stream_t stream) {
+  if (num_tokens < 0 || num_seqs < 0 || num_seqs > 65535) return PA_ERR_SHAPE;
+  if (num_tokens == 0 || num_seqs == 0) return PA_OK;
+  if (!key || !value || !k_cache || !v_cache || !k_scales || !v_scales || !block_tables ||
+      !cu_q || !context_lens)
+    return PA_ERR_NULL;
+  if (!valid_dtype(in_dtype)) return PA_ERR_DTYPE;
+  if (num_kv_heads <= 0 || num_kv_heads > 65535 || num_blocks <= 0 || max_blocks_per_seq <= 0)
+    return PA_ERR_SHAPE;
+  if (head_dim != 64 && head_dim != 96 && head_dim != 128) return PA_ERR_HEAD_DIM;
+  if (block_size != 16 && block_size != 32 && block_size != 64) return PA_ERR_BLOCK_SIZE;
+  if ((int64_t)max_blocks_per_seq * block_size > INT32_MAX) return PA_ERR_SHAPE;
+  if (!token_stride_ok(key_stride, num_kv_heads, head_dim, in_dtype) ||
+      !token_stride_ok(value_stride, num_kv_heads, head_dim, in_dtype))
+    return PA_ERR_SHAPE;
+  // a CTA per page (as many as the tokens can touch), kv head and K or V
+  const int64_t pages = (int64_t)num_tokens < num_tokens / block_size + 2ll * num_seqs
+                            ? num_tokens
+                            : num_tokens / block_size + 2ll * num_seqs;
+  if (pages * 2 * num_kv_heads > INT32_MAX) return PA_ERR_SHAPE;
+  if (!aligned16(key) || !aligned16(value) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      !aligned_to(k_scales, 4) || !aligned_to(v_scales, 4))
+    return PA_ERR_ALIGN;
+  AppendParams p{};
+  p.key = key;
+  p.value = value;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.k_scales = k_scales;
+  p.v_scales = v_scales;
+  p.block_tables = block_tables;
+  p.cu_q = cu_q;
+  p.context_lens = context_lens;
+  p.key_stride = key_stride;
+  p.value_stride = value_stride;
+  p.err = error_word();
+  p.tokens = num_tokens;
+  p.num_seqs = num_seqs;
+  p.kv_heads = num_kv_heads;
+  p.block_size = block_size;
+  p.num_blocks = num_blocks;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.items = static_cast<int>(pages);
+  return launch_append(p, in_dtype, head_dim, reinterpret_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+PA_API pa_status pa_decode_fp8_block(void* out, const void* query, const uint8_t* k_cache,
+                                     const uint8_t* v_cache, const float* k_scales,
+                                     const float* v_scales, const int32_t* block_tables,
+                                     const int32_t* context_lens, int num_seqs, int num_heads,
+                                     int num_kv_heads, int head_dim, int block_size,
+                                     int num_blocks, int max_blocks_per_seq, float scale,
+                                     pa_dtype q_dtype, void* workspace, size_t workspace_bytes,
+                                     pa_stream_t stream) {
+  // the shared checks, on the shape with a native cache
+  DecodeShape a{num_seqs, num_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                max_blocks_per_seq, 0, q_dtype, PA_KV_AUTO, 1.f, 1.f};
+  pa_status rc = check_decode(a, out, query, k_cache, v_cache, block_tables, context_lens);
+  if (rc != PA_OK || num_seqs == 0) return rc;
+  if (q_dtype != PA_BF16 && q_dtype != PA_F16) return PA_ERR_DTYPE;
+  if (!k_scales || !v_scales || !workspace) return PA_ERR_NULL;
+  a.kv_dtype = PA_KV_FP8_BLOCK;
+  if (decode_is_tma_staged(a) && (long long)num_blocks * num_kv_heads * block_size > kMaxTcRows)
+    return PA_ERR_SHAPE;
+  const int GT = group_bucket(num_heads / num_kv_heads);
+  if (workspace_bytes < balanced_bytes(GT, head_dim)) return PA_ERR_WORKSPACE;
+  if (!aligned16(workspace) || !aligned_to(k_scales, 4) || !aligned_to(v_scales, 4))
+    return PA_ERR_ALIGN;
+  DecodeParams p = make_params(a, query, k_cache, v_cache, block_tables, context_lens, scale,
+                               error_word());
+  p.k_scales = k_scales;
+  p.v_scales = v_scales;
+  p.out = out;
+  rc = pa_decode_workspace_clear(workspace, workspace_bytes, stream);
+  if (rc != PA_OK) return rc;
+  const BalancedWs w = balanced_carve(workspace, GT, head_dim);
+  p.piece_o = w.piece_o;
+  p.piece_ml = w.piece_ml;
+  p.arrived = w.arrived;
+  p.num_splits = 1;
+  p.pages_per_split = 1;
+  return run_decode(p, a, dim3(0, 1, 1), kModeBalanced, nullptr,
+                    reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
 // ================================================================ pool sizing
 PA_API int64_t pa_block_budget(pa_budget_kind kind, double amount, size_t available_bytes,
                                int num_layers, int num_kv_heads, int head_dim, int block_size,
@@ -1634,13 +1860,16 @@ PA_API int64_t pa_block_budget(pa_budget_kind kind, double amount, size_t availa
   if (num_layers <= 0 || num_kv_heads <= 0 || block_size <= 0) return PA_ERR_SHAPE;
   if (head_dim <= 0) return PA_ERR_HEAD_DIM;
   if (!valid_dtype(dtype) ||
-      (kv_dtype != PA_KV_AUTO && kv_dtype != PA_KV_FP8_E4M3 && kv_dtype != PA_KV_INT8))
+      (kv_dtype != PA_KV_AUTO && kv_dtype != PA_KV_FP8_E4M3 && kv_dtype != PA_KV_INT8 &&
+       kv_dtype != PA_KV_FP8_BLOCK))
     return PA_ERR_DTYPE;
   if (!(amount >= 0.0) || !isfinite(amount)) return PA_ERR_SHAPE;
   const int64_t elem = kv_dtype != PA_KV_AUTO ? 1 : (dtype == PA_F32 ? 4 : 2);
   // bytes of one cached row: its elements, plus its fp32 scale for INT8
   const double row_bytes = (double)head_dim * elem + (kv_dtype == PA_KV_INT8 ? 4.0 : 0.0);
-  const double block_bytes = (double)num_layers * 2.0 * num_kv_heads * block_size * row_bytes;
+  const double page_scale = kv_dtype == PA_KV_FP8_BLOCK ? 4.0 : 0.0;
+  const double block_bytes =
+      (double)num_layers * 2.0 * num_kv_heads * (block_size * row_bytes + page_scale);
   double blocks = 0.0;
   switch (kind) {
     case PA_BUDGET_MB:

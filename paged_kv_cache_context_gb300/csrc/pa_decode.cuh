@@ -160,8 +160,8 @@ constexpr bool tc16_eligible(int q_dtype, int kv_dtype, int D, int GT, int BS) {
 }
 constexpr bool tc8_eligible(int q_dtype, int kv_dtype, int D, int GT, int BS) {
   return PA_DECODE_TC8 != 0 && (q_dtype == PA_BF16 || q_dtype == PA_F16) &&
-         (kv_dtype == PA_KV_FP8_E4M3 || kv_dtype == PA_KV_INT8) && D % 32 == 0 && D <= 128 &&
-         GT <= 8 && BS >= 16 && BS <= 64 && BS % 16 == 0;
+         (kv_dtype == PA_KV_FP8_E4M3 || kv_dtype == PA_KV_INT8 || kv_dtype == PA_KV_FP8_BLOCK) &&
+         D % 32 == 0 && D <= 128 && GT <= 8 && BS >= 16 && BS <= 64 && BS % 16 == 0;
 }
 constexpr bool tma_staged(int q_dtype, int kv_dtype, int D, int GT, int BS) {
   return tc16_eligible(q_dtype, kv_dtype, D, GT, BS) ||
@@ -190,6 +190,10 @@ struct KvCode<E4M3> {
 template <>
 struct KvCode<I8> {
   static constexpr int value = PA_KV_INT8;
+};
+template <>
+struct KvCode<E4M3B> {
+  static constexpr int value = PA_KV_FP8_BLOCK;
 };
 template <typename QT, typename CT, int D, int GT, int BS>
 constexpr bool uses_tc() {
@@ -240,8 +244,8 @@ struct DecodeParams {
   const void* query;    // [S][Hq][D] of QT
   const uint8_t* k_cache;
   const uint8_t* v_cache;
-  const float* k_scales;        // INT8 cache: one scale per cached row, [NB][Hkv][bs]
-  const float* v_scales;
+  const float* k_scales;        // INT8 cache: one scale per cached row, [NB][Hkv][bs];
+  const float* v_scales;        // block-scaled FP8 cache: one per page, [NB][Hkv]
   const int32_t* block_tables;  // [S][MB]
   const int32_t* context_lens;  // [S]
   unsigned* err;
@@ -332,6 +336,10 @@ struct Layout {
   // an INT8 cache stages its pages' row scales too (BS floats each for K and V)
   static constexpr bool ROW_SCALES = std::is_same<CT, I8>::value;
   static constexpr int SCB = ROW_SCALES ? BS * 4 : 0;
+  // a block-scaled FP8 cache's stages have a K and a V scale each, beside the descriptors
+  static constexpr bool PAGE_SCALES = std::is_same<CT, E4M3B>::value;
+  // weights that meet a V scale before they are rounded, held at the top of f16's range
+  static constexpr bool TOPPED = SCORED || PAGE_SCALES;
   static constexpr int OFF_Q = 2 * PAGE + 2 * SCB;
   // K page | V page | (K row scales | V row scales) | q rows; the swizzled
   // boxes of the tensor-core layout start on 1024-byte boundaries
@@ -352,7 +360,8 @@ struct Layout {
   // dynamic shared memory layout
   static constexpr int OFF_BAR = STAGES * STAGE;
   static constexpr int OFF_DESC = round_up(OFF_BAR + (2 * STAGES + 1) * 8, 16);
-  static constexpr int OFF_SCR = round_up(OFF_DESC + STAGES * 16, 16);
+  static constexpr int OFF_PSC = OFF_DESC + STAGES * 16;
+  static constexpr int OFF_SCR = round_up(OFF_PSC + (PAGE_SCALES ? STAGES * 8 : 0), 16);
   static constexpr int OFF_MSTAT = OFF_SCR + NC * SCR * 4;  // [3][NC][GT]
   static constexpr int OFF_MACC = round_up(OFF_MSTAT + 3 * NC * GT * 4, 16);
   static constexpr int OFF_MISC = OFF_MACC + (MERGE_IN_STAGE ? 0 : MACC);
@@ -882,7 +891,7 @@ __device__ __forceinline__ void begin_piece_tc8(Tc8State<D>& st, const uint8_t* 
 // S^T = K Q^T over the slice of rows [r0, r0 + 16) of a staged K page: the
 // log2-unit logits of heads 2t (x[0], x[2]) and 2t + 1 (x[1], x[3]) for rows
 // r0 + kr (x[0], x[1]) and r0 + 8 + kr (x[2], x[3]); rows at or past r0 + lim
-// are masked. ks: the page's K row scales (INT8), else unused.
+// are masked. ks: the page's K row scales (INT8) or K scale (block-scaled FP8), else unused.
 template <typename Ly, typename CT, int D>
 __device__ __forceinline__ void tc8_logits(const Tc8State<D>& st, const uint8_t* kpage,
                                            const float* ks, int r0, int kr, int t, int lim,
@@ -919,6 +928,9 @@ __device__ __forceinline__ void tc8_logits(const Tc8State<D>& st, const uint8_t*
   if constexpr (Ly::ROW_SCALES) {
     sa *= ks[ra];
     sb *= ks[rb];
+  } else if constexpr (Ly::PAGE_SCALES) {
+    sa *= ks[0];
+    sb = sa;
   }
   const bool ok0 = kr < lim, ok1 = kr + 8 < lim;
   x[0] = ok0 ? sacc[0] * sa : -INFINITY;
@@ -964,8 +976,8 @@ __device__ __forceinline__ void tc8_pv(Tc8State<D>& st, const uint8_t* vpage, in
 // slices, slice warp * SW + j being rows [r0, r0 + 16) of page pr of the R
 // staged pages (pr = slice / SPP, r0 = 16 (slice mod SPP)); rows[r] is the
 // number of attended rows of page r (0 for pages not in this iteration); Ks
-// and Vs hold the pages' row scales (INT8). The slices share one
-// running-max update.
+// and Vs hold the pages' row scales (INT8) or point at their one scale (block-scaled FP8).
+// The slices share one running-max update.
 template <typename Ly, typename CT, int D>
 __device__ __forceinline__ void process_tc8(Tc8State<D>& st, const uint8_t* const (&Kp)[Ly::R],
                                             const uint8_t* const (&Vp)[Ly::R],
@@ -1035,8 +1047,19 @@ __device__ __forceinline__ void process_tc8(Tc8State<D>& st, const uint8_t* cons
   }
   st.s_top[0] = fmaxf(st.s_top[0], tm0);
   st.s_top[1] = fmaxf(st.s_top[1], tm1);
-  if constexpr (Ly::SCORED) {
+  if constexpr (Ly::TOPPED) {
     float top = kScoredTop;
+    if constexpr (Ly::PAGE_SCALES) {
+      // as below, of the slices' pages (warp-uniform)
+      uint32_t most = 0;
+#pragma unroll
+      for (int j = 0; j < SW; ++j)
+        if (lim[j] > 0) {
+          const uint32_t b = __float_as_uint(vsc[j][0]) & 0x7FFFFFFFu;
+          if (b < 0x7F800000u) most = max(most, b);
+        }
+      top -= static_cast<float>(min(max(static_cast<int>(most >> 23) - 126, -60), 60));
+    }
     if constexpr (Ly::ROW_SCALES) {
       // the largest V scale of the attended rows is below 2^e (the bits of numbers that
       // are not negative are in their order; infinities and NaN are left out); held to
@@ -1083,9 +1106,10 @@ __device__ __forceinline__ void process_tc8(Tc8State<D>& st, const uint8_t* cons
     for (int e = 0; e < 4; ++e)
       pw[e] = x[j][e] == -INFINITY ? 0.f : exp2f(x[j][e] - st.m_run[e & 1]);
     __half2 p01, p23;
-    if constexpr (Ly::ROW_SCALES) {
+    if constexpr (Ly::ROW_SCALES || Ly::PAGE_SCALES) {
       // masked rows keep a zero weight, whatever their scale holds
-      const float va = vsc[j][r0[j] + kr], vb = vsc[j][r0[j] + 8 + kr];
+      const float va = vsc[j][Ly::PAGE_SCALES ? 0 : r0[j] + kr];
+      const float vb = vsc[j][Ly::PAGE_SCALES ? 0 : r0[j] + 8 + kr];
       st.l_run[0] += pw[0] + pw[2];
       st.l_run[1] += pw[1] + pw[3];
       p01 = __floats2half2_rn(pw[0] == 0.f ? 0.f : pw[0] * va, pw[1] == 0.f ? 0.f : pw[1] * va);
@@ -1584,7 +1608,7 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p) {
   if (threadIdx.x == 0) {
 #pragma unroll
     for (int i = 0; i < STAGES; ++i) {
-      mbar_init(&full[i], 1);
+      mbar_init(&full[i], Ly::PAGE_SCALES ? 2 : 1);  // (the scales' copies arrive too)
       mbar_init(&empty[i], NC);
     }
     mbar_init(cbar, NC);
@@ -1690,6 +1714,17 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p) {
                        qbytes, &full[slot]);
           } else {
             mbar_arrive(&full[slot]);
+          }
+          if constexpr (Ly::PAGE_SCALES) {
+            if (ok) {
+              float* psc = reinterpret_cast<float*>(smem + Ly::OFF_PSC) + 2 * slot;
+              const size_t so = (size_t)bid * Hkv + g;
+              cp_async4(psc, p.k_scales + so);
+              cp_async4(psc + 1, p.v_scales + so);
+              cp_async_arrive(&full[slot]);
+            } else {
+              mbar_arrive(&full[slot]);
+            }
           }
           ++issued;
         }
@@ -1809,8 +1844,13 @@ __device__ __forceinline__ void decode_body(const DecodeParams& p) {
       }
       Kp[r] = stage;
       Vp[r] = stage + Ly::PAGE;
-      Ks[r] = reinterpret_cast<const float*>(stage + 2 * Ly::PAGE);
-      Vs[r] = reinterpret_cast<const float*>(stage + 2 * Ly::PAGE + Ly::SCB);
+      if constexpr (Ly::PAGE_SCALES) {
+        Ks[r] = reinterpret_cast<const float*>(smem + Ly::OFF_PSC) + 2 * slot;
+        Vs[r] = Ks[r] + 1;
+      } else {
+        Ks[r] = reinterpret_cast<const float*>(stage + 2 * Ly::PAGE);
+        Vs[r] = reinterpret_cast<const float*>(stage + 2 * Ly::PAGE + Ly::SCB);
+      }
       lim[r] = d.x - warp * TPW;
       rows[r] = d.x;
       last_flags = d.z;
@@ -2015,6 +2055,38 @@ cudaError_t dispatch_decode(const DecodeParams& prm, dim3 grid, int D, int GT, i
 #undef PA_CASE_BS
 }
 
+// A block-scaled FP8 cache: the balanced mode only (its entry point wants a workspace).
+template <typename QT, int D, int GT>
+cudaError_t dispatch_block_bs(const DecodeParams& prm, dim3 grid, int BS, cudaStream_t stream) {
+  switch (BS) {
+    case 16: return launch_decode<QT, E4M3B, D, GT, 16, kModeBalanced>(prm, grid, nullptr, stream);
+    case 32: return launch_decode<QT, E4M3B, D, GT, 32, kModeBalanced>(prm, grid, nullptr, stream);
+    case 64: return launch_decode<QT, E4M3B, D, GT, 64, kModeBalanced>(prm, grid, nullptr, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+template <typename QT, int D>
+cudaError_t dispatch_block_gt(const DecodeParams& prm, dim3 grid, int GT, int BS,
+                              cudaStream_t stream) {
+  switch (GT) {
+    case 1: return dispatch_block_bs<QT, D, 1>(prm, grid, BS, stream);
+    case 2: return dispatch_block_bs<QT, D, 2>(prm, grid, BS, stream);
+    case 4: return dispatch_block_bs<QT, D, 4>(prm, grid, BS, stream);
+    case 8: return dispatch_block_bs<QT, D, 8>(prm, grid, BS, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+template <typename QT>
+cudaError_t dispatch_block(const DecodeParams& prm, dim3 grid, int D, int GT, int BS,
+                           cudaStream_t stream) {
+  switch (D) {
+    case 64: return dispatch_block_gt<QT, 64>(prm, grid, GT, BS, stream);
+    case 96: return dispatch_block_gt<QT, 96>(prm, grid, GT, BS, stream);
+    case 128: return dispatch_block_gt<QT, 128>(prm, grid, GT, BS, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
 template <typename QT, typename CT, int D, int GT>
 cudaError_t dispatch_scored_bs(const DecodeParams& prm, dim3 grid, int BS, int* ctas,
                                cudaStream_t stream) {
@@ -2072,3 +2144,8 @@ PA_DECLARE_SCORED(pa_dispatch_scored_bf16_e4m3);
 PA_DECLARE_SCORED(pa_dispatch_scored_f16_e4m3);
 PA_DECLARE_SCORED(pa_dispatch_scored_bf16_i8);
 PA_DECLARE_SCORED(pa_dispatch_scored_f16_i8);
+#define PA_DECLARE_BLOCK(NAME)                                                           \
+  cudaError_t NAME(const pa::DecodeParams& prm, dim3 grid, int D, int GT, int BS, \
+                   cudaStream_t stream)
+PA_DECLARE_BLOCK(pa_dispatch_block_bf16);
+PA_DECLARE_BLOCK(pa_dispatch_block_f16);

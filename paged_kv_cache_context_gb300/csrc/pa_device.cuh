@@ -101,6 +101,17 @@ __device__ __forceinline__ void bulk_g2s(void* smem_dst, const void* gmem_src, u
       : "memory");
 }
 
+// Four bytes global -> shared, asynchronously, and an arrival on `bar` once this
+// thread's copies so far have landed (the arrival is one of the barrier's count).
+__device__ __forceinline__ void cp_async4(void* smem_dst, const void* gmem_src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(smem_dst)), "l"(gmem_src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+
 // 2-D tensor copy global -> shared (TMA) of the box at element coordinates
 // (x, y) of the tensor map, completion counted in bytes on an mbarrier of
 // this CTA. `tmap` is the generic address of a tensor map held in kernel
@@ -323,6 +334,14 @@ struct Elem<E4M3> {
   static constexpr int bytes = 1;
 };
 
+// FP8 E4M3 cache element of a cache with one fp32 scale per (block, kv head) for K and
+// one for V, held beside the pages.
+struct E4M3B {};
+template <>
+struct Elem<E4M3B> {
+  static constexpr int bytes = 1;
+};
+
 // INT8 cache element (one two's-complement byte) with one fp32 scale per
 // cached row, held beside the pages.
 struct I8 {};
@@ -488,6 +507,10 @@ __device__ __forceinline__ void widen8<E4M3>(uint32_t w, uint32_t& lo, uint32_t&
       "cvt.rn.f16x2.e4m3x2 %0, l16;\n\tcvt.rn.f16x2.e4m3x2 %1, h16;\n\t}"
       : "=r"(lo), "=r"(hi)
       : "r"(w));
+}
+template <>
+__device__ __forceinline__ void widen8<E4M3B>(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  widen8<E4M3>(w, lo, hi);
 }
 template <>
 __device__ __forceinline__ void widen8<I8>(uint32_t w, uint32_t& lo, uint32_t& hi) {

@@ -15,6 +15,7 @@ mismatch raises ``ValueError`` and nothing is enqueued.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional, Tuple
 
@@ -25,12 +26,13 @@ LIB_PATH = os.path.join(_HERE, "_lib", "libpagedattn.so")
 
 # enums of include/pa.h
 PA_F32, PA_BF16, PA_F16 = 0, 1, 2
-PA_KV_AUTO, PA_KV_FP8_E4M3, PA_KV_INT8 = 0, 1, 2
+PA_KV_AUTO, PA_KV_FP8_E4M3, PA_KV_INT8, PA_KV_FP8_BLOCK = 0, 1, 2, 3
 PA_ERR_DEVICE = -9
 DEVERR_BITS = {1: "slot", 2: "block_id", 4: "context_len", 8: "timeout", 16: "seq"}
 
 _DTYPE = {torch.float32: PA_F32, torch.bfloat16: PA_BF16, torch.float16: PA_F16}
-_KV = {"auto": PA_KV_AUTO, "fp8_e4m3": PA_KV_FP8_E4M3, "int8": PA_KV_INT8}
+_KV = {"auto": PA_KV_AUTO, "fp8_e4m3": PA_KV_FP8_E4M3, "int8": PA_KV_INT8,
+       "fp8_block": PA_KV_FP8_BLOCK}
 
 _lib = None
 
@@ -50,6 +52,7 @@ def lib() -> ctypes.CDLL:
                               "paged_kv_cache_context_gb300.build.build()")
         L = ctypes.CDLL(LIB_PATH)
         P, I, F, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+        N = ctypes.c_int64
         sig = {
             "pa_slot_mapping": [P, P, P, P, I, I, I, I, I, P],
             "pa_reshape_and_cache": [P, P, P, P, P, I, I, I, I, I, I, I, F, F, P],
@@ -88,6 +91,11 @@ def lib() -> ctypes.CDLL:
                                       P],
             "pa_evict_select": [P, P, P, P, I, I, I, I, I, I, P],
             "pa_compact": [P, P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, P],
+            "pa_norm_rope": [P, P, P, P, P, P, P, P, I, I, I, I, I, I, N, N, N, N, F, I, I, P],
+            "pa_norm_rope_and_cache": [P, P, P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, N,
+                                       N, N, N, F, I, I, I, F, F, P],
+            "pa_append_fp8_block": [P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, N, N, I, P],
+            "pa_decode_fp8_block": [P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, F, I, P, Z, P],
             "pa_decode_static_scratch": [P, P, P, P, P, P, I, I, I, I, I, I, I, F, I, I, I, F,
                                          F, P],
             "pa_get_device_error": [P, P],
@@ -806,6 +814,182 @@ def compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Te
         _check_scores(scores, bt[0], k[1], bt[1] * k[2])
     _check(lib().pa_compact(*ptrs, bt[0], k[1], kp[1], kp[2], k[3], k[2], k[0], bt[1],
                             k_cache.element_size(), _stream(stream)), "pa_compact")
+
+
+def rope_turns(inv_freq, device=None) -> torch.Tensor:
+    """The `turns` of norm_rope from frequencies in radians per position.
+
+    inv_freq [R / 2], or [A, R / 2] for positions of A axes (0 where an axis does not turn a
+    pair), taken in 64 bits. Returns int64 [A, R / 2] on `device` (inv_freq's by default):
+    the fraction of a turn per position in units of 2^-64. Made once, as weights are.
+    """
+    f = torch.as_tensor(inv_freq)
+    _need(f.dim() in (1, 2), "inv_freq: expected [rot_dim / 2] or [num_axes, rot_dim / 2]")
+    f = f[None] if f.dim() == 1 else f
+    dev = f.device if device is None else device
+    f = f.detach().to("cpu", torch.float64)
+    _need(bool(torch.isfinite(f).all()), "inv_freq: expected finite numbers")
+    # the fraction of a turn in [-1/2, 1/2], as two whole numbers of 32 bits (a double holds
+    # each exactly)
+    part = f / (2.0 * math.pi)
+    part = (part - part.round()) * 2.0 ** 32
+    high = part.floor()
+    low = ((part - high) * 2.0 ** 32).floor()
+    turns = (high.to(torch.int64) << 32) + low.to(torch.int64)
+    return turns.to(dev).contiguous()
+
+
+def _heads(name: str, t) -> torch.Tensor:
+    """t [num_tokens, heads, head_dim] with its heads dense (tokens may be strided)."""
+    _need(isinstance(t, torch.Tensor) and t.dim() == 3,
+          f"{name}: expected a tensor [num_tokens, heads, head_dim]")
+    D = t.shape[2]
+    _need((t.stride(2) == 1 or D == 1) and (t.stride(1) == D or t.shape[1] == 1),
+          f"{name}: the heads of a token must be contiguous")
+    return t
+
+
+def _token_stride(t: torch.Tensor) -> int:
+    """Elements between tokens (one token: its own size)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _rope_args(query, key, q_weight, k_weight, turns, positions):
+    """(T, Hq, Hkv, D, R, A) of consistent arguments; raises on others."""
+    T, Hq, D = query.shape
+    _need(key.shape[0] == T and key.shape[2] == D,
+          f"key: shape {tuple(key.shape)}, expected {T} tokens of head_dim {D}")
+    _need(query.dtype in _DTYPE, f"query: unsupported dtype {query.dtype}")
+    _dtype("key", key, query.dtype)
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _shape(name, w, (D,))
+            _dtype(name, w, torch.float32)
+    _need(turns.dim() == 2, "turns: expected [num_axes, rot_dim / 2]")
+    _dtype("turns", turns, torch.int64)
+    A = turns.shape[0]
+    _need(positions.shape == (A, T) or (A == 1 and positions.shape == (T,)),
+          f"positions: shape {tuple(positions.shape)}, expected [{A}, {T}]")
+    _dtype("positions", positions, torch.int32)
+    return T, Hq, key.shape[1], D, 2 * turns.shape[1], A
+
+
+def _strided(stream, names: str, *tensors):
+    """Device pointers of tensors on the current device, whatever their strides."""
+    _pointers(stream, names, *(t if t is None or t.is_contiguous() else t[:1, :1, :1]
+                               for t in tensors))
+    return [None if t is None else t.data_ptr() for t in tensors]
+
+
+def norm_rope(q_out: torch.Tensor, k_out: torch.Tensor, query: torch.Tensor, key: torch.Tensor,
+              turns: torch.Tensor, positions: torch.Tensor,
+              q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+              eps: float = 1e-6, interleaved: bool = False, stream=None):
+    """pa_norm_rope: the norm of every head of query [T, Hq, D] and key [T, Hkv, D] (weights
+    fp32 [D], None: no norm) and the rotation of its first R dims by positions int32 [A, T]
+    ([T] for one axis) with turns [A, R / 2] (see rope_turns); pairs (i, i + R / 2), or with
+    interleaved (2i, 2i + 1). Tokens may be strided (views of one projection's output); the
+    outputs may be the inputs."""
+    for name, t in (("q_out", q_out), ("k_out", k_out), ("query", query), ("key", key)):
+        _heads(name, t)
+    ptrs = _strided(stream, "q_out k_out query key q_weight k_weight turns positions", q_out,
+                    k_out, query, key, q_weight, k_weight, turns, positions)
+    T, Hq, Hkv, D, R, A = _rope_args(query, key, q_weight, k_weight, turns, positions)
+    for name, t, like in (("q_out", q_out, query), ("k_out", k_out, key)):
+        _shape(name, t, like.shape)
+        _dtype(name, t, like.dtype)
+    _check(lib().pa_norm_rope(*ptrs, T, Hq, Hkv, D, R, A, _token_stride(q_out),
+                              _token_stride(k_out), _token_stride(query), _token_stride(key),
+                              eps, int(interleaved), _DTYPE[query.dtype], _stream(stream)),
+           "pa_norm_rope")
+
+
+def norm_rope_and_cache(q_out: torch.Tensor, query: torch.Tensor, key: torch.Tensor,
+                        value: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                        slot_mapping_: torch.Tensor, turns: torch.Tensor,
+                        positions: torch.Tensor, q_weight: Optional[torch.Tensor] = None,
+                        k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                        interleaved: bool = False, kv_dtype: str = "auto", k_scale: float = 1.0,
+                        v_scale: float = 1.0, stream=None):
+    """pa_norm_rope_and_cache: norm_rope whose keys go, with value [T, Hkv, D], to their cache
+    slots (as reshape_and_cache after it, bit for bit)."""
+    for name, t in (("q_out", q_out), ("query", query), ("key", key), ("value", value)):
+        _heads(name, t)
+    ptrs = _strided(stream, "q_out query key value", q_out, query, key, value)
+    ptrs += _pointers(stream, "k_cache v_cache slot_mapping q_weight k_weight turns positions",
+                      k_cache, v_cache, slot_mapping_, q_weight, k_weight, turns, positions)
+    T, Hq, Hkv, D, R, A = _rope_args(query, key, q_weight, k_weight, turns, positions)
+    _shape("q_out", q_out, query.shape)
+    _dtype("q_out", q_out, query.dtype)
+    _shape("value", value, key.shape)
+    _dtype("value", value, key.dtype)
+    _need(kv_dtype in ("auto", "fp8_e4m3"), f"kv_dtype: {kv_dtype!r} is not 'auto' or 'fp8_e4m3'")
+    _check_caches(k_cache, v_cache, Hkv, D, _CACHE_DTYPE.get(kv_dtype, key.dtype))
+    _shape("slot_mapping", slot_mapping_, (T,))
+    _dtype("slot_mapping", slot_mapping_, torch.int64)
+    NB, _, bs, _ = k_cache.shape
+    _check(lib().pa_norm_rope_and_cache(*ptrs, T, Hq, Hkv, D, R, A, bs, NB, _token_stride(q_out),
+                                        _token_stride(query), _token_stride(key),
+                                        _token_stride(value), eps, int(interleaved),
+                                        _DTYPE[query.dtype], _KV[kv_dtype], k_scale, v_scale,
+                                        _stream(stream)), "pa_norm_rope_and_cache")
+
+
+def _check_page_scales(k_scales, v_scales, k_cache):
+    for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+        _shape(name, t, k_cache.shape[:2])
+        _dtype(name, t, torch.float32)
+
+
+def append_fp8_block(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor,
+                     v_cache: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor,
+                     block_tables: torch.Tensor, cu_q: torch.Tensor, context_lens: torch.Tensor,
+                     stream=None):
+    """pa_append_fp8_block: key / value [T, Hkv, D] (offsets cu_q [S + 1], the last tokens of
+    each sequence's context; tokens may be strided) into FP8 E4M3 caches (uint8 codes) with a
+    scale per block and kv head (fp32 [NB, Hkv])."""
+    _heads("key", key)
+    _heads("value", value)
+    ptrs = _strided(stream, "key value", key, value)
+    ptrs += _pointers(stream, "k_cache v_cache k_scales v_scales block_tables cu_q context_lens",
+                      k_cache, v_cache, k_scales, v_scales, block_tables, cu_q, context_lens)
+    T, H, D = key.shape
+    _shape("value", value, key.shape)
+    _need(key.dtype in _DTYPE, f"key: unsupported dtype {key.dtype}")
+    _dtype("value", value, key.dtype)
+    _check_caches(k_cache, v_cache, H, D, torch.uint8)
+    _check_page_scales(k_scales, v_scales, k_cache)
+    _need(block_tables.dim() == 2, "block_tables: expected [num_seqs, max_blocks_per_seq]")
+    _dtype("block_tables", block_tables, torch.int32)
+    S, MB = block_tables.shape
+    _shape("cu_q", cu_q, (S + 1,))
+    _dtype("cu_q", cu_q, torch.int32)
+    _shape("context_lens", context_lens, (S,))
+    _dtype("context_lens", context_lens, torch.int32)
+    NB, _, bs, _ = k_cache.shape
+    _check(lib().pa_append_fp8_block(*ptrs, T, S, H, D, bs, NB, MB, _token_stride(key),
+                                     _token_stride(value), _DTYPE[key.dtype], _stream(stream)),
+           "pa_append_fp8_block")
+
+
+def decode_fp8_block(out: torch.Tensor, query: torch.Tensor, k_cache: torch.Tensor,
+                     v_cache: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor,
+                     block_tables: torch.Tensor, context_lens: torch.Tensor, num_kv_heads: int,
+                     scale: float, workspace: torch.Tensor, stream=None):
+    """pa_decode_fp8_block: decode over the cache of append_fp8_block (workspace:
+    decode_workspace_size bytes)."""
+    *ptrs, ws = _pointers(stream, "out query k_cache v_cache k_scales v_scales block_tables "
+                          "context_lens workspace", out, query, k_cache, v_cache, k_scales,
+                          v_scales, block_tables, context_lens, workspace)
+    _check_decode_args(out, query, k_cache, v_cache, block_tables, context_lens, num_kv_heads,
+                       torch.uint8)
+    _need(query.dtype in _DTYPE, f"query: unsupported dtype {query.dtype}")
+    _check_page_scales(k_scales, v_scales, k_cache)
+    S, Hq, D = query.shape
+    NB, _, bs, _ = k_cache.shape
+    _check(lib().pa_decode_fp8_block(*ptrs, S, Hq, num_kv_heads, D, bs, NB,
+                                     block_tables.shape[1], scale, _DTYPE[query.dtype], ws,
+                                     _nbytes(workspace), _stream(stream)), "pa_decode_fp8_block")
 
 
 PA_BUDGET_MB, PA_BUDGET_FRACTION, PA_BUDGET_CONTEXT = 0, 1, 2

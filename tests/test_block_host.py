@@ -1,0 +1,150 @@
+"""Norm with rotation, and the block-scaled FP8 cache, without a GPU: refusals of the C ABI (fake
+pointers are never dereferenced), the binding's checks, the angles' fixed point, the budget."""
+import math
+
+import pytest
+import torch
+
+from _block_cache import power_above
+from paged_kv_cache_context_gb300 import pa
+
+P = 4096  # a fake, 16-byte aligned, never-dereferenced pointer
+BIG = 1 << 40
+
+
+@pytest.fixture(scope="module")
+def L():
+    from paged_kv_cache_context_gb300 import build
+    build.build()
+    return pa.lib()
+
+
+def rope(L, **kw):
+    a = dict(qo=P, ko=P, q=P, k=P, qw=P, kw=P, tu=P, pos=P, T=3, Hq=8, Hkv=2, D=128, R=128, A=1,
+             so=1024, sk=256, si=1024, sj=256, eps=1e-6, inter=0, dt=1)
+    a.update(kw)
+    return L.pa_norm_rope(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(q=None), -1), (dict(ko=None), -1), (dict(pos=None), -1), (dict(tu=None), -1),
+    (dict(dt=3), -2), (dict(dt=-1), -2), (dict(T=-1), -3), (dict(Hq=0), -3), (dict(Hkv=0), -3),
+    (dict(R=8), -3), (dict(R=144), -3), (dict(R=-16), -3), (dict(A=0), -3), (dict(A=9), -3),
+    (dict(eps=-1.0), -3), (dict(eps=float("nan")), -3), (dict(eps=float("inf")), -3),
+    (dict(si=1023), -3), (dict(si=1028), -3), (dict(sj=255), -3), (dict(so=0), -3),
+    (dict(sk=-256), -3), (dict(si=1 << 40), -3),
+    (dict(D=120), -4), (dict(D=0), -4), (dict(D=272), -4),
+    (dict(q=P + 8), -10), (dict(ko=P + 2), -10), (dict(qw=P + 4), -10), (dict(tu=P + 4), -10),
+    (dict(pos=P + 2), -10),
+])
+def test_norm_rope_rejects_bad_arguments_on_host(L, kw, code):
+    assert rope(L, **kw) == code
+    assert rope(L, T=0, q=None) == 0
+
+
+def store(L, **kw):
+    a = dict(qo=P, q=P, k=P, v=P, kc=P, vc=P, slots=P, qw=P, kw=P, tu=P, pos=P, T=3, Hq=8, Hkv=2,
+             D=128, R=128, A=1, bs=32, NB=4, so=1024, si=1024, sj=256, sv=256, eps=1e-6, inter=0,
+             dt=1, kv=0, k1=1.0, v1=1.0)
+    a.update(kw)
+    return L.pa_norm_rope_and_cache(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(v=None), -1), (dict(slots=None), -1), (dict(kc=None), -1), (dict(kv=2), -2),
+    (dict(kv=3), -2), (dict(dt=5), -2), (dict(NB=0), -3), (dict(sv=100), -3), (dict(R=24), -3),
+    (dict(D=100), -4), (dict(bs=0), -5), (dict(bs=1025), -5), (dict(vc=P + 4), -10),
+    (dict(slots=P + 4), -10), (dict(kv=1, k1=0.0), -11), (dict(kv=1, v1=float("nan")), -11),
+])
+def test_norm_rope_and_cache_rejects_bad_arguments_on_host(L, kw, code):
+    assert store(L, **kw) == code
+    assert store(L, T=0, q=None) == 0
+
+
+def append(L, **kw):
+    a = dict(k=P, v=P, kc=P, vc=P, ks=P, vs=P, bt=P, cu=P, cl=P, T=8, S=2, H=2, D=128, bs=32,
+             NB=10, MB=4, sk=256, sv=256, dt=1)
+    a.update(kw)
+    return L.pa_append_fp8_block(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(k=None), -1), (dict(vs=None), -1), (dict(cu=None), -1), (dict(dt=9), -2),
+    (dict(T=-1), -3), (dict(S=-1), -3), (dict(S=70000), -3), (dict(H=0), -3), (dict(NB=0), -3),
+    (dict(MB=0), -3), (dict(MB=1 << 27), -3), (dict(sk=255), -3), (dict(sv=257), -3),
+    (dict(T=1 << 30, S=60000, H=60, sk=1 << 14, sv=1 << 14), -3),
+    (dict(D=80), -4), (dict(D=256), -4), (dict(bs=8), -5), (dict(bs=128), -5),
+    (dict(kc=P + 8), -10), (dict(v=P + 2), -10), (dict(ks=P + 2), -10),
+])
+def test_append_rejects_bad_arguments_on_host(L, kw, code):
+    assert append(L, **kw) == code
+    assert append(L, T=0, k=None) == 0 and append(L, S=0, k=None) == 0
+
+
+def decode(L, **kw):
+    a = dict(out=P, q=P, kc=P, vc=P, ks=P, vs=P, bt=P, cl=P, S=2, Hq=8, Hkv=2, D=128, bs=32,
+             NB=10, MB=4, scale=0.1, qd=1, ws=P, wsb=BIG)
+    a.update(kw)
+    return L.pa_decode_fp8_block(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(q=None), -1), (dict(ks=None), -1), (dict(ws=None), -1), (dict(qd=0), -2),
+    (dict(qd=7), -2), (dict(Hq=7), -3), (dict(Hq=18), -3), (dict(S=-1), -3), (dict(NB=0), -3),
+    (dict(NB=1 << 26, Hkv=8), -3), (dict(D=80), -4), (dict(bs=8), -5), (dict(wsb=1 << 20), -7),
+    (dict(ws=P + 8), -10), (dict(kc=P + 2), -10), (dict(vs=P + 2), -10),
+])
+def test_decode_rejects_bad_arguments_on_host(L, kw, code):
+    assert decode(L, **kw) == code
+    assert decode(L, S=0, q=None) == 0
+
+
+def test_the_other_decodes_refuse_the_block_scaled_kind(L):
+    f = L.pa_decode
+    assert f(P, P, P, P, P, P, 2, 8, 2, 128, 32, 10, 4, 0.1, 0, 1, 3, 1.0, 1.0, None, 0, None) == -2
+    assert L.pa_reshape_and_cache(P, P, P, P, P, 2, 2, 128, 32, 10, 1, 3, 1.0, 1.0, None) == -2
+
+
+def test_block_budget_counts_the_page_scales(L):
+    n = pa.block_budget(4, 8, 128, 32, torch.bfloat16, "fp8_block", mb=64)
+    assert n == (64 << 20) // (4 * 2 * 8 * (32 * 128 + 4))
+    assert pa.block_budget(1, 1, 64, 16, torch.float16, "fp8_block", context_tokens=33) == 3
+
+
+def test_turns_are_exact_modulo_one():
+    f = torch.tensor([1.0, 0.1, 1e-4, -0.3, 7.0, 0.0, 2 * math.pi], dtype=torch.float64)
+    turns = pa.rope_turns(f)
+    assert turns.shape == (1, 7) and turns.dtype == torch.int64
+    for pos in (0, 1, -5, 131071, 2 ** 31 - 1, -2 ** 31):
+        for i, x in enumerate(f.tolist()):
+            got = (pos * int(turns[0, i])) % 2 ** 64 / 2 ** 64
+            want = math.cos(pos * x), math.sin(pos * x)
+            # an angle in 64 bits is off by 2^-52 of itself, a fraction by 2^-52 of a turn a step
+            tol = 2.0 ** -50 * (1 + abs(pos) * (abs(x) + 7))
+            assert abs(math.cos(2 * math.pi * got) - want[0]) <= tol
+            assert abs(math.sin(2 * math.pi * got) - want[1]) <= tol
+    two = pa.rope_turns(torch.rand(3, 8, dtype=torch.float64))
+    assert two.shape == (3, 8) and two.is_contiguous()
+    with pytest.raises(ValueError):
+        pa.rope_turns(torch.tensor([1.0, float("inf")]))
+    with pytest.raises(ValueError):
+        pa.rope_turns(torch.ones(2, 2, 2))
+
+
+def test_powers():
+    for a, s in ((448.0, 1.0), (448.5, 2.0), (1.0, 2.0 ** -8), (1.75, 2.0 ** -8), (1.76, 2.0 ** -7),
+                 (0.0, 0.0), (1e-45, 2.0 ** -126)):
+        assert power_above(a) == s
+
+
+def test_binding_refuses_what_it_cannot_pass():
+    q, k = torch.zeros(3, 8, 128), torch.zeros(3, 2, 128)
+    tu, pos = torch.zeros(1, 64, dtype=torch.int64), torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        pa.norm_rope(q, k, q, k, tu, pos)
+    with pytest.raises(ValueError, match="contiguous"):
+        pa.norm_rope(q, k, q.transpose(0, 1).contiguous().transpose(0, 1), k, tu, pos)
+    with pytest.raises(ValueError, match="query"):
+        pa.norm_rope(q, k, q[0], k, tu, pos)
+    with pytest.raises(ValueError, match="contiguous"):
+        pa.append_fp8_block(k[:, :, ::2], k[:, :, ::2], *[k] * 7)
