@@ -810,6 +810,49 @@ pa_status pa_decode_fp8_block(void* out, const void* query, const uint8_t* k_cac
                               void* workspace, size_t workspace_bytes, pa_stream_t stream);
 
 /*
+ * pa_prefill_fp8_block -- causal attention of several tokens a sequence over the
+ * cache of pa_append_fp8_block: whole prompts, chunks of them, packed and ragged.
+ *
+ * Source: "PagedAttention in mistral.rs", the prefill beside the paged decode and "KV
+ * Cache Quantization". Same computation and arguments as pa_prefill (token i of
+ * sequence s's chunk is at position n_s - q_len_s + i and attends to every position
+ * up to its own), with K and V as pa_decode_fp8_block. On the tensor cores the codes are
+ * widened exactly to f16 and q is carried in f16 (exact for a bf16 query inside f16's
+ * range); the weights, with their page's V scale, are rounded to f16 and keep their
+ * precision down to 2^-21 of the row's largest product of weight and scale; the running
+ * sum takes them unrounded; fp32 accumulation; output rounded to q_dtype. V scales are
+ * taken from 2^-60 to 2^60: a smaller one counts as zero, a larger one as 2^60.
+ * A NaN code in V makes that element NaN for the rows that see it, and it may for rows up to
+ * 127 tokens before it (a weight of zero times NaN); rows of a block past n_s may hold
+ * anything.
+ *
+ * out, query   : [T][Hq][D] of q_dtype (BF16 or F16, else PA_ERR_DTYPE).
+ * block_tables : int32 [S][MB].  cu_q : int32 [S + 1].  context_lens : int32 [S].
+ * workspace    : at least pa_prefill_fp8_block_workspace_size() bytes (PA_ERR_NULL /
+ *                PA_ERR_WORKSPACE), 16-byte aligned; contents on entry do not matter.
+ *                Calls that may overlap on the GPU need one each.
+ * max_q_len    : a bound on the chunks' lengths; whether max_q_len * G is above 128
+ *                chooses the tiles.
+ * Supported: D 64, 96 or 128 (PA_ERR_HEAD_DIM); bs 16, 32 or 64 (PA_ERR_BLOCK_SIZE);
+ * G in 1..8; 1 <= max_q_len <= T (PA_ERR_SHAPE). Pages come by 1-D bulk copies (no limit on
+ * the cache's rows). Device-side checks as pa_prefill: offsets that do not fit or a
+ * q_len above max_q_len set PA_DEVERR_SEQ and that sequence is not written; n_s < q_len_s or
+ * n_s > MB * bs sets PA_DEVERR_CONTEXT_LEN and its rows are zero; a block id outside [0, NB)
+ * sets PA_DEVERR_BLOCK_ID and reads as zeros. Pointers 16-byte aligned (scales 4). T == 0
+ * or S == 0 is a no-op. Two launches, without atomics: the same inputs give the same bits on
+ * the same device.
+ */
+size_t pa_prefill_fp8_block_workspace_size(int num_heads, int num_kv_heads, int head_dim);
+pa_status pa_prefill_fp8_block(void* out, const void* query, const uint8_t* k_cache,
+                               const uint8_t* v_cache, const float* k_scales,
+                               const float* v_scales, const int32_t* block_tables,
+                               const int32_t* cu_q, const int32_t* context_lens, int num_tokens,
+                               int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                               int block_size, int num_blocks, int max_blocks_per_seq,
+                               int max_q_len, float scale, pa_dtype q_dtype, void* workspace,
+                               size_t workspace_bytes, pa_stream_t stream);
+
+/*
  * pa_decode_partials -- the split phase of pa_decode with an explicit plan.
  *
  * For split i of (s, h) (slots [i*P*bs, (i+1)*P*bs) intersected with

@@ -13,6 +13,7 @@
 
 #include "pa_append.cuh"
 #include "pa_cascade.cuh"
+#include "pa_chunk.cuh"
 #include "pa_decode.cuh"
 #include "pa_device.cuh"
 #include "pa_evict.cuh"
@@ -1849,6 +1850,79 @@ PA_API pa_status pa_decode_fp8_block(void* out, const void* query, const uint8_t
   p.pages_per_split = 1;
   return run_decode(p, a, dim3(0, 1, 1), kModeBalanced, nullptr,
                     reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+PA_API size_t pa_prefill_fp8_block_workspace_size(int num_heads, int num_kv_heads,
+                                                  int head_dim) {
+  if (num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads != 0 ||
+      (head_dim != 64 && head_dim != 96 && head_dim != 128))
+    return 0;
+  return chunk_workspace_bytes(head_dim);
+}
+
+PA_API pa_status pa_prefill_fp8_block(void* out, const void* query, const uint8_t* k_cache,
+                                      const uint8_t* v_cache, const float* k_scales,
+                                      const float* v_scales, const int32_t* block_tables,
+                                      const int32_t* cu_q, const int32_t* context_lens,
+                                      int num_tokens, int num_seqs, int num_heads,
+                                      int num_kv_heads, int head_dim, int block_size,
+                                      int num_blocks, int max_blocks_per_seq, int max_q_len,
+                                      float scale, pa_dtype q_dtype, void* workspace,
+                                      size_t workspace_bytes, pa_stream_t stream) {
+  if (num_tokens < 0 || num_seqs < 0 || num_seqs > 65535) return PA_ERR_SHAPE;
+  if (num_tokens == 0 || num_seqs == 0) return PA_OK;
+  if (!out || !query || !k_cache || !v_cache || !k_scales || !v_scales || !block_tables ||
+      !cu_q || !context_lens || !workspace)
+    return PA_ERR_NULL;
+  if (q_dtype != PA_BF16 && q_dtype != PA_F16) return PA_ERR_DTYPE;
+  if (num_heads <= 0 || num_kv_heads <= 0 || num_kv_heads > 65535 ||
+      num_heads % num_kv_heads != 0 || num_heads / num_kv_heads > 8)
+    return PA_ERR_SHAPE;
+  if (head_dim != 64 && head_dim != 96 && head_dim != 128) return PA_ERR_HEAD_DIM;
+  if (block_size != 16 && block_size != 32 && block_size != 64) return PA_ERR_BLOCK_SIZE;
+  if (num_blocks <= 0 || max_blocks_per_seq <= 0 || max_q_len < 1 || max_q_len > num_tokens)
+    return PA_ERR_SHAPE;
+  // 32-bit positions (of whole tiles), (block, kv head) indexes and rows
+  if ((int64_t)max_blocks_per_seq * block_size > INT32_MAX - kChunkMaxTile ||
+      (int64_t)num_blocks * num_kv_heads > INT32_MAX ||
+      (int64_t)num_tokens * num_heads > INT32_MAX)
+    return PA_ERR_SHAPE;
+  if (workspace_bytes < chunk_workspace_bytes(head_dim)) return PA_ERR_WORKSPACE;
+  if (!aligned16(out) || !aligned16(query) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      !aligned16(workspace) || !aligned_to(k_scales, 4) || !aligned_to(v_scales, 4))
+    return PA_ERR_ALIGN;
+  constexpr float kLog2e = 1.4426950408889634f;
+  constexpr size_t kSlotRows = (size_t)kChunkMaxCtas * 2 * kChunkRows;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  ChunkParams p{};
+  p.out = out;
+  p.query = query;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.k_scales = k_scales;
+  p.v_scales = v_scales;
+  p.block_tables = block_tables;
+  p.cu_q = cu_q;
+  p.context_lens = context_lens;
+  p.part_o = reinterpret_cast<float4*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(ws + kSlotRows * head_dim * 4);
+  p.starts = reinterpret_cast<int4*>(ws + kSlotRows * (head_dim * 4 + 8));
+  p.total = reinterpret_cast<long long*>(p.starts + kChunkMaxCtas);
+  p.err = error_word();
+  p.num_seqs = num_seqs;
+  p.num_heads = num_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.group = num_heads / num_kv_heads;
+  p.block_size = block_size;
+  p.num_blocks = num_blocks;
+  p.num_tokens = num_tokens;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.max_q_len = max_q_len;
+  p.scale_log2 = scale * kLog2e;
+  return (q_dtype == PA_BF16 ? launch_chunk_bf16 : launch_chunk_f16)(
+             p, head_dim, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? PA_OK
              : PA_ERR_CUDA;
 }

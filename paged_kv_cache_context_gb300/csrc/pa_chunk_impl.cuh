@@ -1,0 +1,938 @@
+// pa_chunk_impl.cuh -- causal attention of chunks of tokens over a block-scaled FP8
+// cache, on the fifth-generation tensor cores (instantiated per query type by
+// pa_chunk_bf16.cu and pa_chunk_f16.cu, which build in parallel).
+//
+// Mathematics. The row of a token at position i: out = sum_{j <= i} p_j V_j with p
+// the softmax of scale q.K_j, K_j = ks code, V_j = vs code with the scales of j's page.
+// One pass over the cache with a running reference and sum in 32 bits. A token's
+// K scale multiplies its logit x; its V scale goes into the exponent: the tensor cores take
+// w_j = 2^(x_j + log2 vs_j - mu) beside the bare codes, and the sum takes w_j / vs_j
+// per 16 tokens (a page is 16 tokens at least). The reference m is the running maximum of
+// x_j + log2 vs_j, so it is the row's largest product that f16's range is fitted to
+// (mu = m - 7: weights reach 2^15 and keep full precision 2^-21 below), whatever the
+// pages' scales. log2 vs is held to [-60, 60]; a page below counts as zeros.
+//
+// Work. Units are K/V tiles of (sequence, kv head, row tile) in that order; every
+// CTA takes an equal contiguous share, so prompts, ragged chunks and a few rows over
+// a long context fill the GPU alike. A row tile that lies inside one share is finished
+// there; one that is cut leaves un-normalised partial rows, which a second launch
+// joins in order (no atomics: the same inputs give the same bits).
+//
+// CTA:
+//   four warps a query tile of 128 rows  softmax, thread t owns row t (TMEM lane t)
+//   one warp    MMA issue, TMEM allocation
+//   one warp    copies of K and V codes and their pages' scales
+//   four warps  codes widened exactly to f16 in the swizzled tiles
+// S = Q K^T goes to TMEM; the weights go back over it as the A operand of O += P V. With
+// two query tiles (many rows: 128-token tiles, one CTA an SM) one's softmax runs under
+// the other's products, and each widened tile serves both; with one (128 rows a kv head
+// at most: 64-token tiles, two CTAs an SM) S has two buffers, and the next tile's
+// product runs under this one's softmax.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
+#include "pa_chunk.cuh"
+#include "pa_device.cuh"
+#include "pa_tc05.cuh"
+
+namespace pa {
+namespace {
+
+constexpr float kChunkTop = 7.f;    // the largest weights' exponent above the reference
+constexpr float kChunkLazy = 8.f;   // how far the reference may lie behind
+constexpr int kChunkScaleRing = 8;  // tiles whose scales are kept
+
+// NQ: query tiles of a CTA.
+template <int D, int NQ>
+struct ChunkLayout {
+  static constexpr int DV = D == 96 ? 128 : D;   // columns of O (whole 64-element blocks of V)
+  static constexpr int KB = DV / 64;             // 128-byte column blocks of a row
+  static constexpr int TT = NQ == 2 ? 128 : 64;  // tokens of a tile
+  static constexpr int NG = TT / 16;             // scale groups of a tile
+  static constexpr int ROWS = NQ * kChunkRows;
+  static constexpr int SMX = 4 * NQ;  // softmax warps
+  static constexpr int MMA_WARP = SMX, COPY_WARP = SMX + 1, CONV_WARP = SMX + 2;
+  static constexpr int CONV = 128;  // widening threads
+  static constexpr int THREADS = CONV_WARP * 32 + CONV;
+  static constexpr int CTAS = NQ == 2 ? 1 : 2;           // per SM
+  static constexpr int QBYTES1 = KB * kChunkRows * 128;  // a query tile: [KB][128 rows][128 B]
+  static constexpr int SLOT = KB * TT * 128;             // a K or V tile: [KB][TT tokens][128 B]
+  static constexpr int RAW = TT * D;                     // its codes: [TT][D]
+  static constexpr int SLOTS = DV == 128 ? 3 : 4;
+  static constexpr int RSLOTS = 4;
+  static constexpr int OFF_KV = NQ * QBYTES1;
+  static constexpr int OFF_RAW = OFF_KV + SLOTS * SLOT;
+  static constexpr int OFF_SC = OFF_RAW + RSLOTS * RAW;  // [ring][NG] of float4
+  static constexpr int OFF_BAR = OFF_SC + kChunkScaleRing * NG * 16;
+  static constexpr int NBAR = 2 * SLOTS + 2 * RSLOTS + 2 + 2 + 2 + NQ + kChunkScaleRing;
+  static constexpr int OFF_MISC = (OFF_BAR + NBAR * 8 + 15) / 16 * 16;
+  static constexpr int SMEM = OFF_MISC + 64;
+  // TMEM columns: S buffer b at b TT, O of query tile q at 2 TT + q DV
+  static constexpr uint32_t TMEM_COLS = 2 * TT + NQ * DV <= 256 ? 256 : 512;
+  static_assert(2 * TT + NQ * DV <= (int)TMEM_COLS && CTAS * TMEM_COLS <= 512, "TMEM columns");
+  static_assert(OFF_BAR % 16 == 0 && OFF_RAW % 16 == 0 && RAW % 16 == 0, "alignment");
+  static_assert(SMEM <= (CTAS == 2 ? 113 : 227) * 1024, "CTAs per SM");
+  // The copy warp is at most RSLOTS + SLOTS half tiles and the one it waits for ahead of
+  // the tile whose V is in use.
+  static_assert((RSLOTS + SLOTS) / 2 + 2 < kChunkScaleRing, "scales in use are not overwritten");
+};
+
+// sum of floor((a i + b) / m) over i in [0, n), m a power of two (all >= 0; by turns of
+// Euclid's algorithm on a and m).
+__device__ __forceinline__ long long floor_sum(long long n, int m, int a, long long b) {
+  unsigned long long sum = 0, N = n, M = m, A = a, B = b;
+  while (N > 0) {
+    // (small divisors: 32-bit divisions where the operands allow)
+    const unsigned long long qa = A / M;
+    sum += N * (N - 1) / 2 * qa;
+    A -= qa * M;
+    const unsigned long long qb = B >> 32 ? B / M : static_cast<uint32_t>(B) / static_cast<uint32_t>(M);
+    sum += N * qb;
+    B -= qb * M;
+    const unsigned long long y = A * N + B;
+    if (y < M) break;
+    N = y >> 32 ? y / M : static_cast<uint32_t>(y) / static_cast<uint32_t>(M);
+    B = y - N * M;
+    const unsigned long long t = A;
+    A = M;
+    M = t;
+  }
+  return static_cast<long long>(sum);
+}
+
+// A sequence's rows and tiles; RT = 0 when it has no work. Impossible offsets
+// (nothing is written) and lengths (zero rows) are flagged with `flag`.
+struct ChunkSeq {
+  int q0, q_len, n, RT;
+  bool zero;  // the rows exist, but not their context
+};
+__device__ __forceinline__ ChunkSeq chunk_seq(const ChunkParams& p, int s, bool flag) {
+  ChunkSeq q{};
+  q.q0 = p.cu_q[s];
+  const int n = p.context_lens[s];
+  const long long len = (long long)p.cu_q[s + 1] - q.q0;
+  if (len < 0 || q.q0 < 0 || q.q0 + len > p.num_tokens || len > p.max_q_len) {
+    if (flag) raise_error(p.err, PA_DEVERR_SEQ);
+    return q;
+  }
+  q.q_len = static_cast<int>(len);
+  if (q.q_len == 0) return q;
+  q.n = n;
+  if (q.n < q.q_len || q.n > (long long)p.max_blocks_per_seq * p.block_size) {
+    if (flag) raise_error(p.err, PA_DEVERR_CONTEXT_LEN);
+    q.zero = true;
+    return q;
+  }
+  q.RT = static_cast<int>(((long long)q.q_len + p.tile_tokens - 1) / p.tile_tokens);
+  return q;
+}
+// K/V tiles of row tile rt, and of the row tiles before it.
+template <int TT>
+__device__ __forceinline__ int chunk_tiles(const ChunkParams& p, const ChunkSeq& q, int rt) {
+  const long long end = (long long)(rt + 1) * p.tile_tokens;
+  const int last = end < q.q_len ? static_cast<int>(end) : q.q_len;  // tokens up to its last
+  return (q.n - q.q_len + last + TT - 1) / TT;
+}
+template <int TT>
+__device__ __forceinline__ long long chunk_before(const ChunkParams& p, const ChunkSeq& q, int rt) {
+  return floor_sum(rt, TT, p.tile_tokens,
+                   (long long)(q.n - q.q_len) + p.tile_tokens + TT - 1);
+}
+template <int TT>
+__device__ __forceinline__ long long chunk_head_units(const ChunkParams& p, const ChunkSeq& q) {
+  return q.RT == 0 ? 0
+                   : chunk_before<TT>(p, q, q.RT - 1) + chunk_tiles<TT>(p, q, q.RT - 1);
+}
+__device__ __forceinline__ long long chunk_share(long long P, int C) { return (P + C - 1) / C; }
+
+// Walk over the pieces of a CTA's share: the current piece is tiles [tile, tile + len)
+// of the T of (s, g, rt), `left` units of the share from it on.
+template <int TT>
+struct ChunkWalk {
+  ChunkSeq q;
+  int s, g, rt, tile, len, T;
+  long long left;
+  __device__ __forceinline__ void set(const ChunkParams& p, const int* misc, long long n) {
+    s = misc[0];
+    g = misc[1];
+    rt = misc[2];
+    tile = misc[3];
+    left = n;
+    q = chunk_seq(p, s, false);
+    T = chunk_tiles<TT>(p, q, rt);
+    len = static_cast<int>(left < T - tile ? left : T - tile);
+  }
+  __device__ __forceinline__ void next(const ChunkParams& p) {
+    left -= len;
+    tile += len;
+    if (left <= 0) return;
+    if (tile == T) {
+      tile = 0;
+      if (++rt == q.RT) {
+        rt = 0;
+        if (++g == p.num_kv_heads) {
+          g = 0;
+          do {
+            ++s;
+            q = chunk_seq(p, s, false);
+          } while (q.RT == 0 && s + 1 < p.num_seqs);
+        }
+      }
+      T = chunk_tiles<TT>(p, q, rt);
+    }
+    len = static_cast<int>(left < T - tile ? left : T - tile);
+  }
+  // rows of the current row tile
+  __device__ __forceinline__ int rows(const ChunkParams& p) const {
+    const long long left_tokens = q.q_len - (long long)rt * p.tile_tokens;
+    return static_cast<int>(left_tokens < p.tile_tokens ? left_tokens : p.tile_tokens) * p.group;
+  }
+};
+
+// The largest x + log2 vs of N tokens (N / 16 groups, their scales in sc: K scale times
+// the logit scale, log2 of the V scale). Without masks it is the largest product that
+// counts, and multiplying by a scale that is not negative keeps the order.
+template <int N>
+__device__ __forceinline__ float chunk_max(const uint32_t (&s)[N], const float4* sc, bool plain,
+                                           int lim) {
+  float best = -INFINITY;
+#pragma unroll
+  for (int g = 0; g < N / 16; ++g) {
+    const float4 c = sc[g];
+    if (plain) {
+      float a[2] = {__uint_as_float(s[16 * g]), __uint_as_float(s[16 * g + 1])};
+#pragma unroll
+      for (int e = 2; e < 16; e += 2) {
+        a[0] = fmaxf(a[0], __uint_as_float(s[16 * g + e]));
+        a[1] = fmaxf(a[1], __uint_as_float(s[16 * g + e + 1]));
+      }
+      best = fmaxf(best, fmaf(fmaxf(a[0], a[1]), c.x, c.y));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float x = fmaf(__uint_as_float(s[16 * g + e]), c.x, c.y);
+        best = fmaxf(best, 16 * g + e < lim ? x : -INFINITY);
+      }
+    }
+  }
+  return best;
+}
+
+// The weights of N tokens in pairs of f16, and their share of the sum.
+template <bool MASKED, int N>
+__device__ __forceinline__ void chunk_weigh(const uint32_t (&s)[N], const float4* sc, float mu,
+                                            int lim, float& sum, uint32_t (&pk)[N / 2]) {
+#pragma unroll
+  for (int g = 0; g < N / 16; ++g) {
+    const float4 c = sc[g];
+    const float2 k2 = make_float2(c.x, c.x), b2 = make_float2(c.y - mu, c.y - mu);
+    float2 part = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+      const int i = 16 * g + e;
+      const float2 x =
+          __ffma2_rn(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), k2, b2);
+      float2 w = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+      if constexpr (MASKED) {
+        w.x = i < lim ? w.x : 0.f;
+        w.y = i + 1 < lim ? w.y : 0.f;
+      }
+      part = __fadd2_rn(part, w);
+      pk[i / 2] = Mma<__half>::pack(w.x, w.y);
+    }
+    sum = fmaf(part.x + part.y, c.z, sum);
+  }
+}
+
+template <typename QT, int D, int NQ>
+__global__ void __launch_bounds__(ChunkLayout<D, NQ>::THREADS, ChunkLayout<D, NQ>::CTAS)
+    chunk_attention_kernel(const __grid_constant__ ChunkParams p) {
+  using Ly = ChunkLayout<D, NQ>;
+  constexpr int KB = Ly::KB, NS = Ly::SLOTS, RS = Ly::RSLOTS, ROWS = Ly::ROWS, TT = Ly::TT;
+  constexpr int DV = Ly::DV, NG = Ly::NG;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Ly::OFF_BAR);  // [NS] a widened tile is there
+  uint64_t* empty = full + NS;        // [NS] its products are done
+  uint64_t* raw_full = empty + NS;    // [RS] codes have landed
+  uint64_t* raw_empty = raw_full + RS;  // [RS] and have been read
+  uint64_t* s_full = raw_empty + RS;  // [2] S is in its buffer
+  uint64_t* p_full = s_full + 2;      // [2] the weights are
+  uint64_t* pv_done = p_full + 2;     // [2] and have been used
+  uint64_t* q_full = pv_done + 2;     // [NQ]
+  uint64_t* sc_full = q_full + NQ;    // [ring] a tile's scales are there
+  int* misc = reinterpret_cast<int*>(smem + Ly::OFF_MISC);                     // s, g, rt, tile
+  long long* misc64 = reinterpret_cast<long long*>(smem + Ly::OFF_MISC + 16);  // units
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Ly::OFF_MISC + 32);
+  float4* sc = reinterpret_cast<float4*>(smem + Ly::OFF_SC);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cta = blockIdx.x, C = p.ctas, S = p.num_seqs;
+  const int Hq = p.num_heads, Hkv = p.num_kv_heads, G = p.group, bs = p.block_size;
+  unsigned* err = p.err;
+
+  pdl_wait();
+  pdl_trigger();
+  // ---- this CTA's share (copy warp); barriers, TMEM; sequences whose length is
+  // impossible get zero rows
+  if (warp == Ly::COPY_WARP) {
+    auto head_units = [&](int s) -> long long {
+      return s < S ? chunk_head_units<TT>(p, chunk_seq(p, s, false)) : 0;
+    };
+    const long long u0 = head_units(lane) * Hkv, incl0 = warp_incl(u0, lane);
+    long long P = __shfl_sync(0xffffffffu, incl0, 31);
+    for (int b = 32; b < S; b += 32)
+      P += __shfl_sync(0xffffffffu, warp_incl(head_units(b + lane) * Hkv, lane), 31);
+    const long long U = chunk_share(P, C);
+    const long long lo = min(cta * U, P), hi = min(lo + U, P);
+    int4 at = make_int4(0, 0, 0, 0);
+    if (lo < hi) {
+      long long run = 0;
+      for (int b = 0; b < S; b += 32) {
+        const long long u = b == 0 ? u0 : head_units(b + lane) * Hkv;
+        const long long incl = b == 0 ? incl0 : warp_incl(u, lane);
+        const unsigned hit = __ballot_sync(0xffffffffu, run + incl > lo);
+        if (hit) {
+          const int src = __ffs(hit) - 1;
+          at.x = b + src;
+          const ChunkSeq q = chunk_seq(p, at.x, false);
+          const long long per = __shfl_sync(0xffffffffu, u, src) / Hkv;
+          long long rem = lo - (run + __shfl_sync(0xffffffffu, incl - u, src));
+          at.y = static_cast<int>(rem / per);
+          rem -= at.y * per;
+          // the last row tile that begins at or before `rem`: 32 candidates at a time
+          int a = 0, e = q.RT;
+          while (e - a > 1) {
+            const int step = (e - a + 31) / 32, cand = a + lane * step;
+            const bool ok = cand < e && chunk_before<TT>(p, q, cand) <= rem;
+            const int k = __popc(__ballot_sync(0xffffffffu, ok)) - 1;
+            a += k * step;
+            e = min(e, a + step);
+          }
+          at.z = a;
+          at.w = static_cast<int>(rem - chunk_before<TT>(p, q, a));
+          break;
+        }
+        run += __shfl_sync(0xffffffffu, incl, 31);
+      }
+    }
+    if (lane == 0) {
+      misc[0] = at.x;
+      misc[1] = at.y;
+      misc[2] = at.z;
+      misc[3] = at.w;
+      misc64[0] = hi - lo;
+      p.starts[cta] = at;  // for the join
+      if (cta == 0) *p.total = P;
+    }
+  } else if (warp == Ly::MMA_WARP) {
+    tmem_alloc(tmem_slot, Ly::TMEM_COLS);
+    if (lane == 0) {
+      for (int i = 0; i < NS; ++i) {
+        mbar_init(&full[i], Ly::CONV);
+        mbar_init(&empty[i], 1);
+      }
+      for (int i = 0; i < RS; ++i) {
+        mbar_init(&raw_full[i], 1);
+        mbar_init(&raw_empty[i], Ly::CONV / 32);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&s_full[i], 1);
+        mbar_init(&p_full[i], kChunkRows);
+        mbar_init(&pv_done[i], 1);
+      }
+      for (int i = 0; i < NQ; ++i) mbar_init(&q_full[i], kChunkRows);
+      for (int i = 0; i < kChunkScaleRing; ++i) mbar_init(&sc_full[i], 1);
+      fence_mbar_init();
+    }
+  } else if (warp < 4) {
+    for (int s = cta; s < S; s += C) {
+      const ChunkSeq q = chunk_seq(p, s, tid == 0);
+      if (!q.zero) continue;
+      QT* o = static_cast<QT*>(p.out) + (size_t)q.q0 * Hq * D;
+      const size_t cells = (size_t)q.q_len * Hq * D;
+      for (size_t i = tid; i < cells; i += kChunkRows) o[i] = Elem<QT>::from_f32(0.f);
+    }
+  }
+  tc05_fence_before();
+  __syncthreads();
+  tc05_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const long long units = misc64[0];
+  const bool aligned = (smem_u32(smem) & 1023u) == 0;
+  if (!aligned && tid == 0) raise_error(err, PA_DEVERR_TIMEOUT);  // never: see __align__ above
+
+  if (units > 0 && aligned) {
+    ChunkWalk<TT> w;
+    w.set(p, misc, units);
+    // query tiles of the current piece that have rows (the first always has)
+    auto live_tiles = [&]() -> int { return NQ == 1 ? 1 : (w.rows(p) > kChunkRows ? 2 : 1); };
+    if (warp == Ly::COPY_WARP) {
+      // ================================================ copies: K0 V0 K1 V1 ...
+      const int sh = 31 - __clz(bs), pages = TT >> sh;  // block_size is a power of two
+      int rs = 0;       // next raw slot
+      uint32_t ph = 1;  // parity of its last release
+      int filled = 0;   // slots filled (no further than RS)
+      int ring = 0;     // where the tile's scales go
+      bool ok = true;
+      // Lane g looks at 16 tokens of a tile: their page's index among all (block, kv
+      // head) pages (-1 past the sequence's end, -2 for a bad id) and what the softmax
+      // and the widening want to know of them: K scale times the logit scale, log2 of
+      // the V scale and one over it, and as bits: 1 where K counts, 2 times the rows of V.
+      auto lookup = [&](int i, int& y, float4& f) {
+        const int t = (w.tile + i) * TT + 16 * lane;
+        y = -1;
+        f = make_float4(0.f, 0.f, 1.f, 0.f);
+        if (lane >= NG || t >= w.q.n) return;
+        const int b = __ldg(p.block_tables + (size_t)w.s * p.max_blocks_per_seq + (t >> sh));
+        if (b < 0 || b >= p.num_blocks) {
+          raise_error(err, PA_DEVERR_BLOCK_ID);
+          y = -2;
+          f.y = -60.f;  // tokens of zeros: their weights count, small beside any value's
+          f.z = 0x1p60f;
+          return;
+        }
+        y = b * Hkv + w.g;
+        const float vs = __ldg(p.v_scales + y);
+        const float lv = fminf(fmaxf(log2f(fabsf(vs)), -60.f), 60.f);  // (NaN: -60)
+        f.x = p.scale_log2 * __ldg(p.k_scales + y);
+        f.y = lv;
+        f.z = exp2f(-lv);
+        const int rows = min(16, w.q.n - t);
+        f.w = __int_as_float(1 | (fabsf(vs) >= 0x1p-60f ? 2 * rows : 0));
+      };
+      int len = uniform(w.len);
+      while (len > 0 && ok) {
+        int y_next;
+        float4 f_next;
+        lookup(0, y_next, f_next);
+        for (int i = 0; i < len && ok; ++i) {
+          const int y_here = y_next;
+          const float4 f_here = f_next;
+          int y[TT / 16];
+#pragma unroll
+          for (int pp = 0; pp < TT / 16; ++pp)
+            y[pp] = __shfl_sync(0xffffffffu, y_here, (pp << sh) >> 4 & 31);
+          if (i + 1 < len) lookup(i + 1, y_next, f_next);
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            if (filled >= RS) ok = warp_wait(&raw_empty[rs], ph);
+            if (!ok) break;
+            if (kv == 0) {  // the tile's scales, before its codes
+              if (lane < NG) sc[ring * NG + lane] = f_here;
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sc_full[ring]);
+            }
+            uint8_t* raw = smem + Ly::OFF_RAW + rs * Ly::RAW;
+            if (elect_one()) {
+              uint32_t bytes = 0;
+#pragma unroll
+              for (int pp = 0; pp < TT / 16; ++pp)
+                if (pp < pages && y[pp] >= 0) bytes += D << sh;
+              mbar_arrive_expect_tx(&raw_full[rs], bytes);
+#pragma unroll
+              for (int pp = 0; pp < TT / 16; ++pp)
+                if (pp < pages && y[pp] >= 0)
+                  bulk_g2s(raw + (pp << sh) * D, (kv ? p.v_cache : p.k_cache) +
+                                                     ((size_t)y[pp] << sh) * D,
+                           D << sh, &raw_full[rs]);
+            }
+            __syncwarp();
+            if (filled < RS) ++filled;
+            if (++rs == RS) {
+              rs = 0;
+              ph ^= 1;
+            }
+          }
+          ring = (ring + 1) % kChunkScaleRing;
+        }
+        w.next(p);
+        len = uniform(w.left > 0 ? w.len : 0);
+      }
+      if (!ok && lane == 0) raise_error(err, PA_DEVERR_TIMEOUT);
+      // never leave with copies in flight: the last fill of every slot (a slot before
+      // `rs` was filled in phase ph ^ 1, one from it on in the phase before)
+      for (int j = 0; j < filled; ++j)
+        if (!warp_wait(&raw_full[j], (j < rs ? ph ^ 1 : ph) & 1) && lane == 0)
+          raise_error(err, PA_DEVERR_TIMEOUT);
+    } else if (warp == Ly::MMA_WARP) {
+      // ================================================ MMA issue
+      constexpr uint32_t idesc_s = umma_idesc_f16(false, kChunkRows, TT, false);
+      constexpr uint32_t idesc_o = umma_idesc_f16(false, kChunkRows, DV, true);
+      // low words of the operands' descriptors: an address adds its 16-byte units
+      const uint32_t dq = desc_lo(smem_u32(smem), 16);
+      const uint32_t dk0 = desc_lo(smem_u32(smem + Ly::OFF_KV), 16);
+      const uint32_t dv0 = desc_lo(smem_u32(smem + Ly::OFF_KV), TT * 128);
+      const uint32_t tb = uniform(tmem);
+      const uint32_t uo = tb + 2 * TT;
+      int ks = 0, vs = 1;         // slots of the next K and V tile
+      uint32_t kph = 0, vph = 0;  // and their phases
+      auto step2 = [&](int& sl, uint32_t& ph) {
+        sl += 2;
+        if (sl >= NS) {
+          sl -= NS;
+          ph ^= 1;
+        }
+      };
+      uint32_t cs[NQ] = {}, cd[NQ] = {};  // tiles whose S, whose P V has been issued
+      // (buffer and use of it of a query tile's c-th tile)
+      auto buf = [](int q, uint32_t c) -> uint32_t { return NQ == 2 ? q : c & 1; };
+      auto use = [](uint32_t c) -> uint32_t { return NQ == 2 ? c : c >> 1; };
+      // S of query tile q on the K tile in slot ks; `last`: the slot's last reader
+      auto issue_s = [&](int q, bool last) -> bool {
+        const uint32_t b = buf(q, cs[q]), u = use(cs[q]);
+        if (!warp_wait(&full[ks], kph)) return false;
+        // the weights that lie over S's columns have been used
+        if (u >= 1 && !warp_wait(&pv_done[b], (u - 1) & 1)) return false;
+        tc05_fence_after();
+        const uint32_t dk = dk0 + ks * (Ly::SLOT >> 4), dqt = dq + q * (Ly::QBYTES1 >> 4);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss(tb + b * TT, dqt + ((kk >> 2) * (kChunkRows * 128) + (kk & 3) * 32) / 16,
+                   dk + ((kk >> 2) * (TT * 128) + (kk & 3) * 32) / 16, idesc_s, kk > 0);
+          umma_commit(&s_full[b]);
+          if (last) umma_commit(&empty[ks]);
+        }
+        __syncwarp();
+        ++cs[q];
+        if (last) step2(ks, kph);
+        return true;
+      };
+      // O += P V of query tile q on the V tile in slot vs
+      auto issue_pv = [&](int q, bool accumulate, bool last) -> bool {
+        const uint32_t b = buf(q, cd[q]), u = use(cd[q]);
+        if (!warp_wait(&full[vs], vph) || !warp_wait(&p_full[b], u & 1)) return false;
+        tc05_fence_after();
+        const uint32_t dv = dv0 + vs * (Ly::SLOT >> 4), tp = tb + b * TT;
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < TT / 16; ++kk)
+            mma_ts(uo + q * DV, tp + kk * 8, dv + kk * (2048 / 16), idesc_o, kk > 0 || accumulate);
+          umma_commit(&pv_done[b]);
+          if (last) umma_commit(&empty[vs]);
+        }
+        __syncwarp();
+        ++cd[q];
+        if (last) step2(vs, vph);
+        return true;
+      };
+      bool ok = true;
+      int len = uniform(w.len);
+      for (int piece[2] = {0, 0}; len > 0 && ok;) {
+        const int nq = uniform(live_tiles());
+#pragma unroll
+        for (int q = 0; q < NQ; ++q)
+          if (q < nq) {
+            ok = ok && warp_wait(&q_full[q], piece[q]++ & 1);
+            ok = ok && issue_s(q, q == nq - 1);
+          }
+        for (int i = 0; i < len && ok; ++i) {
+          if constexpr (NQ == 1) {
+            if (i + 1 < len) ok = issue_s(0, true);
+            ok = ok && issue_pv(0, i > 0, true);
+          } else {
+#pragma unroll
+            for (int q = 0; q < NQ; ++q)
+              if (q < nq) {
+                ok = ok && issue_pv(q, i > 0, q == nq - 1);
+                if (i + 1 < len) ok = ok && issue_s(q, q == nq - 1);
+              }
+          }
+        }
+        w.next(p);
+        len = uniform(w.left > 0 ? w.len : 0);
+      }
+      if (!ok && lane == 0) raise_error(err, PA_DEVERR_TIMEOUT);
+    } else if (warp >= Ly::CONV_WARP) {
+      // ================================================ codes widened to f16
+      // A thread takes 16 codes at a time; rows that hold no tokens become zeros.
+      constexpr int CPR = D / 16, NJ = TT * CPR / Ly::CONV;
+      static_assert(TT * CPR % Ly::CONV == 0, "chunks of a tile");
+      const int cid = tid - Ly::CONV_WARP * 32;
+      bool ok = true;
+      int sl = 0, rs = 0, filled = 0, ring = 0;
+      uint32_t ph = 1, rph = 0;
+      for (long long k = 0; k < 2 * units && ok; ++k) {
+        const bool is_v = k & 1;
+        ok = warp_wait(&raw_full[rs], rph);
+        if (ok && filled >= NS) ok = warp_wait(&empty[sl], ph);
+        if (!ok) break;
+        uint8_t* dst = smem + Ly::OFF_KV + sl * Ly::SLOT;
+        const uint4* raw = reinterpret_cast<const uint4*>(smem + Ly::OFF_RAW + rs * Ly::RAW);
+        const float4* scg = sc + ring * NG;
+#pragma unroll 4
+        for (int j = 0; j < NJ; ++j) {
+          const int i = cid + j * Ly::CONV, row = i / CPR, c16 = i % CPR;
+          uint4 src = raw[i];
+          const int what = __float_as_int(scg[row >> 4].w);
+          if (is_v ? 2 * (row & 15) >= (what & ~1) : what == 0) src = make_uint4(0u, 0u, 0u, 0u);
+          uint4 o[2];
+          widen8<E4M3>(src.x, o[0].x, o[0].y);
+          widen8<E4M3>(src.y, o[0].z, o[0].w);
+          widen8<E4M3>(src.z, o[1].x, o[1].y);
+          widen8<E4M3>(src.w, o[1].z, o[1].w);
+          // the second column block's lanes store their odd chunk first, so that
+          // the eight lanes of a row (D 128) cover all banks
+          const int sw = (KB == 2 && c16 >= 4) ? 1 : 0;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int ch = 2 * c16 + (h ^ sw);
+            *reinterpret_cast<uint4*>(dst + (ch >> 3) * (TT * 128) + row * 128 +
+                                      (((ch & 7) ^ (row & 7)) << 4)) = sw ^ h ? o[1] : o[0];
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&full[sl]);
+        // the codes have been used, not only asked for: the copies of the next ones may
+        // overwrite them
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&raw_empty[rs]);
+        if (filled < NS) ++filled;
+        if (++sl == NS) {
+          sl = 0;
+          ph ^= 1;
+        }
+        if (++rs == RS) {
+          rs = 0;
+          rph ^= 1;
+        }
+        if (is_v) ring = (ring + 1) % kChunkScaleRing;
+      }
+      if (!ok && lane == 0) raise_error(err, PA_DEVERR_TIMEOUT);
+    } else {
+      // ================================================ softmax, a row per thread
+      // (tcgen05.ld / st are warp-wide: every decision that leads to one is taken by
+      // the whole warp)
+      const int q = warp / 4;    // query tile
+      const int r1 = tid & 127;  // row in it: TMEM lane
+      const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const uint32_t t_o = tmem + 2 * TT + q * DV + lane_off;
+      uint8_t* qrow = smem + q * Ly::QBYTES1 + r1 * 128;
+      uint32_t ct = 0;  // tiles of the CTA before the piece
+      uint32_t c = 0;   // tiles this query tile has taken
+      bool failed = false;
+      // the row of the current piece
+      int pos = 0;        // its position
+      uint32_t orow = 0;  // (a row is 128 bytes or more: 32 bits hold any that fits the memory)
+      bool live = false;
+      auto set_row = [&]() {
+        const int r = q * kChunkRows + r1;
+        live = r < w.rows(p);
+        const int token = live ? w.rt * p.tile_tokens + r / G : 0;
+        pos = w.q.n - w.q.q_len + token;
+        orow = static_cast<uint32_t>(w.q.q0 + token) * Hq + w.g * G + (live ? r % G : 0);
+      };
+      constexpr int QCH = D / 8;  // 16-byte chunks of a query row
+      auto load_q = [&]() {
+        const uint8_t* src = static_cast<const uint8_t*>(p.query) + (size_t)orow * D * 2;
+#pragma unroll
+        for (int ch = 0; ch < QCH; ++ch)
+          cp_async16(smem_u32(qrow) + (ch >> 3) * (kChunkRows * 128) + (((ch & 7) ^ (r1 & 7)) << 4),
+                     src + ch * 16, live);
+      };
+      set_row();
+      bool work = q < live_tiles();
+      if (work) load_q();
+      for (int piece = 0; w.left > 0; ++piece) {
+        if (work) {
+          cp_async_wait_all();
+          if constexpr (std::is_same<QT, __nv_bfloat16>::value) {
+            // q is carried in f16 (exact inside f16's range)
+#pragma unroll
+            for (int ch = 0; ch < QCH; ++ch) {
+              uint4* q16 = reinterpret_cast<uint4*>(qrow + (ch >> 3) * (kChunkRows * 128) +
+                                                    (((ch & 7) ^ (r1 & 7)) << 4));
+              uint4 v = *q16;
+              uint32_t* e = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const __nv_bfloat162 b = *reinterpret_cast<const __nv_bfloat162*>(&e[j]);
+                const __half2 h = __floats2half2_rn(__low2float(b), __high2float(b));
+                e[j] = *reinterpret_cast<const uint32_t*>(&h);
+              }
+              *q16 = v;
+            }
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(&q_full[q]);
+
+          // a warp without rows only keeps the barriers' count (its rows of S, P and O may
+          // hold anything: no product mixes rows)
+          const bool warp_live = q * kChunkRows + (warp & 3) * 32 < w.rows(p);
+          const int first_pos = __reduce_min_sync(0xffffffffu, live ? pos : 0x7FFFFFFF);
+          float m = -INFINITY, l = 0.f;
+          for (int i = 0; i < w.len; ++i, ++c) {
+            const uint32_t b = NQ == 2 ? q : c & 1, u = NQ == 2 ? c : c >> 1;
+            const int t0 = (w.tile + i) * TT;
+            if (!warp_wait(&s_full[b], u & 1)) {
+              failed = true;
+              break;
+            }
+            if (warp_live) {
+              const uint32_t x = ct + i;
+              const float4* sct = sc + (x % kChunkScaleRing) * NG;
+              if (!warp_wait(&sc_full[x % kChunkScaleRing], (x / kChunkScaleRing) & 1)) {
+                failed = true;
+                break;
+              }
+              tc05_fence_after();
+              __syncwarp();
+              const uint32_t t_s = tmem + b * TT + lane_off;
+              const bool masked = t0 + TT - 1 > first_pos;  // warp-uniform
+              const int lim = live ? pos - t0 + 1 : 0;      // tokens of the tile that the row sees
+              const bool plain = !masked && p.scale_log2 >= 0.f;
+              float mx = -INFINITY;
+#pragma unroll
+              for (int h = 0; h < TT / 32; ++h) {
+                uint32_t sr[32];
+                tmem_ld32(t_s + 32 * h, sr);
+                tmem_wait_ld();
+                mx = fmaxf(mx, chunk_max(sr, sct + 2 * h, plain, masked ? lim - 32 * h : 32));
+              }
+              if (__any_sync(0xffffffffu, mx > m + kChunkLazy)) {
+                const float mn = fmaxf(m, mx);
+                if (i > 0) {
+                  // O holds the tiles so far: scale it by 2^(m - mn) once the last P V
+                  // has landed
+                  const uint32_t cp = c - 1, bp = NQ == 2 ? q : cp & 1, up = NQ == 2 ? cp : cp >> 1;
+                  if (!warp_wait(&pv_done[bp], up & 1)) {
+                    failed = true;
+                    break;
+                  }
+                  tc05_fence_after();
+                  __syncwarp();
+                  const float al = mn == -INFINITY ? 1.f : exp2f(m - mn);
+#pragma unroll
+                  for (int c0 = 0; c0 < D; c0 += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(t_o + c0, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                      o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+                    tmem_st16(t_o + c0, o);
+                  }
+                  tmem_wait_st();
+                  l *= al;
+                }
+                m = mn;
+              }
+              const float mu = m == -INFINITY ? 0.f : m - kChunkTop;  // (nothing seen yet: zeros)
+              // weights over the logits that have been read
+#pragma unroll
+              for (int h = 0; h < TT / 32; ++h) {
+                uint32_t sr[32], pk[16];
+                tmem_ld32(t_s + 32 * h, sr);
+                tmem_wait_ld();
+                if (masked)
+                  chunk_weigh<true>(sr, sct + 2 * h, mu, lim - 32 * h, l, pk);
+                else
+                  chunk_weigh<false>(sr, sct + 2 * h, mu, 32, l, pk);
+                tmem_st16(t_s + 16 * h, pk);
+              }
+              tmem_wait_st();
+            }
+            tc05_fence_before();
+            mbar_arrive(&p_full[b]);
+          }
+          if (failed) break;
+          // ---- the row's output, or its partial
+          const bool whole = w.len == w.T, was_live = live;
+          const uint32_t out_row = orow;
+          // the next piece's query is on its way meanwhile (all S products on this one's
+          // have completed)
+          ct += w.len;
+          w.next(p);
+          if (w.left > 0) {
+            set_row();
+            work = q < live_tiles();
+            if (work) load_q();
+          }
+          const uint32_t cl = c - 1, bl = NQ == 2 ? q : cl & 1, ul = NQ == 2 ? cl : cl >> 1;
+          if (!warp_wait(&pv_done[bl], ul & 1)) {
+            failed = true;
+            break;
+          }
+          tc05_fence_after();
+          __syncwarp();
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          const size_t slot = (size_t)cta * 2 + (piece > 0 ? 1 : 0);
+          QT* dst = static_cast<QT*>(p.out) + (size_t)out_row * D;
+          float4* po = p.part_o + slot * (D / 4) * ROWS + q * kChunkRows + r1;
+          if (warp_live) {
+#pragma unroll
+            for (int c0 = 0; c0 < D; c0 += 32) {
+              uint32_t o[32];
+              tmem_ld32(t_o + c0, o);
+              tmem_wait_ld();
+              if (was_live && whole) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                  uint4 v;
+                  v.x = Mma<QT>::pack(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+                  v.y = Mma<QT>::pack(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+                  v.z = Mma<QT>::pack(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
+                  v.w = Mma<QT>::pack(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
+                  *reinterpret_cast<uint4*>(dst + c0 + e) = v;
+                }
+              } else if (was_live) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 4)
+                  po[(size_t)((c0 + e) / 4) * ROWS] =
+                      make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
+                                  __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+              }
+            }
+          }
+          if (!whole && was_live)
+            p.part_ml[slot * ROWS + q * kChunkRows + r1] = make_float2(m, l);
+          // the accumulator has been read before the next piece's weights (whose arrival
+          // lets the products overwrite it) are announced
+          tc05_fence_before();
+        } else {
+          // no rows for this query tile in the piece
+          ct += w.len;
+          w.next(p);
+          if (w.left > 0) {
+            set_row();
+            work = q < live_tiles();
+            if (work) load_q();
+          }
+        }
+      }
+      if (failed) raise_error(err, PA_DEVERR_TIMEOUT);
+    }
+  }
+  // every TMEM access is done before the columns are released
+  tc05_fence_before();
+  __syncthreads();
+  tc05_fence_after();
+  if (warp == Ly::MMA_WARP) {
+    __syncwarp();
+    tmem_dealloc(tmem, Ly::TMEM_COLS);
+  }
+}
+
+// Joins the partial rows of the row tiles that the shares cut: with a running maximum M
+// of the pieces' references m_j, out = sum_j 2^(m_j - M) o_j / sum_j 2^(m_j - M) l_j.
+// CTA (slice of columns, share): the first share that begins inside a row tile joins it. A
+// thread takes four columns of one row, rows fastest, as the partials are stored.
+constexpr int kChunkJoinThreads = 256;
+template <typename QT, int D, int NQ>
+__global__ void __launch_bounds__(kChunkJoinThreads)
+    chunk_join_kernel(const __grid_constant__ ChunkParams p) {
+  constexpr int R = ChunkLayout<D, NQ>::ROWS, TT = ChunkLayout<D, NQ>::TT;
+  constexpr int SIDE = kChunkJoinThreads / R;  // column groups side by side
+  const int tid = threadIdx.x, c = blockIdx.y + 1;
+  pdl_wait();
+  pdl_trigger();
+  const int4 at = __ldcg(p.starts + c);
+  const long long P = __ldcg(p.total);
+  if (at.w == 0) return;  // the share begins with a row tile, or is empty
+  const long long U = chunk_share(P, p.ctas);
+  const long long seg0 = c * U - at.w;  // the row tile's first unit
+  const int c0 = static_cast<int>(seg0 / U);
+  if (c0 + 1 != c) return;  // another share joins it
+  const ChunkSeq q = chunk_seq(p, at.x, false);
+  const int T = chunk_tiles<TT>(p, q, at.z);
+  const int n = static_cast<int>((seg0 + T - 1) / U) - c0 + 1;
+  // piece j sits in CTA c0 + j: in its first slot unless it began after other work
+  const int first = seg0 != c0 * U ? 1 : 0;
+  const int lr = tid % R;
+  const long long token = (long long)at.z * p.tile_tokens + lr / p.group;
+  if (lr >= p.tile_tokens * p.group || token >= q.q_len) return;
+  const int c4 = blockIdx.x * SIDE + tid / R;
+  const float2* ml = p.part_ml + (size_t)c0 * 2 * R + lr;
+  const float4* po = p.part_o + ((size_t)c0 * 2 * (D / 4) + c4) * R + lr;
+  constexpr int J = 4;  // pieces whose loads are in flight together
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float M = -INFINITY, l = 0.f;
+  for (int j0 = 0; j0 < n; j0 += J) {
+    float2 h[J];
+    float4 v[J];
+#pragma unroll
+    for (int u = 0; u < J; ++u) {
+      const int j = j0 + u, sl = 2 * j + (j == 0 ? first : 0);
+      h[u] = make_float2(-INFINITY, 0.f);
+      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (j < n) {
+        h[u] = __ldcg(ml + (size_t)sl * R);
+        v[u] = __ldcg(po + (size_t)sl * (D / 4) * R);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < J; ++u) {
+      if (h[u].y == 0.f) continue;  // nothing seen in the piece (a NaN stays one)
+      if (h[u].x > M) {
+        const float f = exp2f(M - h[u].x);
+        l *= f;
+        acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+        M = h[u].x;
+      }
+      const float f = exp2f(h[u].x - M);
+      l = fmaf(f, h[u].y, l);
+      acc.x = fmaf(f, v[u].x, acc.x);
+      acc.y = fmaf(f, v[u].y, acc.y);
+      acc.z = fmaf(f, v[u].z, acc.z);
+      acc.w = fmaf(f, v[u].w, acc.w);
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  QT* out = static_cast<QT*>(p.out) +
+            ((size_t)(q.q0 + token) * p.num_heads + at.y * p.group + lr % p.group) * D + 4 * c4;
+  *reinterpret_cast<uint2*>(out) = make_uint2(Mma<QT>::pack(acc.x * inv, acc.y * inv),
+                                              Mma<QT>::pack(acc.z * inv, acc.w * inv));
+}
+
+template <typename QT, int D, int NQ>
+cudaError_t launch_chunk_nq(ChunkParams& p, cudaStream_t st) {
+  using Ly = ChunkLayout<D, NQ>;
+  auto kern = chunk_attention_kernel<QT, D, NQ>;
+  static int configured_devices = 0;  // bit per device id < 32
+  static int device_sms[32] = {};
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 32 && (__atomic_load_n(&configured_devices, __ATOMIC_ACQUIRE) & (1 << dev))) {
+    sms = __atomic_load_n(&device_sms[dev], __ATOMIC_RELAXED);
+  } else {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Ly::SMEM);
+    if (e != cudaSuccess) return e;
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 32) {
+      __atomic_store_n(&device_sms[dev], sms, __ATOMIC_RELAXED);
+      __atomic_fetch_or(&configured_devices, 1 << dev, __ATOMIC_RELEASE);
+    }
+  }
+  // (the workspace holds kChunkMaxCtas CTAs of 128 rows)
+  p.ctas = (sms * 2 < kChunkMaxCtas ? sms * 2 : kChunkMaxCtas) / NQ;
+  p.tile_tokens = Ly::ROWS / p.group;
+  e = launch_pdl(kern, dim3(p.ctas), dim3(Ly::THREADS), Ly::SMEM, st, p);
+  if (e != cudaSuccess || p.ctas < 2) return e;
+  constexpr int kSlices = D / 4 / (kChunkJoinThreads / Ly::ROWS);
+  return launch_pdl(chunk_join_kernel<QT, D, NQ>, dim3(kSlices, p.ctas - 1),
+                    dim3(kChunkJoinThreads), 0, st, p);
+}
+
+template <typename QT, int D>
+cudaError_t launch_chunk_d(ChunkParams& p, cudaStream_t st) {
+  return (long long)p.max_q_len * p.group > kChunkRows ? launch_chunk_nq<QT, D, 2>(p, st)
+                                                       : launch_chunk_nq<QT, D, 1>(p, st);
+}
+
+template <typename QT>
+cudaError_t launch_chunk(ChunkParams& p, int D, cudaStream_t st) {
+  switch (D) {
+    case 64: return launch_chunk_d<QT, 64>(p, st);
+    case 96: return launch_chunk_d<QT, 96>(p, st);
+    case 128: return launch_chunk_d<QT, 128>(p, st);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace
+}  // namespace pa

@@ -64,6 +64,7 @@
 #include <type_traits>
 
 #include "pa_device.cuh"
+#include "pa_tc05.cuh"
 #include "pa_tree.cuh"
 
 namespace pa {
@@ -169,14 +170,6 @@ struct TreeSpot {
   long long total, base;  // base: units before sequence s
   int s;
 };
-__device__ __forceinline__ long long warp_incl(long long v, int lane) {
-#pragma unroll
-  for (int off = 1; off < 32; off *= 2) {
-    const long long u = __shfl_up_sync(0xffffffffu, v, off);
-    if (lane >= off) v += u;
-  }
-  return v;
-}
 __device__ __forceinline__ long long tree_units(const TreeParams& p, int s, int lane_ok) {
   if (!lane_ok) return 0;
   const TreeSeq q = tree_seq(p, s, false);
@@ -226,59 +219,6 @@ struct TreeWalk {
     len = static_cast<int>(left < q.T - tile ? left : q.T - tile);
   }
 };
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(valid ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_wait_all() {
-  asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
-}
-
-// Operand descriptors of 128-byte swizzled tiles, split in words: the high
-// word (stride 1024 bytes, descriptor version, swizzle kind) is the same for
-// all, the low one holds the address and the leading offset in 16-byte units.
-constexpr uint32_t kTreeDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint32_t tree_desc_lo(uint32_t saddr, uint32_t lbo) {
-  return ((saddr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16);
-}
-// One lane of a converged warp. The copy and MMA warps run their loops whole
-// and let one lane issue: addresses and descriptors stay warp-uniform, which
-// the issuing instructions take from uniform registers (a loop inside a
-// one-lane branch moves every operand there first: 86 clocks per product
-// instead of the tensor core's 48 to 64).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t ok;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.b32 %0, 1, 0, p;\n\t}"
-               : "=r"(ok));
-  return ok != 0;
-}
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
-}
-__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
-
-// D (TMEM) [+]= A (smem) x B (smem).
-__device__ __forceinline__ void tree_mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
-                                            uint32_t idesc, bool accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %5, 0;\n\t"
-      "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_lo), "r"(b_lo), "n"(kTreeDescHi), "r"(idesc), "r"(accumulate ? 1u : 0u)
-      : "memory");
-}
-// D (TMEM) [+]= A (TMEM, 16-bit pairs along K in 32-bit columns) x B (smem).
-__device__ __forceinline__ void tree_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
-                                            uint32_t idesc, bool accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %5, 0;\n\t"
-      "mov.b64 db, {%2, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "r"(b_lo), "n"(kTreeDescHi), "r"(idesc), "r"(accumulate ? 1u : 0u)
-      : "memory");
-}
 
 // The tokens [t0, t0 + 64) that a node sees, as bits: context tokens,
 // and nodes by the node's mask words (bits past the sequence's end are off).
@@ -379,30 +319,6 @@ __device__ __forceinline__ void part_weights(const uint32_t (&s)[N], const float
     pk[e / 2] = Mma<T>::pack(w.x, w.y);
   }
 }
-
-// 16 consecutive 32-bit columns of this thread's TMEM lane.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15])
-      : "memory");
-}
-
-// 16 or 32 columns.
-__device__ __forceinline__ void tmem_ld_n(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
-__device__ __forceinline__ void tmem_ld_n(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16(taddr, r); }
 
 template <typename QT, int D, int KC, int NQ>
 __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, KC, NQ>::CTAS)
@@ -632,9 +548,9 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
       constexpr uint32_t idesc_s = umma_idesc_f16(kBf16, kTreeRows, TT, false);
       constexpr uint32_t idesc_o = umma_idesc_f16(kBf16, kTreeRows, D, true);
       // low words of the operands' descriptors: an address adds its 16-byte units
-      const uint32_t dq = tree_desc_lo(smem_u32(smem), 16);
-      const uint32_t dk0 = tree_desc_lo(smem_u32(smem + Ly::OFF_KV), 16);
-      const uint32_t dv0 = tree_desc_lo(smem_u32(smem + Ly::OFF_KV), TT * 128);
+      const uint32_t dq = desc_lo(smem_u32(smem), 16);
+      const uint32_t dk0 = desc_lo(smem_u32(smem + Ly::OFF_KV), 16);
+      const uint32_t dv0 = desc_lo(smem_u32(smem + Ly::OFF_KV), TT * 128);
       const uint32_t tb = uniform(tmem);
       const uint32_t us = tb, up = tb + 64, uo = tb + NQ * 128;
       int ks = 0, vs = 1;         // slots of the next K and V tile
@@ -664,7 +580,7 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            tree_mma_ss(us + q * TT, dqt + ((kk >> 2) * (kTreeRows * 128) + (kk & 3) * 32) / 16,
+            mma_ss(us + q * TT, dqt + ((kk >> 2) * (kTreeRows * 128) + (kk & 3) * 32) / 16,
                         dk + ((kk >> 2) * (TT * 128) + (kk & 3) * 32) / 16, idesc_s, kk > 0);
           umma_commit(&s_full[q]);
           if (last) umma_commit(&empty[ks]);
@@ -684,7 +600,7 @@ __global__ void __launch_bounds__(TreeLayout<D, KC, NQ>::THREADS, TreeLayout<D, 
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < TT / 16; ++kk)
-            tree_mma_ts(uo + q * D, tp + kk * 8 + (INPL && kk >= 4 ? 64 : 0), dv + kk * (2048 / 16),
+            mma_ts(uo + q * D, tp + kk * 8 + (INPL && kk >= 4 ? 64 : 0), dv + kk * (2048 / 16),
                         idesc_o, kk > 0 || accumulate);
           umma_commit(&pv_done[2 * q + b]);
           if (last) umma_commit(&empty[vs]);

@@ -96,6 +96,9 @@ def lib() -> ctypes.CDLL:
                                        N, N, N, F, I, I, I, F, F, P],
             "pa_append_fp8_block": [P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, N, N, I, P],
             "pa_decode_fp8_block": [P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, F, I, P, Z, P],
+            "pa_prefill_fp8_block_workspace_size": [I, I, I],
+            "pa_prefill_fp8_block": [P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, F, I, P,
+                                     Z, P],
             "pa_decode_static_scratch": [P, P, P, P, P, P, I, I, I, I, I, I, I, F, I, I, I, F,
                                          F, P],
             "pa_get_device_error": [P, P],
@@ -109,6 +112,7 @@ def lib() -> ctypes.CDLL:
         L.pa_decode_workspace_size.restype = Z
         L.pa_decode_cascade_workspace_size.restype = Z
         L.pa_tree_workspace_size.restype = Z
+        L.pa_prefill_fp8_block_workspace_size.restype = Z
         L.pa_decode_scored_workspace_size.restype = Z
         L.pa_block_budget.restype = ctypes.c_int64
         L.pa_status_string.restype = ctypes.c_char_p
@@ -990,6 +994,40 @@ def decode_fp8_block(out: torch.Tensor, query: torch.Tensor, k_cache: torch.Tens
     _check(lib().pa_decode_fp8_block(*ptrs, S, Hq, num_kv_heads, D, bs, NB,
                                      block_tables.shape[1], scale, _DTYPE[query.dtype], ws,
                                      _nbytes(workspace), _stream(stream)), "pa_decode_fp8_block")
+
+
+def prefill_fp8_block_workspace_size(num_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    return int(lib().pa_prefill_fp8_block_workspace_size(num_heads, num_kv_heads, head_dim))
+
+
+def prefill_fp8_block(out: torch.Tensor, query: torch.Tensor, k_cache: torch.Tensor,
+                      v_cache: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor,
+                      block_tables: torch.Tensor, cu_q: torch.Tensor, context_lens: torch.Tensor,
+                      num_kv_heads: int, max_q_len: int, scale: float, workspace: torch.Tensor,
+                      stream=None):
+    """pa_prefill_fp8_block: causal attention of query [T, Hq, D] (the last tokens of each
+    sequence's context, offsets cu_q [S + 1]) over the cache of append_fp8_block."""
+    *ptrs, ws = _pointers(stream, "out query k_cache v_cache k_scales v_scales block_tables cu_q "
+                          "context_lens workspace", out, query, k_cache, v_cache, k_scales,
+                          v_scales, block_tables, cu_q, context_lens, workspace)
+    _need(query.dim() == 3, "query: expected [num_tokens, num_heads, head_dim]")
+    _shape("out", out, query.shape)
+    _dtype("out", out, query.dtype)
+    _need(query.dtype in _DTYPE, f"query: unsupported dtype {query.dtype}")
+    T, Hq, D = query.shape
+    _check_caches(k_cache, v_cache, num_kv_heads, D, torch.uint8)
+    _check_page_scales(k_scales, v_scales, k_cache)
+    _need(block_tables.dim() == 2, "block_tables: expected [num_seqs, max_blocks_per_seq]")
+    _dtype("block_tables", block_tables, torch.int32)
+    S, MB = block_tables.shape
+    _shape("cu_q", cu_q, (S + 1,))
+    _dtype("cu_q", cu_q, torch.int32)
+    _shape("context_lens", context_lens, (S,))
+    _dtype("context_lens", context_lens, torch.int32)
+    NB, _, bs, _ = k_cache.shape
+    _check(lib().pa_prefill_fp8_block(*ptrs, T, S, Hq, num_kv_heads, D, bs, NB, MB, max_q_len,
+                                      scale, _DTYPE[query.dtype], ws, _nbytes(workspace),
+                                      _stream(stream)), "pa_prefill_fp8_block")
 
 
 PA_BUDGET_MB, PA_BUDGET_FRACTION, PA_BUDGET_CONTEXT = 0, 1, 2

@@ -1,6 +1,7 @@
 """Norm with rotation, and the block-scaled FP8 cache, without a GPU: refusals of the C ABI (fake
 pointers are never dereferenced), the binding's checks, the angles' fixed point, the budget."""
 import math
+import random
 
 import pytest
 import torch
@@ -97,6 +98,68 @@ def decode(L, **kw):
 def test_decode_rejects_bad_arguments_on_host(L, kw, code):
     assert decode(L, **kw) == code
     assert decode(L, S=0, q=None) == 0
+
+
+def prefill(L, **kw):
+    a = dict(out=P, q=P, kc=P, vc=P, ks=P, vs=P, bt=P, cu=P, cl=P, T=8, S=2, Hq=8, Hkv=2, D=128,
+             bs=32, NB=10, MB=4, mq=4, scale=0.1, qd=1, ws=P, wsb=BIG)
+    a.update(kw)
+    return L.pa_prefill_fp8_block(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(q=None), -1), (dict(ks=None), -1), (dict(cu=None), -1), (dict(ws=None), -1),
+    (dict(qd=0), -2), (dict(qd=7), -2), (dict(Hq=7), -3), (dict(Hq=18), -3), (dict(S=-1), -3),
+    (dict(S=70000), -3), (dict(T=-1), -3), (dict(NB=0), -3), (dict(MB=0), -3), (dict(mq=0), -3),
+    (dict(mq=9), -3), (dict(MB=1 << 26), -3), (dict(NB=1 << 30, Hkv=8), -3),
+    (dict(T=1 << 29, mq=1), -3), (dict(D=80), -4), (dict(bs=8), -5), (dict(wsb=1 << 20), -7),
+    (dict(ws=P + 8), -10), (dict(kc=P + 2), -10), (dict(vs=P + 2), -10),
+])
+def test_prefill_rejects_bad_arguments_on_host(L, kw, code):
+    assert prefill(L, **kw) == code
+    assert prefill(L, S=0, q=None) == 0 and prefill(L, T=0, q=None) == 0
+    n = L.pa_prefill_fp8_block_workspace_size(8, 2, 128)
+    assert n > L.pa_prefill_fp8_block_workspace_size(8, 2, 64) > 0 and prefill(L, wsb=n - 1) == -7
+    assert L.pa_prefill_fp8_block_workspace_size(8, 3, 128) == 0
+    assert L.pa_prefill_fp8_block_workspace_size(8, 2, 80) == 0
+
+
+def floor_sum(n, m, a, b):
+    """The kernel's sum of floor((a i + b) / m) over [0, n), restated."""
+    s, N, M, A, B = 0, n, m, a, b
+    while N > 0:
+        s += N * (N - 1) // 2 * (A // M)
+        A %= M
+        s += N * (B // M)
+        B %= M
+        y = A * N + B
+        if y < M:
+            break
+        N, B = y // M, y % M
+        A, M = M, A
+    return s
+
+
+def test_the_shares_cover_every_tile_once():
+    """The prefill's arithmetic restated: units before a row tile, and the search for a share's
+    first one."""
+    rng = random.Random(5)
+    for _ in range(300):
+        tt, tokens = rng.choice([(64, 128), (128, 256)])
+        tokens //= rng.choice([1, 2, 3, 4, 5, 6, 7, 8])
+        q_len, pos0 = rng.randint(1, 5000), rng.randint(0, 9000)
+        rts = -(-q_len // tokens)
+        tiles = [-(-(pos0 + min((r + 1) * tokens, q_len)) // tt) for r in range(rts)]
+        before = [floor_sum(r, tt, tokens, pos0 + tokens + tt - 1) for r in range(rts)]
+        assert before == [sum(tiles[:r]) for r in range(rts)]
+        for rem in [0, sum(tiles) - 1] + [rng.randrange(sum(tiles)) for _ in range(5)]:
+            a, e = 0, rts
+            while e - a > 1:
+                step = (e - a + 31) // 32
+                k = sum(c < e and before[c] <= rem for c in range(a, a + 32 * step, step)) - 1
+                a += k * step
+                e = min(e, a + step)
+            assert before[a] <= rem < before[a] + tiles[a]
 
 
 def test_the_other_decodes_refuse_the_block_scaled_kind(L):

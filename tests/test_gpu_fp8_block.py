@@ -278,6 +278,152 @@ def test_decode_of_an_empty_batch_and_on_another_stream():
     assert torch.equal(a, out)
 
 
+# ------------------------------------------------------------------ prefill
+def prefill(c, q, news, scale, ws=None, out=None, stream=None, max_new=None):
+    d = c.dev()
+    if ws is None:
+        n = pa.prefill_fp8_block_workspace_size(q.shape[1], c.H, c.D)
+        ws = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
+    out = torch.full_like(q, float("nan")) if out is None else out
+    cu = i32([0] + list(np.cumsum(news)))
+    pa.prefill_fp8_block(out, q, d["k"], d["v"], d["ks"], d["vs"], d["tables"], cu, d["lens"], c.H,
+                         max_new or max(news), scale, ws, stream=stream)
+    return out
+
+
+def check_prefill(c, G, q, news, out, scale, every=1):
+    got, qd = out.double().cpu().numpy(), q.double().cpu().numpy()
+    at = 0
+    for s, (n, t) in enumerate(zip(c.lens, news)):
+        for g in range(c.H if t else 0):
+            K, V, codes, vs = c.rows(s, g)
+            for i in sorted(set(list(range(0, t, every)) + [t - 1])):
+                for h in range(g * G, (g + 1) * G):
+                    seen = np.arange(n) <= n - t + i
+                    o, bound = row_bound(qd[at + i, h], K, V, codes, vs, seen, scale, q.dtype)
+                    assert (np.abs(got[at + i, h] - o) <= bound).all(), (s, i, h)
+        at += t
+    assert np.isfinite(got[:at]).all()
+
+
+def queries(news, heads, D, dtype, seed=3):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(sum(news), heads, D, generator=g) * 1.5).to(dtype)
+
+
+PREFILLS = [
+    # dtype, D, Hkv, G, bs, lens, news, spread, check every
+    (torch.bfloat16, 128, 1, 4, 32, [1], [1], 3, 1),
+    (torch.bfloat16, 128, 2, 4, 32, [5, 64, 33, 100], [5, 1, 3, 31], 3, 1),
+    (torch.float16, 64, 1, 8, 16, [16, 17, 0, 130], [16, 16, 0, 7], 6, 1),
+    (torch.bfloat16, 96, 2, 1, 64, [100, 127], [100, 128 - 1], 3, 5),
+    (torch.bfloat16, 128, 1, 4, 32, [300, 129, 700], [300, 64, 33], 3, 7),
+    (torch.float16, 128, 2, 3, 32, [257, 86], [257, 86], 8, 9),
+    (torch.bfloat16, 96, 1, 5, 16, [400, 51], [333, 51], 3, 11),
+    (torch.float16, 64, 2, 2, 64, [1000], [1000], 3, 41),
+    (torch.bfloat16, 64, 1, 7, 16, [200, 1, 90], [150, 1, 90], 10, 13),
+    (torch.bfloat16, 128, 1, 8, 32, [2500], [2], 3, 1),
+    (torch.bfloat16, 128, 1, 1, 32, [6000], [1], 3, 1),
+    (torch.bfloat16, 128, 8, 4, 32, [(37 * s) % 90 for s in range(40)],
+     [min((37 * s) % 90, 1 + s % 5) for s in range(40)], 3, 1),
+    (torch.float16, 64, 1, 4, 32, [128 + s for s in range(70)], [s for s in range(70)], 3, 17),
+]
+
+
+@pytest.mark.parametrize("dtype,D,Hkv,G,bs,lens,news,spread,every", PREFILLS)
+def test_prefill_matches_the_definition(dtype, D, Hkv, G, bs, lens, news, spread, every):
+    pa.get_device_error()
+    c = BlockCache(lens, Hkv, D, bs, seed=D + G, spread=spread)
+    q = queries(news, Hkv * G, D, dtype)
+    out = prefill(c, q.cuda(), news, default_scale(D))
+    assert pa.get_device_error() == 0
+    check_prefill(c, G, q, news, out, default_scale(D), every)
+    assert torch.equal(out, prefill(c, q.cuda(), news, default_scale(D)))  # the same bits again
+
+
+def test_prefill_of_one_token_is_the_decode():
+    c = BlockCache([400, 31, 64], 2, 128, 32, seed=2)
+    q = queries([1, 1, 1], 8, 128, torch.float16)
+    a, b = prefill(c, q.cuda(), [1, 1, 1], 0.1), decode(c, q.cuda(), 0.1)
+    check_prefill(c, 4, q, [1, 1, 1], a, 0.1)
+    check_decode(c, 4, q, b, 0.1)
+
+
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 3.0])
+@pytest.mark.parametrize("news", [[20], [150]])
+def test_prefill_with_other_scales(scale, news):
+    c = BlockCache([150], 1, 64, 32, seed=12)
+    q = queries(news, 4, 64, torch.bfloat16)
+    check_prefill(c, 4, q, news, prefill(c, q.cuda(), news, scale), scale, 7)
+
+
+@pytest.mark.parametrize("base", [-58, -30, 20, 50])
+@pytest.mark.parametrize("news", [[20, 40], [180, 3]])
+def test_prefill_over_small_and_large_scales(base, news):
+    c = BlockCache([300, 40], 2, 128, 32, seed=base % 97, spread=2, base=base)
+    c.ks = torch.where(c.ks.isnan(), c.ks, torch.exp2(c.ks.log2() - base - 6))  # K as usual
+    q = queries(news, 8, 128, torch.bfloat16)
+    check_prefill(c, 4, q, news, prefill(c, q.cuda(), news, default_scale(128)),
+                  default_scale(128), 17)
+
+
+def test_prefill_with_pages_of_zeros_and_scales_that_are_no_powers():
+    c = BlockCache([200], 1, 64, 16, seed=8, spread=2)
+    c.ks *= 1.3
+    c.vs *= 0.77
+    for p in (0, 3, 7):
+        blk = int(c.tables[0, p])
+        c.ks[blk], c.vs[blk] = 0.0, 0.0
+    for news in ([30], [200]):
+        q = queries(news, 4, 64, torch.float16)
+        check_prefill(c, 4, q, news, prefill(c, q.cuda(), news, 0.3), 0.3, 3)
+
+
+def test_prefill_flags_what_does_not_fit():
+    """Bad blocks read as zeros, bad lengths give zero rows, bad offsets leave theirs."""
+    pa.get_device_error()
+    c = BlockCache([100, 64, 200, 50], 2, 128, 32, seed=5)
+    news = [40, 64, 50, 50]
+    q = queries(news, 4, 128, torch.bfloat16).cuda()
+    good = prefill(c, q, news, 0.1)
+    assert pa.get_device_error() == 0
+    d = c.dev()
+    bad = int(c.tables[0, 1])
+    d["tables"][0, 1] = 10 ** 7
+    d["lens"][1] = 63  # fewer than its new tokens
+    out = prefill(c, q, news, 0.1)
+    assert pa.get_device_error() == 2 | 4
+    assert torch.equal(out[104:], good[104:]) and bool((out[40:104] == 0).all())
+    c.k[bad], c.v[bad] = 0, 0
+    c.ks[bad], c.vs[bad] = 1.0, 1.0
+    check_prefill(c, 2, q.cpu()[:40], [40], out[:40], 0.1, 3)
+    c2 = BlockCache([100, 64, 200, 50], 2, 128, 32, seed=5)
+    out = prefill(c2, q, news, 0.1, max_new=63)
+    assert pa.get_device_error() == 16
+    assert bool(out[40:104].isnan().all()) and torch.equal(out[:40], good[:40])
+    assert torch.equal(out[104:], good[104:])
+
+
+def test_prefill_captured_and_replayed_on_another_stream():
+    c = BlockCache([170, 33], 2, 128, 32, seed=6)
+    news = [170, 20]
+    q = queries(news, 8, 128, torch.float16).cuda()
+    a = prefill(c, q, news, 0.1)
+    st = torch.cuda.Stream()
+    ws = torch.zeros(pa.prefill_fp8_block_workspace_size(8, 2, 128), dtype=torch.uint8, device="cuda")
+    out, cu, d = torch.zeros_like(q), i32([0, 170, 190]), c.dev()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        pa.prefill_fp8_block(out, q, d["k"], d["v"], d["ks"], d["vs"], d["tables"], cu, d["lens"], 2,
+                             170, 0.1, ws, stream=st)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a, out)
+
+
 # ------------------------------------------------------------------ together
 def test_projection_to_attention_step_by_step():
     """norm_rope, append and decode as a model's layer calls them, against the definition over the
