@@ -45,6 +45,9 @@ namespace {
 constexpr float kChunkTop = 7.f;    // the largest weights' exponent above the reference
 constexpr float kChunkLazy = 8.f;   // how far the reference may lie behind
 constexpr int kChunkScaleRing = 8;  // tiles whose scales are kept
+// Bits kept beside the scales of 16 tokens: their K counts (it is zeros where the block id
+// is bad); K, and V, of the tile's every token count; from bit 8 on the rows of V that do.
+enum : int { kChunkKeyed = 1, kChunkAllK = 2, kChunkAllV = 4 };
 
 // NQ: query tiles of a CTA.
 template <int D, int NQ>
@@ -62,6 +65,9 @@ struct ChunkLayout {
   static constexpr int QBYTES1 = KB * kChunkRows * 128;  // a query tile: [KB][128 rows][128 B]
   static constexpr int SLOT = KB * TT * 128;             // a K or V tile: [KB][TT tokens][128 B]
   static constexpr int RAW = TT * D;                     // its codes: [TT][D]
+  // What a piece costs besides its tiles (query in, output out, an empty pipeline), in
+  // tiles: shares are cut by this cost.
+  static constexpr int PIECE = 1;
   static constexpr int SLOTS = DV == 128 ? 3 : 4;
   static constexpr int RSLOTS = 4;
   static constexpr int OFF_KV = NQ * QBYTES1;
@@ -130,28 +136,30 @@ __device__ __forceinline__ ChunkSeq chunk_seq(const ChunkParams& p, int s, bool 
   q.RT = static_cast<int>(((long long)q.q_len + p.tile_tokens - 1) / p.tile_tokens);
   return q;
 }
-// K/V tiles of row tile rt, and of the row tiles before it.
-template <int TT>
+// K/V tiles of row tile rt, and the units of the row tiles before it: a row tile is PIECE
+// units without a tile and one for each of its tiles.
+template <class Ly>
 __device__ __forceinline__ int chunk_tiles(const ChunkParams& p, const ChunkSeq& q, int rt) {
   const long long end = (long long)(rt + 1) * p.tile_tokens;
   const int last = end < q.q_len ? static_cast<int>(end) : q.q_len;  // tokens up to its last
-  return (q.n - q.q_len + last + TT - 1) / TT;
+  return (q.n - q.q_len + last + Ly::TT - 1) / Ly::TT;
 }
-template <int TT>
+template <class Ly>
 __device__ __forceinline__ long long chunk_before(const ChunkParams& p, const ChunkSeq& q, int rt) {
-  return floor_sum(rt, TT, p.tile_tokens,
-                   (long long)(q.n - q.q_len) + p.tile_tokens + TT - 1);
+  return floor_sum(rt, Ly::TT, p.tile_tokens,
+                   (long long)(q.n - q.q_len) + p.tile_tokens + Ly::TT - 1) +
+         (long long)rt * Ly::PIECE;
 }
-template <int TT>
+template <class Ly>
 __device__ __forceinline__ long long chunk_head_units(const ChunkParams& p, const ChunkSeq& q) {
   return q.RT == 0 ? 0
-                   : chunk_before<TT>(p, q, q.RT - 1) + chunk_tiles<TT>(p, q, q.RT - 1);
+                   : chunk_before<Ly>(p, q, q.RT - 1) + chunk_tiles<Ly>(p, q, q.RT - 1) + Ly::PIECE;
 }
 __device__ __forceinline__ long long chunk_share(long long P, int C) { return (P + C - 1) / C; }
 
 // Walk over the pieces of a CTA's share: the current piece is tiles [tile, tile + len)
-// of the T of (s, g, rt), `left` units of the share from it on.
-template <int TT>
+// of the T of (s, g, rt), `left` units of the share from it on (none: no more pieces).
+template <class Ly>
 struct ChunkWalk {
   ChunkSeq q;
   int s, g, rt, tile, len, T;
@@ -160,10 +168,11 @@ struct ChunkWalk {
     s = misc[0];
     g = misc[1];
     rt = misc[2];
-    tile = misc[3];
-    left = n;
+    const int skip = max(Ly::PIECE - misc[3], 0);
+    tile = misc[3] + skip - Ly::PIECE;
+    left = n - skip;
     q = chunk_seq(p, s, false);
-    T = chunk_tiles<TT>(p, q, rt);
+    T = chunk_tiles<Ly>(p, q, rt);
     len = static_cast<int>(left < T - tile ? left : T - tile);
   }
   __device__ __forceinline__ void next(const ChunkParams& p) {
@@ -171,6 +180,8 @@ struct ChunkWalk {
     tile += len;
     if (left <= 0) return;
     if (tile == T) {
+      left -= Ly::PIECE;
+      if (left <= 0) return;
       tile = 0;
       if (++rt == q.RT) {
         rt = 0;
@@ -182,7 +193,7 @@ struct ChunkWalk {
           } while (q.RT == 0 && s + 1 < p.num_seqs);
         }
       }
-      T = chunk_tiles<TT>(p, q, rt);
+      T = chunk_tiles<Ly>(p, q, rt);
     }
     len = static_cast<int>(left < T - tile ? left : T - tile);
   }
@@ -193,58 +204,45 @@ struct ChunkWalk {
   }
 };
 
-// The largest x + log2 vs of N tokens (N / 16 groups, their scales in sc: K scale times
-// the logit scale, log2 of the V scale). Without masks it is the largest product that
-// counts, and multiplying by a scale that is not negative keeps the order.
-template <int N>
-__device__ __forceinline__ float chunk_max(const uint32_t (&s)[N], const float4* sc, bool plain,
-                                           int lim) {
-  float best = -INFINITY;
+// 32 logits as they come from TMEM to x + log2 vs - mu (sc: their two groups' K scale times
+// the logit scale, and log2 of the V scale), and the largest of them.
+__device__ __forceinline__ float chunk_logits(uint32_t (&s)[32], const float4* sc, float mu,
+                                              bool masked, int lim) {
 #pragma unroll
-  for (int g = 0; g < N / 16; ++g) {
-    const float4 c = sc[g];
-    if (plain) {
-      float a[2] = {__uint_as_float(s[16 * g]), __uint_as_float(s[16 * g + 1])};
+  for (int g = 0; g < 2; ++g) {
+    const float2 c = *reinterpret_cast<const float2*>(sc + g);
+    const float2 k2 = make_float2(c.x, c.x), b2 = make_float2(c.y - mu, c.y - mu);
 #pragma unroll
-      for (int e = 2; e < 16; e += 2) {
-        a[0] = fmaxf(a[0], __uint_as_float(s[16 * g + e]));
-        a[1] = fmaxf(a[1], __uint_as_float(s[16 * g + e + 1]));
-      }
-      best = fmaxf(best, fmaf(fmaxf(a[0], a[1]), c.x, c.y));
-    } else {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float x = fmaf(__uint_as_float(s[16 * g + e]), c.x, c.y);
-        best = fmaxf(best, 16 * g + e < lim ? x : -INFINITY);
-      }
+    for (int e = 16 * g; e < 16 * g + 16; e += 2) {
+      const float2 x =
+          __ffma2_rn(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), k2, b2);
+      s[e] = __float_as_uint(x.x);
+      s[e + 1] = __float_as_uint(x.y);
     }
   }
-  return best;
-}
-
-// The weights of N tokens in pairs of f16, and their share of the sum.
-template <bool MASKED, int N>
-__device__ __forceinline__ void chunk_weigh(const uint32_t (&s)[N], const float4* sc, float mu,
-                                            int lim, float& sum, uint32_t (&pk)[N / 2]) {
+  if (masked) {
 #pragma unroll
-  for (int g = 0; g < N / 16; ++g) {
-    const float4 c = sc[g];
-    const float2 k2 = make_float2(c.x, c.x), b2 = make_float2(c.y - mu, c.y - mu);
+    for (int e = 0; e < 32; ++e) s[e] = e < lim ? s[e] : 0xFF800000u;
+  }
+  float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int e = 0; e < 32; ++e) a[e & 3] = fmaxf(a[e & 3], __uint_as_float(s[e]));
+  return fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
+}
+// Their weights in pairs of f16, and their share of the sum.
+__device__ __forceinline__ void chunk_weigh(const uint32_t (&s)[32], const float4* sc, float& sum,
+                                            uint32_t (&pk)[16]) {
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
     float2 part = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int e = 0; e < 16; e += 2) {
-      const int i = 16 * g + e;
-      const float2 x =
-          __ffma2_rn(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), k2, b2);
-      float2 w = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-      if constexpr (MASKED) {
-        w.x = i < lim ? w.x : 0.f;
-        w.y = i + 1 < lim ? w.y : 0.f;
-      }
+    for (int e = 16 * g; e < 16 * g + 16; e += 2) {
+      const float2 w = make_float2(ex2_approx(__uint_as_float(s[e])),
+                                   ex2_approx(__uint_as_float(s[e + 1])));
       part = __fadd2_rn(part, w);
-      pk[i / 2] = Mma<__half>::pack(w.x, w.y);
+      pk[e / 2] = Mma<__half>::pack(w.x, w.y);
     }
-    sum = fmaf(part.x + part.y, c.z, sum);
+    sum = fmaf(part.x + part.y, sc[g].z, sum);
   }
 }
 
@@ -279,7 +277,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, NQ>::THREADS, ChunkLayout<D, NQ
   // impossible get zero rows
   if (warp == Ly::COPY_WARP) {
     auto head_units = [&](int s) -> long long {
-      return s < S ? chunk_head_units<TT>(p, chunk_seq(p, s, false)) : 0;
+      return s < S ? chunk_head_units<Ly>(p, chunk_seq(p, s, false)) : 0;
     };
     const long long u0 = head_units(lane) * Hkv, incl0 = warp_incl(u0, lane);
     long long P = __shfl_sync(0xffffffffu, incl0, 31);
@@ -306,13 +304,13 @@ __global__ void __launch_bounds__(ChunkLayout<D, NQ>::THREADS, ChunkLayout<D, NQ
           int a = 0, e = q.RT;
           while (e - a > 1) {
             const int step = (e - a + 31) / 32, cand = a + lane * step;
-            const bool ok = cand < e && chunk_before<TT>(p, q, cand) <= rem;
+            const bool ok = cand < e && chunk_before<Ly>(p, q, cand) <= rem;
             const int k = __popc(__ballot_sync(0xffffffffu, ok)) - 1;
             a += k * step;
             e = min(e, a + step);
           }
           at.z = a;
-          at.w = static_cast<int>(rem - chunk_before<TT>(p, q, a));
+          at.w = static_cast<int>(rem - chunk_before<Ly>(p, q, a));
           break;
         }
         run += __shfl_sync(0xffffffffu, incl, 31);
@@ -365,7 +363,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, NQ>::THREADS, ChunkLayout<D, NQ
   if (!aligned && tid == 0) raise_error(err, PA_DEVERR_TIMEOUT);  // never: see __align__ above
 
   if (units > 0 && aligned) {
-    ChunkWalk<TT> w;
+    ChunkWalk<Ly> w;
     w.set(p, misc, units);
     // query tiles of the current piece that have rows (the first always has)
     auto live_tiles = [&]() -> int { return NQ == 1 ? 1 : (w.rows(p) > kChunkRows ? 2 : 1); };
@@ -380,7 +378,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, NQ>::THREADS, ChunkLayout<D, NQ
       // Lane g looks at 16 tokens of a tile: their page's index among all (block, kv
       // head) pages (-1 past the sequence's end, -2 for a bad id) and what the softmax
       // and the widening want to know of them: K scale times the logit scale, log2 of
-      // the V scale and one over it, and as bits: 1 where K counts, 2 times the rows of V.
+      // the V scale and one over it, and what counts, as bits.
       auto lookup = [&](int i, int& y, float4& f) {
         const int t = (w.tile + i) * TT + 16 * lane;
         y = -1;
@@ -401,9 +399,9 @@ __global__ void __launch_bounds__(ChunkLayout<D, NQ>::THREADS, ChunkLayout<D, NQ
         f.y = lv;
         f.z = exp2f(-lv);
         const int rows = min(16, w.q.n - t);
-        f.w = __int_as_float(1 | (fabsf(vs) >= 0x1p-60f ? 2 * rows : 0));
+        f.w = __int_as_float(kChunkKeyed | (fabsf(vs) >= 0x1p-60f ? rows << 8 : 0));
       };
-      int len = uniform(w.len);
+      int len = uniform(w.left > 0 ? w.len : 0);
       while (len > 0 && ok) {
         int y_next;
         float4 f_next;
@@ -421,7 +419,12 @@ __global__ void __launch_bounds__(ChunkLayout<D, NQ>::THREADS, ChunkLayout<D, NQ
             if (filled >= RS) ok = warp_wait(&raw_empty[rs], ph);
             if (!ok) break;
             if (kv == 0) {  // the tile's scales, before its codes
-              if (lane < NG) sc[ring * NG + lane] = f_here;
+              const int what = __float_as_int(f_here.w);
+              const bool all_k = __all_sync(0xffffffffu, lane >= NG || (what & kChunkKeyed));
+              const bool all_v = __all_sync(0xffffffffu, lane >= NG || (what >> 8) == 16);
+              float4 f = f_here;
+              f.w = __int_as_float(what | (all_k ? kChunkAllK : 0) | (all_v ? kChunkAllV : 0));
+              if (lane < NG) sc[ring * NG + lane] = f;
               __syncwarp();
               if (lane == 0) mbar_arrive(&sc_full[ring]);
             }
@@ -520,7 +523,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, NQ>::THREADS, ChunkLayout<D, NQ
         return true;
       };
       bool ok = true;
-      int len = uniform(w.len);
+      int len = uniform(w.left > 0 ? w.len : 0);
       for (int piece[2] = {0, 0}; len > 0 && ok;) {
         const int nq = uniform(live_tiles());
 #pragma unroll
@@ -555,33 +558,45 @@ __global__ void __launch_bounds__(ChunkLayout<D, NQ>::THREADS, ChunkLayout<D, NQ
       bool ok = true;
       int sl = 0, rs = 0, filled = 0, ring = 0;
       uint32_t ph = 1, rph = 0;
-      for (long long k = 0; k < 2 * units && ok; ++k) {
-        const bool is_v = k & 1;
+      for (int i2 = 0; w.left > 0 && ok;) {
+        const bool is_v = i2 & 1;
         ok = warp_wait(&raw_full[rs], rph);
         if (ok && filled >= NS) ok = warp_wait(&empty[sl], ph);
         if (!ok) break;
         uint8_t* dst = smem + Ly::OFF_KV + sl * Ly::SLOT;
         const uint4* raw = reinterpret_cast<const uint4*>(smem + Ly::OFF_RAW + rs * Ly::RAW);
         const float4* scg = sc + ring * NG;
-#pragma unroll 4
-        for (int j = 0; j < NJ; ++j) {
-          const int i = cid + j * Ly::CONV, row = i / CPR, c16 = i % CPR;
-          uint4 src = raw[i];
-          const int what = __float_as_int(scg[row >> 4].w);
-          if (is_v ? 2 * (row & 15) >= (what & ~1) : what == 0) src = make_uint4(0u, 0u, 0u, 0u);
-          uint4 o[2];
-          widen8<E4M3>(src.x, o[0].x, o[0].y);
-          widen8<E4M3>(src.y, o[0].z, o[0].w);
-          widen8<E4M3>(src.z, o[1].x, o[1].y);
-          widen8<E4M3>(src.w, o[1].z, o[1].w);
-          // the second column block's lanes store their odd chunk first, so that
-          // the eight lanes of a row (D 128) cover all banks
-          const int sw = (KB == 2 && c16 >= 4) ? 1 : 0;
+        const bool every = __float_as_int(scg[0].w) & (is_v ? kChunkAllV : kChunkAllK);
+        uint4 src[4];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int ch = 2 * c16 + (h ^ sw);
-            *reinterpret_cast<uint4*>(dst + (ch >> 3) * (TT * 128) + row * 128 +
-                                      (((ch & 7) ^ (row & 7)) << 4)) = sw ^ h ? o[1] : o[0];
+        for (int j0 = 0; j0 < NJ; j0 += 4) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (j0 + x < NJ) src[x] = raw[cid + (j0 + x) * Ly::CONV];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int j = j0 + x;
+            if (j >= NJ) break;
+            const int i = cid + j * Ly::CONV, row = i / CPR, c16 = i % CPR;
+            if (!every) {
+              const int what = __float_as_int(scg[row >> 4].w);
+              if (is_v ? (row & 15) >= (what >> 8) : !(what & 1))
+                src[x] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            uint4 o[2];
+            widen8<E4M3>(src[x].x, o[0].x, o[0].y);
+            widen8<E4M3>(src[x].y, o[0].z, o[0].w);
+            widen8<E4M3>(src[x].z, o[1].x, o[1].y);
+            widen8<E4M3>(src[x].w, o[1].z, o[1].w);
+            // the second column block's lanes store their odd chunk first, so that
+            // the eight lanes of a row (D 128) cover all banks
+            const int sw = (KB == 2 && c16 >= 4) ? 1 : 0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int ch = 2 * c16 + (h ^ sw);
+              *reinterpret_cast<uint4*>(dst + (ch >> 3) * (TT * 128) + row * 128 +
+                                        (((ch & 7) ^ (row & 7)) << 4)) = sw ^ h ? o[1] : o[0];
+            }
           }
         }
         fence_proxy_async_smem();
@@ -600,6 +615,10 @@ __global__ void __launch_bounds__(ChunkLayout<D, NQ>::THREADS, ChunkLayout<D, NQ
           rph ^= 1;
         }
         if (is_v) ring = (ring + 1) % kChunkScaleRing;
+        if (++i2 == 2 * w.len) {
+          i2 = 0;
+          w.next(p);
+        }
       }
       if (!ok && lane == 0) raise_error(err, PA_DEVERR_TIMEOUT);
     } else {
@@ -625,45 +644,56 @@ __global__ void __launch_bounds__(ChunkLayout<D, NQ>::THREADS, ChunkLayout<D, NQ
         pos = w.q.n - w.q.q_len + token;
         orow = static_cast<uint32_t>(w.q.q0 + token) * Hq + w.g * G + (live ? r % G : 0);
       };
+      // the row's query into shared memory, in f16 (exact inside f16's range): every S
+      // product on the last piece's has completed
       constexpr int QCH = D / 8;  // 16-byte chunks of a query row
       auto load_q = [&]() {
         const uint8_t* src = static_cast<const uint8_t*>(p.query) + (size_t)orow * D * 2;
+        // (eight at a time: all in flight at once cost registers that other branches lack)
+        constexpr int B = QCH % 8 == 0 ? 8 : QCH;
 #pragma unroll
-        for (int ch = 0; ch < QCH; ++ch)
-          cp_async16(smem_u32(qrow) + (ch >> 3) * (kChunkRows * 128) + (((ch & 7) ^ (r1 & 7)) << 4),
-                     src + ch * 16, live);
-      };
-      set_row();
-      bool work = q < live_tiles();
-      if (work) load_q();
-      for (int piece = 0; w.left > 0; ++piece) {
-        if (work) {
-          cp_async_wait_all();
-          if constexpr (std::is_same<QT, __nv_bfloat16>::value) {
-            // q is carried in f16 (exact inside f16's range)
+        for (int c0 = 0; c0 < QCH; c0 += B) {
+          uint4 v[B];
 #pragma unroll
-            for (int ch = 0; ch < QCH; ++ch) {
-              uint4* q16 = reinterpret_cast<uint4*>(qrow + (ch >> 3) * (kChunkRows * 128) +
-                                                    (((ch & 7) ^ (r1 & 7)) << 4));
-              uint4 v = *q16;
-              uint32_t* e = reinterpret_cast<uint32_t*>(&v);
+          for (int x = 0; x < B; ++x)
+            v[x] = live ? __ldg(reinterpret_cast<const uint4*>(src) + c0 + x)
+                        : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int x = 0; x < B; ++x) {
+            const int ch = c0 + x;
+            if constexpr (std::is_same<QT, __nv_bfloat16>::value) {
+              uint32_t* e = reinterpret_cast<uint32_t*>(&v[x]);
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 const __nv_bfloat162 b = *reinterpret_cast<const __nv_bfloat162*>(&e[j]);
                 const __half2 h = __floats2half2_rn(__low2float(b), __high2float(b));
                 e[j] = *reinterpret_cast<const uint32_t*>(&h);
               }
-              *q16 = v;
             }
+            *reinterpret_cast<uint4*>(qrow + (ch >> 3) * (kChunkRows * 128) +
+                                      (((ch & 7) ^ (r1 & 7)) << 4)) = v[x];
           }
-          fence_proxy_async_smem();
-          mbar_arrive(&q_full[q]);
-
-          // a warp without rows only keeps the barriers' count (its rows of S, P and O may
-          // hold anything: no product mixes rows)
-          const bool warp_live = q * kChunkRows + (warp & 3) * 32 < w.rows(p);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&q_full[q]);
+      };
+      bool work = false;
+      if (w.left > 0) {
+        set_row();
+        work = q < live_tiles();
+        if (work) load_q();
+      }
+      for (int piece = 0; w.left > 0; ++piece) {
+        const bool here = work, was_live = live;
+        const uint32_t out_row = orow;
+        // a warp without rows only keeps the barriers' count (its rows of S, P and O may
+        // hold anything: no product mixes rows)
+        const bool warp_live = here && q * kChunkRows + (warp & 3) * 32 < w.rows(p);
+        const bool whole = w.len == w.T;
+        float m = -INFINITY, l = 0.f;
+        if (here) {
           const int first_pos = __reduce_min_sync(0xffffffffu, live ? pos : 0x7FFFFFFF);
-          float m = -INFINITY, l = 0.f;
+          float mu = 0.f;  // what weights are held relative to: m - 7 (nothing seen yet: 0)
           for (int i = 0; i < w.len; ++i, ++c) {
             const uint32_t b = NQ == 2 ? q : c & 1, u = NQ == 2 ? c : c >> 1;
             const int t0 = (w.tile + i) * TT;
@@ -682,56 +712,78 @@ __global__ void __launch_bounds__(ChunkLayout<D, NQ>::THREADS, ChunkLayout<D, NQ
               __syncwarp();
               const uint32_t t_s = tmem + b * TT + lane_off;
               const bool masked = t0 + TT - 1 > first_pos;  // warp-uniform
-              const int lim = live ? pos - t0 + 1 : 0;      // tokens of the tile that the row sees
-              const bool plain = !masked && p.scale_log2 >= 0.f;
-              float mx = -INFINITY;
+              const int lim = live ? pos - t0 + 1 : 0;      // tokens that the row sees
+              // 32 logits become weights, over columns whose logits have been read; the next 32
+              // are on their way meanwhile
+              auto part = [&](uint32_t (&sr)[32], int h) -> bool {
+                const float mx = chunk_logits(sr, sct + 2 * h, mu, masked, lim - 32 * h);
+                // (with nothing seen yet any logit moves the reference)
+                if (__any_sync(0xffffffffu, m == -INFINITY ? mx != -INFINITY
+                                                          : mx > kChunkTop + kChunkLazy)) {
+                  // whole numbers, so that what is there is scaled by powers of two: exactly
+                  const float mn = mx == -INFINITY ? m : fmaxf(m, ceilf(mx + mu));
+                  const float al = m == -INFINITY ? 1.f : exp2f(m - mn);
+                  if (i > 0) {  // O holds the tiles so far, once the last P V has landed
+                    const uint32_t cp = c - 1, bp = NQ == 2 ? q : cp & 1, up = NQ == 2 ? cp : cp >> 1;
+                    if (!warp_wait(&pv_done[bp], up & 1)) return false;
+                    tc05_fence_after();
+                    __syncwarp();
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D; c0 += 16) {
+                      uint32_t o[16];
+                      tmem_ld16(t_o + c0, o);
+                      tmem_wait_ld();
 #pragma unroll
-              for (int h = 0; h < TT / 32; ++h) {
-                uint32_t sr[32];
-                tmem_ld32(t_s + 32 * h, sr);
-                tmem_wait_ld();
-                mx = fmaxf(mx, chunk_max(sr, sct + 2 * h, plain, masked ? lim - 32 * h : 32));
-              }
-              if (__any_sync(0xffffffffu, mx > m + kChunkLazy)) {
-                const float mn = fmaxf(m, mx);
-                if (i > 0) {
-                  // O holds the tiles so far: scale it by 2^(m - mn) once the last P V
-                  // has landed
-                  const uint32_t cp = c - 1, bp = NQ == 2 ? q : cp & 1, up = NQ == 2 ? cp : cp >> 1;
-                  if (!warp_wait(&pv_done[bp], up & 1)) {
-                    failed = true;
-                    break;
+                      for (int e = 0; e < 16; ++e)
+                        o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+                      tmem_st16(t_o + c0, o);
+                    }
                   }
-                  tc05_fence_after();
-                  __syncwarp();
-                  const float al = mn == -INFINITY ? 1.f : exp2f(m - mn);
+                  if (h > 0) {  // and the weights of this tile that are there
+                    tmem_wait_st();
+#pragma unroll 1
+                    for (int k = 0; k < h; ++k) {
+                      uint32_t o[16];
+                      tmem_ld16(t_s + 16 * k, o);
+                      tmem_wait_ld();
 #pragma unroll
-                  for (int c0 = 0; c0 < D; c0 += 16) {
-                    uint32_t o[16];
-                    tmem_ld16(t_o + c0, o);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                      o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
-                    tmem_st16(t_o + c0, o);
+                      for (int e = 0; e < 16; ++e) {
+                        const float2 x = __half22float2(*reinterpret_cast<__half2*>(&o[e]));
+                        o[e] = Mma<__half>::pack(x.x * al, x.y * al);
+                      }
+                      tmem_st16(t_s + 16 * k, o);
+                    }
                   }
-                  tmem_wait_st();
                   l *= al;
-                }
-                m = mn;
-              }
-              const float mu = m == -INFINITY ? 0.f : m - kChunkTop;  // (nothing seen yet: zeros)
-              // weights over the logits that have been read
+                  m = mn;
+                  const float to = m == -INFINITY ? 0.f : m - kChunkTop;
+                  const float down = to - mu;
+                  mu = to;
 #pragma unroll
-              for (int h = 0; h < TT / 32; ++h) {
-                uint32_t sr[32], pk[16];
-                tmem_ld32(t_s + 32 * h, sr);
-                tmem_wait_ld();
-                if (masked)
-                  chunk_weigh<true>(sr, sct + 2 * h, mu, lim - 32 * h, l, pk);
-                else
-                  chunk_weigh<false>(sr, sct + 2 * h, mu, 32, l, pk);
+                  for (int e = 0; e < 32; ++e)
+                    sr[e] = __float_as_uint(__uint_as_float(sr[e]) - down);
+                }
+                uint32_t pk[16];
+                chunk_weigh(sr, sct + 2 * h, l, pk);
                 tmem_st16(t_s + 16 * h, pk);
+                return true;
+              };
+              uint32_t ra[32], rb[32];
+              tmem_ld32(t_s, ra);
+              tmem_wait_ld();
+              bool fine = true;
+#pragma unroll 1
+              for (int h = 0; h < TT / 32 && fine; h += 2) {
+                tmem_ld32(t_s + 32 * (h + 1), rb);
+                fine = part(ra, h);
+                tmem_wait_ld();
+                if (h + 2 < TT / 32) tmem_ld32(t_s + 32 * (h + 2), ra);
+                fine = fine && part(rb, h + 1);
+                tmem_wait_ld();
+              }
+              if (!fine) {
+                failed = true;
+                break;
               }
               tmem_wait_st();
             }
@@ -739,18 +791,17 @@ __global__ void __launch_bounds__(ChunkLayout<D, NQ>::THREADS, ChunkLayout<D, NQ
             mbar_arrive(&p_full[b]);
           }
           if (failed) break;
+        }
+        // the next piece's query, so that its first product runs under what follows
+        ct += w.len;
+        w.next(p);
+        if (w.left > 0) {
+          set_row();
+          work = q < live_tiles();
+          if (work) load_q();
+        }
+        if (here) {
           // ---- the row's output, or its partial
-          const bool whole = w.len == w.T, was_live = live;
-          const uint32_t out_row = orow;
-          // the next piece's query is on its way meanwhile (all S products on this one's
-          // have completed)
-          ct += w.len;
-          w.next(p);
-          if (w.left > 0) {
-            set_row();
-            work = q < live_tiles();
-            if (work) load_q();
-          }
           const uint32_t cl = c - 1, bl = NQ == 2 ? q : cl & 1, ul = NQ == 2 ? cl : cl >> 1;
           if (!warp_wait(&pv_done[bl], ul & 1)) {
             failed = true;
@@ -763,7 +814,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, NQ>::THREADS, ChunkLayout<D, NQ
           QT* dst = static_cast<QT*>(p.out) + (size_t)out_row * D;
           float4* po = p.part_o + slot * (D / 4) * ROWS + q * kChunkRows + r1;
           if (warp_live) {
-#pragma unroll
+#pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 32) {
               uint32_t o[32];
               tmem_ld32(t_o + c0, o);
@@ -792,15 +843,6 @@ __global__ void __launch_bounds__(ChunkLayout<D, NQ>::THREADS, ChunkLayout<D, NQ
           // the accumulator has been read before the next piece's weights (whose arrival
           // lets the products overwrite it) are announced
           tc05_fence_before();
-        } else {
-          // no rows for this query tile in the piece
-          ct += w.len;
-          w.next(p);
-          if (w.left > 0) {
-            set_row();
-            work = q < live_tiles();
-            if (work) load_q();
-          }
         }
       }
       if (failed) raise_error(err, PA_DEVERR_TIMEOUT);
@@ -818,29 +860,30 @@ __global__ void __launch_bounds__(ChunkLayout<D, NQ>::THREADS, ChunkLayout<D, NQ
 
 // Joins the partial rows of the row tiles that the shares cut: with a running maximum M
 // of the pieces' references m_j, out = sum_j 2^(m_j - M) o_j / sum_j 2^(m_j - M) l_j.
-// CTA (slice of columns, share): the first share that begins inside a row tile joins it. A
+// CTA (slice of columns, share): the first share that begins inside a row tile's tiles joins it. A
 // thread takes four columns of one row, rows fastest, as the partials are stored.
 constexpr int kChunkJoinThreads = 256;
 template <typename QT, int D, int NQ>
 __global__ void __launch_bounds__(kChunkJoinThreads)
     chunk_join_kernel(const __grid_constant__ ChunkParams p) {
-  constexpr int R = ChunkLayout<D, NQ>::ROWS, TT = ChunkLayout<D, NQ>::TT;
+  using Ly = ChunkLayout<D, NQ>;
+  constexpr int R = Ly::ROWS;
   constexpr int SIDE = kChunkJoinThreads / R;  // column groups side by side
   const int tid = threadIdx.x, c = blockIdx.y + 1;
   pdl_wait();
   pdl_trigger();
   const int4 at = __ldcg(p.starts + c);
   const long long P = __ldcg(p.total);
-  if (at.w == 0) return;  // the share begins with a row tile, or is empty
+  if (at.w <= Ly::PIECE) return;  // the share begins with a row tile, or is empty
   const long long U = chunk_share(P, p.ctas);
-  const long long seg0 = c * U - at.w;  // the row tile's first unit
-  const int c0 = static_cast<int>(seg0 / U);
+  const long long seg0 = c * U - at.w, tile0 = seg0 + Ly::PIECE;  // the row tile's units, tiles
+  const int c0 = static_cast<int>(tile0 / U);
   if (c0 + 1 != c) return;  // another share joins it
   const ChunkSeq q = chunk_seq(p, at.x, false);
-  const int T = chunk_tiles<TT>(p, q, at.z);
-  const int n = static_cast<int>((seg0 + T - 1) / U) - c0 + 1;
+  const int T = chunk_tiles<Ly>(p, q, at.z);
+  const int n = static_cast<int>((tile0 + T - 1) / U) - c0 + 1;
   // piece j sits in CTA c0 + j: in its first slot unless it began after other work
-  const int first = seg0 != c0 * U ? 1 : 0;
+  const int first = c0 * U < seg0 ? 1 : 0;
   const int lr = tid % R;
   const long long token = (long long)at.z * p.tile_tokens + lr / p.group;
   if (lr >= p.tile_tokens * p.group || token >= q.q_len) return;

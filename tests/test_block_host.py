@@ -141,8 +141,8 @@ def floor_sum(n, m, a, b):
 
 
 def test_the_shares_cover_every_tile_once():
-    """The prefill's arithmetic restated: units before a row tile, and the search for a share's
-    first one."""
+    """The prefill's arithmetic restated: units before a row tile (one besides its tiles each),
+    the search for a share's first one, and the shares' pieces."""
     rng = random.Random(5)
     for _ in range(300):
         tt, tokens = rng.choice([(64, 128), (128, 256)])
@@ -150,16 +150,43 @@ def test_the_shares_cover_every_tile_once():
         q_len, pos0 = rng.randint(1, 5000), rng.randint(0, 9000)
         rts = -(-q_len // tokens)
         tiles = [-(-(pos0 + min((r + 1) * tokens, q_len)) // tt) for r in range(rts)]
-        before = [floor_sum(r, tt, tokens, pos0 + tokens + tt - 1) for r in range(rts)]
-        assert before == [sum(tiles[:r]) for r in range(rts)]
-        for rem in [0, sum(tiles) - 1] + [rng.randrange(sum(tiles)) for _ in range(5)]:
+        before = [floor_sum(r, tt, tokens, pos0 + tokens + tt - 1) + r for r in range(rts)]
+        assert before == [sum(tiles[:r]) + r for r in range(rts)]
+        total = sum(tiles) + rts
+        for rem in [0, total - 1] + [rng.randrange(total) for _ in range(5)]:
             a, e = 0, rts
             while e - a > 1:
                 step = (e - a + 31) // 32
                 k = sum(c < e and before[c] <= rem for c in range(a, a + 32 * step, step)) - 1
                 a += k * step
                 e = min(e, a + step)
-            assert before[a] <= rem < before[a] + tiles[a]
+            assert before[a] <= rem < before[a] + tiles[a] + 1
+        # every CTA walks its share; a row tile's pieces are those that its join looks for
+        ctas = rng.choice([1, 2, 7, 152, 304])
+        share = -(-total // ctas)
+        pieces = {}
+        for c in range(ctas):
+            lo = min(c * share, total)
+            left = min(lo + share, total) - lo
+            if left == 0:
+                continue
+            r = max(i for i in range(rts) if before[i] <= lo)
+            skip = max(1 - (lo - before[r]), 0)
+            tile, left, index = lo - before[r] + skip - 1, left - skip, 0
+            while left > 0:
+                n = min(left, tiles[r] - tile)
+                pieces.setdefault(r, []).append((c, min(index, 1), tile, n))
+                index, left, tile = index + 1, left - n, tile + n
+                if left > 0 and tile == tiles[r]:
+                    left, tile, r = left - 1, 0, r + 1
+        for r in range(rts):
+            assert [p[2] for p in pieces[r]] == [sum(p[3] for p in pieces[r][:j])
+                                                 for j in range(len(pieces[r]))]
+            assert sum(p[3] for p in pieces[r]) == tiles[r]
+            c0 = (before[r] + 1) // share
+            n = (before[r] + tiles[r]) // share - c0 + 1
+            first = 1 if c0 * share < before[r] else 0
+            assert [p[:2] for p in pieces[r]] == [(c0 + j, first if j == 0 else 0) for j in range(n)]
 
 
 def test_the_other_decodes_refuse_the_block_scaled_kind(L):
