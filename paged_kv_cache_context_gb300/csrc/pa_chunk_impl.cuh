@@ -44,6 +44,7 @@ namespace {
 
 constexpr float kChunkTop = 7.f;    // the largest weights' exponent above the reference
 constexpr float kChunkLazy = 8.f;   // how far the reference may lie behind
+constexpr uint32_t kChunkPolls = 1u << 22;  // polls of a wait before it gives up
 constexpr int kChunkScaleRing = 8;  // tiles whose scales are kept
 // Bits kept beside the scales of 16 tokens: their K counts (it is zeros where the block id
 // is bad); K, and V, of the tile's every token count; from bit 8 on the rows of V that do.
@@ -56,8 +57,9 @@ struct ChunkLayout {
   static constexpr int KB = DV / 64;             // 128-byte column blocks of a row
   static constexpr int TT = NQ == 2 ? 128 : 64;  // tokens of a tile
   static constexpr int NG = TT / 16;             // scale groups of a tile
+  static constexpr int HALVES = TT / 64;         // parts whose weights are handed on together
   static constexpr int ROWS = NQ * kChunkRows;
-  static constexpr int SMX = 4 * NQ;  // softmax warps
+  static constexpr int SMX = 4 * NQ;  // softmax warps, a thread per row
   static constexpr int MMA_WARP = SMX, COPY_WARP = SMX + 1, CONV_WARP = SMX + 2;
   static constexpr int CONV = 128;  // widening threads
   static constexpr int THREADS = CONV_WARP * 32 + CONV;
@@ -74,7 +76,7 @@ struct ChunkLayout {
   static constexpr int OFF_RAW = OFF_KV + SLOTS * SLOT;
   static constexpr int OFF_SC = OFF_RAW + RSLOTS * RAW;  // [ring][NG] of float4
   static constexpr int OFF_BAR = OFF_SC + kChunkScaleRing * NG * 16;
-  static constexpr int NBAR = 2 * SLOTS + 2 * RSLOTS + 2 + 2 + 2 + NQ + kChunkScaleRing;
+  static constexpr int NBAR = 2 * SLOTS + 2 * RSLOTS + 6 + 2 * HALVES + NQ + kChunkScaleRing;
   static constexpr int OFF_MISC = (OFF_BAR + NBAR * 8 + 15) / 16 * 16;
   static constexpr int SMEM = OFF_MISC + 64;
   // TMEM columns: S buffer b at b TT, O of query tile q at 2 TT + q DV
@@ -89,7 +91,7 @@ struct ChunkLayout {
 
 // sum of floor((a i + b) / m) over i in [0, n), m a power of two (all >= 0; by turns of
 // Euclid's algorithm on a and m).
-__device__ __forceinline__ long long floor_sum(long long n, int m, int a, long long b) {
+__device__ __noinline__ long long floor_sum(long long n, int m, int a, long long b) {
   unsigned long long sum = 0, N = n, M = m, A = a, B = b;
   while (N > 0) {
     // (small divisors: 32-bit divisions where the operands allow)
@@ -204,72 +206,628 @@ struct ChunkWalk {
   }
 };
 
-// 32 logits as they come from TMEM to x + log2 vs - mu (sc: their two groups' K scale times
-// the logit scale, and log2 of the V scale), and the largest of them.
-__device__ __forceinline__ float chunk_logits(uint32_t (&s)[32], const float4* sc, float mu,
-                                              bool masked, int lim) {
-#pragma unroll
-  for (int g = 0; g < 2; ++g) {
-    const float2 c = *reinterpret_cast<const float2*>(sc + g);
-    const float2 k2 = make_float2(c.x, c.x), b2 = make_float2(c.y - mu, c.y - mu);
-#pragma unroll
-    for (int e = 16 * g; e < 16 * g + 16; e += 2) {
-      const float2 x =
-          __ffma2_rn(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), k2, b2);
-      s[e] = __float_as_uint(x.x);
-      s[e + 1] = __float_as_uint(x.y);
-    }
-  }
-  if (masked) {
-#pragma unroll
-    for (int e = 0; e < 32; ++e) s[e] = e < lim ? s[e] : 0xFF800000u;
-  }
-  float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-  for (int e = 0; e < 32; ++e) a[e & 3] = fmaxf(a[e & 3], __uint_as_float(s[e]));
-  return fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
+__device__ __forceinline__ void st_global_v8(void* dst, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
-// Their weights in pairs of f16, and their share of the sum.
-__device__ __forceinline__ void chunk_weigh(const uint32_t (&s)[32], const float4* sc, float& sum,
+
+// A bounded wait of a whole warp, by polls (each of which waits a while by itself): a few
+// instructions where one by the clock, inlined some thirty times, spread the roles' loops
+// over more than the instruction cache.
+__device__ __forceinline__ bool chunk_wait(uint64_t* bar, uint32_t parity) {
+  bool ok = false;
+#pragma unroll 1
+  for (uint32_t n = 0; !ok && n < kChunkPolls; ++n) ok = mbar_try_wait(bar, parity);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// The weights 2^y of 32 tokens in pairs of f16; `sum` takes them over their two groups' V scale.
+__device__ __forceinline__ void chunk_weigh(const float2 (&y)[16], const float4* sc, float& sum,
                                             uint32_t (&pk)[16]) {
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
     float2 part = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int e = 16 * g; e < 16 * g + 16; e += 2) {
-      const float2 w = make_float2(ex2_approx(__uint_as_float(s[e])),
-                                   ex2_approx(__uint_as_float(s[e + 1])));
+    for (int e = 8 * g; e < 8 * g + 8; ++e) {
+      const float2 w = make_float2(ex2_approx(y[e].x), ex2_approx(y[e].y));
       part = __fadd2_rn(part, w);
-      pk[e / 2] = Mma<__half>::pack(w.x, w.y);
+      pk[e] = Mma<__half>::pack(w.x, w.y);
     }
     sum = fmaf(part.x + part.y, sc[g].z, sum);
   }
+}
+__device__ __forceinline__ float chunk_largest(const float2 (&y)[16]) {
+  float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int e = 0; e < 16; ++e) a[e & 3] = fmaxf(a[e & 3], fmaxf(y[e].x, y[e].y));
+  return fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
+}
+
+// Shared memory, at an offset that the compiler does not know to be zero: what it derives for
+// one role is not computed, and kept in registers, ahead of all of them (that spilled).
+template <class Ly>
+struct ChunkSmem {
+  uint8_t* base;
+  uint64_t* full;       // [SLOTS] a widened tile is there
+  uint64_t* empty;      // [SLOTS] its products are done
+  uint64_t* raw_full;   // [RSLOTS] codes have landed
+  uint64_t* raw_empty;  // [RSLOTS] and have been read
+  uint64_t* s_full;     // [2] S is in its buffer
+  uint64_t* p_full;     // [2][HALVES] the weights of 64 tokens are
+  uint64_t* half_done;  // [2] the first 64 tokens' have been used
+  uint64_t* pv_done;    // [2] all have
+  uint64_t* q_full;     // [NQ] the queries are there
+  uint64_t* sc_full;    // [ring] a tile's scales are
+  float4* sc;           // [ring][NG]
+  int* misc;            // the share: sequence, kv head, row tile, first unit
+  long long* units;     // and its length
+  uint32_t* tmem;
+  __device__ __forceinline__ ChunkSmem() {
+    extern __shared__ __align__(1024) uint8_t dynamic_smem[];
+    uint32_t zero = 0;
+    asm volatile("" : "+r"(zero));
+    uint8_t* smem = dynamic_smem + zero;
+    base = smem;
+    full = reinterpret_cast<uint64_t*>(smem + Ly::OFF_BAR);
+    empty = full + Ly::SLOTS;
+    raw_full = empty + Ly::SLOTS;
+    raw_empty = raw_full + Ly::RSLOTS;
+    s_full = raw_empty + Ly::RSLOTS;
+    p_full = s_full + 2;
+    half_done = p_full + 2 * Ly::HALVES;
+    pv_done = half_done + 2;
+    q_full = pv_done + 2;
+    sc_full = q_full + Ly::ROWS / kChunkRows;
+    sc = reinterpret_cast<float4*>(smem + Ly::OFF_SC);
+    misc = reinterpret_cast<int*>(smem + Ly::OFF_MISC);
+    units = reinterpret_cast<long long*>(smem + Ly::OFF_MISC + 16);
+    tmem = reinterpret_cast<uint32_t*>(smem + Ly::OFF_MISC + 32);
+  }
+};
+
+// ---- copies, one warp: K0 V0 K1 V1 ... and the tiles' scales
+template <int D, int NQ>
+__device__ __forceinline__ void chunk_copy(const ChunkParams& p) {
+  using Ly = ChunkLayout<D, NQ>;
+  constexpr int RS = Ly::RSLOTS, TT = Ly::TT, NG = Ly::NG;
+  const ChunkSmem<Ly> sm;
+  const int lane = threadIdx.x & 31, Hkv = p.num_kv_heads, bs = p.block_size;
+  ChunkWalk<Ly> w;
+  w.set(p, sm.misc, *sm.units);
+  const int sh = 31 - __clz(bs);  // block_size is a power of two
+  const int pages = TT >> sh;     // of a tile: at most 8
+  int rs = 0;       // next raw slot
+  uint32_t ph = 1;  // parity of its last release
+  int filled = 0;   // slots filled (no further than RS)
+  int ring = 0;     // where the tile's scales go
+  bool ok = true;
+  // One tile behind: the next tile's pages and scales are looked up before this one's copies
+  // are issued, so that what they are found by is not waited for.
+  int y = -1;
+  float4 f = make_float4(0.f, 0.f, 1.f, 0.f);
+  bool more = w.left > 0;
+  for (int i = 0, first = 1; ok; first = 0) {
+    const int y_here = y;
+    float4 f_here = f;
+    // Lane g looks at 16 tokens of a tile: their page's index among all (block, kv head) pages
+    // (-1 past the sequence's end or for a bad id) and what the softmax and the widening want
+    // to know of them: K scale times the logit scale, log2 of the V scale and one over it,
+    // and what counts, as bits.
+    y = -1;
+    f = make_float4(0.f, 0.f, 1.f, 0.f);
+    if (more) {
+      const int t = (w.tile + i) * TT + 16 * lane;
+      if (lane < NG && t < w.q.n) {
+        const int b = __ldg(p.block_tables + (size_t)w.s * p.max_blocks_per_seq + (t >> sh));
+        if (b < 0 || b >= p.num_blocks) {
+          raise_error(p.err, PA_DEVERR_BLOCK_ID);
+          f.y = -60.f;  // tokens of zeros: their weights count, small beside any value's
+          f.z = 0x1p60f;
+        } else {
+          y = b * Hkv + w.g;
+          const float vs = __ldg(p.v_scales + y);
+          const float lv = fminf(fmaxf(log2f(fabsf(vs)), -60.f), 60.f);  // (NaN: -60)
+          f.x = p.scale_log2 * __ldg(p.k_scales + y);
+          f.y = lv;
+          f.z = exp2f(-lv);
+          const int rows = min(16, w.q.n - t);
+          f.w = __int_as_float(kChunkKeyed | (fabsf(vs) >= 0x1p-60f ? rows << 8 : 0));
+        }
+      }
+      if (++i == w.len) {
+        i = 0;
+        w.next(p);
+      }
+    }
+    if (!first) {
+      const int what = __float_as_int(f_here.w);
+      const bool all_k = __all_sync(0xffffffffu, lane >= NG || (what & kChunkKeyed));
+      const bool all_v = __all_sync(0xffffffffu, lane >= NG || (what >> 8) == 16);
+      f_here.w = __int_as_float(what | (all_k ? kChunkAllK : 0) | (all_v ? kChunkAllV : 0));
+      // lane pp copies page pp (whose first 16 tokens lane pp bs / 16 has looked at)
+      const int page = __shfl_sync(0xffffffffu, y_here, (lane << sh) >> 4 & 31);
+      const bool copies = lane < pages && page >= 0;
+      const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, copies)) * (D << sh);
+#pragma unroll 1
+      for (int kv = 0; kv < 2; ++kv) {
+        if (filled >= RS) ok = chunk_wait(&sm.raw_empty[rs], ph);
+        if (!ok) break;
+        if (kv == 0) {  // the tile's scales, before its codes
+          if (lane < NG) sm.sc[ring * NG + lane] = f_here;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.sc_full[ring]);
+        }
+        if (lane == 0) mbar_arrive_expect_tx(&sm.raw_full[rs], bytes);
+        __syncwarp();
+        if (copies)
+          bulk_g2s(sm.base + Ly::OFF_RAW + rs * Ly::RAW + (lane << sh) * D,
+                   (kv ? p.v_cache : p.k_cache) + ((size_t)page << sh) * D, D << sh,
+                   &sm.raw_full[rs]);
+        __syncwarp();
+        if (filled < RS) ++filled;
+        if (++rs == RS) {
+          rs = 0;
+          ph ^= 1;
+        }
+      }
+      ring = (ring + 1) % kChunkScaleRing;
+    }
+    if (!more) break;
+    more = w.left > 0;
+  }
+  if (!ok && lane == 0) raise_error(p.err, PA_DEVERR_TIMEOUT);
+  // never leave with copies in flight: the last fill of every slot (a slot before `rs` was
+  // filled in phase ph ^ 1, one from it on in the phase before)
+  for (int j = 0; j < filled; ++j)
+    if (!chunk_wait(&sm.raw_full[j], (j < rs ? ph ^ 1 : ph) & 1) && lane == 0)
+      raise_error(p.err, PA_DEVERR_TIMEOUT);
+}
+
+// ---- products, one warp
+template <int D, int NQ>
+__device__ __forceinline__ void chunk_issue(const ChunkParams& p) {
+  using Ly = ChunkLayout<D, NQ>;
+  constexpr int NS = Ly::SLOTS, TT = Ly::TT, DV = Ly::DV, HALVES = Ly::HALVES;
+  const ChunkSmem<Ly> sm;
+  const int lane = threadIdx.x & 31;
+  ChunkWalk<Ly> w;
+  w.set(p, sm.misc, *sm.units);
+  // query tiles of the current piece that have rows (the first always has)
+  auto live_tiles = [&]() -> int { return NQ == 1 ? 1 : (w.rows(p) > kChunkRows ? 2 : 1); };
+  constexpr uint32_t idesc_s = umma_idesc_f16(false, kChunkRows, TT, false);
+  constexpr uint32_t idesc_o = umma_idesc_f16(false, kChunkRows, DV, true);
+  // low words of the operands' descriptors: an address adds its 16-byte units
+  const uint32_t dq = desc_lo(smem_u32(sm.base), 16);
+  const uint32_t dk0 = desc_lo(smem_u32(sm.base + Ly::OFF_KV), 16);
+  const uint32_t dv0 = desc_lo(smem_u32(sm.base + Ly::OFF_KV), TT * 128);
+  const uint32_t tb = uniform(*sm.tmem);
+  const uint32_t uo = tb + 2 * TT;
+  int ks = 0, vs = 1;         // slots of the next K and V tile
+  uint32_t kph = 0, vph = 0;  // and their phases
+  auto step2 = [&](int& sl, uint32_t& ph) {
+    sl += 2;
+    if (sl >= NS) {
+      sl -= NS;
+      ph ^= 1;
+    }
+  };
+  // (buffer and use of it of a query tile's c-th tile)
+  auto buf = [](int q, uint32_t c) -> uint32_t { return NQ == 2 ? q : c & 1; };
+  auto use = [](uint32_t c) -> uint32_t { return NQ == 2 ? c : c >> 1; };
+  // S of query tile q's c-th tile on the K tile in slot ks; `last`: the slot's last reader
+  auto issue_s = [&](int q, uint32_t c, bool last) -> bool {
+    const uint32_t b = buf(q, c), u = use(c);
+    if (!chunk_wait(&sm.full[ks], kph)) return false;
+    // the weights that lie over S's columns have been used
+    if (u >= 1 && !chunk_wait(&sm.pv_done[b], (u - 1) & 1)) return false;
+    tc05_fence_after();
+    const uint32_t dk = dk0 + ks * (Ly::SLOT >> 4), dqt = dq + q * (Ly::QBYTES1 >> 4);
+    if (elect_one()) {
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+        mma_ss(tb + b * TT, dqt + ((kk >> 2) * (kChunkRows * 128) + (kk & 3) * 32) / 16,
+               dk + ((kk >> 2) * (TT * 128) + (kk & 3) * 32) / 16, idesc_s, kk > 0);
+      umma_commit(&sm.s_full[b]);
+      if (last) umma_commit(&sm.empty[ks]);
+    }
+    __syncwarp();
+    if (last) step2(ks, kph);
+    return true;
+  };
+  // O += P V of query tile q's c-th tile on the V tile in slot vs
+  auto issue_pv = [&](int q, uint32_t c, bool accumulate, bool last) -> bool {
+    const uint32_t b = buf(q, c), u = use(c);
+    if (!chunk_wait(&sm.full[vs], vph)) return false;
+    const uint32_t dv = dv0 + vs * (Ly::SLOT >> 4), tp = tb + b * TT;
+#pragma unroll 1
+    for (int h = 0; h < HALVES; ++h) {
+      if (!chunk_wait(&sm.p_full[b * HALVES + h], u & 1)) return false;
+      tc05_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_ts(uo + q * DV, tp + h * 32 + kk * 8, dv + (h * 4 + kk) * (2048 / 16), idesc_o,
+                 kk > 0 || h > 0 || accumulate);
+        if (h + 1 < HALVES) {
+          umma_commit(&sm.half_done[b]);
+        } else {
+          umma_commit(&sm.pv_done[b]);
+          if (last) umma_commit(&sm.empty[vs]);
+        }
+      }
+      __syncwarp();
+    }
+    if (last) step2(vs, vph);
+    return true;
+  };
+  bool ok = true;
+  int len = uniform(w.left > 0 ? w.len : 0);
+  // (tiles that the two query tiles took in the pieces before, and those pieces)
+  uint32_t c0 = 0, c1 = 0, pieces0 = 0, pieces1 = 0;
+  while (len > 0 && ok) {
+    const int nq = uniform(live_tiles());
+    // a round: every query tile's P V of one tile (but in the first) and S of the next (but
+    // in the last), with one query tile each tile's S ahead of the P V of the one before
+#pragma unroll 1
+    for (int i = -1; i < len && ok; ++i) {
+#pragma unroll 1
+      for (int q = 0; q < nq && ok; ++q) {
+        const uint32_t c = (q ? c1 : c0) + i;
+        if (NQ == 2 && i >= 0) ok = issue_pv(q, c, i > 0, q == nq - 1);
+        if (ok && i < 0) ok = chunk_wait(&sm.q_full[q], (q ? pieces1 : pieces0) & 1);
+        if (ok && i + 1 < len) ok = issue_s(q, c + 1, q == nq - 1);
+        if (NQ == 1 && ok && i >= 0) ok = issue_pv(q, c, i > 0, true);
+      }
+    }
+    c0 += len;
+    ++pieces0;
+    if (nq == 2) {
+      c1 += len;
+      ++pieces1;
+    }
+    w.next(p);
+    len = uniform(w.left > 0 ? w.len : 0);
+  }
+  if (!ok && lane == 0) raise_error(p.err, PA_DEVERR_TIMEOUT);
+}
+
+// ---- codes widened to f16, four warps
+template <int D, int NQ>
+__device__ __forceinline__ void chunk_widen(const ChunkParams& p) {
+  using Ly = ChunkLayout<D, NQ>;
+  constexpr int KB = Ly::KB, NS = Ly::SLOTS, RS = Ly::RSLOTS, TT = Ly::TT, NG = Ly::NG;
+  const ChunkSmem<Ly> sm;
+  const int tid = threadIdx.x, lane = tid & 31;
+  ChunkWalk<Ly> w;
+  w.set(p, sm.misc, *sm.units);
+  // A thread takes 16 codes at a time; rows that hold no tokens become zeros.
+  constexpr int CPR = D / 16, NJ = TT * CPR / Ly::CONV;
+  static_assert(TT * CPR % Ly::CONV == 0, "chunks of a tile");
+  const int cid = tid - Ly::CONV_WARP * 32;
+  bool ok = true;
+  int sl = 0, rs = 0, filled = 0, ring = 0;
+  uint32_t ph = 1, rph = 0;
+  for (int i2 = 0; w.left > 0 && ok;) {
+    const bool is_v = i2 & 1;
+    ok = chunk_wait(&sm.raw_full[rs], rph);
+    if (ok && filled >= NS) ok = chunk_wait(&sm.empty[sl], ph);
+    if (!ok) break;
+    uint8_t* dst = sm.base + Ly::OFF_KV + sl * Ly::SLOT;
+    const uint4* raw = reinterpret_cast<const uint4*>(sm.base + Ly::OFF_RAW + rs * Ly::RAW);
+    const float4* scg = sm.sc + ring * NG;
+    const bool every = __float_as_int(scg[0].w) & (is_v ? kChunkAllV : kChunkAllK);
+    constexpr int NX = NJ % 4 == 0 ? 4 : NJ % 3 == 0 ? 3 : 2;  // read together
+    static_assert(NJ % NX == 0, "whole rounds");
+#pragma unroll 1
+    for (int j0 = 0; j0 < NJ; j0 += NX) {
+      uint4 src[NX];
+#pragma unroll
+      for (int x = 0; x < NX; ++x) src[x] = raw[cid + (j0 + x) * Ly::CONV];
+#pragma unroll
+      for (int x = 0; x < NX; ++x) {
+        const int j = j0 + x;
+        const int i = cid + j * Ly::CONV, row = i / CPR, c16 = i % CPR;
+        if (!every) {
+          const int what = __float_as_int(scg[row >> 4].w);
+          if (is_v ? (row & 15) >= (what >> 8) : !(what & 1))
+            src[x] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        uint4 o[2];
+        widen8<E4M3>(src[x].x, o[0].x, o[0].y);
+        widen8<E4M3>(src[x].y, o[0].z, o[0].w);
+        widen8<E4M3>(src[x].z, o[1].x, o[1].y);
+        widen8<E4M3>(src[x].w, o[1].z, o[1].w);
+        // the second column block's lanes store their odd chunk first, so that
+        // the eight lanes of a row (D 128) cover all banks
+        const int sw = (KB == 2 && c16 >= 4) ? 1 : 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int ch = 2 * c16 + (h ^ sw);
+          *reinterpret_cast<uint4*>(dst + (ch >> 3) * (TT * 128) + row * 128 +
+                                    (((ch & 7) ^ (row & 7)) << 4)) = sw ^ h ? o[1] : o[0];
+        }
+      }
+    }
+    fence_proxy_async_smem();
+    // (the codes have been used, not only asked for: the copies of the next ones may
+    // overwrite them)
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(&sm.full[sl]);
+      mbar_arrive(&sm.raw_empty[rs]);
+    }
+    if (filled < NS) ++filled;
+    if (++sl == NS) {
+      sl = 0;
+      ph ^= 1;
+    }
+    if (++rs == RS) {
+      rs = 0;
+      rph ^= 1;
+    }
+    if (is_v) ring = (ring + 1) % kChunkScaleRing;
+    if (++i2 == 2 * w.len) {
+      i2 = 0;
+      w.next(p);
+    }
+  }
+  if (!ok && lane == 0) raise_error(p.err, PA_DEVERR_TIMEOUT);
+}
+
+// ---- softmax, a row per thread
+// (tcgen05.ld / st are warp-wide: every decision that leads to one is taken by the whole warp)
+template <typename QT, int D, int NQ>
+__device__ __forceinline__ void chunk_softmax(const ChunkParams& p) {
+  using Ly = ChunkLayout<D, NQ>;
+  constexpr int ROWS = Ly::ROWS, TT = Ly::TT, DV = Ly::DV, NG = Ly::NG, HALVES = Ly::HALVES;
+  const ChunkSmem<Ly> sm;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
+  const int G = p.group;
+  ChunkWalk<Ly> w;
+  w.set(p, sm.misc, *sm.units);
+  const int q = warp / 4;    // query tile
+  const int r1 = tid & 127;  // row of it: TMEM lane
+  const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+  const uint32_t t_o = *sm.tmem + 2 * TT + q * DV + lane_off;
+  uint8_t* qrow = sm.base + q * Ly::QBYTES1 + r1 * 128;
+  uint32_t ct = 0;  // tiles of the CTA before the piece
+  uint32_t c = 0;   // tiles this query tile has taken
+  bool failed = false;
+  // the row of a piece: its output row, whether it has one, its warp any, its query tile any
+  uint32_t orow = 0;  // (a row is 128 bytes or more: 32 bits hold any that fits the memory)
+  bool live = false, warp_live = false, work = false, whole = false;
+  float m = -INFINITY, l = 0.f;  // its reference and sum
+  // One piece behind: a piece's query goes to shared memory, so that its first product runs,
+  // before the output of the one before is stored.
+#pragma unroll 1
+  for (int piece = 0;; ++piece) {
+    const bool more = w.left > 0;
+    const uint32_t orow_b = orow;
+    const bool live_b = live, warp_live_b = warp_live, work_b = work, whole_b = whole;
+    int pos = 0;  // the row's position
+    if (more) {
+      const int rows = w.rows(p), r = q * kChunkRows + r1;
+      live = r < rows;
+      warp_live = q * kChunkRows + (warp & 3) * 32 < rows;
+      work = q * kChunkRows < rows;
+      whole = w.len == w.T;
+      const int token = live ? w.rt * p.tile_tokens + r / G : 0;
+      pos = w.q.n - w.q.q_len + token;
+      orow = static_cast<uint32_t>(w.q.q0 + token) * p.num_heads + w.g * G + (live ? r % G : 0);
+      if (work) {
+        // the row's query in f16 (exact inside f16's range): every S product on the last
+        // piece's has completed
+        constexpr int QCH = D / 8, B = 4;  // 16-byte chunks, and those in flight together
+        const uint4* src =
+            reinterpret_cast<const uint4*>(static_cast<const QT*>(p.query) + (size_t)orow * D);
+#pragma unroll 1
+        for (int c0 = 0; c0 < QCH; c0 += B) {
+          uint4 v[B];
+#pragma unroll
+          for (int x = 0; x < B; ++x)
+            v[x] = live ? __ldg(src + c0 + x) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int x = 0; x < B; ++x) {
+            const int ch = c0 + x;
+            if constexpr (std::is_same<QT, __nv_bfloat16>::value) {
+              uint32_t* e = reinterpret_cast<uint32_t*>(&v[x]);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const __nv_bfloat162 b = *reinterpret_cast<const __nv_bfloat162*>(&e[j]);
+                const __half2 h = __floats2half2_rn(__low2float(b), __high2float(b));
+                e[j] = *reinterpret_cast<const uint32_t*>(&h);
+              }
+            }
+            *reinterpret_cast<uint4*>(qrow + (ch >> 3) * (kChunkRows * 128) +
+                                      (((ch & 7) ^ (r1 & 7)) << 4)) = v[x];
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.q_full[q]);
+      }
+    }
+    if (work_b) {
+      // ---- the last piece's output, or its partial
+      const uint32_t cl = c - 1, bl = NQ == 2 ? q : cl & 1, ul = NQ == 2 ? cl : cl >> 1;
+      if (!chunk_wait(&sm.pv_done[bl], ul & 1)) {
+        failed = true;
+        break;
+      }
+      tc05_fence_after();
+      __syncwarp();
+      if (warp_live_b) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
+        const size_t slot = (size_t)cta * 2 + (piece > 1 ? 1 : 0);
+        QT* dst = static_cast<QT*>(p.out) + (size_t)orow_b * D;
+        float4* po = p.part_o + slot * (D / 4) * ROWS + q * kChunkRows + r1;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 16) {
+          uint32_t o[16];
+          tmem_ld16(t_o + c0, o);
+          tmem_wait_ld();
+          if (live_b && whole_b) {
+            uint32_t v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              v[k] = Mma<QT>::pack(__uint_as_float(o[2 * k]) * inv,
+                                   __uint_as_float(o[2 * k + 1]) * inv);
+            // whole sectors where the output allows it (a row is a multiple of 32 bytes)
+            if (wide) {
+              st_global_v8(dst + c0, v);
+            } else {
+              *reinterpret_cast<uint4*>(dst + c0) = make_uint4(v[0], v[1], v[2], v[3]);
+              *reinterpret_cast<uint4*>(dst + c0 + 8) = make_uint4(v[4], v[5], v[6], v[7]);
+            }
+          } else if (live_b) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+              po[(size_t)((c0 + e) / 4) * ROWS] =
+                  make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
+                              __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+          }
+        }
+        if (!whole_b && live_b) p.part_ml[slot * ROWS + q * kChunkRows + r1] = make_float2(m, l);
+      }
+      // the accumulator has been read before the next weights (whose arrival lets the
+      // products overwrite it) are announced
+      tc05_fence_before();
+    }
+    if (!more) break;
+    m = -INFINITY;
+    l = 0.f;
+    const int len = w.len;
+    if (work) {
+      float mu = 0.f;  // what weights are held relative to: m - 7 (nothing seen yet: 0)
+      const int first_pos = __reduce_min_sync(0xffffffffu, live ? pos : 0x7FFFFFFF);
+#pragma unroll 1
+      for (int i = 0; i < len; ++i, ++c) {
+        const uint32_t b = NQ == 2 ? q : c & 1, u = NQ == 2 ? c : c >> 1;
+        const int t0 = (w.tile + i) * TT;
+        if (!chunk_wait(&sm.s_full[b], u & 1)) {
+          failed = true;
+          break;
+        }
+        const uint32_t x = ct + i;
+        const float4* sct = sm.sc + (x % kChunkScaleRing) * NG;
+        if (!chunk_wait(&sm.sc_full[x % kChunkScaleRing], (x / kChunkScaleRing) & 1)) {
+          failed = true;
+          break;
+        }
+        tc05_fence_after();
+        __syncwarp();
+        const uint32_t t_s = *sm.tmem + b * TT + lane_off;
+        const bool masked = t0 + TT - 1 > first_pos;  // warp-uniform
+        const int lim = live ? pos - t0 + 1 : 0;      // tokens of the tile that the row sees
+        // 32 tokens at a time, in one small loop (the roles share the instruction cache): their
+        // weights relative to the reference as it is, and again, should one of them not fit,
+        // relative to one that moved. They go over columns whose logits have been read, 64
+        // tokens' together on to the products. The next logits are on their way meanwhile.
+        // (A warp without rows does the same on what its rows of S hold: no product mixes rows.)
+        uint32_t raw[32];
+        tmem_ld32(t_s, raw);
+#pragma unroll 1
+        for (int h = 0; h < 2 * HALVES; ++h) {
+          const float4* sch = sct + 2 * h;
+          float2 y[16];
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 k = *reinterpret_cast<const float2*>(sch + e / 8);
+            y[e] = __ffma2_rn(
+                make_float2(__uint_as_float(raw[2 * e]), __uint_as_float(raw[2 * e + 1])),
+                make_float2(k.x, k.x), make_float2(k.y - mu, k.y - mu));
+          }
+          if (h + 1 < 2 * HALVES) tmem_ld32(t_s + 32 * h + 32, raw);
+          if (masked) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              y[e].x = 2 * e < lim - 32 * h ? y[e].x : -INFINITY;
+              y[e].y = 2 * e + 1 < lim - 32 * h ? y[e].y : -INFINITY;
+            }
+          }
+          uint32_t pk[16];
+          float sum = 0.f;
+          const float mx = chunk_largest(y);
+          chunk_weigh(y, sch, sum, pk);
+          // (with nothing seen yet any logit moves the reference)
+          if (__builtin_expect(__any_sync(0xffffffffu, m == -INFINITY ? mx != -INFINITY
+                                                                    : mx > kChunkTop + kChunkLazy),
+                               0)) {
+            // whole numbers, so that what is there is scaled by powers of two: exactly
+            const float mn = mx == -INFINITY ? m : fmaxf(m, ceilf(mx + mu));
+            const float al = m == -INFINITY ? 1.f : exp2f(m - mn);
+            if (i > 0 || h >= 2) {
+              // O holds the tokens so far, once their products have landed
+              const uint32_t cp = c - 1, bp = NQ == 2 ? q : cp & 1, up = NQ == 2 ? cp : cp >> 1;
+              if (!chunk_wait(h >= 2 ? &sm.half_done[b] : &sm.pv_done[bp],
+                              (h >= 2 ? u : up) & 1)) {
+                failed = true;
+                break;
+              }
+              tc05_fence_after();
+              __syncwarp();
+#pragma unroll 1
+              for (int c0 = 0; c0 < D; c0 += 16) {
+                uint32_t o[16];
+                tmem_ld16(t_o + c0, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                  o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+                tmem_st16(t_o + c0, o);
+              }
+            }
+            if (h & 1) {  // weights that have not been handed on yet
+              uint32_t o[16];
+              tmem_wait_st();
+              tmem_ld16(t_s + 16 * h - 16, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float2 v = __half22float2(*reinterpret_cast<__half2*>(&o[e]));
+                o[e] = Mma<__half>::pack(v.x * al, v.y * al);
+              }
+              tmem_st16(t_s + 16 * h - 16, o);
+            }
+            l *= al;
+            m = mn;
+            const float to = m == -INFINITY ? 0.f : m - kChunkTop, down = to - mu;
+            mu = to;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[e] = make_float2(y[e].x - down, y[e].y - down);
+            sum = 0.f;
+            chunk_weigh(y, sch, sum, pk);
+          }
+          l += sum;
+          tmem_st16(t_s + 16 * h, pk);
+          if (h & 1) {
+            tmem_wait_st();
+            tc05_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.p_full[b * HALVES + h / 2]);
+          }
+        }
+        if (failed) break;
+      }
+      if (failed) break;
+    }
+    ct += len;
+    w.next(p);
+  }
+  if (failed && lane == 0) raise_error(p.err, PA_DEVERR_TIMEOUT);
 }
 
 template <typename QT, int D, int NQ>
 __global__ void __launch_bounds__(ChunkLayout<D, NQ>::THREADS, ChunkLayout<D, NQ>::CTAS)
     chunk_attention_kernel(const __grid_constant__ ChunkParams p) {
   using Ly = ChunkLayout<D, NQ>;
-  constexpr int KB = Ly::KB, NS = Ly::SLOTS, RS = Ly::RSLOTS, ROWS = Ly::ROWS, TT = Ly::TT;
-  constexpr int DV = Ly::DV, NG = Ly::NG;
-  extern __shared__ __align__(1024) uint8_t smem[];
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Ly::OFF_BAR);  // [NS] a widened tile is there
-  uint64_t* empty = full + NS;        // [NS] its products are done
-  uint64_t* raw_full = empty + NS;    // [RS] codes have landed
-  uint64_t* raw_empty = raw_full + RS;  // [RS] and have been read
-  uint64_t* s_full = raw_empty + RS;  // [2] S is in its buffer
-  uint64_t* p_full = s_full + 2;      // [2] the weights are
-  uint64_t* pv_done = p_full + 2;     // [2] and have been used
-  uint64_t* q_full = pv_done + 2;     // [NQ]
-  uint64_t* sc_full = q_full + NQ;    // [ring] a tile's scales are there
-  int* misc = reinterpret_cast<int*>(smem + Ly::OFF_MISC);                     // s, g, rt, tile
-  long long* misc64 = reinterpret_cast<long long*>(smem + Ly::OFF_MISC + 16);  // units
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Ly::OFF_MISC + 32);
-  float4* sc = reinterpret_cast<float4*>(smem + Ly::OFF_SC);
+  constexpr int NS = Ly::SLOTS, RS = Ly::RSLOTS;
+  const ChunkSmem<Ly> sm;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int cta = blockIdx.x, C = p.ctas, S = p.num_seqs;
-  const int Hq = p.num_heads, Hkv = p.num_kv_heads, G = p.group, bs = p.block_size;
-  unsigned* err = p.err;
+  const int cta = blockIdx.x, C = p.ctas, S = p.num_seqs, Hq = p.num_heads, Hkv = p.num_kv_heads;
 
   pdl_wait();
   pdl_trigger();
@@ -317,32 +875,33 @@ __global__ void __launch_bounds__(ChunkLayout<D, NQ>::THREADS, ChunkLayout<D, NQ
       }
     }
     if (lane == 0) {
-      misc[0] = at.x;
-      misc[1] = at.y;
-      misc[2] = at.z;
-      misc[3] = at.w;
-      misc64[0] = hi - lo;
+      sm.misc[0] = at.x;
+      sm.misc[1] = at.y;
+      sm.misc[2] = at.z;
+      sm.misc[3] = at.w;
+      *sm.units = hi - lo;
       p.starts[cta] = at;  // for the join
       if (cta == 0) *p.total = P;
     }
   } else if (warp == Ly::MMA_WARP) {
-    tmem_alloc(tmem_slot, Ly::TMEM_COLS);
+    tmem_alloc(sm.tmem, Ly::TMEM_COLS);
     if (lane == 0) {
       for (int i = 0; i < NS; ++i) {
-        mbar_init(&full[i], Ly::CONV);
-        mbar_init(&empty[i], 1);
+        mbar_init(&sm.full[i], Ly::CONV / 32);
+        mbar_init(&sm.empty[i], 1);
       }
       for (int i = 0; i < RS; ++i) {
-        mbar_init(&raw_full[i], 1);
-        mbar_init(&raw_empty[i], Ly::CONV / 32);
+        mbar_init(&sm.raw_full[i], 1);
+        mbar_init(&sm.raw_empty[i], Ly::CONV / 32);
       }
       for (int i = 0; i < 2; ++i) {
-        mbar_init(&s_full[i], 1);
-        mbar_init(&p_full[i], kChunkRows);
-        mbar_init(&pv_done[i], 1);
+        mbar_init(&sm.s_full[i], 1);
+        for (int h = 0; h < Ly::HALVES; ++h) mbar_init(&sm.p_full[i * Ly::HALVES + h], 4);
+        mbar_init(&sm.half_done[i], 1);
+        mbar_init(&sm.pv_done[i], 1);
       }
-      for (int i = 0; i < NQ; ++i) mbar_init(&q_full[i], kChunkRows);
-      for (int i = 0; i < kChunkScaleRing; ++i) mbar_init(&sc_full[i], 1);
+      for (int i = 0; i < NQ; ++i) mbar_init(&sm.q_full[i], 4);
+      for (int i = 0; i < kChunkScaleRing; ++i) mbar_init(&sm.sc_full[i], 1);
       fence_mbar_init();
     }
   } else if (warp < 4) {
@@ -357,496 +916,19 @@ __global__ void __launch_bounds__(ChunkLayout<D, NQ>::THREADS, ChunkLayout<D, NQ
   tc05_fence_before();
   __syncthreads();
   tc05_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  const long long units = misc64[0];
-  const bool aligned = (smem_u32(smem) & 1023u) == 0;
-  if (!aligned && tid == 0) raise_error(err, PA_DEVERR_TIMEOUT);  // never: see __align__ above
+  const uint32_t tmem = *sm.tmem;
+  const bool aligned = (smem_u32(sm.base) & 1023u) == 0;
+  if (!aligned && tid == 0) raise_error(p.err, PA_DEVERR_TIMEOUT);  // never: see __align__ above
 
-  if (units > 0 && aligned) {
-    ChunkWalk<Ly> w;
-    w.set(p, misc, units);
-    // query tiles of the current piece that have rows (the first always has)
-    auto live_tiles = [&]() -> int { return NQ == 1 ? 1 : (w.rows(p) > kChunkRows ? 2 : 1); };
-    if (warp == Ly::COPY_WARP) {
-      // ================================================ copies: K0 V0 K1 V1 ...
-      const int sh = 31 - __clz(bs), pages = TT >> sh;  // block_size is a power of two
-      int rs = 0;       // next raw slot
-      uint32_t ph = 1;  // parity of its last release
-      int filled = 0;   // slots filled (no further than RS)
-      int ring = 0;     // where the tile's scales go
-      bool ok = true;
-      // Lane g looks at 16 tokens of a tile: their page's index among all (block, kv
-      // head) pages (-1 past the sequence's end, -2 for a bad id) and what the softmax
-      // and the widening want to know of them: K scale times the logit scale, log2 of
-      // the V scale and one over it, and what counts, as bits.
-      auto lookup = [&](int i, int& y, float4& f) {
-        const int t = (w.tile + i) * TT + 16 * lane;
-        y = -1;
-        f = make_float4(0.f, 0.f, 1.f, 0.f);
-        if (lane >= NG || t >= w.q.n) return;
-        const int b = __ldg(p.block_tables + (size_t)w.s * p.max_blocks_per_seq + (t >> sh));
-        if (b < 0 || b >= p.num_blocks) {
-          raise_error(err, PA_DEVERR_BLOCK_ID);
-          y = -2;
-          f.y = -60.f;  // tokens of zeros: their weights count, small beside any value's
-          f.z = 0x1p60f;
-          return;
-        }
-        y = b * Hkv + w.g;
-        const float vs = __ldg(p.v_scales + y);
-        const float lv = fminf(fmaxf(log2f(fabsf(vs)), -60.f), 60.f);  // (NaN: -60)
-        f.x = p.scale_log2 * __ldg(p.k_scales + y);
-        f.y = lv;
-        f.z = exp2f(-lv);
-        const int rows = min(16, w.q.n - t);
-        f.w = __int_as_float(kChunkKeyed | (fabsf(vs) >= 0x1p-60f ? rows << 8 : 0));
-      };
-      int len = uniform(w.left > 0 ? w.len : 0);
-      while (len > 0 && ok) {
-        int y_next;
-        float4 f_next;
-        lookup(0, y_next, f_next);
-        for (int i = 0; i < len && ok; ++i) {
-          const int y_here = y_next;
-          const float4 f_here = f_next;
-          int y[TT / 16];
-#pragma unroll
-          for (int pp = 0; pp < TT / 16; ++pp)
-            y[pp] = __shfl_sync(0xffffffffu, y_here, (pp << sh) >> 4 & 31);
-          if (i + 1 < len) lookup(i + 1, y_next, f_next);
-#pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            if (filled >= RS) ok = warp_wait(&raw_empty[rs], ph);
-            if (!ok) break;
-            if (kv == 0) {  // the tile's scales, before its codes
-              const int what = __float_as_int(f_here.w);
-              const bool all_k = __all_sync(0xffffffffu, lane >= NG || (what & kChunkKeyed));
-              const bool all_v = __all_sync(0xffffffffu, lane >= NG || (what >> 8) == 16);
-              float4 f = f_here;
-              f.w = __int_as_float(what | (all_k ? kChunkAllK : 0) | (all_v ? kChunkAllV : 0));
-              if (lane < NG) sc[ring * NG + lane] = f;
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&sc_full[ring]);
-            }
-            uint8_t* raw = smem + Ly::OFF_RAW + rs * Ly::RAW;
-            if (elect_one()) {
-              uint32_t bytes = 0;
-#pragma unroll
-              for (int pp = 0; pp < TT / 16; ++pp)
-                if (pp < pages && y[pp] >= 0) bytes += D << sh;
-              mbar_arrive_expect_tx(&raw_full[rs], bytes);
-#pragma unroll
-              for (int pp = 0; pp < TT / 16; ++pp)
-                if (pp < pages && y[pp] >= 0)
-                  bulk_g2s(raw + (pp << sh) * D, (kv ? p.v_cache : p.k_cache) +
-                                                     ((size_t)y[pp] << sh) * D,
-                           D << sh, &raw_full[rs]);
-            }
-            __syncwarp();
-            if (filled < RS) ++filled;
-            if (++rs == RS) {
-              rs = 0;
-              ph ^= 1;
-            }
-          }
-          ring = (ring + 1) % kChunkScaleRing;
-        }
-        w.next(p);
-        len = uniform(w.left > 0 ? w.len : 0);
-      }
-      if (!ok && lane == 0) raise_error(err, PA_DEVERR_TIMEOUT);
-      // never leave with copies in flight: the last fill of every slot (a slot before
-      // `rs` was filled in phase ph ^ 1, one from it on in the phase before)
-      for (int j = 0; j < filled; ++j)
-        if (!warp_wait(&raw_full[j], (j < rs ? ph ^ 1 : ph) & 1) && lane == 0)
-          raise_error(err, PA_DEVERR_TIMEOUT);
-    } else if (warp == Ly::MMA_WARP) {
-      // ================================================ MMA issue
-      constexpr uint32_t idesc_s = umma_idesc_f16(false, kChunkRows, TT, false);
-      constexpr uint32_t idesc_o = umma_idesc_f16(false, kChunkRows, DV, true);
-      // low words of the operands' descriptors: an address adds its 16-byte units
-      const uint32_t dq = desc_lo(smem_u32(smem), 16);
-      const uint32_t dk0 = desc_lo(smem_u32(smem + Ly::OFF_KV), 16);
-      const uint32_t dv0 = desc_lo(smem_u32(smem + Ly::OFF_KV), TT * 128);
-      const uint32_t tb = uniform(tmem);
-      const uint32_t uo = tb + 2 * TT;
-      int ks = 0, vs = 1;         // slots of the next K and V tile
-      uint32_t kph = 0, vph = 0;  // and their phases
-      auto step2 = [&](int& sl, uint32_t& ph) {
-        sl += 2;
-        if (sl >= NS) {
-          sl -= NS;
-          ph ^= 1;
-        }
-      };
-      uint32_t cs[NQ] = {}, cd[NQ] = {};  // tiles whose S, whose P V has been issued
-      // (buffer and use of it of a query tile's c-th tile)
-      auto buf = [](int q, uint32_t c) -> uint32_t { return NQ == 2 ? q : c & 1; };
-      auto use = [](uint32_t c) -> uint32_t { return NQ == 2 ? c : c >> 1; };
-      // S of query tile q on the K tile in slot ks; `last`: the slot's last reader
-      auto issue_s = [&](int q, bool last) -> bool {
-        const uint32_t b = buf(q, cs[q]), u = use(cs[q]);
-        if (!warp_wait(&full[ks], kph)) return false;
-        // the weights that lie over S's columns have been used
-        if (u >= 1 && !warp_wait(&pv_done[b], (u - 1) & 1)) return false;
-        tc05_fence_after();
-        const uint32_t dk = dk0 + ks * (Ly::SLOT >> 4), dqt = dq + q * (Ly::QBYTES1 >> 4);
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss(tb + b * TT, dqt + ((kk >> 2) * (kChunkRows * 128) + (kk & 3) * 32) / 16,
-                   dk + ((kk >> 2) * (TT * 128) + (kk & 3) * 32) / 16, idesc_s, kk > 0);
-          umma_commit(&s_full[b]);
-          if (last) umma_commit(&empty[ks]);
-        }
-        __syncwarp();
-        ++cs[q];
-        if (last) step2(ks, kph);
-        return true;
-      };
-      // O += P V of query tile q on the V tile in slot vs
-      auto issue_pv = [&](int q, bool accumulate, bool last) -> bool {
-        const uint32_t b = buf(q, cd[q]), u = use(cd[q]);
-        if (!warp_wait(&full[vs], vph) || !warp_wait(&p_full[b], u & 1)) return false;
-        tc05_fence_after();
-        const uint32_t dv = dv0 + vs * (Ly::SLOT >> 4), tp = tb + b * TT;
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < TT / 16; ++kk)
-            mma_ts(uo + q * DV, tp + kk * 8, dv + kk * (2048 / 16), idesc_o, kk > 0 || accumulate);
-          umma_commit(&pv_done[b]);
-          if (last) umma_commit(&empty[vs]);
-        }
-        __syncwarp();
-        ++cd[q];
-        if (last) step2(vs, vph);
-        return true;
-      };
-      bool ok = true;
-      int len = uniform(w.left > 0 ? w.len : 0);
-      for (int piece[2] = {0, 0}; len > 0 && ok;) {
-        const int nq = uniform(live_tiles());
-#pragma unroll
-        for (int q = 0; q < NQ; ++q)
-          if (q < nq) {
-            ok = ok && warp_wait(&q_full[q], piece[q]++ & 1);
-            ok = ok && issue_s(q, q == nq - 1);
-          }
-        for (int i = 0; i < len && ok; ++i) {
-          if constexpr (NQ == 1) {
-            if (i + 1 < len) ok = issue_s(0, true);
-            ok = ok && issue_pv(0, i > 0, true);
-          } else {
-#pragma unroll
-            for (int q = 0; q < NQ; ++q)
-              if (q < nq) {
-                ok = ok && issue_pv(q, i > 0, q == nq - 1);
-                if (i + 1 < len) ok = ok && issue_s(q, q == nq - 1);
-              }
-          }
-        }
-        w.next(p);
-        len = uniform(w.left > 0 ? w.len : 0);
-      }
-      if (!ok && lane == 0) raise_error(err, PA_DEVERR_TIMEOUT);
-    } else if (warp >= Ly::CONV_WARP) {
-      // ================================================ codes widened to f16
-      // A thread takes 16 codes at a time; rows that hold no tokens become zeros.
-      constexpr int CPR = D / 16, NJ = TT * CPR / Ly::CONV;
-      static_assert(TT * CPR % Ly::CONV == 0, "chunks of a tile");
-      const int cid = tid - Ly::CONV_WARP * 32;
-      bool ok = true;
-      int sl = 0, rs = 0, filled = 0, ring = 0;
-      uint32_t ph = 1, rph = 0;
-      for (int i2 = 0; w.left > 0 && ok;) {
-        const bool is_v = i2 & 1;
-        ok = warp_wait(&raw_full[rs], rph);
-        if (ok && filled >= NS) ok = warp_wait(&empty[sl], ph);
-        if (!ok) break;
-        uint8_t* dst = smem + Ly::OFF_KV + sl * Ly::SLOT;
-        const uint4* raw = reinterpret_cast<const uint4*>(smem + Ly::OFF_RAW + rs * Ly::RAW);
-        const float4* scg = sc + ring * NG;
-        const bool every = __float_as_int(scg[0].w) & (is_v ? kChunkAllV : kChunkAllK);
-        uint4 src[4];
-#pragma unroll
-        for (int j0 = 0; j0 < NJ; j0 += 4) {
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            if (j0 + x < NJ) src[x] = raw[cid + (j0 + x) * Ly::CONV];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int j = j0 + x;
-            if (j >= NJ) break;
-            const int i = cid + j * Ly::CONV, row = i / CPR, c16 = i % CPR;
-            if (!every) {
-              const int what = __float_as_int(scg[row >> 4].w);
-              if (is_v ? (row & 15) >= (what >> 8) : !(what & 1))
-                src[x] = make_uint4(0u, 0u, 0u, 0u);
-            }
-            uint4 o[2];
-            widen8<E4M3>(src[x].x, o[0].x, o[0].y);
-            widen8<E4M3>(src[x].y, o[0].z, o[0].w);
-            widen8<E4M3>(src[x].z, o[1].x, o[1].y);
-            widen8<E4M3>(src[x].w, o[1].z, o[1].w);
-            // the second column block's lanes store their odd chunk first, so that
-            // the eight lanes of a row (D 128) cover all banks
-            const int sw = (KB == 2 && c16 >= 4) ? 1 : 0;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int ch = 2 * c16 + (h ^ sw);
-              *reinterpret_cast<uint4*>(dst + (ch >> 3) * (TT * 128) + row * 128 +
-                                        (((ch & 7) ^ (row & 7)) << 4)) = sw ^ h ? o[1] : o[0];
-            }
-          }
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(&full[sl]);
-        // the codes have been used, not only asked for: the copies of the next ones may
-        // overwrite them
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&raw_empty[rs]);
-        if (filled < NS) ++filled;
-        if (++sl == NS) {
-          sl = 0;
-          ph ^= 1;
-        }
-        if (++rs == RS) {
-          rs = 0;
-          rph ^= 1;
-        }
-        if (is_v) ring = (ring + 1) % kChunkScaleRing;
-        if (++i2 == 2 * w.len) {
-          i2 = 0;
-          w.next(p);
-        }
-      }
-      if (!ok && lane == 0) raise_error(err, PA_DEVERR_TIMEOUT);
-    } else {
-      // ================================================ softmax, a row per thread
-      // (tcgen05.ld / st are warp-wide: every decision that leads to one is taken by
-      // the whole warp)
-      const int q = warp / 4;    // query tile
-      const int r1 = tid & 127;  // row in it: TMEM lane
-      const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-      const uint32_t t_o = tmem + 2 * TT + q * DV + lane_off;
-      uint8_t* qrow = smem + q * Ly::QBYTES1 + r1 * 128;
-      uint32_t ct = 0;  // tiles of the CTA before the piece
-      uint32_t c = 0;   // tiles this query tile has taken
-      bool failed = false;
-      // the row of the current piece
-      int pos = 0;        // its position
-      uint32_t orow = 0;  // (a row is 128 bytes or more: 32 bits hold any that fits the memory)
-      bool live = false;
-      auto set_row = [&]() {
-        const int r = q * kChunkRows + r1;
-        live = r < w.rows(p);
-        const int token = live ? w.rt * p.tile_tokens + r / G : 0;
-        pos = w.q.n - w.q.q_len + token;
-        orow = static_cast<uint32_t>(w.q.q0 + token) * Hq + w.g * G + (live ? r % G : 0);
-      };
-      // the row's query into shared memory, in f16 (exact inside f16's range): every S
-      // product on the last piece's has completed
-      constexpr int QCH = D / 8;  // 16-byte chunks of a query row
-      auto load_q = [&]() {
-        const uint8_t* src = static_cast<const uint8_t*>(p.query) + (size_t)orow * D * 2;
-        // (eight at a time: all in flight at once cost registers that other branches lack)
-        constexpr int B = QCH % 8 == 0 ? 8 : QCH;
-#pragma unroll
-        for (int c0 = 0; c0 < QCH; c0 += B) {
-          uint4 v[B];
-#pragma unroll
-          for (int x = 0; x < B; ++x)
-            v[x] = live ? __ldg(reinterpret_cast<const uint4*>(src) + c0 + x)
-                        : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-          for (int x = 0; x < B; ++x) {
-            const int ch = c0 + x;
-            if constexpr (std::is_same<QT, __nv_bfloat16>::value) {
-              uint32_t* e = reinterpret_cast<uint32_t*>(&v[x]);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const __nv_bfloat162 b = *reinterpret_cast<const __nv_bfloat162*>(&e[j]);
-                const __half2 h = __floats2half2_rn(__low2float(b), __high2float(b));
-                e[j] = *reinterpret_cast<const uint32_t*>(&h);
-              }
-            }
-            *reinterpret_cast<uint4*>(qrow + (ch >> 3) * (kChunkRows * 128) +
-                                      (((ch & 7) ^ (r1 & 7)) << 4)) = v[x];
-          }
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(&q_full[q]);
-      };
-      bool work = false;
-      if (w.left > 0) {
-        set_row();
-        work = q < live_tiles();
-        if (work) load_q();
-      }
-      for (int piece = 0; w.left > 0; ++piece) {
-        const bool here = work, was_live = live;
-        const uint32_t out_row = orow;
-        // a warp without rows only keeps the barriers' count (its rows of S, P and O may
-        // hold anything: no product mixes rows)
-        const bool warp_live = here && q * kChunkRows + (warp & 3) * 32 < w.rows(p);
-        const bool whole = w.len == w.T;
-        float m = -INFINITY, l = 0.f;
-        if (here) {
-          const int first_pos = __reduce_min_sync(0xffffffffu, live ? pos : 0x7FFFFFFF);
-          float mu = 0.f;  // what weights are held relative to: m - 7 (nothing seen yet: 0)
-          for (int i = 0; i < w.len; ++i, ++c) {
-            const uint32_t b = NQ == 2 ? q : c & 1, u = NQ == 2 ? c : c >> 1;
-            const int t0 = (w.tile + i) * TT;
-            if (!warp_wait(&s_full[b], u & 1)) {
-              failed = true;
-              break;
-            }
-            if (warp_live) {
-              const uint32_t x = ct + i;
-              const float4* sct = sc + (x % kChunkScaleRing) * NG;
-              if (!warp_wait(&sc_full[x % kChunkScaleRing], (x / kChunkScaleRing) & 1)) {
-                failed = true;
-                break;
-              }
-              tc05_fence_after();
-              __syncwarp();
-              const uint32_t t_s = tmem + b * TT + lane_off;
-              const bool masked = t0 + TT - 1 > first_pos;  // warp-uniform
-              const int lim = live ? pos - t0 + 1 : 0;      // tokens that the row sees
-              // 32 logits become weights, over columns whose logits have been read; the next 32
-              // are on their way meanwhile
-              auto part = [&](uint32_t (&sr)[32], int h) -> bool {
-                const float mx = chunk_logits(sr, sct + 2 * h, mu, masked, lim - 32 * h);
-                // (with nothing seen yet any logit moves the reference)
-                if (__any_sync(0xffffffffu, m == -INFINITY ? mx != -INFINITY
-                                                          : mx > kChunkTop + kChunkLazy)) {
-                  // whole numbers, so that what is there is scaled by powers of two: exactly
-                  const float mn = mx == -INFINITY ? m : fmaxf(m, ceilf(mx + mu));
-                  const float al = m == -INFINITY ? 1.f : exp2f(m - mn);
-                  if (i > 0) {  // O holds the tiles so far, once the last P V has landed
-                    const uint32_t cp = c - 1, bp = NQ == 2 ? q : cp & 1, up = NQ == 2 ? cp : cp >> 1;
-                    if (!warp_wait(&pv_done[bp], up & 1)) return false;
-                    tc05_fence_after();
-                    __syncwarp();
-#pragma unroll 1
-                    for (int c0 = 0; c0 < D; c0 += 16) {
-                      uint32_t o[16];
-                      tmem_ld16(t_o + c0, o);
-                      tmem_wait_ld();
-#pragma unroll
-                      for (int e = 0; e < 16; ++e)
-                        o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
-                      tmem_st16(t_o + c0, o);
-                    }
-                  }
-                  if (h > 0) {  // and the weights of this tile that are there
-                    tmem_wait_st();
-#pragma unroll 1
-                    for (int k = 0; k < h; ++k) {
-                      uint32_t o[16];
-                      tmem_ld16(t_s + 16 * k, o);
-                      tmem_wait_ld();
-#pragma unroll
-                      for (int e = 0; e < 16; ++e) {
-                        const float2 x = __half22float2(*reinterpret_cast<__half2*>(&o[e]));
-                        o[e] = Mma<__half>::pack(x.x * al, x.y * al);
-                      }
-                      tmem_st16(t_s + 16 * k, o);
-                    }
-                  }
-                  l *= al;
-                  m = mn;
-                  const float to = m == -INFINITY ? 0.f : m - kChunkTop;
-                  const float down = to - mu;
-                  mu = to;
-#pragma unroll
-                  for (int e = 0; e < 32; ++e)
-                    sr[e] = __float_as_uint(__uint_as_float(sr[e]) - down);
-                }
-                uint32_t pk[16];
-                chunk_weigh(sr, sct + 2 * h, l, pk);
-                tmem_st16(t_s + 16 * h, pk);
-                return true;
-              };
-              uint32_t ra[32], rb[32];
-              tmem_ld32(t_s, ra);
-              tmem_wait_ld();
-              bool fine = true;
-#pragma unroll 1
-              for (int h = 0; h < TT / 32 && fine; h += 2) {
-                tmem_ld32(t_s + 32 * (h + 1), rb);
-                fine = part(ra, h);
-                tmem_wait_ld();
-                if (h + 2 < TT / 32) tmem_ld32(t_s + 32 * (h + 2), ra);
-                fine = fine && part(rb, h + 1);
-                tmem_wait_ld();
-              }
-              if (!fine) {
-                failed = true;
-                break;
-              }
-              tmem_wait_st();
-            }
-            tc05_fence_before();
-            mbar_arrive(&p_full[b]);
-          }
-          if (failed) break;
-        }
-        // the next piece's query, so that its first product runs under what follows
-        ct += w.len;
-        w.next(p);
-        if (w.left > 0) {
-          set_row();
-          work = q < live_tiles();
-          if (work) load_q();
-        }
-        if (here) {
-          // ---- the row's output, or its partial
-          const uint32_t cl = c - 1, bl = NQ == 2 ? q : cl & 1, ul = NQ == 2 ? cl : cl >> 1;
-          if (!warp_wait(&pv_done[bl], ul & 1)) {
-            failed = true;
-            break;
-          }
-          tc05_fence_after();
-          __syncwarp();
-          const float inv = l == 0.f ? 0.f : 1.f / l;
-          const size_t slot = (size_t)cta * 2 + (piece > 0 ? 1 : 0);
-          QT* dst = static_cast<QT*>(p.out) + (size_t)out_row * D;
-          float4* po = p.part_o + slot * (D / 4) * ROWS + q * kChunkRows + r1;
-          if (warp_live) {
-#pragma unroll 1
-            for (int c0 = 0; c0 < D; c0 += 32) {
-              uint32_t o[32];
-              tmem_ld32(t_o + c0, o);
-              tmem_wait_ld();
-              if (was_live && whole) {
-#pragma unroll
-                for (int e = 0; e < 32; e += 8) {
-                  uint4 v;
-                  v.x = Mma<QT>::pack(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
-                  v.y = Mma<QT>::pack(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-                  v.z = Mma<QT>::pack(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
-                  v.w = Mma<QT>::pack(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
-                  *reinterpret_cast<uint4*>(dst + c0 + e) = v;
-                }
-              } else if (was_live) {
-#pragma unroll
-                for (int e = 0; e < 32; e += 4)
-                  po[(size_t)((c0 + e) / 4) * ROWS] =
-                      make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
-                                  __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
-              }
-            }
-          }
-          if (!whole && was_live)
-            p.part_ml[slot * ROWS + q * kChunkRows + r1] = make_float2(m, l);
-          // the accumulator has been read before the next piece's weights (whose arrival
-          // lets the products overwrite it) are announced
-          tc05_fence_before();
-        }
-      }
-      if (failed) raise_error(err, PA_DEVERR_TIMEOUT);
-    }
+  if (*sm.units > 0 && aligned) {
+    if (warp == Ly::MMA_WARP)
+      chunk_issue<D, NQ>(p);
+    else if (warp == Ly::COPY_WARP)
+      chunk_copy<D, NQ>(p);
+    else if (warp >= Ly::CONV_WARP)
+      chunk_widen<D, NQ>(p);
+    else
+      chunk_softmax<QT, D, NQ>(p);
   }
   // every TMEM access is done before the columns are released
   tc05_fence_before();
