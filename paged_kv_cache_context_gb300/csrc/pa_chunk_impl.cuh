@@ -44,7 +44,9 @@ namespace {
 
 constexpr float kChunkTop = 7.f;    // the largest weights' exponent above the reference
 constexpr float kChunkLazy = 8.f;   // how far the reference may lie behind
-constexpr uint32_t kChunkPolls = 1u << 22;  // polls of a wait before it gives up
+// Polls of a wait before it gives up, and how long each may wait by itself (a hint, of which
+// the hardware keeps about 4 us): a quarter of a second.
+constexpr uint32_t kChunkPolls = 1u << 16, kChunkPollNs = 10000;
 constexpr int kChunkScaleRing = 8;  // tiles whose scales are kept
 // Bits kept beside the scales of 16 tokens: their K counts (it is zeros where the block id
 // is bad); K, and V, of the tile's every token count; from bit 8 on the rows of V that do.
@@ -216,10 +218,17 @@ __device__ __forceinline__ void st_global_v8(void* dst, const uint32_t (&v)[8]) 
 // instructions where one by the clock, inlined some thirty times, spread the roles' loops
 // over more than the instruction cache.
 __device__ __forceinline__ bool chunk_wait(uint64_t* bar, uint32_t parity) {
-  bool ok = false;
+  uint32_t ok = 0;
 #pragma unroll 1
-  for (uint32_t n = 0; !ok && n < kChunkPolls; ++n) ok = mbar_try_wait(bar, parity);
-  return __all_sync(0xffffffffu, ok);
+  for (uint32_t n = 0; !ok && n < kChunkPolls; ++n)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "n"(kChunkPollNs)
+        : "memory");
+  return __all_sync(0xffffffffu, ok != 0);
 }
 
 // The weights 2^y of 32 tokens in pairs of f16; `sum` takes them over their two groups' V scale.
@@ -505,6 +514,17 @@ __device__ __forceinline__ void chunk_widen(const ChunkParams& p) {
   constexpr int CPR = D / 16, NJ = TT * CPR / Ly::CONV;
   static_assert(TT * CPR % Ly::CONV == 0, "chunks of a tile");
   const int cid = tid - Ly::CONV_WARP * 32;
+  // Row and column of the thread's j-th 16 codes. At head_dim 128 eight neighbouring lanes take
+  // the first half of an even row and the second of the odd one after it, or the other way
+  // round: their reads and, swizzled, their writes cover all banks.
+  auto chunk_row = [&](int j) -> int {
+    if constexpr (D == 128) return 16 * j + (cid >> 2 & 15);
+    return (cid + j * Ly::CONV) / CPR;
+  };
+  auto chunk_col = [&](int j) -> int {
+    if constexpr (D == 128) return (cid & 3) + ((cid >> 2 ^ cid >> 6) & 1) * 4;
+    return (cid + j * Ly::CONV) % CPR;
+  };
   bool ok = true;
   int sl = 0, rs = 0, filled = 0, ring = 0;
   uint32_t ph = 1, rph = 0;
@@ -523,29 +543,25 @@ __device__ __forceinline__ void chunk_widen(const ChunkParams& p) {
     for (int j0 = 0; j0 < NJ; j0 += NX) {
       uint4 src[NX];
 #pragma unroll
-      for (int x = 0; x < NX; ++x) src[x] = raw[cid + (j0 + x) * Ly::CONV];
+      for (int x = 0; x < NX; ++x) src[x] = raw[chunk_row(j0 + x) * CPR + chunk_col(j0 + x)];
 #pragma unroll
       for (int x = 0; x < NX; ++x) {
         const int j = j0 + x;
-        const int i = cid + j * Ly::CONV, row = i / CPR, c16 = i % CPR;
+        const int row = chunk_row(j), c16 = chunk_col(j);
         if (!every) {
           const int what = __float_as_int(scg[row >> 4].w);
-          if (is_v ? (row & 15) >= (what >> 8) : !(what & 1))
-            src[x] = make_uint4(0u, 0u, 0u, 0u);
+          if (is_v ? (row & 15) >= (what >> 8) : !(what & 1)) src[x] = make_uint4(0u, 0u, 0u, 0u);
         }
         uint4 o[2];
         widen8<E4M3>(src[x].x, o[0].x, o[0].y);
         widen8<E4M3>(src[x].y, o[0].z, o[0].w);
         widen8<E4M3>(src[x].z, o[1].x, o[1].y);
         widen8<E4M3>(src[x].w, o[1].z, o[1].w);
-        // the second column block's lanes store their odd chunk first, so that
-        // the eight lanes of a row (D 128) cover all banks
-        const int sw = (KB == 2 && c16 >= 4) ? 1 : 0;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int ch = 2 * c16 + (h ^ sw);
+          const int ch = 2 * c16 + h;
           *reinterpret_cast<uint4*>(dst + (ch >> 3) * (TT * 128) + row * 128 +
-                                    (((ch & 7) ^ (row & 7)) << 4)) = sw ^ h ? o[1] : o[0];
+                                    (((ch & 7) ^ (row & 7)) << 4)) = o[h];
         }
       }
     }
@@ -740,7 +756,11 @@ __device__ __forceinline__ void chunk_softmax(const ChunkParams& p) {
                 make_float2(__uint_as_float(raw[2 * e]), __uint_as_float(raw[2 * e + 1])),
                 make_float2(k.x, k.x), make_float2(k.y - mu, k.y - mu));
           }
-          if (h + 1 < 2 * HALVES) tmem_ld32(t_s + 32 * h + 32, raw);
+          // (All of raw has been used before it is loaded again, and it always is, the last time
+          // with columns that nobody looks at: otherwise each register costs a move.)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) asm volatile("" : "+f"(y[e].x), "+f"(y[e].y));
+          tmem_ld32(t_s + 32 * ((h + 1) % (2 * HALVES)), raw);
           if (masked) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
@@ -810,6 +830,7 @@ __device__ __forceinline__ void chunk_softmax(const ChunkParams& p) {
             if (lane == 0) mbar_arrive(&sm.p_full[b * HALVES + h / 2]);
           }
         }
+        tmem_wait_ld();
         if (failed) break;
       }
       if (failed) break;
