@@ -12,9 +12,10 @@
 //
 // What bounds it: the new rows are read once and their codes written once, HBM
 // for prompts; for single tokens the launch and three dependent loads (lengths,
-// table, scale beside rows). Work: a CTA per (page, kv head, K or V), which holds
-// the page's new rows in registers between the maximum and the codes; no page is
-// met by two CTAs, so there are no atomics and the same inputs give the same bits.
+// table, scale beside rows). Work: a warp per (page, kv head, K or V), which holds
+// up to 4096 elements of the page's new rows in registers between the maximum and the
+// codes (a page of more is read a second time, from L2); no page is met by two
+// warps, so there are no atomics and the same inputs give the same bits.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -58,46 +59,108 @@ __device__ __forceinline__ uint32_t power_above(uint32_t a) {
   return static_cast<uint32_t>(max(k, -126) + 127) << 23;
 }
 
-// Eight floats of eight neighbouring elements.
+// Eight neighbouring elements as they are in memory, their largest magnitude as bits (that
+// of infinities or NaN where there are any), and as floats.
 template <typename IT>
-__device__ __forceinline__ void load8(const IT* src, uint4 (&w)[Elem<IT>::bytes / 2]) {
-  w[0] = *reinterpret_cast<const uint4*>(src);
-  if constexpr (Elem<IT>::bytes == 4) w[1] = *(reinterpret_cast<const uint4*>(src) + 1);
+struct Raw {
+  uint4 w[Elem<IT>::bytes / 2];
+  __device__ __forceinline__ void load(const IT* src) {
+    w[0] = *reinterpret_cast<const uint4*>(src);
+    if constexpr (Elem<IT>::bytes == 4) w[1] = *(reinterpret_cast<const uint4*>(src) + 1);
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    constexpr int E = 4 / Elem<IT>::bytes;
+#pragma unroll
+    for (int i = 0; i < Elem<IT>::bytes / 2; ++i) {
+      widen_word<IT>(w[i].x, x + 4 * E * i);
+      widen_word<IT>(w[i].y, x + 4 * E * i + E);
+      widen_word<IT>(w[i].z, x + 4 * E * i + 2 * E);
+      widen_word<IT>(w[i].w, x + 4 * E * i + 3 * E);
+    }
+  }
+};
+// The largest of two words' elements' magnitudes: the bits without the sign are in their
+// order, 16 by 16 for the 16-bit types.
+template <typename IT>
+__device__ __forceinline__ uint32_t max_bits(uint32_t a, uint32_t b) {
+  if constexpr (Elem<IT>::bytes == 4) return max(a, b & 0x7FFFFFFFu);
+  return __vmaxu2(a, b & 0x7FFF7FFFu);
 }
 template <typename IT>
-__device__ __forceinline__ void widen8f(const uint4 (&w)[Elem<IT>::bytes / 2], float (&x)[8]) {
-  constexpr int E = 4 / Elem<IT>::bytes;
+__device__ __forceinline__ uint32_t max_bits(uint32_t a, const Raw<IT>& r) {
 #pragma unroll
   for (int i = 0; i < Elem<IT>::bytes / 2; ++i) {
-    widen_word<IT>(w[i].x, x + 4 * E * i);
-    widen_word<IT>(w[i].y, x + 4 * E * i + E);
-    widen_word<IT>(w[i].z, x + 4 * E * i + 2 * E);
-    widen_word<IT>(w[i].w, x + 4 * E * i + 3 * E);
+    a = max_bits<IT>(a, r.w[i].x);
+    a = max_bits<IT>(a, r.w[i].y);
+    a = max_bits<IT>(a, r.w[i].z);
+    a = max_bits<IT>(a, r.w[i].w);
+  }
+  return a;
+}
+// The magnitude that max_bits has found, as the bits of a float.
+template <typename IT>
+__device__ __forceinline__ uint32_t top_bits(uint32_t a) {
+  if constexpr (Elem<IT>::bytes == 4) {
+    return a;
+  } else {
+    float x[2];
+    widen_word<IT>(max(a >> 16, a & 0xFFFFu), x);
+    return __float_as_uint(x[0]);
   }
 }
-
-// x / s, exactly where s is a power of two (inv its reciprocal, else 0).
-__device__ __forceinline__ float over(float x, float s, float inv) {
-  return inv != 0.f ? x * inv : isnan(x) ? x : __fdiv_rn(x, s);
+// The largest finite magnitude among eight elements.
+template <typename IT>
+__device__ __forceinline__ uint32_t finite_bits(const Raw<IT>& r) {
+  uint32_t most = 0;
+  float x[8];
+  r.get(x);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t a = __float_as_uint(x[j]) & 0x7FFFFFFFu;
+    if (a < 0x7F800000u) most = max(most, a);
+  }
+  return most;
 }
 
-// NV: 8-element chunks a thread holds.
-template <typename IT, int D, int NV>
+// Two E4M3 codes (round to nearest even, saturating; a NaN gives a NaN code).
+__device__ __forceinline__ uint32_t codes2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Eight codes of x / s, where s is a power of two by its reciprocal inv (exactly), else 0.
+template <typename IT>
+__device__ __forceinline__ uint2 codes8(const Raw<IT>& r, float s, float inv) {
+  float x[8];
+  r.get(x);
+  if (inv != 0.f) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] *= inv;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = __fdiv_rn(x[j], s);
+  }
+  return make_uint2(codes2(x[0], x[1]) | codes2(x[2], x[3]) << 16,
+                    codes2(x[4], x[5]) | codes2(x[6], x[7]) << 16);
+}
+
+// NV: 8-element chunks a lane holds; ALL: they hold any page's new rows.
+template <typename IT, int D, int NV, bool ALL>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int CPR = D / 8;  // chunks of a row
-  __shared__ uint32_t top[kAppendThreads / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int H = p.kv_heads, bs = p.block_size, sh = 31 - __clz(bs);
-  const int lanes_of_page = 2 * H;
-  const int item = blockIdx.x / lanes_of_page, which = blockIdx.x % lanes_of_page;
+  const int index = blockIdx.x * (kAppendThreads / 32) + warp;
+  const int item = index / (2 * H), which = index - item * (2 * H);
   const bool is_v = which >= H;
   const int g = is_v ? which - H : which;
   pdl_wait();
   pdl_trigger();
+  if (item >= p.items) return;
 
-  // ---- the sequence and page of this item (every warp by itself, 32 sequences at a
-  // time); the first CTA goes on to the end and flags what does not fit
-  const bool reporter = blockIdx.x == 0 && warp == 0;
+  // ---- the sequence and page of this item (32 sequences at a time); the first warp goes on to
+  // the end and flags what does not fit
+  const bool reporter = index == 0;
   long long before = 0;  // pages of the sequences before this round's
   int s = -1, q0 = 0, len = 0, n = 0, page = 0;
   for (int b = 0; b < p.num_seqs && (s < 0 || reporter); b += 32) {
@@ -120,53 +183,56 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     }
     before += __shfl_sync(0xffffffffu, incl, 31);
   }
-  // offsets that name tokens twice reach more pages than there are CTAs
+  // offsets that name tokens twice reach more pages than there are warps for
   if (reporter && lane == 0 && before > p.items) raise_error(p.err, PA_DEVERR_SEQ);
   if (s < 0) return;
   const int begin = n - len;
   page += begin >> sh;
   const int b = p.block_tables[(size_t)s * p.max_blocks_per_seq + page];
-  if (b < 0 || b >= p.num_blocks) {
-    if (tid == 0) raise_error(p.err, PA_DEVERR_BLOCK_ID);
-    return;
-  }
   const int row0 = max(begin - (page << sh), 0);          // rows the page has already
   const int row1 = min(n - (page << sh), bs);             // and those after this
-  const size_t at = (size_t)b * H + g;                    // the page among all
-  uint8_t* codes = (is_v ? p.v_cache : p.k_cache) + (at << sh) * D;
-  float* scale = (is_v ? p.v_scales : p.k_scales) + at;
-  const float was = row0 > 0 ? *scale : 0.f;
-
-  // ---- the new rows, and their largest finite magnitude
   const int64_t stride = is_v ? p.value_stride : p.key_stride;
   const IT* src = static_cast<const IT*>(is_v ? p.value : p.key) +
                   (int64_t)(q0 + (page << sh) + row0 - begin) * stride + (int64_t)g * D;
   const int chunks = (row1 - row0) * CPR;
-  uint4 raw[NV][Elem<IT>::bytes / 2];
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int ch = tid + v * kAppendThreads;
-    if (ch < chunks) load8<IT>(src + (int64_t)(ch / CPR) * stride + 8 * (ch % CPR), raw[v]);
+  auto chunk = [&](int ch) { return src + (int64_t)(ch / CPR) * stride + 8 * (ch % CPR); };
+
+  // ---- the new rows, and their largest finite magnitude
+  Raw<IT> raw[NV];
+  uint32_t most = 0;
+  if constexpr (!ALL) {
+    for (int ch = lane + 32 * NV; ch < chunks; ch += 32) {
+      raw[0].load(chunk(ch));
+      most = max_bits(most, raw[0]);
+    }
   }
-  uint32_t most = 0;  // (the bits of numbers that are not negative are in their order)
 #pragma unroll
   for (int v = 0; v < NV; ++v)
-    if (tid + v * kAppendThreads < chunks) {
-      float x[8];
-      widen8f<IT>(raw[v], x);
+    if (lane + 32 * v < chunks) raw[v].load(chunk(lane + 32 * v));
+  if (b < 0 || b >= p.num_blocks) {
+    if (lane == 0) raise_error(p.err, PA_DEVERR_BLOCK_ID);
+    return;
+  }
+  const size_t at = (size_t)b * H + g;                    // the page among all
+  uint8_t* codes = (is_v ? p.v_cache : p.k_cache) + (at << sh) * D;
+  float* scale = (is_v ? p.v_scales : p.k_scales) + at;
+  const float was = row0 > 0 ? *scale : 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t a = __float_as_uint(x[j]) & 0x7FFFFFFFu;
-        if (a < 0x7F800000u) most = max(most, a);
-      }
+  for (int v = 0; v < NV; ++v)
+    if (lane + 32 * v < chunks) most = max_bits(most, raw[v]);
+  most = __reduce_max_sync(0xffffffffu, top_bits<IT>(most));
+  if (most >= 0x7F800000u) {  // (rare: infinities or NaN among them)
+    most = 0;
+    for (int ch = lane; ch < chunks; ch += 32) {
+      Raw<IT> r;
+      r.load(chunk(ch));
+      most = max(most, finite_bits(r));
     }
-  most = __reduce_max_sync(0xffffffffu, most);
-  if (lane == 0) top[warp] = most;
-  __syncthreads();  // (and everybody has read the old scale)
-#pragma unroll
-  for (int w = 0; w < kAppendThreads / 32; ++w) most = max(most, top[w]);
+    most = __reduce_max_sync(0xffffffffu, most);
+  }
   const float now = fmaxf(was, __uint_as_float(power_above(most)));
-  if (tid == 0) *scale = now;
+  __syncwarp();  // (everybody has read the old scale)
+  if (lane == 0) *scale = now;
   const float div = now == 0.f ? 1.f : now;  // (all zeros: codes of zero)
   const uint32_t bits = __float_as_uint(div);
   // the reciprocal of a power of two (a scale from elsewhere may be none)
@@ -175,22 +241,20 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
                         : 0.f;
 
   // ---- codes
+  uint8_t* dst = codes + (size_t)row0 * D;
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int ch = tid + v * kAppendThreads;
-    if (ch < chunks) {
-      float x[8];
-      widen8f<IT>(raw[v], x);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = over(x[j], div, inv);
-      *reinterpret_cast<uint2*>(codes + (size_t)row0 * D + 8 * ch) =
-          make_uint2(e4m3x2_from_float2(x[0], x[1]) | e4m3x2_from_float2(x[2], x[3]) << 16,
-                     e4m3x2_from_float2(x[4], x[5]) | e4m3x2_from_float2(x[6], x[7]) << 16);
+  for (int v = 0; v < NV; ++v)
+    if (lane + 32 * v < chunks)
+      *reinterpret_cast<uint2*>(dst + 8 * (lane + 32 * v)) = codes8(raw[v], div, inv);
+  if constexpr (!ALL) {
+    for (int ch = lane + 32 * NV; ch < chunks; ch += 32) {
+      raw[0].load(chunk(ch));
+      *reinterpret_cast<uint2*>(dst + 8 * ch) = codes8(raw[0], div, inv);
     }
   }
   if (row0 > 0 && now != was) {
     const float ratio = __fdiv_rn(was, div);
-    for (int i = tid; i < row0 * (D / 16); i += kAppendThreads) {
+    for (int i = lane; i < row0 * (D / 16); i += 32) {
       uint4* w = reinterpret_cast<uint4*>(codes) + i;
       uint4 c = *w;
       uint32_t* e = reinterpret_cast<uint32_t*>(&c);
@@ -198,8 +262,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
       for (int j = 0; j < 4; ++j) {
         float x[4];
         widen_word<E4M3>(e[j], x);
-        e[j] = e4m3x2_from_float2(x[0] * ratio, x[1] * ratio) |
-               e4m3x2_from_float2(x[2] * ratio, x[3] * ratio) << 16;
+        e[j] = codes2(x[0] * ratio, x[1] * ratio) | codes2(x[2] * ratio, x[3] * ratio) << 16;
       }
       *w = c;
     }
@@ -208,12 +271,17 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
 
 template <typename IT, int D>
 cudaError_t launch_append_d(AppendParams& p, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>(p.items) * 2u * p.kv_heads), block(kAppendThreads);
-  // chunks that a page of new rows can have (a page of 32 rows of 128: 512)
-  constexpr int kFew = 4;
-  return p.block_size * (D / 8) <= kFew * kAppendThreads
-             ? launch_pdl(append_kernel<IT, D, kFew>, grid, block, 0, st, p)
-             : launch_pdl(append_kernel<IT, D, 2 * kFew>, grid, block, 0, st, p);
+  const int64_t warps = (int64_t)p.items * 2 * p.kv_heads;
+  const dim3 grid(static_cast<unsigned>((warps + kAppendThreads / 32 - 1) / (kAppendThreads / 32)));
+  const dim3 block(kAppendThreads);
+  // chunks of a page's rows: 512 (32 rows of 128), and 16 a lane
+  constexpr int kHeld = Elem<IT>::bytes == 4 ? 8 : 16;
+  // (no more than a row or two of every page: single tokens)
+  if (p.tokens <= 2 * p.num_seqs)
+    return launch_pdl(append_kernel<IT, D, 1, false>, grid, block, 0, st, p);
+  return p.block_size * (D / 8) <= kHeld * 32
+             ? launch_pdl(append_kernel<IT, D, kHeld, true>, grid, block, 0, st, p)
+             : launch_pdl(append_kernel<IT, D, kHeld, false>, grid, block, 0, st, p);
 }
 
 template <typename IT>

@@ -22,7 +22,7 @@ struct AppendParams {
   unsigned* err;
   int tokens, num_seqs, kv_heads, block_size, num_blocks, max_blocks_per_seq;
   // most pages that the batch's tokens can touch: a sequence's len tokens lie in at most
-  // len pages and in at most len / bs + 2 (items * 2 * Hkv CTAs, below 2^31)
+  // len pages and in at most len / bs + 2 (items * 2 * Hkv warps, below 2^31)
   int items;
 };
 

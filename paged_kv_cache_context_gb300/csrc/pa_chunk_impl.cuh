@@ -505,7 +505,7 @@ __device__ __forceinline__ void chunk_issue(const ChunkParams& p) {
 template <int D, int NQ>
 __device__ __forceinline__ void chunk_widen(const ChunkParams& p) {
   using Ly = ChunkLayout<D, NQ>;
-  constexpr int KB = Ly::KB, NS = Ly::SLOTS, RS = Ly::RSLOTS, TT = Ly::TT, NG = Ly::NG;
+  constexpr int NS = Ly::SLOTS, RS = Ly::RSLOTS, TT = Ly::TT, NG = Ly::NG;
   const ChunkSmem<Ly> sm;
   const int tid = threadIdx.x, lane = tid & 31;
   ChunkWalk<Ly> w;

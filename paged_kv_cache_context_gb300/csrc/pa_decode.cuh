@@ -1985,7 +1985,8 @@ __global__ void __launch_bounds__(Layout<QT, CT, D, GT, BS, MODE>::THREADS,
 
 // Host side: launch one instantiation in the given mode. In balanced mode a
 // grid.x of 0 asks for the kernel's resident capacity (SMs x CTAs per SM,
-// at most kMaxBalancedCtas); the grid size used is returned in *ctas.
+// at most kMaxBalancedCtas), another for that many CTAs at most; the grid size used is
+// returned in *ctas.
 template <typename QT, typename CT, int D, int GT, int BS, int MODE>
 cudaError_t launch_decode(const DecodeParams& prm, dim3 grid, int* ctas, cudaStream_t stream) {
   using Ly = Layout<QT, CT, D, GT, BS, MODE>;
@@ -2009,8 +2010,10 @@ cudaError_t launch_decode(const DecodeParams& prm, dim3 grid, int* ctas, cudaStr
       __atomic_fetch_or(&configured_devices, 1 << dev, __ATOMIC_RELEASE);
     }
   }
-  if (MODE != kModeSplit && grid.x == 0)
-    grid.x = dev < 32 && capacity[dev] > 0 ? capacity[dev] : kMaxBalancedCtas;
+  if (MODE != kModeSplit) {  // (the caller's grid.x, if any, is the most it wants)
+    const unsigned cap = dev < 32 && capacity[dev] > 0 ? capacity[dev] : kMaxBalancedCtas;
+    if (grid.x == 0 || grid.x > cap) grid.x = cap;
+  }
   if (ctas) *ctas = static_cast<int>(grid.x);
   return launch_pdl(kern, grid, dim3(Ly::THREADS), Ly::SMEM, stream, prm);
 }

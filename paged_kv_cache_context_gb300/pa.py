@@ -880,9 +880,60 @@ def _rope_args(query, key, q_weight, k_weight, turns, positions):
 
 def _strided(stream, names: str, *tensors):
     """Device pointers of tensors on the current device, whatever their strides."""
-    _pointers(stream, names, *(t if t is None or t.is_contiguous() else t[:1, :1, :1]
+    cur = _raw_device() if torch.cuda.is_initialized() else -1
+    out = []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+        elif isinstance(t, torch.Tensor) and t.get_device() == cur >= 0:
+            out.append(t.data_ptr())
+        else:
+            break
+    if len(out) == len(tensors) and (stream is None or stream.device.index == cur):
+        return out
+    _pointers(stream, names, *(t.new_empty(0) if isinstance(t, torch.Tensor) else t
                                for t in tensors))
-    return [None if t is None else t.data_ptr() for t in tensors]
+    raise ValueError("tensors are not on the current device")
+
+
+def _dense_heads(t, shape, dtype) -> bool:
+    """Whether t [T, heads, D] of that shape and type has its heads dense."""
+    if t.shape != shape or t.dtype != dtype:
+        return False
+    st, D = t.stride(), shape[2]
+    return st[2] == 1 and (st[1] == D or shape[1] == 1)
+
+
+def _rope_sizes(query, key, others, q_weight, k_weight, turns, positions):
+    """(T, Hq, Hkv, D, R, A) of consistent arguments; raises on others. others: further
+    tensors by name, with the tensor whose shape and type they have."""
+    q, k, tu = query.shape, key.shape, turns.shape
+    if (len(q) == len(k) == 3 and len(tu) == 2 and k[0] == q[0] and k[2] == q[2] and
+            query.dtype in _DTYPE and _dense_heads(query, q, query.dtype) and
+            _dense_heads(key, k, query.dtype) and
+            all(_dense_heads(t, like.shape, query.dtype) for _, t, like in others) and
+            (q_weight is None or q_weight.shape == q[2:] and q_weight.dtype == torch.float32 and
+             q_weight.is_contiguous()) and
+            (k_weight is None or k_weight.shape == q[2:] and k_weight.dtype == torch.float32 and
+             k_weight.is_contiguous()) and
+            turns.dtype == torch.int64 and turns.is_contiguous() and
+            positions.dtype == torch.int32 and positions.is_contiguous() and
+            (positions.shape == (tu[0], q[0]) or tu[0] == 1 and positions.shape == q[:1])):
+        return q[0], q[1], k[1], q[2], 2 * tu[1], tu[0]
+    _heads("query", query)
+    _heads("key", key)
+    sizes = _rope_args(query, key, q_weight, k_weight, turns, positions)
+    for name, t, like in others:
+        _heads(name, t)
+        _shape(name, t, like.shape)
+        _dtype(name, t, query.dtype)
+    for name, t in (("q_weight", q_weight), ("k_weight", k_weight), ("turns", turns),
+                    ("positions", positions)):
+        _need(t is None or t.is_contiguous(), f"{name}: must be contiguous")
+    return sizes
+
+
+_ROPE = "query key q_weight k_weight turns positions"
 
 
 def norm_rope(q_out: torch.Tensor, k_out: torch.Tensor, query: torch.Tensor, key: torch.Tensor,
@@ -894,18 +945,13 @@ def norm_rope(q_out: torch.Tensor, k_out: torch.Tensor, query: torch.Tensor, key
     ([T] for one axis) with turns [A, R / 2] (see rope_turns); pairs (i, i + R / 2), or with
     interleaved (2i, 2i + 1). Tokens may be strided (views of one projection's output); the
     outputs may be the inputs."""
-    for name, t in (("q_out", q_out), ("k_out", k_out), ("query", query), ("key", key)):
-        _heads(name, t)
-    ptrs = _strided(stream, "q_out k_out query key q_weight k_weight turns positions", q_out,
-                    k_out, query, key, q_weight, k_weight, turns, positions)
-    T, Hq, Hkv, D, R, A = _rope_args(query, key, q_weight, k_weight, turns, positions)
-    for name, t, like in (("q_out", q_out, query), ("k_out", k_out, key)):
-        _shape(name, t, like.shape)
-        _dtype(name, t, like.dtype)
-    _check(lib().pa_norm_rope(*ptrs, T, Hq, Hkv, D, R, A, _token_stride(q_out),
-                              _token_stride(k_out), _token_stride(query), _token_stride(key),
-                              eps, int(interleaved), _DTYPE[query.dtype], _stream(stream)),
-           "pa_norm_rope")
+    sizes = _rope_sizes(query, key, (("q_out", q_out, query), ("k_out", k_out, key)), q_weight,
+                        k_weight, turns, positions)
+    ptrs = _strided(stream, "q_out k_out " + _ROPE, q_out, k_out, query, key, q_weight, k_weight,
+                    turns, positions)
+    _check(lib().pa_norm_rope(*ptrs, *sizes, _token_stride(q_out), _token_stride(k_out),
+                              _token_stride(query), _token_stride(key), eps, interleaved,
+                              _DTYPE[query.dtype], _stream(stream)), "pa_norm_rope")
 
 
 def norm_rope_and_cache(q_out: torch.Tensor, query: torch.Tensor, key: torch.Tensor,
@@ -917,32 +963,53 @@ def norm_rope_and_cache(q_out: torch.Tensor, query: torch.Tensor, key: torch.Ten
                         v_scale: float = 1.0, stream=None):
     """pa_norm_rope_and_cache: norm_rope whose keys go, with value [T, Hkv, D], to their cache
     slots (as reshape_and_cache after it, bit for bit)."""
-    for name, t in (("q_out", q_out), ("query", query), ("key", key), ("value", value)):
-        _heads(name, t)
-    ptrs = _strided(stream, "q_out query key value", q_out, query, key, value)
-    ptrs += _pointers(stream, "k_cache v_cache slot_mapping q_weight k_weight turns positions",
-                      k_cache, v_cache, slot_mapping_, q_weight, k_weight, turns, positions)
-    T, Hq, Hkv, D, R, A = _rope_args(query, key, q_weight, k_weight, turns, positions)
-    _shape("q_out", q_out, query.shape)
-    _dtype("q_out", q_out, query.dtype)
-    _shape("value", value, key.shape)
-    _dtype("value", value, key.dtype)
+    sizes = _rope_sizes(query, key, (("q_out", q_out, query), ("value", value, key)), q_weight,
+                        k_weight, turns, positions)
     _need(kv_dtype in ("auto", "fp8_e4m3"), f"kv_dtype: {kv_dtype!r} is not 'auto' or 'fp8_e4m3'")
+    T, _, Hkv, D, _, _ = sizes
     _check_caches(k_cache, v_cache, Hkv, D, _CACHE_DTYPE.get(kv_dtype, key.dtype))
     _shape("slot_mapping", slot_mapping_, (T,))
     _dtype("slot_mapping", slot_mapping_, torch.int64)
-    NB, _, bs, _ = k_cache.shape
-    _check(lib().pa_norm_rope_and_cache(*ptrs, T, Hq, Hkv, D, R, A, bs, NB, _token_stride(q_out),
-                                        _token_stride(query), _token_stride(key),
-                                        _token_stride(value), eps, int(interleaved),
-                                        _DTYPE[query.dtype], _KV[kv_dtype], k_scale, v_scale,
-                                        _stream(stream)), "pa_norm_rope_and_cache")
+    _need(k_cache.is_contiguous() and v_cache.is_contiguous() and slot_mapping_.is_contiguous(),
+          "tensors must be contiguous")
+    ptrs = _strided(stream, "q_out query key value k_cache v_cache slot_mapping q_weight k_weight "
+                    "turns positions", q_out, query, key, value, k_cache, v_cache, slot_mapping_,
+                    q_weight, k_weight, turns, positions)
+    _check(lib().pa_norm_rope_and_cache(*ptrs, *sizes, k_cache.shape[2], k_cache.shape[0],
+                                        _token_stride(q_out), _token_stride(query),
+                                        _token_stride(key), _token_stride(value), eps,
+                                        interleaved, _DTYPE[query.dtype], _KV[kv_dtype], k_scale,
+                                        v_scale, _stream(stream)), "pa_norm_rope_and_cache")
 
 
 def _check_page_scales(k_scales, v_scales, k_cache):
     for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
         _shape(name, t, k_cache.shape[:2])
         _dtype(name, t, torch.float32)
+
+
+def _block_args(k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, num_kv_heads: int,
+                head_dim: int, cu_q=None):
+    """(NB, bs, S, MB) of a consistent block-scaled cache and its tables; raises on others."""
+    k, bt = k_cache.shape, block_tables.shape
+    if (len(k) == 4 and len(bt) == 2 and k[1] == num_kv_heads and k[3] == head_dim and
+            v_cache.shape == k and k_cache.dtype == v_cache.dtype == torch.uint8 and
+            k_scales.shape == v_scales.shape == k[:2] and
+            k_scales.dtype == v_scales.dtype == torch.float32 and
+            context_lens.shape == bt[:1] and (cu_q is None or cu_q.shape == (bt[0] + 1,)) and
+            block_tables.dtype == context_lens.dtype == torch.int32 and
+            (cu_q is None or cu_q.dtype == torch.int32)):
+        return k[0], k[2], bt[0], bt[1]
+    _check_caches(k_cache, v_cache, num_kv_heads, head_dim, torch.uint8)
+    _check_page_scales(k_scales, v_scales, k_cache)
+    _need(len(bt) == 2, "block_tables: expected [num_seqs, max_blocks_per_seq]")
+    _dtype("block_tables", block_tables, torch.int32)
+    if cu_q is not None:
+        _shape("cu_q", cu_q, (bt[0] + 1,))
+        _dtype("cu_q", cu_q, torch.int32)
+    _shape("context_lens", context_lens, bt[:1])
+    _dtype("context_lens", context_lens, torch.int32)
+    raise ValueError("inconsistent arguments")
 
 
 def append_fp8_block(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor,
@@ -952,28 +1019,22 @@ def append_fp8_block(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tens
     """pa_append_fp8_block: key / value [T, Hkv, D] (offsets cu_q [S + 1], the last tokens of
     each sequence's context; tokens may be strided) into FP8 E4M3 caches (uint8 codes) with a
     scale per block and kv head (fp32 [NB, Hkv])."""
-    _heads("key", key)
-    _heads("value", value)
+    kv = key.shape
+    if not (len(kv) == 3 and key.dtype in _DTYPE and _dense_heads(key, kv, key.dtype) and
+            _dense_heads(value, kv, key.dtype)):
+        _heads("key", key)
+        _heads("value", value)
+        _need(key.dtype in _DTYPE, f"key: unsupported dtype {key.dtype}")
+        _shape("value", value, kv)
+        _dtype("value", value, key.dtype)
+    NB, bs, S, MB = _block_args(k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+                                kv[1], kv[2], cu_q)
     ptrs = _strided(stream, "key value", key, value)
     ptrs += _pointers(stream, "k_cache v_cache k_scales v_scales block_tables cu_q context_lens",
                       k_cache, v_cache, k_scales, v_scales, block_tables, cu_q, context_lens)
-    T, H, D = key.shape
-    _shape("value", value, key.shape)
-    _need(key.dtype in _DTYPE, f"key: unsupported dtype {key.dtype}")
-    _dtype("value", value, key.dtype)
-    _check_caches(k_cache, v_cache, H, D, torch.uint8)
-    _check_page_scales(k_scales, v_scales, k_cache)
-    _need(block_tables.dim() == 2, "block_tables: expected [num_seqs, max_blocks_per_seq]")
-    _dtype("block_tables", block_tables, torch.int32)
-    S, MB = block_tables.shape
-    _shape("cu_q", cu_q, (S + 1,))
-    _dtype("cu_q", cu_q, torch.int32)
-    _shape("context_lens", context_lens, (S,))
-    _dtype("context_lens", context_lens, torch.int32)
-    NB, _, bs, _ = k_cache.shape
-    _check(lib().pa_append_fp8_block(*ptrs, T, S, H, D, bs, NB, MB, _token_stride(key),
-                                     _token_stride(value), _DTYPE[key.dtype], _stream(stream)),
-           "pa_append_fp8_block")
+    _check(lib().pa_append_fp8_block(*ptrs, kv[0], S, kv[1], kv[2], bs, NB, MB,
+                                     _token_stride(key), _token_stride(value), _DTYPE[key.dtype],
+                                     _stream(stream)), "pa_append_fp8_block")
 
 
 def decode_fp8_block(out: torch.Tensor, query: torch.Tensor, k_cache: torch.Tensor,
@@ -985,15 +1046,17 @@ def decode_fp8_block(out: torch.Tensor, query: torch.Tensor, k_cache: torch.Tens
     *ptrs, ws = _pointers(stream, "out query k_cache v_cache k_scales v_scales block_tables "
                           "context_lens workspace", out, query, k_cache, v_cache, k_scales,
                           v_scales, block_tables, context_lens, workspace)
-    _check_decode_args(out, query, k_cache, v_cache, block_tables, context_lens, num_kv_heads,
-                       torch.uint8)
-    _need(query.dtype in _DTYPE, f"query: unsupported dtype {query.dtype}")
-    _check_page_scales(k_scales, v_scales, k_cache)
-    S, Hq, D = query.shape
-    NB, _, bs, _ = k_cache.shape
-    _check(lib().pa_decode_fp8_block(*ptrs, S, Hq, num_kv_heads, D, bs, NB,
-                                     block_tables.shape[1], scale, _DTYPE[query.dtype], ws,
-                                     _nbytes(workspace), _stream(stream)), "pa_decode_fp8_block")
+    q = query.shape
+    NB, bs, S, MB = _block_args(k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+                                num_kv_heads, q[-1])
+    if not (len(q) == 3 and q[0] == S and out.shape == q and query.dtype in _DTYPE and
+            out.dtype == query.dtype):
+        _check_decode_args(out, query, k_cache, v_cache, block_tables, context_lens, num_kv_heads,
+                           torch.uint8)
+        _need(query.dtype in _DTYPE, f"query: unsupported dtype {query.dtype}")
+    _check(lib().pa_decode_fp8_block(*ptrs, S, q[1], num_kv_heads, q[2], bs, NB, MB, scale,
+                                     _DTYPE[query.dtype], ws, _nbytes(workspace),
+                                     _stream(stream)), "pa_decode_fp8_block")
 
 
 def prefill_fp8_block_workspace_size(num_heads: int, num_kv_heads: int, head_dim: int) -> int:
@@ -1010,24 +1073,19 @@ def prefill_fp8_block(out: torch.Tensor, query: torch.Tensor, k_cache: torch.Ten
     *ptrs, ws = _pointers(stream, "out query k_cache v_cache k_scales v_scales block_tables cu_q "
                           "context_lens workspace", out, query, k_cache, v_cache, k_scales,
                           v_scales, block_tables, cu_q, context_lens, workspace)
-    _need(query.dim() == 3, "query: expected [num_tokens, num_heads, head_dim]")
-    _shape("out", out, query.shape)
-    _dtype("out", out, query.dtype)
-    _need(query.dtype in _DTYPE, f"query: unsupported dtype {query.dtype}")
-    T, Hq, D = query.shape
-    _check_caches(k_cache, v_cache, num_kv_heads, D, torch.uint8)
-    _check_page_scales(k_scales, v_scales, k_cache)
-    _need(block_tables.dim() == 2, "block_tables: expected [num_seqs, max_blocks_per_seq]")
-    _dtype("block_tables", block_tables, torch.int32)
-    S, MB = block_tables.shape
-    _shape("cu_q", cu_q, (S + 1,))
-    _dtype("cu_q", cu_q, torch.int32)
-    _shape("context_lens", context_lens, (S,))
-    _dtype("context_lens", context_lens, torch.int32)
-    NB, _, bs, _ = k_cache.shape
-    _check(lib().pa_prefill_fp8_block(*ptrs, T, S, Hq, num_kv_heads, D, bs, NB, MB, max_q_len,
-                                      scale, _DTYPE[query.dtype], ws, _nbytes(workspace),
-                                      _stream(stream)), "pa_prefill_fp8_block")
+    q = query.shape
+    if not (len(q) == 3 and out.shape == q and query.dtype in _DTYPE and
+            out.dtype == query.dtype):
+        _need(len(q) == 3, "query: expected [num_tokens, num_heads, head_dim]")
+        _shape("out", out, q)
+        _dtype("out", out, query.dtype)
+        _need(False, f"query: unsupported dtype {query.dtype}")
+    NB, bs, S, MB = _block_args(k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+                                num_kv_heads, q[2], cu_q)
+    _check(lib().pa_prefill_fp8_block(*ptrs, q[0], S, q[1], num_kv_heads, q[2], bs, NB, MB,
+                                      max_q_len, scale, _DTYPE[query.dtype], ws,
+                                      _nbytes(workspace), _stream(stream)),
+           "pa_prefill_fp8_block")
 
 
 PA_BUDGET_MB, PA_BUDGET_FRACTION, PA_BUDGET_CONTEXT = 0, 1, 2

@@ -238,3 +238,34 @@ def test_binding_refuses_what_it_cannot_pass():
         pa.norm_rope(q, k, q[0], k, tu, pos)
     with pytest.raises(ValueError, match="contiguous"):
         pa.append_fp8_block(k[:, :, ::2], k[:, :, ::2], *[k] * 7)
+    with pytest.raises(ValueError, match="key"):
+        pa.norm_rope(q, k, q, k[:2], tu, pos)
+    with pytest.raises(ValueError, match="positions"):
+        pa.norm_rope(q, k, q, k, tu, pos.long())
+    with pytest.raises(ValueError, match="q_weight"):
+        pa.norm_rope(q, k, q, k, tu, pos, q_weight=torch.ones(64))
+    with pytest.raises(ValueError, match="q_out"):
+        pa.norm_rope(q.half(), k, q, k, tu, pos)
+    kc = torch.zeros(4, 2, 32, 128)
+    slots = torch.zeros(3, dtype=torch.int64)
+    with pytest.raises(ValueError, match="kv_dtype"):
+        pa.norm_rope_and_cache(q, q, k, k, kc, kc, slots, tu, pos, kv_dtype="int8")
+    with pytest.raises(ValueError, match="slot_mapping"):
+        pa.norm_rope_and_cache(q, q, k, k, kc, kc, slots.int(), tu, pos)
+    with pytest.raises(ValueError, match="k_cache"):
+        pa.norm_rope_and_cache(q, q, k, k, kc.half(), kc.half(), slots, tu, pos)
+    codes, sc = kc.to(torch.uint8), torch.zeros(4, 2)
+    bt, cu, n = (torch.zeros(s, dtype=torch.int32) for s in ((1, 4), (2,), (1,)))
+    for bad, name in (((codes, codes.int(), sc, sc, bt, cu, n), "v_cache"),
+                      ((codes, codes, sc[:3], sc, bt, cu, n), "k_scales"),
+                      ((codes, codes, sc, sc.double(), bt, cu, n), "v_scales"),
+                      ((codes, codes, sc, sc, bt[0], cu, n), "block_tables"),
+                      ((codes, codes, sc, sc, bt, cu[:1], n), "cu_q"),
+                      ((codes, codes, sc, sc, bt, cu, n.long()), "context_lens"),
+                      ((codes, codes, sc, sc, bt, cu, n), "CUDA tensor")):
+        with pytest.raises(ValueError, match=name):
+            pa.append_fp8_block(k, k, *bad)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        pa.decode_fp8_block(q, q, codes, codes, sc, sc, bt, n, 2, 0.1, codes)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        pa.prefill_fp8_block(q, q, codes, codes, sc, sc, bt, cu, n, 2, 3, 0.1, codes)
