@@ -246,6 +246,21 @@ __device__ __forceinline__ void chunk_weigh(const float2 (&y)[16], const float4*
     sum = fmaf(part.x + part.y, sc[g].z, sum);
   }
 }
+// That sum of the weights as they were rounded; where f16's range has taken weights of pages
+// of tiny V scales away (they count in the sum), which shows, the sum as it is.
+__device__ __forceinline__ float chunk_rounded_sum(const uint32_t (&pk)[16], const float4* sc,
+                                                   float sum) {
+  float rounded = 0.f;
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    float2 part = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int e = 8 * g; e < 8 * g + 8; ++e)
+      part = __fadd2_rn(part, __half22float2(*reinterpret_cast<const __half2*>(&pk[e])));
+    rounded = fmaf(part.x + part.y, sc[g].z, rounded);
+  }
+  return fabsf(rounded - sum) <= 0x1.01p-11f * sum ? rounded : sum;
+}
 __device__ __forceinline__ float chunk_largest(const float2 (&y)[16]) {
   float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -820,6 +835,10 @@ __device__ __forceinline__ void chunk_softmax(const ChunkParams& p) {
             for (int e = 0; e < 16; ++e) y[e] = make_float2(y[e].x - down, y[e].y - down);
             sum = 0.f;
             chunk_weigh(y, sch, sum, pk);
+            // f16 outputs, so that rounding moves a mean of a few tokens (all of them come here:
+            // the first do) by its share of v - mean alone: a lone token's output is its V
+            // exactly. Beside bf16's own rounding it is nothing; of all weights it cost 11 %.
+            if (std::is_same<QT, __half>::value) sum = chunk_rounded_sum(pk, sch, sum);
           }
           l += sum;
           tmem_st16(t_s + 16 * h, pk);

@@ -340,6 +340,10 @@ struct Layout {
   static constexpr bool PAGE_SCALES = std::is_same<CT, E4M3B>::value;
   // weights that meet a V scale before they are rounded, held at the top of f16's range
   static constexpr bool TOPPED = SCORED || PAGE_SCALES;
+  // f16 outputs: under a V scale that is a power of two the sum takes the weights as they are
+  // rounded, so that the rounding moves the mean by its share of v - mean alone (a lone
+  // token's output is its V exactly); beside bf16's own rounding it is nothing
+  static constexpr bool ROUNDED_SUM = PAGE_SCALES && std::is_same<QT, __half>::value;
   static constexpr int OFF_Q = 2 * PAGE + 2 * SCB;
   // K page | V page | (K row scales | V row scales) | q rows; the swizzled
   // boxes of the tensor-core layout start on 1024-byte boundaries
@@ -1110,6 +1114,11 @@ __device__ __forceinline__ void process_tc8(Tc8State<D>& st, const uint8_t* cons
       // masked rows keep a zero weight, whatever their scale holds
       const float va = vsc[j][Ly::PAGE_SCALES ? 0 : r0[j] + kr];
       const float vb = vsc[j][Ly::PAGE_SCALES ? 0 : r0[j] + 8 + kr];
+      if (Ly::ROUNDED_SUM && (__float_as_uint(va) & 0x7FFFFFu) == 0) {
+        const float2 w01 = to_11_bits(make_float2(pw[0], pw[1]));
+        const float2 w23 = to_11_bits(make_float2(pw[2], pw[3]));
+        pw[0] = w01.x, pw[1] = w01.y, pw[2] = w23.x, pw[3] = w23.y;
+      }
       st.l_run[0] += pw[0] + pw[2];
       st.l_run[1] += pw[1] + pw[3];
       p01 = __floats2half2_rn(pw[0] == 0.f ? 0.f : pw[0] * va, pw[1] == 0.f ? 0.f : pw[1] * va);

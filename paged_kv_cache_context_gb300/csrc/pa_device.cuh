@@ -133,6 +133,13 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
+// w rounded to the 11 bits that f16 keeps, at any exponent (Dekker's splitting: c - (c - w) for
+// c = (2^13 + 1) w, whose roundings take w's last 13 bits off).
+__device__ __forceinline__ float2 to_11_bits(float2 w) {
+  const float2 c = __fmul2_rn(w, make_float2(8193.f, 8193.f)), minus = make_float2(-1.f, -1.f);
+  return __ffma2_rn(minus, __ffma2_rn(minus, w, c), c);
+}
+
 // ---------------------------------------------------------------- tcgen05
 // Fifth-generation tensor-core MMAs with accumulators in tensor memory
 // (TMEM: 128 lanes x 512 columns of 32 bits per SM), issued by one thread,

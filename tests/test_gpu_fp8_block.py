@@ -349,6 +349,19 @@ def test_prefill_of_one_token_is_the_decode():
     check_decode(c, 4, q, b, 0.1)
 
 
+@pytest.mark.parametrize("D,Hkv,G,bs", [(128, 2, 4, 32), (64, 1, 8, 16), (96, 3, 1, 64)])
+def test_a_lone_token_answers_its_value_exactly(D, Hkv, G, bs):
+    """With one weight the mean is V whatever the weight is: f16 holds a code times a power
+    of two (2^-6 to 2^-9 here) as it is, so its rounding may not show."""
+    c = BlockCache([1, 1], Hkv, D, bs, seed=4, spread=3)
+    q = queries([1, 1], Hkv * G, D, torch.float16)
+    for out in (decode(c, q.cuda(), 0.3), prefill(c, q.cuda(), [1, 1], 0.3)):
+        for s in range(2):
+            for g in range(Hkv):
+                v = torch.from_numpy(c.rows(s, g)[1][0])
+                assert (out[s, g * G:(g + 1) * G].double().cpu() == v).all(), (s, g)
+
+
 @pytest.mark.parametrize("scale", [-0.2, 0.0, 3.0])
 @pytest.mark.parametrize("news", [[20], [150]])
 def test_prefill_with_other_scales(scale, news):
@@ -426,8 +439,8 @@ def test_prefill_captured_and_replayed_on_another_stream():
 
 # ------------------------------------------------------------------ together
 def test_projection_to_attention_step_by_step():
-    """norm_rope, append and decode as a model's layer calls them, against the definition over the
-    codes that are in the cache; and those codes against the rows that were written."""
+    """norm_rope, append, prefill and decode as a model's layer calls them, against the definition
+    over the codes that are in the cache; and those codes against the rows that were written."""
     pa.get_device_error()
     H, G, D, bs, S = 2, 4, 128, 32, 3
     pool = Pool(S, 90, H, D, bs, 40)
@@ -449,12 +462,14 @@ def test_projection_to_attention_step_by_step():
         for s, a in enumerate(news):
             rows[s].append(k[at: at + a].cpu())
             at += a
-        if min(news) != 1 or max(news) != 1:
-            continue
         c = pool.c
         c.lens, c._dev = pool.lens, dict(pool.d, lens=i32(pool.lens))
-        out = decode(c, q.contiguous(), default_scale(D))
-        check_decode(c, G, q, out, default_scale(D))
+        if min(news) == max(news) == 1:
+            out = decode(c, q.contiguous(), default_scale(D))
+            check_decode(c, G, q, out, default_scale(D))
+        else:
+            out = prefill(c, q.contiguous(), news, default_scale(D))
+            check_prefill(c, G, q, news, out, default_scale(D), 9)
     assert pa.get_device_error() == 0
     for s in range(S):
         want = torch.cat(rows[s]).double()
