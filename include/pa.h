@@ -81,7 +81,7 @@ typedef enum {
     PA_KV_AUTO = 0,
     PA_KV_FP8_E4M3 = 1,
     PA_KV_INT8 = 2,
-    PA_KV_FP8_BLOCK = 3
+    PA_KV_FP8_BLOCK = 4 /* (3 names no type and is refused) */
 } pa_kv_dtype;
 
 /* Bits of the per-device error word (see pa_get_device_error). */

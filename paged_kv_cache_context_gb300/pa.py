@@ -26,7 +26,7 @@ LIB_PATH = os.path.join(_HERE, "_lib", "libpagedattn.so")
 
 # enums of include/pa.h
 PA_F32, PA_BF16, PA_F16 = 0, 1, 2
-PA_KV_AUTO, PA_KV_FP8_E4M3, PA_KV_INT8, PA_KV_FP8_BLOCK = 0, 1, 2, 3
+PA_KV_AUTO, PA_KV_FP8_E4M3, PA_KV_INT8, PA_KV_FP8_BLOCK = 0, 1, 2, 4
 PA_ERR_DEVICE = -9
 DEVERR_BITS = {1: "slot", 2: "block_id", 4: "context_len", 8: "timeout", 16: "seq"}
 

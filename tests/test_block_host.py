@@ -53,7 +53,7 @@ def store(L, **kw):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(v=None), -1), (dict(slots=None), -1), (dict(kc=None), -1), (dict(kv=2), -2),
-    (dict(kv=3), -2), (dict(dt=5), -2), (dict(NB=0), -3), (dict(sv=100), -3), (dict(R=24), -3),
+    (dict(kv=3), -2), (dict(kv=pa.PA_KV_FP8_BLOCK), -2), (dict(dt=5), -2), (dict(NB=0), -3), (dict(sv=100), -3), (dict(R=24), -3),
     (dict(D=100), -4), (dict(bs=0), -5), (dict(bs=1025), -5), (dict(vc=P + 4), -10),
     (dict(slots=P + 4), -10), (dict(kv=1, k1=0.0), -11), (dict(kv=1, v1=float("nan")), -11),
 ])
@@ -191,8 +191,10 @@ def test_the_shares_cover_every_tile_once():
 
 def test_the_other_decodes_refuse_the_block_scaled_kind(L):
     f = L.pa_decode
-    assert f(P, P, P, P, P, P, 2, 8, 2, 128, 32, 10, 4, 0.1, 0, 1, 3, 1.0, 1.0, None, 0, None) == -2
-    assert L.pa_reshape_and_cache(P, P, P, P, P, 2, 2, 128, 32, 10, 1, 3, 1.0, 1.0, None) == -2
+    for kv in (pa.PA_KV_FP8_BLOCK, 3):
+        assert f(P, P, P, P, P, P, 2, 8, 2, 128, 32, 10, 4, 0.1, 0, 1, kv, 1.0, 1.0, None, 0, None) == -2
+        assert L.pa_reshape_and_cache(P, P, P, P, P, 2, 2, 128, 32, 10, 1, kv, 1.0, 1.0, None) == -2
+    assert L.pa_block_budget(0, 1.0, 0, 32, 8, 128, 32, 1, 3) == -2
 
 
 def test_block_budget_counts_the_page_scales(L):
