@@ -249,7 +249,8 @@ __global__ void __launch_bounds__(kRopeThreads, 3)
       const float2 own = __fmul2_rn(x[j], ca[j]);
       x[j] = turns ? __ffma2_rn(y[j], cb[j], own) : own;
     }
-    raw.set(x);
+    // (lanes past a head stay zeros: times a NaN's norm they would be in the next head's sum)
+    if (on) raw.set(x);
   };
   // A head's eight elements into the cache (of a token that has a slot).
   auto cached = [&](Row& raw, void* cache, int h, float scale) {

@@ -212,3 +212,21 @@ def test_values_that_are_not_finite_stay_in_their_heads():
     pa.norm_rope(qo, ko, q, k, turns, pos, qw, kw)
     bad_q, bad_k = ~qo.isfinite().all(-1), ~ko.isfinite().all(-1)
     assert bad_q.sum() == 1 and bad_q[2, 1] and bad_k.sum() == 1 and bad_k[3, 0]
+
+
+@pytest.mark.parametrize("T,D,dtype", [(2, 96, torch.float16), (900, 96, torch.bfloat16),
+                                       (3000, 80, torch.float32), (900, 176, torch.float16)])
+def test_a_head_of_nan_or_zeros_leaves_the_others_of_its_token(T, D, dtype):
+    """Head sizes that leave lanes without elements, and lanes that take many heads; eps = 0 makes
+    a head of zeros NaN."""
+    q, k, v, qw, kw, pos = inputs(T, 20, 4, D, 1, dtype, True, 3)
+    q[:, 1, 3] = float("nan")
+    q[:, 12] = 0
+    k[:, 0, 5] = float("-inf")
+    f = freqs(D - D % 32, 1)
+    qo, ko = (torch.zeros_like(x, memory_format=torch.contiguous_format) for x in (q, k))
+    pa.norm_rope(qo, ko, q, k, pa.rope_turns(f, "cuda"), pos, qw, kw, 0.0)
+    keep = [h for h in range(20) if h not in (1, 12)]
+    assert bool(qo[:, [1, 12]].isnan().any(-1).all())
+    check(qo[:, keep], *turned(q[:, keep], qw, f, pos, 0.0, False))
+    check(ko[:, 1:], *turned(k[:, 1:], kw, f, pos, 0.0, False))
