@@ -145,10 +145,19 @@ __global__ void __launch_bounds__(kRopeThreads, 3)
   for (int i = tid; i < toks * R2; i += kRopeThreads) {
     const int tt = t0 + i / R2, j = i % R2;
     uint64_t a = 0;
-    if (tt < p.tokens)
-      for (int x = 0; x < p.axes; ++x)
-        a += static_cast<uint64_t>(static_cast<int64_t>(p.positions[(size_t)x * p.tokens + tt])) *
-             p.turns[x * R2 + j];
+    for (int x0 = 0; x0 < p.axes; x0 += 4) {  // (four axes' loads in flight together)
+      int32_t pos[4];
+      uint64_t per_step[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const bool there = x0 + x < p.axes && tt < p.tokens;
+        pos[x] = there ? p.positions[(size_t)(x0 + x) * p.tokens + tt] : 0;
+        per_step[x] = there ? p.turns[(x0 + x) * R2 + j] : 0;
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        a += static_cast<uint64_t>(static_cast<int64_t>(pos[x])) * per_step[x];
+    }
     // twice the fraction of a turn: half turns in [-1, 1)
     const float half = static_cast<float>(static_cast<int32_t>(a >> 32)) * 0x1p-31f;
     sincospif(half, &turn[1][i], &turn[0][i]);
