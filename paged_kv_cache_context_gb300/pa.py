@@ -965,17 +965,22 @@ def norm_rope_and_cache(q_out: torch.Tensor, query: torch.Tensor, key: torch.Ten
     slots (as reshape_and_cache after it, bit for bit)."""
     sizes = _rope_sizes(query, key, (("q_out", q_out, query), ("value", value, key)), q_weight,
                         k_weight, turns, positions)
-    _need(kv_dtype in ("auto", "fp8_e4m3"), f"kv_dtype: {kv_dtype!r} is not 'auto' or 'fp8_e4m3'")
-    T, _, Hkv, D, _, _ = sizes
-    _check_caches(k_cache, v_cache, Hkv, D, _CACHE_DTYPE.get(kv_dtype, key.dtype))
-    _shape("slot_mapping", slot_mapping_, (T,))
-    _dtype("slot_mapping", slot_mapping_, torch.int64)
-    _need(k_cache.is_contiguous() and v_cache.is_contiguous() and slot_mapping_.is_contiguous(),
-          "tensors must be contiguous")
+    kc, stored = k_cache.shape, torch.uint8 if kv_dtype == "fp8_e4m3" else key.dtype
+    if not (kv_dtype in ("auto", "fp8_e4m3") and len(kc) == 4 and v_cache.shape == kc and
+            kc[1] == sizes[2] and kc[3] == sizes[3] and
+            k_cache.dtype == v_cache.dtype == stored and slot_mapping_.shape == query.shape[:1] and
+            slot_mapping_.dtype == torch.int64 and k_cache.is_contiguous() and
+            v_cache.is_contiguous() and slot_mapping_.is_contiguous()):
+        _need(kv_dtype in ("auto", "fp8_e4m3"),
+              f"kv_dtype: {kv_dtype!r} is not 'auto' or 'fp8_e4m3'")
+        _check_caches(k_cache, v_cache, sizes[2], sizes[3], stored)
+        _shape("slot_mapping", slot_mapping_, query.shape[:1])
+        _dtype("slot_mapping", slot_mapping_, torch.int64)
+        raise ValueError("k_cache, v_cache, slot_mapping: must be contiguous")
     ptrs = _strided(stream, "q_out query key value k_cache v_cache slot_mapping q_weight k_weight "
                     "turns positions", q_out, query, key, value, k_cache, v_cache, slot_mapping_,
                     q_weight, k_weight, turns, positions)
-    _check(lib().pa_norm_rope_and_cache(*ptrs, *sizes, k_cache.shape[2], k_cache.shape[0],
+    _check(lib().pa_norm_rope_and_cache(*ptrs, *sizes, kc[2], kc[0],
                                         _token_stride(q_out), _token_stride(query),
                                         _token_stride(key), _token_stride(value), eps,
                                         interleaved, _DTYPE[query.dtype], _KV[kv_dtype], k_scale,
