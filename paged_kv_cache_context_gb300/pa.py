@@ -879,58 +879,57 @@ def _rope_args(query, key, q_weight, k_weight, turns, positions):
 
 
 def _strided(stream, names: str, *tensors):
-    """Device pointers of tensors on the current device, whatever their strides."""
+    """Device pointers of tensors on the current device, whatever their strides (None where an
+    optional one is missing)."""
     cur = _raw_device() if torch.cuda.is_initialized() else -1
-    out = []
-    for t in tensors:
-        if t is None:
-            out.append(None)
-        elif isinstance(t, torch.Tensor) and t.get_device() == cur >= 0:
-            out.append(t.data_ptr())
-        else:
-            break
-    if len(out) == len(tensors) and (stream is None or stream.device.index == cur):
-        return out
+    if cur >= 0 and (stream is None or stream.device.index == cur):
+        out = [None if t is None else t.data_ptr() if t.get_device() == cur else -1
+               for t in tensors]
+        if -1 not in out:
+            return out
     _pointers(stream, names, *(t.new_empty(0) if isinstance(t, torch.Tensor) else t
                                for t in tensors))
     raise ValueError("tensors are not on the current device")
 
 
-def _dense_heads(t, shape, dtype) -> bool:
-    """Whether t [T, heads, D] of that shape and type has its heads dense."""
-    if t.shape != shape or t.dtype != dtype:
-        return False
+def _dense_heads(t, shape, dtype) -> int:
+    """Elements between the tokens of t [T, heads, D] (one token: its own size) where it has that
+    shape and type and its heads are dense, else 0."""
+    if t.shape != shape or t.dtype is not dtype:
+        return 0
     st, D = t.stride(), shape[2]
-    return st[2] == 1 and (st[1] == D or shape[1] == 1)
+    if st[2] != 1 or st[1] != D and shape[1] != 1:
+        return 0
+    return st[0] if shape[0] > 1 else shape[1] * D
 
 
-def _rope_sizes(query, key, others, q_weight, k_weight, turns, positions):
-    """(T, Hq, Hkv, D, R, A) of consistent arguments; raises on others. others: further
-    tensors by name, with the tensor whose shape and type they have."""
-    q, k, tu = query.shape, key.shape, turns.shape
-    if (len(q) == len(k) == 3 and len(tu) == 2 and k[0] == q[0] and k[2] == q[2] and
-            query.dtype in _DTYPE and _dense_heads(query, q, query.dtype) and
-            _dense_heads(key, k, query.dtype) and
-            all(_dense_heads(t, like.shape, query.dtype) for _, t, like in others) and
-            (q_weight is None or q_weight.shape == q[2:] and q_weight.dtype == torch.float32 and
-             q_weight.is_contiguous()) and
-            (k_weight is None or k_weight.shape == q[2:] and k_weight.dtype == torch.float32 and
-             k_weight.is_contiguous()) and
-            turns.dtype == torch.int64 and turns.is_contiguous() and
-            positions.dtype == torch.int32 and positions.is_contiguous() and
-            (positions.shape == (tu[0], q[0]) or tu[0] == 1 and positions.shape == q[:1])):
-        return q[0], q[1], k[1], q[2], 2 * tu[1], tu[0]
+def _rope_sizes(query, key, out, other, name, q_weight, k_weight, turns, positions):
+    """(T, Hq, Hkv, D, R, A) of consistent arguments, and the token strides of query, key, out
+    (q_out) and other (`name`: k_out or value); raises on others."""
+    q, k, tu, dtype, f32 = query.shape, key.shape, turns.shape, query.dtype, torch.float32
+    if len(q) == len(k) == 3 and len(tu) == 2 and k[0] == q[0] and k[2] == q[2] and dtype in _DTYPE:
+        strides = (_dense_heads(query, q, dtype), _dense_heads(key, k, dtype),
+                   _dense_heads(out, q, dtype), _dense_heads(other, k, dtype))
+        if (0 not in strides and
+                (q_weight is None or q_weight.shape == q[2:] and q_weight.dtype is f32 and
+                 q_weight.is_contiguous()) and
+                (k_weight is None or k_weight.shape == q[2:] and k_weight.dtype is f32 and
+                 k_weight.is_contiguous()) and
+                turns.dtype is torch.int64 and turns.is_contiguous() and
+                positions.dtype is torch.int32 and positions.is_contiguous() and
+                (positions.shape == (tu[0], q[0]) or tu[0] == 1 and positions.shape == q[:1])):
+            return (q[0], q[1], k[1], q[2], 2 * tu[1], tu[0]), strides
     _heads("query", query)
     _heads("key", key)
     sizes = _rope_args(query, key, q_weight, k_weight, turns, positions)
-    for name, t, like in others:
-        _heads(name, t)
-        _shape(name, t, like.shape)
-        _dtype(name, t, query.dtype)
-    for name, t in (("q_weight", q_weight), ("k_weight", k_weight), ("turns", turns),
-                    ("positions", positions)):
-        _need(t is None or t.is_contiguous(), f"{name}: must be contiguous")
-    return sizes
+    for n, t, like in (("q_out", out, query), (name, other, key)):
+        _heads(n, t)
+        _shape(n, t, like.shape)
+        _dtype(n, t, dtype)
+    for n, t in (("q_weight", q_weight), ("k_weight", k_weight), ("turns", turns),
+                 ("positions", positions)):
+        _need(t is None or t.is_contiguous(), f"{n}: must be contiguous")
+    return sizes, tuple(_token_stride(t) for t in (query, key, out, other))
 
 
 _ROPE = "query key q_weight k_weight turns positions"
@@ -945,12 +944,11 @@ def norm_rope(q_out: torch.Tensor, k_out: torch.Tensor, query: torch.Tensor, key
     ([T] for one axis) with turns [A, R / 2] (see rope_turns); pairs (i, i + R / 2), or with
     interleaved (2i, 2i + 1). Tokens may be strided (views of one projection's output); the
     outputs may be the inputs."""
-    sizes = _rope_sizes(query, key, (("q_out", q_out, query), ("k_out", k_out, key)), q_weight,
-                        k_weight, turns, positions)
+    sizes, (sq, sk, sqo, sko) = _rope_sizes(query, key, q_out, k_out, "k_out", q_weight, k_weight,
+                                            turns, positions)
     ptrs = _strided(stream, "q_out k_out " + _ROPE, q_out, k_out, query, key, q_weight, k_weight,
                     turns, positions)
-    _check(lib().pa_norm_rope(*ptrs, *sizes, _token_stride(q_out), _token_stride(k_out),
-                              _token_stride(query), _token_stride(key), eps, interleaved,
+    _check(lib().pa_norm_rope(*ptrs, *sizes, sqo, sko, sq, sk, eps, interleaved,
                               _DTYPE[query.dtype], _stream(stream)), "pa_norm_rope")
 
 
@@ -963,13 +961,13 @@ def norm_rope_and_cache(q_out: torch.Tensor, query: torch.Tensor, key: torch.Ten
                         v_scale: float = 1.0, stream=None):
     """pa_norm_rope_and_cache: norm_rope whose keys go, with value [T, Hkv, D], to their cache
     slots (as reshape_and_cache after it, bit for bit)."""
-    sizes = _rope_sizes(query, key, (("q_out", q_out, query), ("value", value, key)), q_weight,
-                        k_weight, turns, positions)
+    sizes, (sq, sk, sqo, sv) = _rope_sizes(query, key, q_out, value, "value", q_weight, k_weight,
+                                           turns, positions)
     kc, stored = k_cache.shape, torch.uint8 if kv_dtype == "fp8_e4m3" else key.dtype
     if not (kv_dtype in ("auto", "fp8_e4m3") and len(kc) == 4 and v_cache.shape == kc and
             kc[1] == sizes[2] and kc[3] == sizes[3] and
-            k_cache.dtype == v_cache.dtype == stored and slot_mapping_.shape == query.shape[:1] and
-            slot_mapping_.dtype == torch.int64 and k_cache.is_contiguous() and
+            k_cache.dtype is v_cache.dtype is stored and slot_mapping_.shape == query.shape[:1] and
+            slot_mapping_.dtype is torch.int64 and k_cache.is_contiguous() and
             v_cache.is_contiguous() and slot_mapping_.is_contiguous()):
         _need(kv_dtype in ("auto", "fp8_e4m3"),
               f"kv_dtype: {kv_dtype!r} is not 'auto' or 'fp8_e4m3'")
@@ -980,9 +978,7 @@ def norm_rope_and_cache(q_out: torch.Tensor, query: torch.Tensor, key: torch.Ten
     ptrs = _strided(stream, "q_out query key value k_cache v_cache slot_mapping q_weight k_weight "
                     "turns positions", q_out, query, key, value, k_cache, v_cache, slot_mapping_,
                     q_weight, k_weight, turns, positions)
-    _check(lib().pa_norm_rope_and_cache(*ptrs, *sizes, kc[2], kc[0],
-                                        _token_stride(q_out), _token_stride(query),
-                                        _token_stride(key), _token_stride(value), eps,
+    _check(lib().pa_norm_rope_and_cache(*ptrs, *sizes, kc[2], kc[0], sqo, sq, sk, sv, eps,
                                         interleaved, _DTYPE[query.dtype], _KV[kv_dtype], k_scale,
                                         v_scale, _stream(stream)), "pa_norm_rope_and_cache")
 
@@ -996,14 +992,17 @@ def _check_page_scales(k_scales, v_scales, k_cache):
 def _block_args(k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, num_kv_heads: int,
                 head_dim: int, cu_q=None):
     """(NB, bs, S, MB) of a consistent block-scaled cache and its tables; raises on others."""
-    k, bt = k_cache.shape, block_tables.shape
+    k, bt, i32 = k_cache.shape, block_tables.shape, torch.int32
     if (len(k) == 4 and len(bt) == 2 and k[1] == num_kv_heads and k[3] == head_dim and
-            v_cache.shape == k and k_cache.dtype == v_cache.dtype == torch.uint8 and
+            v_cache.shape == k and k_cache.dtype is v_cache.dtype is torch.uint8 and
             k_scales.shape == v_scales.shape == k[:2] and
-            k_scales.dtype == v_scales.dtype == torch.float32 and
-            context_lens.shape == bt[:1] and (cu_q is None or cu_q.shape == (bt[0] + 1,)) and
-            block_tables.dtype == context_lens.dtype == torch.int32 and
-            (cu_q is None or cu_q.dtype == torch.int32)):
+            k_scales.dtype is v_scales.dtype is torch.float32 and
+            context_lens.shape == bt[:1] and block_tables.dtype is context_lens.dtype is i32 and
+            (cu_q is None or cu_q.dtype is i32 and cu_q.shape == (bt[0] + 1,) and
+             cu_q.is_contiguous()) and
+            k_cache.is_contiguous() and v_cache.is_contiguous() and k_scales.is_contiguous() and
+            v_scales.is_contiguous() and block_tables.is_contiguous() and
+            context_lens.is_contiguous()):
         return k[0], k[2], bt[0], bt[1]
     _check_caches(k_cache, v_cache, num_kv_heads, head_dim, torch.uint8)
     _check_page_scales(k_scales, v_scales, k_cache)
@@ -1014,7 +1013,7 @@ def _block_args(k_cache, v_cache, k_scales, v_scales, block_tables, context_lens
         _dtype("cu_q", cu_q, torch.int32)
     _shape("context_lens", context_lens, bt[:1])
     _dtype("context_lens", context_lens, torch.int32)
-    raise ValueError("inconsistent arguments")
+    raise ValueError("caches, scales, tables, offsets and lengths must be contiguous")
 
 
 def append_fp8_block(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor,
@@ -1024,22 +1023,22 @@ def append_fp8_block(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tens
     """pa_append_fp8_block: key / value [T, Hkv, D] (offsets cu_q [S + 1], the last tokens of
     each sequence's context; tokens may be strided) into FP8 E4M3 caches (uint8 codes) with a
     scale per block and kv head (fp32 [NB, Hkv])."""
-    kv = key.shape
-    if not (len(kv) == 3 and key.dtype in _DTYPE and _dense_heads(key, kv, key.dtype) and
-            _dense_heads(value, kv, key.dtype)):
+    kv, dtype = key.shape, key.dtype
+    ok = len(kv) == 3 and dtype in _DTYPE
+    sk, sv = (_dense_heads(key, kv, dtype), _dense_heads(value, kv, dtype)) if ok else (0, 0)
+    if not (sk and sv):
         _heads("key", key)
         _heads("value", value)
-        _need(key.dtype in _DTYPE, f"key: unsupported dtype {key.dtype}")
+        _need(dtype in _DTYPE, f"key: unsupported dtype {dtype}")
         _shape("value", value, kv)
-        _dtype("value", value, key.dtype)
+        _dtype("value", value, dtype)
     NB, bs, S, MB = _block_args(k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
                                 kv[1], kv[2], cu_q)
-    ptrs = _strided(stream, "key value", key, value)
-    ptrs += _pointers(stream, "k_cache v_cache k_scales v_scales block_tables cu_q context_lens",
-                      k_cache, v_cache, k_scales, v_scales, block_tables, cu_q, context_lens)
-    _check(lib().pa_append_fp8_block(*ptrs, kv[0], S, kv[1], kv[2], bs, NB, MB,
-                                     _token_stride(key), _token_stride(value), _DTYPE[key.dtype],
-                                     _stream(stream)), "pa_append_fp8_block")
+    ptrs = _strided(stream, "key value k_cache v_cache k_scales v_scales block_tables cu_q "
+                    "context_lens", key, value, k_cache, v_cache, k_scales, v_scales, block_tables,
+                    cu_q, context_lens)
+    _check(lib().pa_append_fp8_block(*ptrs, kv[0], S, kv[1], kv[2], bs, NB, MB, sk, sv,
+                                     _DTYPE[dtype], _stream(stream)), "pa_append_fp8_block")
 
 
 def decode_fp8_block(out: torch.Tensor, query: torch.Tensor, k_cache: torch.Tensor,
@@ -1048,17 +1047,19 @@ def decode_fp8_block(out: torch.Tensor, query: torch.Tensor, k_cache: torch.Tens
                      scale: float, workspace: torch.Tensor, stream=None):
     """pa_decode_fp8_block: decode over the cache of append_fp8_block (workspace:
     decode_workspace_size bytes)."""
-    *ptrs, ws = _pointers(stream, "out query k_cache v_cache k_scales v_scales block_tables "
-                          "context_lens workspace", out, query, k_cache, v_cache, k_scales,
-                          v_scales, block_tables, context_lens, workspace)
+    *ptrs, ws = _strided(stream, "out query k_cache v_cache k_scales v_scales block_tables "
+                         "context_lens workspace", out, query, k_cache, v_cache, k_scales,
+                         v_scales, block_tables, context_lens, workspace)
     q = query.shape
     NB, bs, S, MB = _block_args(k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
                                 num_kv_heads, q[-1])
     if not (len(q) == 3 and q[0] == S and out.shape == q and query.dtype in _DTYPE and
-            out.dtype == query.dtype):
+            out.dtype is query.dtype and out.is_contiguous() and query.is_contiguous() and
+            workspace.is_contiguous()):
         _check_decode_args(out, query, k_cache, v_cache, block_tables, context_lens, num_kv_heads,
                            torch.uint8)
         _need(query.dtype in _DTYPE, f"query: unsupported dtype {query.dtype}")
+        raise ValueError("out, query, workspace: must be contiguous")
     _check(lib().pa_decode_fp8_block(*ptrs, S, q[1], num_kv_heads, q[2], bs, NB, MB, scale,
                                      _DTYPE[query.dtype], ws, _nbytes(workspace),
                                      _stream(stream)), "pa_decode_fp8_block")
@@ -1075,16 +1076,18 @@ def prefill_fp8_block(out: torch.Tensor, query: torch.Tensor, k_cache: torch.Ten
                       stream=None):
     """pa_prefill_fp8_block: causal attention of query [T, Hq, D] (the last tokens of each
     sequence's context, offsets cu_q [S + 1]) over the cache of append_fp8_block."""
-    *ptrs, ws = _pointers(stream, "out query k_cache v_cache k_scales v_scales block_tables cu_q "
-                          "context_lens workspace", out, query, k_cache, v_cache, k_scales,
-                          v_scales, block_tables, cu_q, context_lens, workspace)
+    *ptrs, ws = _strided(stream, "out query k_cache v_cache k_scales v_scales block_tables cu_q "
+                         "context_lens workspace", out, query, k_cache, v_cache, k_scales,
+                         v_scales, block_tables, cu_q, context_lens, workspace)
     q = query.shape
     if not (len(q) == 3 and out.shape == q and query.dtype in _DTYPE and
-            out.dtype == query.dtype):
+            out.dtype is query.dtype and out.is_contiguous() and query.is_contiguous() and
+            workspace.is_contiguous()):
         _need(len(q) == 3, "query: expected [num_tokens, num_heads, head_dim]")
         _shape("out", out, q)
         _dtype("out", out, query.dtype)
-        _need(False, f"query: unsupported dtype {query.dtype}")
+        _need(query.dtype in _DTYPE, f"query: unsupported dtype {query.dtype}")
+        raise ValueError("out, query, workspace: must be contiguous")
     NB, bs, S, MB = _block_args(k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
                                 num_kv_heads, q[2], cu_q)
     _check(lib().pa_prefill_fp8_block(*ptrs, q[0], S, q[1], num_kv_heads, q[2], bs, NB, MB,
