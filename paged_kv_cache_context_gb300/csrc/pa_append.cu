@@ -15,7 +15,9 @@
 // table, scale beside rows). Work: a warp per (page, kv head, K or V), which holds
 // up to 4096 elements of the page's new rows in registers between the maximum and the
 // codes (a page of more is read a second time, from L2); no page is met by two
-// warps, so there are no atomics and the same inputs give the same bits.
+// warps, so there are no atomics and the same inputs give the same bits. Measured: 47,662
+// tokens of 2 x 8 heads of 128 from bf16, 47 us (293 MB at 6.2 TB/s, 0.92 of a copy; a CTA per
+// page with two reads of its rows 93 us), 32 single tokens 2.4 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
