@@ -2072,9 +2072,9 @@ cudaError_t dispatch_decode(const DecodeParams& prm, dim3 grid, int D, int GT, i
 // the K scale goes onto the page's logits, the V scale onto its weights before these are
 // rounded, which are held at the top of f16's range by the largest V scale's exponent.
 // Measured: 32 sequences of 512 to 4096 tokens, 32 query and 8 kv heads of 128, bf16, 43 us
-// (154 MB at 3.5 TB/s: the start, the page lists and the ends of 760 CTAs are 20 us of it), 64
-// of 1024 to 8192 with 32 kv heads of 96, f16, 348 us (1838 MB at 5.3 TB/s; issue slots 55 %,
-// each consumer warp's chain of dependent steps the rest), one of 500 tokens 12.8 us.
+// (154 MB at 3.5 TB/s: 25 pages a CTA, beside which its start and end count), 64 of 1024 to
+// 8192 with 32 kv heads of 96, f16, 348 us (1838 MB at 5.3 TB/s; issue slots 55 %, each consumer
+// warp's chain of dependent steps the rest), one of 500 tokens 12.8 us.
 template <typename QT, int D, int GT>
 cudaError_t dispatch_block_bs(const DecodeParams& prm, dim3 grid, int BS, cudaStream_t stream) {
   switch (BS) {
