@@ -795,7 +795,8 @@ pa_status pa_append_fp8_block(const void* key, const void* value, uint8_t* k_cac
  * and V_j likewise. The K scale multiplies the fp32 logit; the V scale the weight, which
  * is then rounded to f16 and keeps its precision down to 2^-21 of the row's largest
  * product for V scales from 2^-60 to 2^60; the running sum takes the weights
- * unrounded; q is carried in f16 (exact for a bf16 query inside f16's range).
+ * unrounded, with f16 queries rounded alike where the V scale is a power of two (a lone
+ * token's output is then its V exactly); q is carried in f16 (exact for a bf16 query inside f16's range).
  * Supported: q_dtype BF16 or F16 (else PA_ERR_DTYPE). workspace: at least
  * pa_decode_workspace_size() bytes (PA_ERR_NULL / PA_ERR_WORKSPACE), 16-byte aligned;
  * contents on entry do not matter; calls that may overlap on the GPU need one each.
@@ -820,7 +821,8 @@ pa_status pa_decode_fp8_block(void* out, const void* query, const uint8_t* k_cac
  * widened exactly to f16 and q is carried in f16 (exact for a bf16 query inside f16's
  * range); the weights, with their page's V scale, are rounded to f16 and keep their
  * precision down to 2^-21 of the row's largest product of weight and scale; the running
- * sum takes them unrounded; fp32 accumulation; output rounded to q_dtype. V scales are
+ * sum takes them unrounded, with f16 queries rounded alike for at least a row's first 32
+ * tokens; fp32 accumulation; output rounded to q_dtype. V scales are
  * taken from 2^-60 to 2^60: a smaller one counts as zero, a larger one as 2^60.
  * A NaN code in V makes that element NaN for the rows that see it, and it may for rows up to
  * 127 tokens before it (a weight of zero times NaN); rows of a block past n_s may hold

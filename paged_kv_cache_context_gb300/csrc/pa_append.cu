@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
   // ---- the sequence and page of this item (32 sequences at a time); the first warp goes on to
   // the end and flags what does not fit
   const bool reporter = index == 0;
-  long long before = 0;  // pages of the sequences before this round's
+  long long before = 0;  // pages of the sequences before these 32
   int s = -1, q0 = 0, len = 0, n = 0, page = 0;
   for (int b = 0; b < p.num_seqs && (s < 0 || reporter); b += 32) {
     AppendSeq q{};
