@@ -481,3 +481,59 @@ def test_projection_to_attention_step_by_step():
             # 2^-9 for what growing has lost)
             tol = np.abs(want[:, h].numpy()) * 2.0 ** -4 * 1.001 + step * 2.0 ** -9
             assert (np.abs(K - want[:, h].numpy()) <= tol).all()
+
+
+def test_blocks_past_32_bit_offsets():
+    """Codes beyond 4 GB of cache: append, decode and prefill as in a small one, bit for bit."""
+    H, D, bs, S = 8, 128, 32, 3
+    lens, news = [70, 33, 200], [70, 1, 64]
+    c = BlockCache(lens, H, D, bs, seed=9)
+    key, value = (x.cuda() for x in draw_rows(sum(news), H, D, torch.bfloat16, 10))
+    q = queries(news, 16, D, torch.bfloat16).cuda()
+    cu = i32([0, 70, 71, 135])
+    small = {x: c.dev()[x].clone() for x in ("k", "v", "ks", "vs")}
+    n = small["k"].shape[0]
+    first = 2 ** 32 // (H * bs * D) + 5
+    big = {x: torch.empty((first + n,) + t.shape[1:], dtype=t.dtype, device="cuda")
+           for x, t in small.items()}
+    for x, t in small.items():
+        big[x][first:] = t
+    results = []
+    for d, off in ((small, 0), (big, first)):
+        tables = torch.where(c.dev()["tables"] < 0, -1, c.dev()["tables"] + off)
+        pa.append_fp8_block(key, value, d["k"], d["v"], d["ks"], d["vs"], tables, cu, i32(lens))
+        assert pa.get_device_error() == 0
+        c._dev = dict(d, tables=tables, lens=i32(lens))
+        one = queries([1] * S, 16, D, torch.bfloat16, 4).cuda()
+        results.append((decode(c, one, 0.1), prefill(c, q, news, 0.1)))
+    for a, b in zip(*results):
+        assert torch.equal(a, b) and bool(a.isfinite().all())
+    for x, t in small.items():
+        assert torch.equal(big[x][first:].view(torch.uint8), t.view(torch.uint8)), x
+
+
+def test_two_streams_at_once():
+    """Calls that overlap, each with its own workspace, answer as alone."""
+    c = BlockCache([900, 40, 333, 2000], 2, 128, 32, seed=14)
+    news = [200, 3, 64, 1]
+    q = queries(news, 8, 128, torch.bfloat16).cuda()
+    one = queries([1] * 4, 8, 128, torch.bfloat16, 5).cuda()
+    want = prefill(c, q, news, 0.1), decode(c, one, 0.1)
+    d, cu = c.dev(), i32([0, 200, 203, 267, 268])
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    pre = [torch.full((pa.prefill_fp8_block_workspace_size(8, 2, 128),), 0xFF, dtype=torch.uint8,
+                      device="cuda") for _ in range(2)]
+    dec = [workspace(4, 8, c) for _ in range(2)]
+    outs = [[torch.empty_like(q if i < 2 else one) for _ in range(10)] for i in range(4)]
+    args = [d[x] for x in ("k", "v", "ks", "vs", "tables")]
+    torch.cuda.synchronize()
+    for k in range(10):
+        for i, st in enumerate(streams):
+            if i < 2:
+                pa.prefill_fp8_block(outs[i][k], q, *args, cu, d["lens"], 2, 200, 0.1, pre[i],
+                                     stream=st)
+            else:
+                pa.decode_fp8_block(outs[i][k], one, *args, d["lens"], 2, 0.1, dec[i - 2],
+                                    stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[i // 2]) for i in range(4) for o in outs[i])
