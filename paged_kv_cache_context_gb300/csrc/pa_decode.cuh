@@ -1018,14 +1018,18 @@ __device__ __forceinline__ void process_tc8(Tc8State<D>& st, const uint8_t* cons
     r0[j] = 16 * (si % SPP);
     lim[j] = n - r0[j];  // warp-uniform
   }
-  // the slices run in row order, so an empty first slice means no work
-  if (lim[0] <= 0) return;
+  // (an empty slice may stand before others: at block_size 16 a slice is a page, and a page whose
+  // block id is outside the pool holds no tokens)
+  bool any = lim[0] > 0;
+#pragma unroll
+  for (int j = 1; j < SW; ++j) any |= lim[j] > 0;
+  if (!any) return;
 
   // ---- logits of every slice; one lazy running-max update for all of them
   float x[SW][4];
 #pragma unroll
   for (int j = 0; j < SW; ++j) {
-    if (j == 0 || lim[j] > 0) {
+    if (lim[j] > 0) {
       tc8_logits<Ly, CT, D>(st, kp[j], ksc[j], r0[j], kr, t, lim[j], q_scale, x[j]);
       if constexpr (Ly::SCORED) {
         float* dst = lg + ((warp * SW + j) / SPP) * Ly::BSZ + r0[j] + kr;
@@ -1104,7 +1108,7 @@ __device__ __forceinline__ void process_tc8(Tc8State<D>& st, const uint8_t* cons
   // then O^T += V^T P^T slice by slice
 #pragma unroll
   for (int j = 0; j < SW; ++j) {
-    if (j > 0 && lim[j] <= 0) continue;
+    if (lim[j] <= 0) continue;
     float pw[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
