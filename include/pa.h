@@ -552,10 +552,10 @@ pa_status pa_tree(void* out, const void* query, const void* k_cache, const void*
  * scales or an FP8 E4M3 cache with per-tensor scales. Same computation,
  * arguments and errors, with the dequantisation, the f16 operands and the
  * additional errors of pa_prefill_int8 / pa_prefill_fp8; pages are moved by
- * 1-D bulk copies (no limit on the cache's rows). INT8: V row scales of any
- * size from 2^-60 to 2^60 are held to the precision above, relative to the
- * largest product of weight and scale (a power of two of the scales is carried
- * apart from the f16 product).
+ * 1-D bulk copies (no limit on the cache's rows). INT8: for V row scales of any
+ * size from 2^-60 to 2^60 products of weight and scale keep their precision down to
+ * 2^-20 of the largest weight times the largest scale among neighbouring tokens (a
+ * tile of up to 128; a power of two of the scales is carried apart from the f16 product).
  */
 pa_status pa_tree_int8(void* out, const void* query, const int8_t* k_cache,
                        const int8_t* v_cache, const float* k_scales, const float* v_scales,
@@ -585,8 +585,10 @@ pa_status pa_tree_fp8(void* out, const void* query, const uint8_t* k_cache,
  *                  that the tensor cores take are rounded as there, but they
  *                  are divided by the sum of the unrounded ones, so out is not
  *                  the same bits; and f16 weights keep their precision down
- *                  to 2^-21 of a row's largest, over INT8 for V row scales of
- *                  any size from 2^-60 to 2^60,
+ *                  to 2^-21 of a row's largest, over INT8 (for V row scales of
+ *                  any size from 2^-60 to 2^60) their products with the scales
+ *                  down to 2^-20 of the largest weight times the largest scale
+ *                  among 32 neighbouring tokens,
  *   scores[s][g][j] += sum over the G heads h of kv head g of softmax(logit_h)_j
  * for j in [0, n_s); other entries are left as they are. scores: in/out, fp32
  * [S][Hkv][MB * bs], in the sequence's own token order (not by block, so
@@ -793,10 +795,11 @@ pa_status pa_append_fp8_block(const void* key, const void* value, uint8_t* k_cac
  * arguments, errors and device-side checks as pa_decode, with
  *   K_j[d] = e4m3(k_cache[blk][g][row][d]) * k_scales[blk][g]
  * and V_j likewise. The K scale multiplies the fp32 logit; the V scale the weight, which
- * is then rounded to f16 and keeps its precision down to 2^-21 of the row's largest
- * product for V scales from 2^-60 to 2^60; the running sum takes the weights
- * unrounded, with f16 queries rounded alike where the V scale is a power of two (a lone
- * token's output is then its V exactly); q is carried in f16 (exact for a bf16 query inside f16's range).
+ * is then rounded to f16 and keeps its precision down to 2^-20 of the row's largest
+ * product of weight and scale for V scales from 2^-60 to 2^60; the running sum takes the
+ * weights unrounded, with f16 queries rounded alike where the V scale is a power of two (a
+ * lone token's output is then its V exactly); q is carried in f16 (exact for a bf16 query
+ * inside f16's range).
  * Supported: q_dtype BF16 or F16 (else PA_ERR_DTYPE). workspace: at least
  * pa_decode_workspace_size() bytes (PA_ERR_NULL / PA_ERR_WORKSPACE), 16-byte aligned;
  * contents on entry do not matter; calls that may overlap on the GPU need one each.

@@ -137,8 +137,8 @@ namespace pa {
 // bits and want the exact normaliser). Weights that are rounded to f16 are held
 // kScoredTop = 7 above the reference of the other modes, over an INT8 cache
 // less the exponent of the slices' largest V scale: the products that the MMA
-// takes reach 2^15 at most and keep f16's precision down to 2^-21 of the largest,
-// whatever the scales' size (sum and output are in the same units).
+// takes reach 2^15 at most and keep f16's precision down to 2^-21 (INT8: 2^-20) of the
+// largest, whatever the scales' size (sum and output are in the same units).
 enum : int { kModeSplit = 0, kModeBalanced = 1, kModeScored = 2 };
 constexpr float kScoredTop = 7.f;
 
@@ -1043,31 +1043,47 @@ __device__ __forceinline__ void process_tc8(Tc8State<D>& st, const uint8_t* cons
     }
   }
   float tm0 = fmaxf(x[0][0], x[0][2]), tm1 = fmaxf(x[0][1], x[0][3]);
+  // A block-scaled cache wants the largest product of weight and V scale: every slice's logits
+  // with its own page's V scale, which is below 2^e and held to [-60, 60], so that the sums
+  // stay inside 32 bits (infinities and NaN count as the least). At block_size 16 the slices are
+  // of two pages, whose largest logits stay the lane's own until the piece ends.
+  constexpr bool kPages = Ly::PAGE_SCALES && SPP % SW != 0;
+  auto exponent = [&](int j) -> float {
+    const uint32_t b = lim[j] > 0 ? __float_as_uint(vsc[j][0]) & 0x7FFFFFFFu : 0u;
+    const int e = b < 0x7F800000u ? static_cast<int>(b >> 23) - 126 : -60;
+    return static_cast<float>(min(max(e, -60), 60));
+  };
+  if constexpr (kPages) {
+    st.s_top[0] = fmaxf(st.s_top[0], tm0);
+    st.s_top[1] = fmaxf(st.s_top[1], tm1);
+    const float e0 = exponent(0);
+    tm0 += e0;
+    tm1 += e0;
+  }
 #pragma unroll
   for (int j = 1; j < SW; ++j) {
-    tm0 = fmaxf(tm0, fmaxf(x[j][0], x[j][2]));
-    tm1 = fmaxf(tm1, fmaxf(x[j][1], x[j][3]));
+    const float u0 = fmaxf(x[j][0], x[j][2]), u1 = fmaxf(x[j][1], x[j][3]);
+    float e = 0.f;
+    if constexpr (kPages) {
+      st.s_top[0] = fmaxf(st.s_top[0], u0);
+      st.s_top[1] = fmaxf(st.s_top[1], u1);
+      e = exponent(j);
+    }
+    tm0 = fmaxf(tm0, kPages ? u0 + e : u0);
+    tm1 = fmaxf(tm1, kPages ? u1 + e : u1);
   }
 #pragma unroll
   for (int off = 4; off < 32; off *= 2) {
     tm0 = fmaxf(tm0, __shfl_xor_sync(0xffffffffu, tm0, off));
     tm1 = fmaxf(tm1, __shfl_xor_sync(0xffffffffu, tm1, off));
   }
-  st.s_top[0] = fmaxf(st.s_top[0], tm0);
-  st.s_top[1] = fmaxf(st.s_top[1], tm1);
+  if constexpr (!kPages) {
+    st.s_top[0] = fmaxf(st.s_top[0], tm0);
+    st.s_top[1] = fmaxf(st.s_top[1], tm1);
+  }
   if constexpr (Ly::TOPPED) {
     float top = kScoredTop;
-    if constexpr (Ly::PAGE_SCALES) {
-      // as below, of the slices' pages (warp-uniform)
-      uint32_t most = 0;
-#pragma unroll
-      for (int j = 0; j < SW; ++j)
-        if (lim[j] > 0) {
-          const uint32_t b = __float_as_uint(vsc[j][0]) & 0x7FFFFFFFu;
-          if (b < 0x7F800000u) most = max(most, b);
-        }
-      top -= static_cast<float>(min(max(static_cast<int>(most >> 23) - 126, -60), 60));
-    }
+    if constexpr (Ly::PAGE_SCALES && !kPages) top -= exponent(0);
     if constexpr (Ly::ROW_SCALES) {
       // the largest V scale of the attended rows is below 2^e (the bits of numbers that
       // are not negative are in their order; infinities and NaN are left out); held to
@@ -1319,6 +1335,10 @@ __device__ __forceinline__ void finish_piece_tc8(Tc8State<D>& st, float* mstat, 
   for (int off = 4; off < 32; off *= 2) {
     l[0] += __shfl_xor_sync(0xffffffffu, l[0], off);
     l[1] += __shfl_xor_sync(0xffffffffu, l[1], off);
+    if constexpr (Ly::PAGE_SCALES && Ly::SPP % Ly::SW != 0) {  // (the others share theirs as they go)
+      st.s_top[0] = fmaxf(st.s_top[0], __shfl_xor_sync(0xffffffffu, st.s_top[0], off));
+      st.s_top[1] = fmaxf(st.s_top[1], __shfl_xor_sync(0xffffffffu, st.s_top[1], off));
+    }
   }
   consumer_sync(cbar, cphase, lane, err);  // every warp is done with the stage
 #pragma unroll
