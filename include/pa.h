@@ -823,10 +823,10 @@ pa_status pa_decode_fp8_block(void* out, const void* query, const uint8_t* k_cac
  * up to its own), with K and V as pa_decode_fp8_block. On the tensor cores the codes are
  * widened exactly to f16 and q is carried in f16 (exact for a bf16 query inside f16's
  * range); the weights, with their page's V scale, are rounded to f16 and keep their
- * precision down to 2^-21 of the row's largest product of weight and scale; the running
+ * precision down to 2^-20 of the row's largest product of weight and scale; the running
  * sum takes them unrounded, with f16 queries rounded alike for at least a row's first 32
- * tokens; fp32 accumulation; output rounded to q_dtype. V scales are
- * taken from 2^-60 to 2^60: a smaller one counts as zero, a larger one as 2^60.
+ * tokens; fp32 accumulation; output rounded to q_dtype. V scales are taken with
+ * magnitudes from 2^-60 to 2^60: a smaller one counts as zero, a larger one as 2^60.
  * A NaN code in V makes that element NaN for the rows that see it, and it may for rows up to
  * 127 tokens before it (a weight of zero times NaN); rows of a block past n_s may hold
  * anything.
