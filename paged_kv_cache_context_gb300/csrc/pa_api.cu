@@ -1926,6 +1926,7 @@ PA_API pa_status pa_prefill_fp8_block(void* out, const void* query, const uint8_
   p.part_ml = reinterpret_cast<float2*>(ws + kSlotRows * head_dim * 4);
   p.starts = reinterpret_cast<int4*>(ws + kSlotRows * (head_dim * 4 + 8));
   p.total = reinterpret_cast<long long*>(p.starts + kChunkMaxCtas);
+  p.nan_from = reinterpret_cast<unsigned long long*>(p.total + 2);
   p.err = error_word();
   p.num_seqs = num_seqs;
   p.num_heads = num_heads;

@@ -13,6 +13,7 @@ constexpr int kChunkMaxTile = 128;  // the most cached tokens of a staged tile
 // Persistent CTAs a workspace is sized for: two per SM of 152 (or one of twice the
 // rows), two partial slots each.
 constexpr int kChunkMaxCtas = 152 * 2;
+constexpr int kChunkNanCols = 128;  // the most columns of V
 
 // Sequence s owns query tokens [cu_q[s], cu_q[s + 1]), the last q_len_s of its
 // n_s cached tokens. A CTA's row tile takes tile_tokens of them for one kv head, as
@@ -33,6 +34,9 @@ struct ChunkParams {
   float2* part_ml;              // [C][2][rows of a CTA]: their reference (log2 units) and sum
   int4* starts;                 // [C]: sequence, kv head, row tile and K/V tile a share starts at
   long long* total;             // units of the batch
+  // [C][kChunkNanCols]: per column of V the first unseen-by-some NaN token of a piece, as
+  // (piece + 1) << 32 | ~token (the batch's tokens; 0: none yet)
+  unsigned long long* nan_from;
   unsigned* err;
   int num_seqs, num_heads, num_kv_heads, group, block_size, num_blocks;
   int num_tokens, max_blocks_per_seq, max_q_len;
@@ -44,7 +48,8 @@ struct ChunkParams {
 // Bytes of the partials (independent of the batch).
 inline size_t chunk_workspace_bytes(int D) {
   const size_t slots = (size_t)kChunkMaxCtas * 2;
-  return slots * kChunkRows * D * 4 + slots * kChunkRows * 8 + kChunkMaxCtas * sizeof(int4) + 16;
+  return slots * kChunkRows * D * 4 + slots * kChunkRows * 8 + kChunkMaxCtas * sizeof(int4) + 16 +
+         (size_t)kChunkMaxCtas * kChunkNanCols * 8;
 }
 
 // Launches the attention and then the join of cut row tiles. D 64, 96 or 128.

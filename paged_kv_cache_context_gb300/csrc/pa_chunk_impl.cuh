@@ -30,6 +30,11 @@
 // at most: 64-token tiles, two CTAs an SM) S has two buffers, and the next tile's
 // product runs under this one's softmax.
 //
+// NaN in V. The products give a masked token the weight zero, and zero times NaN is NaN. So a NaN
+// code of a token that some row of the row tile does not see becomes zero as it is widened, and
+// its token is kept, per column the first of the piece: the rows that see it, those from that
+// token on, get the NaN as their output is stored. Tokens that every row sees keep theirs.
+//
 // What bounds it: the chain of a query tile, S -> softmax -> P V, beside which only the other
 // query tile's runs (TMEM holds two of S and O): about 4500 cycles a tile of 128 tokens, 2800
 // of them softmax. Measured, 32 query and 8 kv heads of 128, bf16: a prompt of 8191 tokens 628
@@ -88,7 +93,7 @@ struct ChunkLayout {
   static constexpr int OFF_BAR = OFF_SC + kChunkScaleRing * NG * 16;
   static constexpr int NBAR = 2 * SLOTS + 2 * RSLOTS + 6 + 2 * HALVES + NQ + kChunkScaleRing;
   static constexpr int OFF_MISC = (OFF_BAR + NBAR * 8 + 15) / 16 * 16;
-  static constexpr int SMEM = OFF_MISC + 64;
+  static constexpr int SMEM = OFF_MISC + 80;
   // TMEM columns: S buffer b at b TT, O of query tile q at 2 TT + q DV
   static constexpr uint32_t TMEM_COLS = 2 * TT + NQ * DV <= 256 ? 256 : 512;
   static_assert(2 * TT + NQ * DV <= (int)TMEM_COLS && CTAS * TMEM_COLS <= 512, "TMEM columns");
@@ -295,6 +300,8 @@ struct ChunkSmem {
   int* misc;            // the share: sequence, kv head, row tile, first unit
   long long* units;     // and its length
   uint32_t* tmem;
+  uint32_t* nan_piece;  // one more than the last piece with tokens in nan_from (0: none)
+  int* done;            // [softmax warps] pieces whose output the warp has stored
   __device__ __forceinline__ ChunkSmem() {
     extern __shared__ __align__(1024) uint8_t dynamic_smem[];
     uint32_t zero = 0;
@@ -315,6 +322,9 @@ struct ChunkSmem {
     misc = reinterpret_cast<int*>(smem + Ly::OFF_MISC);
     units = reinterpret_cast<long long*>(smem + Ly::OFF_MISC + 16);
     tmem = reinterpret_cast<uint32_t*>(smem + Ly::OFF_MISC + 32);
+    nan_piece = tmem + 1;
+    done = reinterpret_cast<int*>(smem + Ly::OFF_MISC + 40);
+    static_assert(Ly::SMX <= 10 && Ly::DV <= kChunkNanCols, "room");
   }
 };
 
@@ -526,6 +536,42 @@ __device__ __forceinline__ void chunk_issue(const ChunkParams& p) {
   if (!ok && lane == 0) raise_error(p.err, PA_DEVERR_TIMEOUT);
 }
 
+// Bytes that are NaN codes, as 0xFF.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
+  return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+}
+// 16 codes of V from column `col` on with NaN codes among them, which not every row sees: zeros
+// in their place, and the token (of the batch) kept for those columns. The piece before is
+// stored first: what was kept for it has then been read.
+template <class Ly>
+__device__ __noinline__ uint4 chunk_keep_nans(const ChunkParams& p, uint4 codes, int col,
+                                              uint32_t token, int piece) {
+  const ChunkSmem<Ly> sm;
+  bool stored = false;
+  for (uint32_t n = 0; !stored && n < kChunkPolls; ++n) {
+    if (n) __nanosleep(2000);
+    stored = true;
+    for (int x = 0; x < Ly::SMX; ++x)
+      stored &= *static_cast<volatile int*>(sm.done + x) >= piece;
+  }
+  __threadfence();
+  if (!stored) raise_error(p.err, PA_DEVERR_TIMEOUT);
+  const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+  uint32_t o[4];
+  const unsigned long long kept = static_cast<unsigned long long>(piece + 1) << 32 | ~token;
+  unsigned long long* from = p.nan_from + (size_t)blockIdx.x * kChunkNanCols + col;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t z = nan_codes(w[j]);
+    o[j] = w[j] & ~z;
+    for (int b = 0; b < 4; ++b)
+      if (stored && (z >> (8 * b) & 1u)) atomicMax(from + 4 * j + b, kept);
+  }
+  if (stored) atomicMax(sm.nan_piece, static_cast<uint32_t>(piece + 1));
+  __threadfence();
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
 // ---- codes widened to f16, four warps
 template <int D, int NQ>
 __device__ __forceinline__ void chunk_widen(const ChunkParams& p) {
@@ -551,17 +597,22 @@ __device__ __forceinline__ void chunk_widen(const ChunkParams& p) {
     return (cid + j * Ly::CONV) % CPR;
   };
   bool ok = true;
-  int sl = 0, rs = 0, filled = 0, ring = 0;
+  int sl = 0, rs = 0, filled = 0, ring = 0, piece = 0;
   uint32_t ph = 1, rph = 0;
   for (int i2 = 0; w.left > 0 && ok;) {
     const bool is_v = i2 & 1;
+    // the tile's tokens from this one on are not seen by every row
+    const int t0 = (w.tile + (i2 >> 1)) * TT;
+    const int ctx = w.q.n - w.q.q_len;  // (and the first token of the chunk)
+    const int unseen = ctx + w.rt * p.tile_tokens + 1 - t0;
     ok = chunk_wait(&sm.raw_full[rs], rph);
     if (ok && filled >= NS) ok = chunk_wait(&sm.empty[sl], ph);
     if (!ok) break;
     uint8_t* dst = sm.base + Ly::OFF_KV + sl * Ly::SLOT;
     const uint4* raw = reinterpret_cast<const uint4*>(sm.base + Ly::OFF_RAW + rs * Ly::RAW);
     const float4* scg = sm.sc + ring * NG;
-    const bool every = __float_as_int(scg[0].w) & (is_v ? kChunkAllV : kChunkAllK);
+    const bool every = is_v ? (__float_as_int(scg[0].w) & kChunkAllV) && unseen >= TT
+                            : (__float_as_int(scg[0].w) & kChunkAllK) != 0;
     constexpr int NX = NJ % 4 == 0 ? 4 : NJ % 3 == 0 ? 3 : 2;  // read together
     static_assert(NJ % NX == 0, "whole rounds");
 #pragma unroll 1
@@ -582,6 +633,11 @@ __device__ __forceinline__ void chunk_widen(const ChunkParams& p) {
             src[x] = make_uint4(src[x].x ^ kSigns, src[x].y ^ kSigns, src[x].z ^ kSigns,
                                 src[x].w ^ kSigns);
           }
+          if (is_v && row >= unseen &&
+              (nan_codes(src[x].x) | nan_codes(src[x].y) | nan_codes(src[x].z) |
+               nan_codes(src[x].w)))
+            src[x] = chunk_keep_nans<Ly>(p, src[x], 16 * c16,
+                                         static_cast<uint32_t>(w.q.q0 + (t0 + row - ctx)), piece);
         }
         uint4 o[2];
         widen8<E4M3>(src[x].x, o[0].x, o[0].y);
@@ -616,6 +672,7 @@ __device__ __forceinline__ void chunk_widen(const ChunkParams& p) {
     if (is_v) ring = (ring + 1) % kChunkScaleRing;
     if (++i2 == 2 * w.len) {
       i2 = 0;
+      ++piece;
       w.next(p);
     }
   }
@@ -648,7 +705,7 @@ __device__ __forceinline__ void chunk_softmax(const ChunkParams& p) {
   // One piece behind: a piece's query goes to shared memory, so that its first product runs,
   // before the output of the one before is stored.
 #pragma unroll 1
-  for (int piece = 0;; ++piece) {
+  for (uint32_t piece = 0;; ++piece) {
     const bool more = w.left > 0;
     const uint32_t orow_b = orow;
     const bool live_b = live, warp_live_b = warp_live, work_b = work, whole_b = whole;
@@ -710,11 +767,21 @@ __device__ __forceinline__ void chunk_softmax(const ChunkParams& p) {
         const size_t slot = (size_t)cta * 2 + (piece > 1 ? 1 : 0);
         QT* dst = static_cast<QT*>(p.out) + (size_t)orow_b * D;
         float4* po = p.part_o + slot * (D / 4) * ROWS + q * kChunkRows + r1;
+        const bool nans = *static_cast<volatile uint32_t*>(sm.nan_piece) == piece;
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 16) {
           uint32_t o[16];
           tmem_ld16(t_o + c0, o);
           tmem_wait_ld();
+          if (nans) {  // (rare)
+            const uint32_t token = orow_b / p.num_heads;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const unsigned long long kept =
+                  __ldcg(p.nan_from + (size_t)cta * kChunkNanCols + c0 + e);
+              if ((kept >> 32) == piece && token >= ~static_cast<uint32_t>(kept)) o[e] = 0x7FFFFFFFu;
+            }
+          }
           if (live_b && whole_b) {
             uint32_t v[8];
 #pragma unroll
@@ -742,6 +809,8 @@ __device__ __forceinline__ void chunk_softmax(const ChunkParams& p) {
       // products overwrite it) are announced
       tc05_fence_before();
     }
+    __syncwarp();
+    if (lane == 0) *static_cast<volatile int*>(sm.done + warp) = piece;
     if (!more) break;
     m = -INFINITY;
     l = 0.f;
@@ -960,6 +1029,12 @@ __global__ void __launch_bounds__(ChunkLayout<D, NQ>::THREADS, ChunkLayout<D, NQ
       for (int i = 0; i < kChunkScaleRing; ++i) mbar_init(&sm.sc_full[i], 1);
       fence_mbar_init();
     }
+  } else if (warp >= Ly::CONV_WARP) {
+    const int x = tid - Ly::CONV_WARP * 32;
+    static_assert(Ly::CONV >= kChunkNanCols, "a thread a column");
+    if (x < kChunkNanCols) p.nan_from[(size_t)cta * kChunkNanCols + x] = 0;
+    if (x < Ly::SMX) sm.done[x] = 0;
+    if (x == 0) *sm.nan_piece = 0;
   } else if (warp < 4) {
     for (int s = cta; s < S; s += C) {
       const ChunkSeq q = chunk_seq(p, s, tid == 0);
