@@ -827,8 +827,8 @@ pa_status pa_decode_fp8_block(void* out, const void* query, const uint8_t* k_cac
  * sum takes them unrounded, with f16 queries rounded alike for at least a row's first 32
  * tokens; fp32 accumulation; output rounded to q_dtype. V scales are taken with
  * magnitudes from 2^-60 to 2^60: a smaller one counts as zero, a larger one as 2^60.
- * A NaN code in V makes that element NaN for the rows that see it and for no others; rows of
- * a block past n_s may hold anything.
+ * A NaN code in V makes that element NaN for the rows that see it and for no others, and a
+ * V scale that is NaN all of theirs; rows of a block past n_s may hold anything.
  *
  * out, query   : [T][Hq][D] of q_dtype (BF16 or F16, else PA_ERR_DTYPE).
  * block_tables : int32 [S][MB].  cu_q : int32 [S + 1].  context_lens : int32 [S].

@@ -11,7 +11,8 @@
 // x_j + log2 vs_j, so it is the row's largest product that f16's range is fitted to
 // (mu = m - 7 with m rounded up to a whole number: weights reach 2^15 and keep full precision
 // 2^-20 below), whatever the pages' scales. log2 |vs| is held to [-60, 60]; a page below counts
-// as zeros. The sign of a V scale goes to the codes as they are widened.
+// as zeros. The sign of a V scale goes to the codes as they are widened, and a scale that is
+// NaN makes them NaN.
 //
 // Work. Units are K/V tiles of (sequence, kv head, row tile) in that order; every
 // CTA takes an equal contiguous share, so prompts, ragged chunks and a few rows over
@@ -62,8 +63,8 @@ constexpr uint32_t kChunkPolls = 1u << 16, kChunkPollNs = 10000;
 constexpr int kChunkScaleRing = 8;  // tiles whose scales are kept
 // Bits kept beside the scales of 16 tokens: their K counts (it is zeros where the block id
 // is bad); K, and V, of the tile's every token count (V as it is); the V scale is below zero;
-// from bit 8 on the rows of V that do.
-enum : int { kChunkKeyed = 1, kChunkAllK = 2, kChunkAllV = 4, kChunkMinusV = 8 };
+// it is NaN; from bit 8 on the rows of V that count.
+enum : int { kChunkKeyed = 1, kChunkAllK = 2, kChunkAllV = 4, kChunkMinusV = 8, kChunkNanV = 16 };
 
 // NQ: query tiles of a CTA.
 template <int D, int NQ>
@@ -375,7 +376,8 @@ __device__ __forceinline__ void chunk_copy(const ChunkParams& p) {
           f.z = exp2f(-lv);
           const int rows = min(16, w.q.n - t);
           f.w = __int_as_float(kChunkKeyed | (vs < 0.f ? kChunkMinusV : 0) |
-                               (fabsf(vs) >= 0x1p-60f ? rows << 8 : 0));
+                               (isnan(vs) ? kChunkNanV : 0) |
+                               (fabsf(vs) < 0x1p-60f ? 0 : rows << 8));
         }
       }
       if (++i == w.len) {
@@ -386,8 +388,9 @@ __device__ __forceinline__ void chunk_copy(const ChunkParams& p) {
     if (!first) {
       const int what = __float_as_int(f_here.w);
       const bool all_k = __all_sync(0xffffffffu, lane >= NG || (what & kChunkKeyed));
-      const bool all_v = __all_sync(0xffffffffu, lane >= NG || ((what >> 8) == 16 &&
-                                                                !(what & kChunkMinusV)));
+      const bool all_v = __all_sync(
+          0xffffffffu,
+          lane >= NG || ((what >> 8) == 16 && !(what & (kChunkMinusV | kChunkNanV))));
       f_here.w = __int_as_float(what | (all_k ? kChunkAllK : 0) | (all_v ? kChunkAllV : 0));
       // lane pp copies page pp (whose first 16 tokens lane pp bs / 16 has looked at)
       const int page = __shfl_sync(0xffffffffu, y_here, (lane << sh) >> 4 & 31);
@@ -628,6 +631,8 @@ __device__ __forceinline__ void chunk_widen(const ChunkParams& p) {
           const int what = __float_as_int(scg[row >> 4].w);
           if (is_v ? (row & 15) >= (what >> 8) : !(what & kChunkKeyed))
             src[x] = make_uint4(0u, 0u, 0u, 0u);
+          else if (is_v && (what & kChunkNanV))
+            src[x] = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
           if (is_v && (what & kChunkMinusV)) {
             constexpr uint32_t kSigns = 0x80808080u;
             src[x] = make_uint4(src[x].x ^ kSigns, src[x].y ^ kSigns, src[x].z ^ kSigns,

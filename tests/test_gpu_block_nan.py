@@ -84,3 +84,27 @@ def test_a_nan_code_in_the_decode(dtype, D, Hkv, G, bs, lens, news):
     assert bool(out[:, :G][bad].isnan().all())
     assert torch.equal(out[:, :G][~bad], clean[:, :G][~bad])
     assert torch.equal(out[:, G:], clean[:, G:])
+
+
+@pytest.mark.parametrize("dtype,D,Hkv,G,bs,lens,news", SHAPES)
+def test_a_nan_scale_of_v_is_nan_for_the_rows_that_see_it(dtype, D, Hkv, G, bs, lens, news):
+    pa.get_device_error()
+    c = BlockCache(lens, Hkv, D, bs, seed=D + 1)
+    q = queries(news, Hkv * G, D, dtype).cuda()
+    clean = prefill(c, q, news, default_scale(D))
+    rng = np.random.default_rng(G)
+    pages = [(s, int(rng.integers(-(-n // bs)))) for s, n in enumerate(lens) if s % 3 == 0]
+    at = [(s, page * bs, dim) for s, page in pages for dim in range(D)]
+    for s, page in pages:
+        c.dev()["vs"][c.tables[s, page].item(), 0] = float("nan")
+    out = prefill(c, q, news, default_scale(D))
+    assert pa.get_device_error() == 0
+    bad = torch.from_numpy(expected(lens, news, Hkv * G, D, at))[:, None, :].expand(-1, G, -1).cuda()
+    assert bool(out[:, :G][bad].isnan().all())
+    # (a row's reference depends on its pages' V scales, NaN among them: rounding may differ)
+    assert bool(out[:, :G][~bad].isfinite().all()) and torch.equal(out[:, G:], clean[:, G:])
+    ones = queries([1] * len(lens), Hkv * G, D, dtype, 5).cuda()
+    one = decode(c, ones, default_scale(D))
+    for s in range(len(lens)):
+        hit = any(s == t for t, _ in pages)
+        assert bool(one[s, :G].isnan().all()) == hit and bool(one[s, G:].isfinite().all())
