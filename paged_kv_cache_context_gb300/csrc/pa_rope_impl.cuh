@@ -88,7 +88,9 @@ __device__ __forceinline__ uint2 rope_codes(const float2 (&x)[4], float scale, f
   uint32_t two[4];
   if (inv != 0.f) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) two[j] = e4m3x2_from_float2(x[j].x * inv, x[j].y * inv);
+    for (int j = 0; j < 4; ++j)  // (a NaN keeps its sign, which a product would not)
+      two[j] = e4m3x2_from_float2(isnan(x[j].x) ? x[j].x : x[j].x * inv,
+                                  isnan(x[j].y) ? x[j].y : x[j].y * inv);
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
