@@ -148,7 +148,11 @@ __global__ void cache_fp8_kernel(const IT* key, const IT* value, uint2* k_cache,
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       // a NaN input keeps its own sign (a NaN quotient's sign is unspecified)
-      const float a = Elem<IT>::to_f32(kp[j]), b = Elem<IT>::to_f32(vp[j]);
+      float a = Elem<IT>::to_f32(kp[j]), b = Elem<IT>::to_f32(vp[j]);
+      if constexpr (std::is_same<IT, __half>::value) {
+        a = nan_signed(a, __half_as_ushort(kp[j]));
+        b = nan_signed(b, __half_as_ushort(vp[j]));
+      }
       xk[j] = isnan(a) ? a : __fdiv_rn(a, k_scale);
       xv[j] = isnan(b) ? b : __fdiv_rn(b, v_scale);
     }

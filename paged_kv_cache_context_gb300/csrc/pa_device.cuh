@@ -543,6 +543,12 @@ __device__ __forceinline__ uint32_t e4m3x2_from_float2(float lo, float hi) {
   return out;
 }
 
+// x, which an element's bits were widened to, with that element's sign where it is NaN: widening
+// f16 drops it.
+__device__ __forceinline__ float nan_signed(float x, uint32_t bits16) {
+  return isnan(x) ? __uint_as_float(0x7FC00000u | (bits16 & 0x8000u) << 16) : x;
+}
+
 // Launch `kern` on `stream` with a programmatic dependency on the previous
 // work in the stream (see pdl_wait / pdl_trigger).
 template <typename... KArgs, typename... Args>

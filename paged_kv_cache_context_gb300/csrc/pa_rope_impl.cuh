@@ -31,6 +31,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "pa_device.cuh"
 #include "pa_rope.cuh"
 
@@ -281,6 +283,12 @@ __global__ void __launch_bounds__(kRopeThreads, 3)
     } else {
       float2 x[4];
       raw.get(x);  // rounded to the input's type first, as two calls would
+      if constexpr (std::is_same<IT, __half>::value) {
+        const uint32_t w[4] = {raw.w[0].x, raw.w[0].y, raw.w[0].z, raw.w[0].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          x[j] = make_float2(nan_signed(x[j].x, w[j]), nan_signed(x[j].y, w[j] >> 16));
+      }
       *reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + at) = rope_codes(x, scale, inv);
     }
   };
