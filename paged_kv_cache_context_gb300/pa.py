@@ -827,7 +827,11 @@ def rope_turns(inv_freq, device=None) -> torch.Tensor:
     pair), taken in 64 bits. Returns int64 [A, R / 2] on `device` (inv_freq's by default):
     the fraction of a turn per position in units of 2^-64. Made once, as weights are.
     """
-    f = torch.as_tensor(inv_freq)
+    try:
+        f = torch.as_tensor(inv_freq)
+    except (TypeError, RuntimeError) as e:
+        raise ValueError("inv_freq: expected numbers") from e
+    _need(not f.is_complex(), "inv_freq: expected real numbers")
     _need(f.dim() in (1, 2), "inv_freq: expected [rot_dim / 2] or [num_axes, rot_dim / 2]")
     f = f[None] if f.dim() == 1 else f
     dev = f.device if device is None else device
@@ -876,6 +880,18 @@ def _rope_args(query, key, q_weight, k_weight, turns, positions):
           f"positions: shape {tuple(positions.shape)}, expected [{A}, {T}]")
     _dtype("positions", positions, torch.int32)
     return T, Hq, key.shape[1], D, 2 * turns.shape[1], A
+
+
+# what the checks run into where an argument is no tensor or has too few dimensions
+_MISFITS = (AttributeError, IndexError, TypeError)
+
+
+def _misfit(names: str, *tensors) -> ValueError:
+    """What is raised then (a norm's weight may be missing)."""
+    for name, t in zip(names.split(), tensors):
+        if not isinstance(t, torch.Tensor) and not (t is None and name.endswith("_weight")):
+            return ValueError(f"{name}: expected a torch tensor")
+    return ValueError(f"too few dimensions among {names}")
 
 
 def _strided(stream, names: str, *tensors):
@@ -932,7 +948,9 @@ def _rope_sizes(query, key, out, other, name, q_weight, k_weight, turns, positio
     return sizes, tuple(_token_stride(t) for t in (query, key, out, other))
 
 
-_ROPE = "query key q_weight k_weight turns positions"
+_ROPE = "q_out k_out query key q_weight k_weight turns positions"
+_ROPE_STORE = ("q_out query key value k_cache v_cache slot_mapping q_weight k_weight turns "
+               "positions")
 
 
 def norm_rope(q_out: torch.Tensor, k_out: torch.Tensor, query: torch.Tensor, key: torch.Tensor,
@@ -944,10 +962,13 @@ def norm_rope(q_out: torch.Tensor, k_out: torch.Tensor, query: torch.Tensor, key
     ([T] for one axis) with turns [A, R / 2] (see rope_turns); pairs (i, i + R / 2), or with
     interleaved (2i, 2i + 1). Tokens may be strided (views of one projection's output); the
     outputs may be the inputs."""
-    sizes, (sq, sk, sqo, sko) = _rope_sizes(query, key, q_out, k_out, "k_out", q_weight, k_weight,
-                                            turns, positions)
-    ptrs = _strided(stream, "q_out k_out " + _ROPE, q_out, k_out, query, key, q_weight, k_weight,
-                    turns, positions)
+    args = q_out, k_out, query, key, q_weight, k_weight, turns, positions
+    try:
+        sizes, (sq, sk, sqo, sko) = _rope_sizes(query, key, q_out, k_out, "k_out", q_weight,
+                                                k_weight, turns, positions)
+        ptrs = _strided(stream, _ROPE, *args)
+    except _MISFITS as e:
+        raise _misfit(_ROPE, *args) from e
     _check(lib().pa_norm_rope(*ptrs, *sizes, sqo, sko, sq, sk, eps, interleaved,
                               _DTYPE[query.dtype], _stream(stream)), "pa_norm_rope")
 
@@ -961,23 +982,27 @@ def norm_rope_and_cache(q_out: torch.Tensor, query: torch.Tensor, key: torch.Ten
                         v_scale: float = 1.0, stream=None):
     """pa_norm_rope_and_cache: norm_rope whose keys go, with value [T, Hkv, D], to their cache
     slots (as reshape_and_cache after it, bit for bit)."""
-    sizes, (sq, sk, sqo, sv) = _rope_sizes(query, key, q_out, value, "value", q_weight, k_weight,
-                                           turns, positions)
-    kc, stored = k_cache.shape, torch.uint8 if kv_dtype == "fp8_e4m3" else key.dtype
-    if not (kv_dtype in ("auto", "fp8_e4m3") and len(kc) == 4 and v_cache.shape == kc and
-            kc[1] == sizes[2] and kc[3] == sizes[3] and
-            k_cache.dtype is v_cache.dtype is stored and slot_mapping_.shape == query.shape[:1] and
-            slot_mapping_.dtype is torch.int64 and k_cache.is_contiguous() and
-            v_cache.is_contiguous() and slot_mapping_.is_contiguous()):
-        _need(kv_dtype in ("auto", "fp8_e4m3"),
-              f"kv_dtype: {kv_dtype!r} is not 'auto' or 'fp8_e4m3'")
-        _check_caches(k_cache, v_cache, sizes[2], sizes[3], stored)
-        _shape("slot_mapping", slot_mapping_, query.shape[:1])
-        _dtype("slot_mapping", slot_mapping_, torch.int64)
-        raise ValueError("k_cache, v_cache, slot_mapping: must be contiguous")
-    ptrs = _strided(stream, "q_out query key value k_cache v_cache slot_mapping q_weight k_weight "
-                    "turns positions", q_out, query, key, value, k_cache, v_cache, slot_mapping_,
-                    q_weight, k_weight, turns, positions)
+    args = (q_out, query, key, value, k_cache, v_cache, slot_mapping_, q_weight, k_weight, turns,
+            positions)
+    try:
+        sizes, (sq, sk, sqo, sv) = _rope_sizes(query, key, q_out, value, "value", q_weight,
+                                               k_weight, turns, positions)
+        kc, stored = k_cache.shape, torch.uint8 if kv_dtype == "fp8_e4m3" else key.dtype
+        if not (kv_dtype in ("auto", "fp8_e4m3") and len(kc) == 4 and v_cache.shape == kc and
+                kc[1] == sizes[2] and kc[3] == sizes[3] and
+                k_cache.dtype is v_cache.dtype is stored and
+                slot_mapping_.shape == query.shape[:1] and slot_mapping_.dtype is torch.int64 and
+                k_cache.is_contiguous() and v_cache.is_contiguous() and
+                slot_mapping_.is_contiguous()):
+            _need(kv_dtype in ("auto", "fp8_e4m3"),
+                  f"kv_dtype: {kv_dtype!r} is not 'auto' or 'fp8_e4m3'")
+            _check_caches(k_cache, v_cache, sizes[2], sizes[3], stored)
+            _shape("slot_mapping", slot_mapping_, query.shape[:1])
+            _dtype("slot_mapping", slot_mapping_, torch.int64)
+            raise ValueError("k_cache, v_cache, slot_mapping: must be contiguous")
+        ptrs = _strided(stream, _ROPE_STORE, *args)
+    except _MISFITS as e:
+        raise _misfit(_ROPE_STORE, *args) from e
     _check(lib().pa_norm_rope_and_cache(*ptrs, *sizes, kc[2], kc[0], sqo, sq, sk, sv, eps,
                                         interleaved, _DTYPE[query.dtype], _KV[kv_dtype], k_scale,
                                         v_scale, _stream(stream)), "pa_norm_rope_and_cache")
@@ -990,15 +1015,16 @@ def _check_page_scales(k_scales, v_scales, k_cache):
 
 
 def _block_args(k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, num_kv_heads: int,
-                head_dim: int, cu_q=None):
-    """(NB, bs, S, MB) of a consistent block-scaled cache and its tables; raises on others."""
+                head_dim: int, cu_q=...):
+    """(NB, bs, S, MB) of a consistent block-scaled cache and its tables (with offsets, where
+    the call has them); raises on others."""
     k, bt, i32 = k_cache.shape, block_tables.shape, torch.int32
     if (len(k) == 4 and len(bt) == 2 and k[1] == num_kv_heads and k[3] == head_dim and
             v_cache.shape == k and k_cache.dtype is v_cache.dtype is torch.uint8 and
             k_scales.shape == v_scales.shape == k[:2] and
             k_scales.dtype is v_scales.dtype is torch.float32 and
             context_lens.shape == bt[:1] and block_tables.dtype is context_lens.dtype is i32 and
-            (cu_q is None or cu_q.dtype is i32 and cu_q.shape == (bt[0] + 1,) and
+            (cu_q is ... or cu_q.dtype is i32 and cu_q.shape == (bt[0] + 1,) and
              cu_q.is_contiguous()) and
             k_cache.is_contiguous() and v_cache.is_contiguous() and k_scales.is_contiguous() and
             v_scales.is_contiguous() and block_tables.is_contiguous() and
@@ -1008,12 +1034,18 @@ def _block_args(k_cache, v_cache, k_scales, v_scales, block_tables, context_lens
     _check_page_scales(k_scales, v_scales, k_cache)
     _need(len(bt) == 2, "block_tables: expected [num_seqs, max_blocks_per_seq]")
     _dtype("block_tables", block_tables, torch.int32)
-    if cu_q is not None:
+    if cu_q is not ...:
         _shape("cu_q", cu_q, (bt[0] + 1,))
         _dtype("cu_q", cu_q, torch.int32)
     _shape("context_lens", context_lens, bt[:1])
     _dtype("context_lens", context_lens, torch.int32)
     raise ValueError("caches, scales, tables, offsets and lengths must be contiguous")
+
+
+_BLOCK_CACHE = "k_cache v_cache k_scales v_scales block_tables"
+_BLOCK_APPEND = "key value " + _BLOCK_CACHE + " cu_q context_lens"
+_BLOCK_DECODE = "out query " + _BLOCK_CACHE + " context_lens workspace"
+_BLOCK_PREFILL = "out query " + _BLOCK_CACHE + " cu_q context_lens workspace"
 
 
 def append_fp8_block(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor,
@@ -1023,20 +1055,22 @@ def append_fp8_block(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tens
     """pa_append_fp8_block: key / value [T, Hkv, D] (offsets cu_q [S + 1], the last tokens of
     each sequence's context; tokens may be strided) into FP8 E4M3 caches (uint8 codes) with a
     scale per block and kv head (fp32 [NB, Hkv])."""
-    kv, dtype = key.shape, key.dtype
-    ok = len(kv) == 3 and dtype in _DTYPE
-    sk, sv = (_dense_heads(key, kv, dtype), _dense_heads(value, kv, dtype)) if ok else (0, 0)
-    if not (sk and sv):
-        _heads("key", key)
-        _heads("value", value)
-        _need(dtype in _DTYPE, f"key: unsupported dtype {dtype}")
-        _shape("value", value, kv)
-        _dtype("value", value, dtype)
-    NB, bs, S, MB = _block_args(k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
-                                kv[1], kv[2], cu_q)
-    ptrs = _strided(stream, "key value k_cache v_cache k_scales v_scales block_tables cu_q "
-                    "context_lens", key, value, k_cache, v_cache, k_scales, v_scales, block_tables,
-                    cu_q, context_lens)
+    args = (key, value, k_cache, v_cache, k_scales, v_scales, block_tables, cu_q, context_lens)
+    try:
+        kv, dtype = key.shape, key.dtype
+        ok = len(kv) == 3 and dtype in _DTYPE
+        sk, sv = (_dense_heads(key, kv, dtype), _dense_heads(value, kv, dtype)) if ok else (0, 0)
+        if not (sk and sv):
+            _heads("key", key)
+            _heads("value", value)
+            _need(dtype in _DTYPE, f"key: unsupported dtype {dtype}")
+            _shape("value", value, kv)
+            _dtype("value", value, dtype)
+        NB, bs, S, MB = _block_args(k_cache, v_cache, k_scales, v_scales, block_tables,
+                                    context_lens, kv[1], kv[2], cu_q)
+        ptrs = _strided(stream, _BLOCK_APPEND, *args)
+    except _MISFITS as e:
+        raise _misfit(_BLOCK_APPEND, *args) from e
     _check(lib().pa_append_fp8_block(*ptrs, kv[0], S, kv[1], kv[2], bs, NB, MB, sk, sv,
                                      _DTYPE[dtype], _stream(stream)), "pa_append_fp8_block")
 
@@ -1047,19 +1081,21 @@ def decode_fp8_block(out: torch.Tensor, query: torch.Tensor, k_cache: torch.Tens
                      scale: float, workspace: torch.Tensor, stream=None):
     """pa_decode_fp8_block: decode over the cache of append_fp8_block (workspace:
     decode_workspace_size bytes)."""
-    *ptrs, ws = _strided(stream, "out query k_cache v_cache k_scales v_scales block_tables "
-                         "context_lens workspace", out, query, k_cache, v_cache, k_scales,
-                         v_scales, block_tables, context_lens, workspace)
-    q = query.shape
-    NB, bs, S, MB = _block_args(k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
-                                num_kv_heads, q[-1])
-    if not (len(q) == 3 and q[0] == S and out.shape == q and query.dtype in _DTYPE and
-            out.dtype is query.dtype and out.is_contiguous() and query.is_contiguous() and
-            workspace.is_contiguous()):
-        _check_decode_args(out, query, k_cache, v_cache, block_tables, context_lens, num_kv_heads,
-                           torch.uint8)
-        _need(query.dtype in _DTYPE, f"query: unsupported dtype {query.dtype}")
-        raise ValueError("out, query, workspace: must be contiguous")
+    args = (out, query, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, workspace)
+    try:
+        *ptrs, ws = _strided(stream, _BLOCK_DECODE, *args)
+        q = query.shape
+        NB, bs, S, MB = _block_args(k_cache, v_cache, k_scales, v_scales, block_tables,
+                                    context_lens, num_kv_heads, q[-1])
+        if not (len(q) == 3 and q[0] == S and out.shape == q and query.dtype in _DTYPE and
+                out.dtype is query.dtype and out.is_contiguous() and query.is_contiguous() and
+                workspace.is_contiguous()):
+            _check_decode_args(out, query, k_cache, v_cache, block_tables, context_lens,
+                               num_kv_heads, torch.uint8)
+            _need(query.dtype in _DTYPE, f"query: unsupported dtype {query.dtype}")
+            raise ValueError("out, query, workspace: must be contiguous")
+    except _MISFITS as e:
+        raise _misfit(_BLOCK_DECODE, *args) from e
     _check(lib().pa_decode_fp8_block(*ptrs, S, q[1], num_kv_heads, q[2], bs, NB, MB, scale,
                                      _DTYPE[query.dtype], ws, _nbytes(workspace),
                                      _stream(stream)), "pa_decode_fp8_block")
@@ -1076,20 +1112,23 @@ def prefill_fp8_block(out: torch.Tensor, query: torch.Tensor, k_cache: torch.Ten
                       stream=None):
     """pa_prefill_fp8_block: causal attention of query [T, Hq, D] (the last tokens of each
     sequence's context, offsets cu_q [S + 1]) over the cache of append_fp8_block."""
-    *ptrs, ws = _strided(stream, "out query k_cache v_cache k_scales v_scales block_tables cu_q "
-                         "context_lens workspace", out, query, k_cache, v_cache, k_scales,
-                         v_scales, block_tables, cu_q, context_lens, workspace)
-    q = query.shape
-    if not (len(q) == 3 and out.shape == q and query.dtype in _DTYPE and
-            out.dtype is query.dtype and out.is_contiguous() and query.is_contiguous() and
-            workspace.is_contiguous()):
-        _need(len(q) == 3, "query: expected [num_tokens, num_heads, head_dim]")
-        _shape("out", out, q)
-        _dtype("out", out, query.dtype)
-        _need(query.dtype in _DTYPE, f"query: unsupported dtype {query.dtype}")
-        raise ValueError("out, query, workspace: must be contiguous")
-    NB, bs, S, MB = _block_args(k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
-                                num_kv_heads, q[2], cu_q)
+    args = (out, query, k_cache, v_cache, k_scales, v_scales, block_tables, cu_q, context_lens,
+            workspace)
+    try:
+        *ptrs, ws = _strided(stream, _BLOCK_PREFILL, *args)
+        q = query.shape
+        if not (len(q) == 3 and out.shape == q and query.dtype in _DTYPE and
+                out.dtype is query.dtype and out.is_contiguous() and query.is_contiguous() and
+                workspace.is_contiguous()):
+            _need(len(q) == 3, "query: expected [num_tokens, num_heads, head_dim]")
+            _shape("out", out, q)
+            _dtype("out", out, query.dtype)
+            _need(query.dtype in _DTYPE, f"query: unsupported dtype {query.dtype}")
+            raise ValueError("out, query, workspace: must be contiguous")
+        NB, bs, S, MB = _block_args(k_cache, v_cache, k_scales, v_scales, block_tables,
+                                    context_lens, num_kv_heads, q[2], cu_q)
+    except _MISFITS as e:
+        raise _misfit(_BLOCK_PREFILL, *args) from e
     _check(lib().pa_prefill_fp8_block(*ptrs, q[0], S, q[1], num_kv_heads, q[2], bs, NB, MB,
                                       max_q_len, scale, _DTYPE[query.dtype], ws,
                                       _nbytes(workspace), _stream(stream)),
