@@ -105,8 +105,9 @@ struct ChunkLayout {
   static_assert((RSLOTS + SLOTS) / 2 + 2 < kChunkScaleRing, "scales in use are not overwritten");
 };
 
-// sum of floor((a i + b) / m) over i in [0, n), m a power of two (all >= 0; by turns of
-// Euclid's algorithm on a and m).
+// sum of floor((a i + b) / m) over i in [0, n), m a power of two (all >= 0): whole parts are
+// taken out and the sum is turned over to one of fewer terms, as Euclid's algorithm goes on a
+// and m (Graham, Knuth and Patashnik, Concrete Mathematics, section 3.5).
 __device__ __noinline__ long long floor_sum(long long n, int m, int a, long long b) {
   unsigned long long sum = 0, N = n, M = m, A = a, B = b;
   while (N > 0) {

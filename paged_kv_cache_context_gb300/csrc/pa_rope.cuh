@@ -1,6 +1,6 @@
 // pa_rope.cuh -- norm and rotation of query and key heads, with or without the
-// write to the paged cache: the launcher's parameters, shared by pa_rope.cu (the
-// kernel) and pa_api.cu (the entry points).
+// write to the paged cache: the launcher's parameters, shared by pa_rope_impl.cuh
+// (the kernel) and pa_api.cu (the entry points).
 #pragma once
 
 #include <cuda_runtime.h>

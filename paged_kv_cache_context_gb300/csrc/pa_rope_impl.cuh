@@ -345,6 +345,7 @@ template <typename IT, int L>
 cudaError_t launch_rope_lanes(RopeParams& p, int store, cudaStream_t st) {
   constexpr int GROUPS = kRopeThreads / L;
   const int rows = p.heads + (store == kRopeRows ? 1 : 2) * p.kv_heads;
+  // (Figures: 32 query and 8 key heads of 128, bf16, without a cache.)
   // A lane group takes up to 20 heads of a token, whose angles and weights it has then worked
   // out once (16384 tokens of 40 heads: 20 a group 73 us, 10 80 and 5 111); fewer where that
   // leaves the GPU short of CTAs (512 tokens: 20 14.4 us, 10 8.4 and 5 6.2). Of a few tokens a

@@ -824,8 +824,9 @@ def rope_turns(inv_freq, device=None) -> torch.Tensor:
     """The `turns` of norm_rope from frequencies in radians per position.
 
     inv_freq [R / 2], or [A, R / 2] for positions of A axes (0 where an axis does not turn a
-    pair), taken in 64 bits. Returns int64 [A, R / 2] on `device` (inv_freq's by default):
-    the fraction of a turn per position in units of 2^-64. Made once, as weights are.
+    pair), taken in 64 bits (an angle is off by about 2^-54 of a turn a position). Returns int64
+    [A, R / 2] on `device` (inv_freq's by default): the fraction of a turn per position in units
+    of 2^-64. Made once, as weights are.
     """
     try:
         f = torch.as_tensor(inv_freq)
