@@ -775,8 +775,8 @@ pa_status pa_norm_rope_and_cache(void* q_out, const void* query, const void* key
  * v_scales     : in/out, fp32 [NB][Hkv]; what a page's scale held before its first row is
  *                written does not matter.
  * block_tables : int32 [S][MB].  cu_q : int32 [S + 1].  context_lens : int32 [S].
- * Precondition: the blocks written belong to one sequence only (pa_copy_blocks first where
- * the last block is shared; its scales are copied by the caller). Rows share their page's
+ * Precondition: the blocks written belong to one sequence only, and to one place of its table
+ * (pa_copy_blocks first where the last block is shared; its scales are copied by the caller). Rows share their page's
  * scale, so pa_compact, which moves rows singly, does not serve this cache.
  * Supported: D 64, 96 or 128 (PA_ERR_HEAD_DIM); bs 16, 32 or 64 (PA_ERR_BLOCK_SIZE); strides
  * that are multiples of 16 bytes (PA_ERR_SHAPE). Device-side checks: offsets that do not fit

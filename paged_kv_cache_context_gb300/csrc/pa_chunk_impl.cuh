@@ -38,9 +38,10 @@
 //
 // What bounds it: the chain of a query tile, S -> softmax -> P V, beside which only the other
 // query tile's runs (TMEM holds two of S and O): about 4500 cycles a tile of 128 tokens, 2800
-// of them softmax. Measured, 32 query and 8 kv heads of 128, bf16: a prompt of 8191 tokens 628
-// us (875 TFLOP/s, 0.45 of a library matrix product's rate), 512 new tokens in each of 32
-// sequences of 512 to 4096 745 us (751 TFLOP/s), 16 new of 16384 42 us.
+// of them softmax. Measured, 32 query and 8 kv heads of 128, bf16: a prompt of 8191 tokens 627
+// us (877 TFLOP/s, 0.45 of a library matrix product's rate), 512 new tokens in each of 32
+// sequences of 512 to 4096 750 us (746 TFLOP/s), 16 new of 16384 41 us. The looking for NaN and
+// the one more store of every CTA's start are 0.5 % of the first two, 2.5 % of the last.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -1180,10 +1181,10 @@ cudaError_t launch_chunk_nq(ChunkParams& p, cudaStream_t st) {
                     dim3(kChunkJoinThreads), 0, st, p);
 }
 
-// Two query tiles where the longest chunk has rows for them (a prompt of 8191 tokens 628 us,
+// Two query tiles where the longest chunk has rows for them (a prompt of 8191 tokens 627 us,
 // with one 876; 64 new of 4096 in 8 sequences 62 and 80), one where half the rows
-// would be empty (8 new of 4096 in 32 sequences 120 us, with two 140; 16 of 16384 in one, where
-// shares are longer than tiles are many, 42 and 36).
+// would be empty (8 new of 4096 in 32 sequences 123 us, with two 140; 16 of 16384 in one, where
+// shares are longer than tiles are many, 41 and 36).
 template <typename QT, int D>
 cudaError_t launch_chunk_d(ChunkParams& p, cudaStream_t st) {
   return (long long)p.max_q_len * p.group > kChunkRows ? launch_chunk_nq<QT, D, 2>(p, st)
