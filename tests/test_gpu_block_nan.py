@@ -108,3 +108,36 @@ def test_a_nan_scale_of_v_is_nan_for_the_rows_that_see_it(dtype, D, Hkv, G, bs, 
     for s in range(len(lens)):
         hit = any(s == t for t, _ in pages)
         assert bool(one[s, :G].isnan().all()) == hit and bool(one[s, G:].isfinite().all())
+
+
+def test_a_nan_that_comes_and_goes_between_replays():
+    """What a launch keeps of NaN is its own: one captured call, replayed over a clean cache, one
+    with NaN and the clean one again, with one workspace throughout."""
+    lens, news, Hkv, G, D, bs = [300, 129], [300, 64], 2, 4, 128, 32
+    c = BlockCache(lens, Hkv, D, bs, seed=31)
+    q = queries(news, Hkv * G, D, torch.float16).cuda()
+    clean = prefill(c, q, news, 0.1)
+    d = c.dev()
+    ws = torch.full((pa.prefill_fp8_block_workspace_size(Hkv * G, Hkv, D),), 0xFF, dtype=torch.uint8,
+                    device="cuda")
+    out = torch.zeros_like(q)
+    cu = torch.tensor([0, 300, 364], dtype=torch.int32, device="cuda")
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        pa.prefill_fp8_block(out, q, d["k"], d["v"], d["ks"], d["vs"], d["tables"], cu, d["lens"],
+                             Hkv, 300, 0.1, ws, stream=st)
+    spot = (c.tables[0, 5].item(), 1, 17, 100)  # position 177, kv head 1
+    was = d["v"][spot].item()
+    for i in range(30):
+        bad = i % 3 == 1
+        d["v"][spot] = NAN if bad else was
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        hit = torch.zeros_like(out, dtype=torch.bool)
+        if bad:
+            hit[177:300, G:, 100] = True
+        assert bool(out[hit].isnan().all()) and torch.equal(out[~hit], clean[~hit]), i
+    assert pa.get_device_error() == 0
