@@ -1018,18 +1018,19 @@ __device__ __forceinline__ void process_tc8(Tc8State<D>& st, const uint8_t* cons
     r0[j] = 16 * (si % SPP);
     lim[j] = n - r0[j];  // warp-uniform
   }
-  // (an empty slice may stand before others: at block_size 16 a slice is a page, and a page whose
-  // block id is outside the pool holds no tokens)
+  // Slices of one page run in row order, so an empty first one means no work. At block_size 16
+  // they are of two pages, and the first, its block id outside the pool, may be empty alone.
+  constexpr bool kTwoPages = SPP % SW != 0;
   bool any = lim[0] > 0;
 #pragma unroll
-  for (int j = 1; j < SW; ++j) any |= lim[j] > 0;
+  for (int j = 1; j < SW; ++j) any |= kTwoPages && lim[j] > 0;
   if (!any) return;
 
   // ---- logits of every slice; one lazy running-max update for all of them
   float x[SW][4];
 #pragma unroll
   for (int j = 0; j < SW; ++j) {
-    if (lim[j] > 0) {
+    if ((!kTwoPages && j == 0) || lim[j] > 0) {
       tc8_logits<Ly, CT, D>(st, kp[j], ksc[j], r0[j], kr, t, lim[j], q_scale, x[j]);
       if constexpr (Ly::SCORED) {
         float* dst = lg + ((warp * SW + j) / SPP) * Ly::BSZ + r0[j] + kr;
@@ -1045,9 +1046,9 @@ __device__ __forceinline__ void process_tc8(Tc8State<D>& st, const uint8_t* cons
   float tm0 = fmaxf(x[0][0], x[0][2]), tm1 = fmaxf(x[0][1], x[0][3]);
   // A block-scaled cache wants the largest product of weight and V scale: every slice's logits
   // with its own page's V scale, which is below 2^e and held to [-60, 60], so that the sums
-  // stay inside 32 bits (infinities and NaN count as the least). At block_size 16 the slices are
-  // of two pages, whose largest logits stay the lane's own until the piece ends.
-  constexpr bool kPages = Ly::PAGE_SCALES && SPP % SW != 0;
+  // stay inside 32 bits (infinities and NaN count as the least). Of two pages the largest logits
+  // stay the lane's own until the piece ends.
+  constexpr bool kPages = Ly::PAGE_SCALES && kTwoPages;
   auto exponent = [&](int j) -> float {
     const uint32_t b = lim[j] > 0 ? __float_as_uint(vsc[j][0]) & 0x7FFFFFFFu : 0u;
     const int e = b < 0x7F800000u ? static_cast<int>(b >> 23) - 126 : -60;
@@ -1124,7 +1125,7 @@ __device__ __forceinline__ void process_tc8(Tc8State<D>& st, const uint8_t* cons
   // then O^T += V^T P^T slice by slice
 #pragma unroll
   for (int j = 0; j < SW; ++j) {
-    if (lim[j] <= 0) continue;
+    if ((kTwoPages || j > 0) && lim[j] <= 0) continue;
     float pw[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
